@@ -24,6 +24,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 KFAC_F16 = 0
 KFAC_F32 = 1
 KFAC_F64 = 2
+KFAC_BF16 = 3
 _STATUS = {0: "KFAC_OK", -1: "KFAC_ERR_INVALID", -2: "KFAC_ERR_UNSUPPORTED",
            -3: "KFAC_ERR_WORKSPACE", -4: "KFAC_ERR_HIP"}
 
@@ -47,6 +48,7 @@ class kfac_bn(ctypes.Structure):
 
 _c = ctypes
 _vp, _i32, _sz, _f32 = _c.c_void_p, _c.c_int32, _c.c_size_t, _c.c_float
+_i64 = _c.c_int64
 _P = _c.POINTER
 
 
@@ -86,6 +88,17 @@ _sig("kfac_bn_update", _i32, _P(kfac_bn), _i32, _i32, _P(_vp), _P(_vp), _P(_vp),
      _f32, _f32, _f32, _vp, _sz, _vp)
 _sig("kfac_bn_diag_noalloc", _i32, _P(kfac_bn), _i32, _i32, _P(_vp), _P(_vp), _P(_vp), _P(_vp), _P(_vp),
      _f32, _f32, _f32, _vp)
+_sig("kfac_grad_norm_workspace", _i32, _i32, _P(_i64), _P(_sz))
+_sig("kfac_grad_norm", _i32, _i32, _P(_i64), _P(_i32), _P(_vp), _vp, _vp, _sz, _vp)
+_sig("kfac_grad_clip", _i32, _i32, _P(_i64), _P(_i32), _P(_vp), _P(_i32), _P(_vp), _f32, _vp, _vp, _sz, _vp)
+_sig("kfac_trust_update", _i32, _i32, _P(_i64), _P(_vp), _P(_i32), _P(_vp), _P(_vp), _f32, _P(_vp), _f32, _f32,
+     _vp, _vp, _sz, _vp)
+_sig("kfac_policy_loss_workspace", _i32, _i32, _i32, _i32, _P(_sz))
+_sig("kfac_policy_loss", _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _f32, _f32, _f32,
+     _i32, _f32, _vp, _vp, _vp, _i64, _vp, _sz, _vp)
+_sig("kfac_preference_loss_workspace", _i32, _i32, _i32, _i32, _P(_sz))
+_sig("kfac_preference_loss", _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _f32, _f32, _f32, _vp,
+     _vp, _vp, _vp, _i64, _vp, _sz, _vp)
 _sig("kfac_timing_kernels", _i32)
 _sig("kfac_kernel_name", _c.c_char_p, _i32)
 _sig("kfac_timing_enable", _i32, _i32)
@@ -150,7 +163,7 @@ def _ws(workspace, nbytes, device):
         workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     ptr = workspace.data_ptr()
     pad = (-ptr) % 256
-    return _vp(ptr + pad), workspace.numel() * workspace.element_size() - pad
+    return _vp(ptr + pad), max(0, workspace.numel() * workspace.element_size() - pad)
 
 
 # ---------------------------------------------------------------------------
@@ -338,6 +351,220 @@ def kfac_bn_diag_noalloc(layers, xhat, gout, fisher, precond, params=None, lr=0.
     _check(_lib.kfac_bn_diag_noalloc(_bns(layers), len(layers), dt, _ptrs(xhat), _ptrs(gout), _ptrs(fisher),
                                      _ptrs(precond), None if params is None else _ptrs(params), float(lr),
                                      float(ema_decay), float(shift), _stream(stream)), "kfac_bn_diag_noalloc")
+
+
+# gradient norm, clipping and the bounded update ------------------------------
+
+_ANY_CODE = {torch.float16: KFAC_F16, torch.float32: KFAC_F32, torch.bfloat16: KFAC_BF16}
+
+
+def _on_device(tensors, what):
+    """Refuses tensors that are not on the current device: the library launches there."""
+    here = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    if any(i != here for i in map(torch.Tensor.get_device, tensors)):
+        raise ValueError(f"{what} must be on the current HIP device")
+
+
+def _listed(tensors, what):
+    """(numel, dtype code, pointers) of contiguous tensors on the current device, as
+    arrays for the library."""
+    _on_device(tensors, what)
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise TypeError(f"{what} must be contiguous")
+    n = max(1, len(tensors))
+    try:
+        codes = [_ANY_CODE[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError(f"{what}: unsupported dtype {e.args[0]}") from None
+    return (list(map(torch.Tensor.numel, tensors)), codes,
+            (_vp * n)(*map(torch.Tensor.data_ptr, tensors)))
+
+
+def _scalar_out(t, n, what):
+    if t.dtype != torch.float32 or t.numel() < n or not t.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous float32 tensor of {n} or more")
+
+
+def _call_ws(workspace, nbytes, device, stream):
+    """_ws and the tensor behind it, to be held until the call has been made. A fresh one is
+    allocated on the stream that the call runs on: its memory is free there, and goes to
+    nothing else before the call's kernels are done."""
+    if workspace is not None:
+        _on_device([workspace], "workspace")
+    elif nbytes:
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    return *_ws(workspace, nbytes, device), workspace
+
+
+def _same_sizes(numel, tensors, what):
+    if list(map(torch.Tensor.numel, tensors)) != numel:
+        raise ValueError(f"{what} must have one tensor of the gradient's size for each gradient")
+
+
+def kfac_grad_norm_workspace(numel):
+    out = _sz()
+    _check(_lib.kfac_grad_norm_workspace(len(numel), (_i64 * max(1, len(numel)))(*numel), _c.byref(out)),
+           "kfac_grad_norm_workspace")
+    return out.value
+
+
+def kfac_grad_norm(grad, norm, workspace=None, stream=None):
+    """norm[0] <- sqrt of the sum of squares over all tensors of grad (float16, bfloat16
+    or float32, each its own; see kfac.h)."""
+    numel, codes, ptrs = _listed(grad, "grad")
+    _on_device([norm], "norm")
+    _scalar_out(norm, 1, "norm")
+    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace(numel), norm.device, stream)
+    k = max(1, len(numel))
+    _check(_lib.kfac_grad_norm(len(numel), (_i64 * k)(*numel), (_i32 * k)(*codes), ptrs, norm.data_ptr(), ws, wsb,
+                               _stream(stream)), "kfac_grad_norm")
+
+
+def kfac_grad_clip(grad, out, max_norm, norm, workspace=None, stream=None):
+    """out[i] <- grad[i] * min(1, max_norm / norm), norm[0] <- the global norm; out[i] is
+    grad[i] or a tensor of its size, of its type or float32 (see kfac.h)."""
+    numel, codes, ptrs = _listed(grad, "grad")
+    _same_sizes(numel, out, "out")
+    _, out_codes, out_ptrs = _listed(out, "out")
+    _on_device([norm], "norm")
+    _scalar_out(norm, 1, "norm")
+    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace(numel), norm.device, stream)
+    k = max(1, len(numel))
+    _check(_lib.kfac_grad_clip(len(numel), (_i64 * k)(*numel), (_i32 * k)(*codes), ptrs, (_i32 * k)(*out_codes),
+                               out_ptrs, float(max_norm), norm.data_ptr(), ws, wsb, _stream(stream)),
+           "kfac_grad_clip")
+
+
+def kfac_trust_update(precond, grad, w, lr, delta, step, fisher=None, shift=0.0, workspace=None, stream=None):
+    """w[i] <- w[i] - s * precond[i], s = min(lr, sqrt(2 delta / |q|)), q = sum of
+    <precond[i], grad[i]>; step[:2] <- s, q. Where grad[i] is None, fisher[i] (diagonal)
+    and shift give the gradient (see kfac.h)."""
+    numel, codes, p_ptrs = _listed(precond, "precond")
+    w_numel, w_codes, w_ptrs = _listed(w, "w")
+    if any(c != KFAC_F32 for c in codes + w_codes):
+        raise TypeError("precond and w must be float32")
+    if w_numel != numel or len(grad) != len(numel) or (fisher is not None and len(fisher) != len(numel)):
+        raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
+    k = max(1, len(numel))
+    if any(t is None for t in grad):
+        if fisher is None or any(g is None and f is None for g, f in zip(grad, fisher)):
+            raise ValueError("an entry without a gradient needs its fisher")
+        given = [i for i, t in enumerate(grad) if t is not None]
+        diagonal = [i for i, t in enumerate(grad) if t is None]
+        g_numel, given_codes, given_ptrs = _listed([grad[i] for i in given], "grad")
+        f_numel, f_codes, diagonal_ptrs = _listed([fisher[i] for i in diagonal], "fisher")
+        if any(c != KFAC_F32 for c in f_codes):
+            raise TypeError("fisher must be float32")
+        if g_numel != [numel[i] for i in given] or f_numel != [numel[i] for i in diagonal]:
+            raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
+        g_codes, g_ptrs, f_ptrs = [KFAC_F32] * len(numel), (_vp * k)(), (_vp * k)()
+        for j, i in enumerate(given):
+            g_codes[i], g_ptrs[i] = given_codes[j], given_ptrs[j]
+        for j, i in enumerate(diagonal):
+            f_ptrs[i] = diagonal_ptrs[j]
+    else:
+        g_numel, g_codes, g_ptrs = _listed(grad, "grad")
+        f_ptrs = None
+        if g_numel != numel:
+            raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
+    _on_device([step], "step")
+    _scalar_out(step, 2, "step")
+    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace(numel), step.device, stream)
+    _check(_lib.kfac_trust_update(len(numel), (_i64 * k)(*numel), p_ptrs, (_i32 * k)(*g_codes), g_ptrs, f_ptrs,
+                                  float(shift), w_ptrs, float(lr), float(delta), step.data_ptr(), ws, wsb,
+                                  _stream(stream)), "kfac_trust_update")
+
+
+# losses over logits -----------------------------------------------------------
+
+def kfac_policy_loss_workspace(rows, vocab, seqs=0):
+    out = _sz()
+    _check(_lib.kfac_policy_loss_workspace(int(rows), int(vocab), int(seqs), _c.byref(out)),
+           "kfac_policy_loss_workspace")
+    return out.value
+
+
+def kfac_preference_loss_workspace(rows, vocab, pairs):
+    out = _sz()
+    _check(_lib.kfac_preference_loss_workspace(int(rows), int(vocab), int(pairs), _c.byref(out)),
+           "kfac_preference_loss_workspace")
+    return out.value
+
+
+def _vector(t, dtype, n, what):
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous {dtype} tensor of {n}")
+    return t.data_ptr()
+
+
+def _logit_rows(logits, dlogits, token, mask, others):
+    """Checks the rows of a loss; (rows, vocab, dtype code, logits pointer and pitch,
+    token, mask, dlogits pointer and pitch)."""
+    if logits.dim() != 2 or logits.dtype not in _ANY_CODE:
+        raise TypeError("logits must be [rows, vocab] in float16, bfloat16 or float32")
+    rows, vocab = logits.shape
+    given = [t for t in (logits, token, mask, dlogits, *others) if t is not None]
+    _on_device(given, "every tensor of the call")
+
+    def pitch(t, what):
+        if (vocab > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < vocab):
+            raise TypeError(f"the rows of {what} must be contiguous and apart")
+        return t.stride(0) if rows > 1 else vocab
+
+    if dlogits is not None and (dlogits.shape != logits.shape or dlogits.dtype != logits.dtype):
+        raise TypeError("dlogits must have the shape and type of logits")
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("mask must be bool or uint8")
+    return (rows, vocab, _ANY_CODE[logits.dtype], logits.data_ptr(), pitch(logits, "logits"),
+            _vector(token, torch.int64, rows, "token"),
+            None if mask is None else _vector(mask, mask.dtype, rows, "mask"),
+            None if dlogits is None else dlogits.data_ptr(), 0 if dlogits is None else pitch(dlogits, "dlogits"))
+
+
+def kfac_policy_loss(logits, token, old_logp, advantage, logp, stats, dlogits=None, ref_logp=None, mask=None,
+                     seq_begin=None, by_sequence=False, clip_low=0.2, clip_high=0.2, kl_coef=0.0, grad_scale=1.0,
+                     workspace=None, stream=None):
+    """Clipped policy loss with a KL term over logits [rows, vocab]: stats[:4] <- loss,
+    its surrogate part, mean KL, clipped share; logp <- the tokens' log-probabilities;
+    dlogits <- grad_scale * gradient of the loss (see kfac.h)."""
+    rows, vocab, code, z, ld, tok, msk, d, ldd = _logit_rows(
+        logits, dlogits, token, mask, (old_logp, advantage, logp, stats, ref_logp, seq_begin))
+    seqs = 0 if seq_begin is None else seq_begin.numel() - 1
+    if seq_begin is not None and seqs < 1:
+        raise ValueError("seq_begin needs one offset more than there are sequences")
+    f32 = torch.float32
+    _scalar_out(stats, 4, "stats")
+    ws, wsb, held = _call_ws(workspace, kfac_policy_loss_workspace(rows, vocab, seqs), logits.device, stream)
+    _check(_lib.kfac_policy_loss(
+        rows, vocab, code, z, ld, tok, msk, seqs,
+        None if seq_begin is None else _vector(seq_begin, torch.int32, seqs + 1, "seq_begin"),
+        _vector(old_logp, f32, rows, "old_logp"),
+        None if ref_logp is None else _vector(ref_logp, f32, rows, "ref_logp"),
+        _vector(advantage, f32, rows, "advantage"), float(clip_low), float(clip_high), float(kl_coef),
+        1 if by_sequence else 0, float(grad_scale), _vector(logp, f32, rows, "logp"), stats.data_ptr(), d, ldd, ws,
+        wsb, _stream(stream)), "kfac_policy_loss")
+
+
+def kfac_preference_loss(logits, token, seq_begin, seq_logp, margin, loss, dlogits=None, ref_logp=None, mask=None,
+                         beta=0.1, label_smoothing=0.0, grad_scale=1.0, workspace=None, stream=None):
+    """Preference loss over pairs of sequences (i preferred to pairs + i) of logits
+    [rows, vocab]: loss[0], margin [pairs], seq_logp [2 * pairs], dlogits <- grad_scale *
+    gradient of the loss (see kfac.h)."""
+    rows, vocab, code, z, ld, tok, msk, d, ldd = _logit_rows(
+        logits, dlogits, token, mask, (seq_begin, seq_logp, margin, loss, ref_logp))
+    if seq_begin.numel() % 2 != 1:
+        raise ValueError("seq_begin needs one offset more than two for each pair")
+    pairs = seq_begin.numel() // 2
+    f32 = torch.float32
+    _scalar_out(loss, 1, "loss")
+    ws, wsb, held = _call_ws(workspace, kfac_preference_loss_workspace(rows, vocab, pairs), logits.device, stream)
+    _check(_lib.kfac_preference_loss(
+        rows, vocab, code, z, ld, tok, msk, pairs, _vector(seq_begin, torch.int32, 2 * pairs + 1, "seq_begin"),
+        None if ref_logp is None else _vector(ref_logp, f32, 2 * pairs, "ref_logp"), float(beta),
+        float(label_smoothing), float(grad_scale), _vector(seq_logp, f32, 2 * pairs, "seq_logp"),
+        _vector(margin, f32, pairs, "margin"), loss.data_ptr(), d, ldd, ws, wsb, _stream(stream)),
+        "kfac_preference_loss")
 
 
 # timing -------------------------------------------------------------------

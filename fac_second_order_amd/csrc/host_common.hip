@@ -5,7 +5,7 @@
 #include <cstring>
 #include <vector>
 
-#include "common.hpp"
+#include "row_ops.hpp"
 
 namespace kfac {
 
@@ -134,13 +134,15 @@ TimerScope::~TimerScope() {
   if (on) hipEventRecord(ev_end, stream);
 }
 
-static const char* const kKernelNames[K_COUNT] = {
+static const char* const kKernelNames[K_TOTAL] = {
     "upload_kernel",      "syrk_tile_kernel",   "syrk_reduce_kernel", "pack_kernel",
     "unpack_kernel",      "inv_prep_kernel",    "inv_pivot_kernel",   "inv_panel_kernel",
     "inv_update_kernel",  "inv_finish_kernel",  "gemm_tn_kernel",     "bn_partial_kernel",
     "bn_finish_kernel",   "gemm_tn64_kernel",   "refine_elementwise_kernels",
     "refine_residual_gemm_tn64_kernel",         "refine_correction_gemm_tn_kernel",
-    "shift_assemble_kernel"};
+    "shift_assemble_kernel", "norm_partial_kernel", "norm_finish_kernel", "grad_scale_kernel",
+    "trust_partial_kernel", "trust_apply_kernel",  "loss_count_kernel",  "policy_rows_kernel",
+    "policy_finish_kernel", "pref_rows_kernel",    "pref_pairs_kernel",  "pref_grad_kernel"};
 
 }  // namespace kfac
 
@@ -163,10 +165,10 @@ const char* kfac_status_string(kfac_status s) {
 
 const char* kfac_last_error(void) { return g_err; }
 
-int32_t kfac_timing_kernels(void) { return K_COUNT; }
+int32_t kfac_timing_kernels(void) { return K_TOTAL; }
 
 const char* kfac_kernel_name(int32_t id) {
-  return (id >= 0 && id < K_COUNT) ? kKernelNames[id] : "";
+  return (id >= 0 && id < K_TOTAL) ? kKernelNames[id] : "";
 }
 
 kfac_status kfac_timing_enable(int32_t on) {
@@ -175,7 +177,7 @@ kfac_status kfac_timing_enable(int32_t on) {
 }
 
 kfac_status kfac_timing_only(int32_t id) {
-  if (id < -1 || id >= K_COUNT) return fail(KFAC_ERR_INVALID, "kfac_timing_only: id %d out of range", id);
+  if (id < -1 || id >= K_TOTAL) return fail(KFAC_ERR_INVALID, "kfac_timing_only: id %d out of range", id);
   g_timing.only = id;
   return KFAC_OK;
 }
@@ -187,7 +189,7 @@ kfac_status kfac_timing_reset(void) {
 }
 
 kfac_status kfac_timing_read(int32_t id, double* total_ms, int64_t* launches) {
-  if (id < 0 || id >= K_COUNT || !total_ms || !launches)
+  if (id < 0 || id >= K_TOTAL || !total_ms || !launches)
     return fail(KFAC_ERR_INVALID, "kfac_timing_read: bad id or NULL output");
   double sum = 0;
   int64_t n = 0;

@@ -56,6 +56,8 @@ typedef int32_t kfac_dtype;
 #define KFAC_F16 0                 /* IEEE binary16 */
 #define KFAC_F32 1                 /* IEEE binary32 */
 #define KFAC_F64 2                 /* IEEE binary64 (accumulation of kfac_precondition_ex) */
+#define KFAC_BF16 3                /* bfloat16 (the losses over logits, and gradients that are
+                                      clipped or measured) */
 
 /* One convolution or fully connected layer. Activations are NHWC [n, h, w, c_in];
  * output gradients are NHWC [n, h_out, w_out, c_out] and must satisfy
@@ -302,6 +304,105 @@ kfac_status kfac_bn_diag_noalloc(const kfac_bn* layers, int32_t count, kfac_dtyp
                                  const void* const* xhat, const void* const* gout,
                                  float* const* fisher, float* const* precond, float* const* params,
                                  float lr, float ema_decay, float shift, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kfac_grad_norm - the global norm of `count` gradients, norm = sqrt(sum of squares over
+ * every element of every tensor).
+ *
+ * Tensor i has numel[i] >= 0 contiguous elements of type dtype[i] (KFAC_F16, KFAC_BF16 or
+ * KFAC_F32, each tensor its own; grad[i] is not looked at where numel[i] is 0). norm
+ * (device, one float) receives the norm; squares are summed in fp64 in an order that the
+ * sizes fix (bit-identical results for the same inputs). A tensor that is given twice
+ * counts twice. An infinity or a NaN in a gradient shows in norm. count 0 gives norm 0.
+ *
+ * kfac_grad_clip - out[i] = c * grad[i], c = max_norm / norm where norm > max_norm and 1
+ * otherwise. out_dtype[i] is dtype[i] or KFAC_F32 (a 16-bit gradient widened for
+ * kfac_precondition); the product is formed in fp32 and rounded once to the type of
+ * out. out[i] may be grad[i] if the types are equal (the gradient is then left alone
+ * where c = 1); otherwise no output may share bytes with any input or other output.
+ * Where the norm, as a float, is not finite, c is 1 and norm tells the caller.
+ * max_norm must be positive and finite. Workspace of both: kfac_grad_norm_workspace.
+ * ------------------------------------------------------------------------- */
+kfac_status kfac_grad_norm_workspace(int32_t count, const int64_t* numel, size_t* bytes);
+kfac_status kfac_grad_norm(int32_t count, const int64_t* numel, const kfac_dtype* dtype,
+                           const void* const* grad, float* norm, void* workspace, size_t ws_bytes,
+                           void* stream);
+kfac_status kfac_grad_clip(int32_t count, const int64_t* numel, const kfac_dtype* dtype,
+                           const void* const* grad, const kfac_dtype* out_dtype, void* const* out,
+                           float max_norm, float* norm, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kfac_trust_update - the update of [OTUNYM] eq. (8) with a bound on its predicted KL
+ * divergence. P is a preconditioned gradient and F the damped Fisher that made it from the
+ * gradient g (F P = g), so that to second order the step s P changes the model's
+ * distribution by s^2/2 <P, F P> = s^2/2 <P, g>. With
+ *   q = sum over the tensors of <P_i, g_i>,  s = min(lr, sqrt(2 delta / |q|)),
+ * w_i <- w_i - s P_i in fp32 for every tensor.
+ *
+ * precond[i], w[i]: numel[i] contiguous fp32 elements. grad[i]: as many of grad_dtype[i]
+ * (KFAC_F16, KFAC_BF16 or KFAC_F32). Where grad[i] is NULL the Fisher is diagonal and
+ * fisher[i] (fp32; kfac_bn_diag's, with its shift) gives g = P (fisher + shift);
+ * fisher may be NULL if every grad[i] is given. step (device, two floats) receives s and
+ * q. q is summed in fp64 in a fixed order. Where q is not finite s is 0 and w is left
+ * alone. w must not share bytes with any other buffer of the call; lr must be finite and
+ * >= 0, delta positive and finite. Workspace: kfac_grad_norm_workspace.
+ * ------------------------------------------------------------------------- */
+kfac_status kfac_trust_update(int32_t count, const int64_t* numel, const float* const* precond,
+                              const kfac_dtype* grad_dtype, const void* const* grad,
+                              const float* const* fisher, float shift, float* const* w, float lr,
+                              float delta, float* step, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Losses over logits. logits holds `rows` rows of `vocab` elements (KFAC_F16, KFAC_BF16 or
+ * KFAC_F32), row t at logits + t*ld, ld >= vocab. Row t predicts token[t] (int64):
+ *   l_t = z_t[token] - log sum_j exp(z_t[j]).
+ * The rows are cut into sequences: sequence s has the rows [seq_begin[s],
+ * seq_begin[s+1]), offsets that do not decrease (device, int32, one more than there are
+ * sequences; they are held to [0, rows], whatever they say). A row counts if it lies in a
+ * sequence, mask[t] (uint8, NULL: all ones) is not 0 and 0 <= token[t] < vocab. Nothing
+ * of a row that does not count is read but its token and mask: logits, log-probabilities and
+ * advantages there may hold anything. dlogits (NULL: the loss alone) receives
+ * grad_scale times the gradient of the loss in the logits, in their type, rounded once
+ * from fp32, at the pitch ld_grad >= vocab: zeros in the rows of a sequence that do not
+ * count. Rows outside every sequence are left as they were, in every output. dlogits may
+ * be logits with ld_grad = ld; otherwise they must not overlap. A logit may be -inf;
+ * +inf, NaN or a row of nothing but -inf makes that row's results NaN.
+ * Results are deterministic.
+ *
+ * kfac_policy_loss - the clipped policy loss with a KL term. With r = exp(l - old_logp),
+ * A = advantage, d = ref_logp - l (all [rows] fp32):
+ *   loss = sum_t weight_t (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                          + kl_coef (exp(d) - d - 1)),
+ *   dloss/dl = weight_t (-[r A <= clip(r) A] r A + kl_coef (1 - exp(d))).
+ * weight_t = 1 / (rows that count), or with by_sequence = 1 the mean over the sequences
+ * that have rows that count of the mean over their rows; 0 if none counts. seq_begin
+ * NULL with seqs 0: one sequence of all rows. ref_logp may be NULL if kl_coef is 0 (the
+ * KL is then reported as 0). logp [rows] receives l (0 in rows of a sequence that do not
+ * count); stats (4 floats): the loss, its first part, the mean KL, the weighted share of
+ * rows where the bound holds the ratio.
+ *
+ * kfac_preference_loss - a loss over pairs of sequences: i is preferred to pairs + i.
+ * With L_s the sum of l over the rows of s that count and R_s = ref_logp[s] (2*pairs
+ * fp32; NULL: zeros),
+ *   x_i = beta ((L_i - R_i) - (L_{pairs+i} - R_{pairs+i})),
+ *   loss = mean_i ((1 - e) log(1 + exp(-x_i)) + e log(1 + exp(x_i))), e = label_smoothing.
+ * seq_logp [2*pairs] receives L, margin [pairs] x, loss one float (0 without pairs).
+ * ------------------------------------------------------------------------- */
+kfac_status kfac_policy_loss_workspace(int32_t rows, int32_t vocab, int32_t seqs, size_t* bytes);
+kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype dtype, const void* logits, int64_t ld,
+                             const int64_t* token, const uint8_t* mask, int32_t seqs,
+                             const int32_t* seq_begin, const float* old_logp, const float* ref_logp,
+                             const float* advantage, float clip_low, float clip_high, float kl_coef,
+                             int32_t by_sequence, float grad_scale, float* logp, float* stats,
+                             void* dlogits, int64_t ld_grad, void* workspace, size_t ws_bytes,
+                             void* stream);
+kfac_status kfac_preference_loss_workspace(int32_t rows, int32_t vocab, int32_t pairs, size_t* bytes);
+kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dtype dtype, const void* logits,
+                                 int64_t ld, const int64_t* token, const uint8_t* mask, int32_t pairs,
+                                 const int32_t* seq_begin, const float* ref_logp, float beta,
+                                 float label_smoothing, float grad_scale, float* seq_logp, float* margin,
+                                 float* loss, void* dlogits, int64_t ld_grad, void* workspace,
+                                 size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Per-kernel event timing, for measurement. When enabled on a thread, every
