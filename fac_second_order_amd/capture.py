@@ -7,7 +7,9 @@ the preconditioned gradients (eq. 7-8); BatchNorm uses the diagonal Fisher. This
 module wires a PyTorch model to the library: hooks hand each convolution's and the
 classifier's input and output gradient, and each BatchNorm's normalised input and
 output gradient, to KfacStep in the layouts of include/kfac.h. PyTorch runs the
-network (forward, backward, loss); every K-FAC number is computed by libkfac.
+network (forward, backward, loss); every K-FAC number is computed by libkfac. For a
+policy, whose rows of logits score the choice that was made, the loss and its gradient
+at the logits are the library's too (policy_backward, preference_backward).
 
 Layout conventions (the library's):
   * activations and output gradients NHWC fp16; a convolution weight [c_out, c_in,
@@ -22,6 +24,7 @@ from dataclasses import dataclass
 import torch
 import torch.nn as nn
 
+from . import _lib as K
 from .step import KfacStep
 
 
@@ -139,13 +142,16 @@ class KfacCapture:
     one fp64-residual refinement step of every inverse. A real gradient lies in the
     range of its layer's factors, so where a factor is rank-deficient (batch smaller
     than its order) and the damping small, the preconditioning products cancel and
-    amplify the inverses' fp32 error; the two options remove most of it."""
+    amplify the inverses' fp32 error; the two options remove most of it. max_grad_norm
+    and trust_radius are passed to KfacStep too: they bound the gradients that are
+    preconditioned and the step that is taken."""
 
     def __init__(self, model, damping=1e-3, ema_decay=0.95, refresh_every=1, precond_accum="f32",
-                 refine_inverse=False):
+                 refine_inverse=False, max_grad_norm=None, trust_radius=None):
         self.model = model
         self.precond_accum = precond_accum
         self.refine_inverse = bool(refine_inverse)
+        self.max_grad_norm, self.trust_radius = max_grad_norm, trust_radius
         self.pairs = list(model.kfac_modules())
         self.damping = damping
         self.ema_decay = ema_decay
@@ -241,6 +247,42 @@ class KfacCapture:
         else:
             m.weight.data.copy_(mat)
 
+    # losses over the model's logits ----------------------------------------------
+    @staticmethod
+    def _logit_rows(logits):
+        """[..., vocab] logits as rows for the library, and a gradient of their size."""
+        z = logits.detach().reshape(-1, logits.shape[-1])
+        if z.stride(1) != 1 or (z.shape[0] > 1 and z.stride(0) < z.shape[1]):
+            z = z.contiguous()
+        return z, torch.zeros(z.shape, dtype=z.dtype, device=z.device)
+
+    def policy_backward(self, logits, token, old_logp, advantage, ref_logp=None, mask=None, seq_begin=None,
+                        by_sequence=False, clip_low=0.2, clip_high=0.2, kl_coef=0.0):
+        """Backward pass of the clipped policy loss with a KL term (kfac_policy_loss) over
+        the model's logits [..., vocab], one token, old log-probability and advantage for
+        each row. Returns (stats, logp): the loss, its surrogate part, the mean KL and
+        the clipped share; the rows' log-probabilities."""
+        z, d = self._logit_rows(logits)
+        logp = torch.zeros(z.shape[0], dtype=torch.float32, device=z.device)
+        stats = torch.zeros(4, dtype=torch.float32, device=z.device)
+        K.kfac_policy_loss(z, token, old_logp, advantage, logp, stats, dlogits=d, ref_logp=ref_logp, mask=mask,
+                           seq_begin=seq_begin, by_sequence=by_sequence, clip_low=clip_low, clip_high=clip_high,
+                           kl_coef=kl_coef)
+        logits.backward(d.view(logits.shape))
+        return stats, logp
+
+    def preference_backward(self, logits, token, seq_begin, ref_logp=None, mask=None, beta=0.1, label_smoothing=0.0):
+        """Backward pass of the preference loss (kfac_preference_loss) over the model's
+        logits [..., vocab], whose rows are the preferred sequences and then the others.
+        Returns (loss, margin, seq_logp)."""
+        z, d = self._logit_rows(logits)
+        pairs = seq_begin.numel() // 2
+        seq_logp, margin, loss = (torch.zeros(n, dtype=torch.float32, device=z.device) for n in (2 * pairs, pairs, 1))
+        K.kfac_preference_loss(z, token, seq_begin, seq_logp, margin, loss, dlogits=d, ref_logp=ref_logp, mask=mask,
+                               beta=beta, label_smoothing=label_smoothing)
+        logits.backward(d.view(logits.shape))
+        return loss, margin, seq_logp
+
     # the K-FAC step -------------------------------------------------------------
     def step(self, lr):
         if any(a is None for a in self.act) or any(g is None for g in self.gout):
@@ -249,7 +291,8 @@ class KfacCapture:
         if self.kstep is None:
             layers, bns = self._geometry()
             self.kstep = KfacStep(layers, bns, dev, damping=self.damping, precond_accum=self.precond_accum,
-                                  refine_inverse=self.refine_inverse)
+                                  refine_inverse=self.refine_inverse, max_grad_norm=self.max_grad_norm,
+                                  trust_radius=self.trust_radius)
             self.master = [self._to_matrix(m) for m, _ in self.pairs]
             self.bn_master = [torch.stack([bn.weight.data.float(), bn.bias.data.float()]).contiguous()
                               for bn in self.bns]

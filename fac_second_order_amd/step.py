@@ -41,10 +41,19 @@ class KfacStep:
     units idle) run on a second stream, together with the preconditioning of their
     layers, while the caller's stream inverts the rest, preconditions their layers
     and does the BatchNorm step. The step joins the two streams before it returns;
-    results are the same bits as with one stream."""
+    results are the same bits as with one stream.
+
+    max_grad_norm: step() first clips the layers' weight gradients by their global norm
+    (kfac_grad_clip) into fp32 copies of its own, which it then preconditions; the
+    gradients may be float16, bfloat16 or float32. self.grad_norm holds the norm.
+
+    trust_radius: step() updates the parameters last and together, by the step s P
+    whose predicted KL divergence s^2/2 <P, gradient> is at most this (kfac_trust_update):
+    s is lr where that is smaller. self.trust holds s and <P, gradient>."""
 
     def __init__(self, layers, bn_layers=(), device="cuda", damping=1e-3, bn_shift=None,
-                 in_dtype=torch.float16, precond_accum="f32", refine_inverse=False, side_stream=True):
+                 in_dtype=torch.float16, precond_accum="f32", refine_inverse=False, side_stream=True,
+                 max_grad_norm=None, trust_radius=None):
         self.layers = list(layers)
         self.bn_layers = list(bn_layers)
         self.device = torch.device(device)
@@ -76,6 +85,14 @@ class KfacStep:
         self.out = [torch.empty(g, a, dtype=f32, device=dev) for g, a in zip(self.d_g, self.d_a)]
         self.refine = bool(refine_inverse)
         self.factor_full = [torch.empty(d, d, dtype=f32, device=dev) for d in self.n_all] if self.refine else []
+        self.max_grad_norm, self.trust_radius = max_grad_norm, trust_radius
+        self.grad_norm = self.trust = None
+        self.clipped = []
+        if max_grad_norm is not None:
+            self.clipped = [torch.empty_like(o) for o in self.out]
+            self.grad_norm = torch.zeros(1, dtype=f32, device=dev)
+        if trust_radius is not None:
+            self.trust = torch.zeros(2, dtype=f32, device=dev)
         self.fisher = [torch.zeros(2, b.c, dtype=f32, device=dev) for b in self.bn_layers]
         self.bn_pre = [torch.empty(2, b.c, dtype=f32, device=dev) for b in self.bn_layers]
         code = K.KFAC_F16 if in_dtype == torch.float16 else K.KFAC_F32
@@ -87,6 +104,9 @@ class KfacStep:
             sizes.append(K.kfac_invert_refine_workspace(self.n_all))
         if self.bn_layers:
             sizes.append(K.kfac_bn_diag_workspace(self.bn_layers))
+        if max_grad_norm is not None or trust_radius is not None:
+            sizes.append(K.kfac_grad_norm_workspace([o.numel() for o in self.out] +
+                                                    [f.numel() for f in self.fisher]))
         # one workspace serves every call on the caller's stream: they run one after
         # another; the second stream has its own
         self.workspace = torch.empty(max(sizes) + 256, dtype=torch.uint8, device=dev)
@@ -233,12 +253,38 @@ class KfacStep:
                              sub(self.bn_pre, idx), sub(bn_params, idx), lr, ema_decay, self.bn_shift,
                              self.workspace, stream)
 
+    def clip(self, grads, stream=None):
+        """The gradients to precondition: clipped by their global norm into self.clipped,
+        or as they are without max_grad_norm."""
+        if self.max_grad_norm is None:
+            return grads
+        K.kfac_grad_clip(grads, self.clipped, self.max_grad_norm, self.grad_norm, self.workspace, stream)
+        return self.clipped
+
+    def _bounded_update(self, grads, weights, bn_params, lr, stream):
+        # every parameter that the step updates takes part in the bound
+        P, g, w, fisher = [], [], [], []
+        if weights is not None:
+            P, g, w, fisher = list(self.out), list(grads), list(weights), [None] * len(self.out)
+        if bn_params is not None:
+            P, w = P + self.bn_pre, w + list(bn_params)
+            g, fisher = g + [None] * len(self.bn_pre), fisher + self.fisher
+        K.kfac_trust_update(P, g, w, lr, self.trust_radius, self.trust, fisher, self.bn_shift, self.workspace, stream)
+
     def step(self, act, gout, grads, xhat=(), bn_gout=(), ema_decay=0.0, refresh=True,
              weights=None, bn_params=None, lr=0.0, stream=None):
         """One step. refresh=False is a stale-curvature step: factors and inverses are
         kept, the gradients are preconditioned with them, and BN divides its fresh
         gradient by the stored Fisher (decay 1 keeps it). Given weights and/or
         bn_params, those are updated in place with learning rate lr."""
+        grads = self.clip(grads, stream)
+        if self.trust_radius is not None:
+            self._step(act, gout, grads, xhat, bn_gout, ema_decay, refresh, None, None, lr, stream)
+            self._bounded_update(grads, weights, bn_params, lr, stream)
+        else:
+            self._step(act, gout, grads, xhat, bn_gout, ema_decay, refresh, weights, bn_params, lr, stream)
+
+    def _step(self, act, gout, grads, xhat, bn_gout, ema_decay, refresh, weights, bn_params, lr, stream):
         if not refresh:
             self.precondition(grads, weights, lr, stream)
             self.bn(xhat, bn_gout, 1.0, bn_params, lr, stream)
