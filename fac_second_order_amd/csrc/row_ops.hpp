@@ -19,6 +19,7 @@ enum RowKernelId {
   K_POLICY_FINISH,
   K_PREF_ROWS,
   K_PREF_PAIRS,
+  K_PREF_FINISH,
   K_PREF_GRAD,
   K_TOTAL
 };
