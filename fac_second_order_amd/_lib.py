@@ -6,6 +6,7 @@ the current torch stream (or the one given) to the library, and raises KfacError
 when the library returns a non-zero status. Nothing here computes any part of the
 K-FAC step, and there is no fallback: without the built library, import fails.
 """
+import array
 import ctypes
 import os
 
@@ -88,11 +89,10 @@ _sig("kfac_bn_update", _i32, _P(kfac_bn), _i32, _i32, _P(_vp), _P(_vp), _P(_vp),
      _f32, _f32, _f32, _vp, _sz, _vp)
 _sig("kfac_bn_diag_noalloc", _i32, _P(kfac_bn), _i32, _i32, _P(_vp), _P(_vp), _P(_vp), _P(_vp), _P(_vp),
      _f32, _f32, _f32, _vp)
-_sig("kfac_grad_norm_workspace", _i32, _i32, _P(_i64), _P(_sz))
-_sig("kfac_grad_norm", _i32, _i32, _P(_i64), _P(_i32), _P(_vp), _vp, _vp, _sz, _vp)
-_sig("kfac_grad_clip", _i32, _i32, _P(_i64), _P(_i32), _P(_vp), _P(_i32), _P(_vp), _f32, _vp, _vp, _sz, _vp)
-_sig("kfac_trust_update", _i32, _i32, _P(_i64), _P(_vp), _P(_i32), _P(_vp), _P(_vp), _f32, _P(_vp), _f32, _f32,
-     _vp, _vp, _sz, _vp)
+_sig("kfac_grad_norm_workspace", _i32, _i32, _vp, _P(_sz))
+_sig("kfac_grad_norm", _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp)
+_sig("kfac_grad_clip", _i32, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _sz, _vp)
+_sig("kfac_trust_update", _i32, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _f32, _f32, _vp, _vp, _sz, _vp)
 _sig("kfac_policy_loss_workspace", _i32, _i32, _i32, _i32, _P(_sz))
 _sig("kfac_policy_loss", _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _f32, _f32, _f32,
      _i32, _f32, _vp, _vp, _vp, _i64, _vp, _sz, _vp)
@@ -356,124 +356,122 @@ def kfac_bn_diag_noalloc(layers, xhat, gout, fisher, precond, params=None, lr=0.
 # gradient norm, clipping and the bounded update ------------------------------
 
 _ANY_CODE = {torch.float16: KFAC_F16, torch.float32: KFAC_F32, torch.bfloat16: KFAC_BF16}
+_device_of = torch.Tensor.get_device
 
 
 def _on_device(tensors, what):
     """Refuses tensors that are not on the current device: the library launches there."""
-    here = torch.cuda.current_device() if torch.cuda.is_available() else -2
-    if any(i != here for i in map(torch.Tensor.get_device, tensors)):
+    at = set(map(_device_of, tensors))
+    if at and (len(at) > 1 or min(at) < 0 or min(at) != torch.cuda.current_device()):
         raise ValueError(f"{what} must be on the current HIP device")
 
 
 def _listed(tensors, what):
-    """(numel, dtype code, pointers) of contiguous tensors on the current device, as
-    arrays for the library."""
+    """(numel, dtype code, addresses) of contiguous tensors on the current device."""
     _on_device(tensors, what)
     if not all(map(torch.Tensor.is_contiguous, tensors)):
         raise TypeError(f"{what} must be contiguous")
-    n = max(1, len(tensors))
     try:
         codes = [_ANY_CODE[t.dtype] for t in tensors]
     except KeyError as e:
         raise TypeError(f"{what}: unsupported dtype {e.args[0]}") from None
-    return (list(map(torch.Tensor.numel, tensors)), codes,
-            (_vp * n)(*map(torch.Tensor.data_ptr, tensors)))
+    return list(map(torch.Tensor.numel, tensors)), codes, list(map(torch.Tensor.data_ptr, tensors))
+
+
+# Lists of integers as C arrays; array.array is several times faster to fill than a ctypes one.
+def _words(values):
+    return array.array("q", values or (0,))
+
+
+def _halfwords(values):
+    return array.array("i", values or (0,))
+
+
+def _at(arr):
+    return arr.buffer_info()[0]
 
 
 def _scalar_out(t, n, what):
     if t.dtype != torch.float32 or t.numel() < n or not t.is_contiguous():
         raise TypeError(f"{what} must be a contiguous float32 tensor of {n} or more")
+    return t.data_ptr()
 
 
-def _call_ws(workspace, nbytes, device, stream):
-    """_ws and the tensor behind it, to be held until the call has been made. A fresh one is
-    allocated on the stream that the call runs on: its memory is free there, and goes to
+def _call_ws(workspace, query, sizes, device, stream):
+    """Aligned address and bytes of the call's workspace, and the tensor behind it, to be held
+    until the call has been made. Without one from the caller, query(*sizes) bytes are
+    allocated on the stream that the call runs on: their memory is free there, and goes to
     nothing else before the call's kernels are done."""
     if workspace is not None:
         _on_device([workspace], "workspace")
-    elif nbytes:
+    else:
         with torch.cuda.stream(stream):
-            workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
-    return *_ws(workspace, nbytes, device), workspace
-
-
-def _same_sizes(numel, tensors, what):
-    if list(map(torch.Tensor.numel, tensors)) != numel:
-        raise ValueError(f"{what} must have one tensor of the gradient's size for each gradient")
+            workspace = torch.empty(query(*sizes) + 256, dtype=torch.uint8, device=device)
+    return *_ws(workspace, 1, device), workspace
 
 
 def kfac_grad_norm_workspace(numel):
     out = _sz()
-    _check(_lib.kfac_grad_norm_workspace(len(numel), (_i64 * max(1, len(numel)))(*numel), _c.byref(out)),
-           "kfac_grad_norm_workspace")
+    n = _words(numel)
+    _check(_lib.kfac_grad_norm_workspace(len(numel), _at(n), _c.byref(out)), "kfac_grad_norm_workspace")
     return out.value
 
 
 def kfac_grad_norm(grad, norm, workspace=None, stream=None):
     """norm[0] <- sqrt of the sum of squares over all tensors of grad (float16, bfloat16
     or float32, each its own; see kfac.h)."""
-    numel, codes, ptrs = _listed(grad, "grad")
+    numel, codes, at = _listed(grad, "grad")
     _on_device([norm], "norm")
-    _scalar_out(norm, 1, "norm")
-    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace(numel), norm.device, stream)
-    k = max(1, len(numel))
-    _check(_lib.kfac_grad_norm(len(numel), (_i64 * k)(*numel), (_i32 * k)(*codes), ptrs, norm.data_ptr(), ws, wsb,
-                               _stream(stream)), "kfac_grad_norm")
+    out = _scalar_out(norm, 1, "norm")
+    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace, (numel,), norm.device, stream)
+    n, c, g = _words(numel), _halfwords(codes), _words(at)
+    _check(_lib.kfac_grad_norm(len(numel), _at(n), _at(c), _at(g), out, ws, wsb, _stream(stream)), "kfac_grad_norm")
 
 
 def kfac_grad_clip(grad, out, max_norm, norm, workspace=None, stream=None):
     """out[i] <- grad[i] * min(1, max_norm / norm), norm[0] <- the global norm; out[i] is
     grad[i] or a tensor of its size, of its type or float32 (see kfac.h)."""
-    numel, codes, ptrs = _listed(grad, "grad")
-    _same_sizes(numel, out, "out")
-    _, out_codes, out_ptrs = _listed(out, "out")
+    numel, codes, at = _listed(grad, "grad")
+    out_numel, out_codes, out_at = _listed(out, "out")
+    if out_numel != numel:
+        raise ValueError("out must have one tensor of the gradient's size for each gradient")
     _on_device([norm], "norm")
-    _scalar_out(norm, 1, "norm")
-    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace(numel), norm.device, stream)
-    k = max(1, len(numel))
-    _check(_lib.kfac_grad_clip(len(numel), (_i64 * k)(*numel), (_i32 * k)(*codes), ptrs, (_i32 * k)(*out_codes),
-                               out_ptrs, float(max_norm), norm.data_ptr(), ws, wsb, _stream(stream)),
-           "kfac_grad_clip")
+    norm_at = _scalar_out(norm, 1, "norm")
+    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace, (numel,), norm.device, stream)
+    n, c, g, oc, o = _words(numel), _halfwords(codes), _words(at), _halfwords(out_codes), _words(out_at)
+    _check(_lib.kfac_grad_clip(len(numel), _at(n), _at(c), _at(g), _at(oc), _at(o), float(max_norm), norm_at, ws, wsb,
+                               _stream(stream)), "kfac_grad_clip")
 
 
 def kfac_trust_update(precond, grad, w, lr, delta, step, fisher=None, shift=0.0, workspace=None, stream=None):
     """w[i] <- w[i] - s * precond[i], s = min(lr, sqrt(2 delta / |q|)), q = sum of
     <precond[i], grad[i]>; step[:2] <- s, q. Where grad[i] is None, fisher[i] (diagonal)
     and shift give the gradient (see kfac.h)."""
-    numel, codes, p_ptrs = _listed(precond, "precond")
-    w_numel, w_codes, w_ptrs = _listed(w, "w")
-    if any(c != KFAC_F32 for c in codes + w_codes):
+    numel, codes, p_at = _listed(precond, "precond")
+    w_numel, w_codes, w_at = _listed(w, "w")
+    if any(k != KFAC_F32 for k in codes + w_codes):
         raise TypeError("precond and w must be float32")
-    if w_numel != numel or len(grad) != len(numel) or (fisher is not None and len(fisher) != len(numel)):
+    if fisher is None:
+        fisher = [None] * len(grad)
+    if len(grad) != len(numel) or len(fisher) != len(numel):
         raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
-    k = max(1, len(numel))
-    if any(t is None for t in grad):
-        if fisher is None or any(g is None and f is None for g, f in zip(grad, fisher)):
-            raise ValueError("an entry without a gradient needs its fisher")
-        given = [i for i, t in enumerate(grad) if t is not None]
-        diagonal = [i for i, t in enumerate(grad) if t is None]
-        g_numel, given_codes, given_ptrs = _listed([grad[i] for i in given], "grad")
-        f_numel, f_codes, diagonal_ptrs = _listed([fisher[i] for i in diagonal], "fisher")
-        if any(c != KFAC_F32 for c in f_codes):
-            raise TypeError("fisher must be float32")
-        if g_numel != [numel[i] for i in given] or f_numel != [numel[i] for i in diagonal]:
-            raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
-        g_codes, g_ptrs, f_ptrs = [KFAC_F32] * len(numel), (_vp * k)(), (_vp * k)()
-        for j, i in enumerate(given):
-            g_codes[i], g_ptrs[i] = given_codes[j], given_ptrs[j]
-        for j, i in enumerate(diagonal):
-            f_ptrs[i] = diagonal_ptrs[j]
-    else:
-        g_numel, g_codes, g_ptrs = _listed(grad, "grad")
-        f_ptrs = None
-        if g_numel != numel:
-            raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
+    # an entry's gradient, or else its Fisher
+    if any(g is None and f is None for g, f in zip(grad, fisher)):
+        raise ValueError("an entry without a gradient needs its fisher")
+    s_numel, s_codes, s_at = _listed([f if g is None else g for g, f in zip(grad, fisher)], "grad and fisher")
+    if s_numel != numel or w_numel != numel:
+        raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
+    diagonal = [g is None for g in grad]
+    if any(d and k != KFAC_F32 for d, k in zip(diagonal, s_codes)):
+        raise TypeError("fisher must be float32")
     _on_device([step], "step")
-    _scalar_out(step, 2, "step")
-    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace(numel), step.device, stream)
-    _check(_lib.kfac_trust_update(len(numel), (_i64 * k)(*numel), p_ptrs, (_i32 * k)(*g_codes), g_ptrs, f_ptrs,
-                                  float(shift), w_ptrs, float(lr), float(delta), step.data_ptr(), ws, wsb,
-                                  _stream(stream)), "kfac_trust_update")
+    step_at = _scalar_out(step, 2, "step")
+    ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace, (numel,), step.device, stream)
+    n, c, p, ww = _words(numel), _halfwords(s_codes), _words(p_at), _words(w_at)
+    g = _words([0 if d else a for d, a in zip(diagonal, s_at)])
+    f = _words([a if d else 0 for d, a in zip(diagonal, s_at)])
+    _check(_lib.kfac_trust_update(len(numel), _at(n), _at(p), _at(c), _at(g), _at(f), float(shift), _at(ww), float(lr),
+                                  float(delta), step_at, ws, wsb, _stream(stream)), "kfac_trust_update")
 
 
 # losses over logits -----------------------------------------------------------
@@ -534,15 +532,15 @@ def kfac_policy_loss(logits, token, old_logp, advantage, logp, stats, dlogits=No
     if seq_begin is not None and seqs < 1:
         raise ValueError("seq_begin needs one offset more than there are sequences")
     f32 = torch.float32
-    _scalar_out(stats, 4, "stats")
-    ws, wsb, held = _call_ws(workspace, kfac_policy_loss_workspace(rows, vocab, seqs), logits.device, stream)
+    stats_at = _scalar_out(stats, 4, "stats")
+    ws, wsb, held = _call_ws(workspace, kfac_policy_loss_workspace, (rows, vocab, seqs), logits.device, stream)
     _check(_lib.kfac_policy_loss(
         rows, vocab, code, z, ld, tok, msk, seqs,
         None if seq_begin is None else _vector(seq_begin, torch.int32, seqs + 1, "seq_begin"),
         _vector(old_logp, f32, rows, "old_logp"),
         None if ref_logp is None else _vector(ref_logp, f32, rows, "ref_logp"),
         _vector(advantage, f32, rows, "advantage"), float(clip_low), float(clip_high), float(kl_coef),
-        1 if by_sequence else 0, float(grad_scale), _vector(logp, f32, rows, "logp"), stats.data_ptr(), d, ldd, ws,
+        1 if by_sequence else 0, float(grad_scale), _vector(logp, f32, rows, "logp"), stats_at, d, ldd, ws,
         wsb, _stream(stream)), "kfac_policy_loss")
 
 
@@ -557,13 +555,13 @@ def kfac_preference_loss(logits, token, seq_begin, seq_logp, margin, loss, dlogi
         raise ValueError("seq_begin needs one offset more than two for each pair")
     pairs = seq_begin.numel() // 2
     f32 = torch.float32
-    _scalar_out(loss, 1, "loss")
-    ws, wsb, held = _call_ws(workspace, kfac_preference_loss_workspace(rows, vocab, pairs), logits.device, stream)
+    loss_at = _scalar_out(loss, 1, "loss")
+    ws, wsb, held = _call_ws(workspace, kfac_preference_loss_workspace, (rows, vocab, pairs), logits.device, stream)
     _check(_lib.kfac_preference_loss(
         rows, vocab, code, z, ld, tok, msk, pairs, _vector(seq_begin, torch.int32, 2 * pairs + 1, "seq_begin"),
         None if ref_logp is None else _vector(ref_logp, f32, 2 * pairs, "ref_logp"), float(beta),
         float(label_smoothing), float(grad_scale), _vector(seq_logp, f32, 2 * pairs, "seq_logp"),
-        _vector(margin, f32, pairs, "margin"), loss.data_ptr(), d, ldd, ws, wsb, _stream(stream)),
+        _vector(margin, f32, pairs, "margin"), loss_at, d, ldd, ws, wsb, _stream(stream)),
         "kfac_preference_loss")
 
 

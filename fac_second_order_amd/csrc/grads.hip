@@ -1,33 +1,241 @@
 // Norms and updates over many tensors: the global gradient norm, clipping by it, and
 // the update whose length is bounded by its predicted KL divergence.
 //
-// A tensor is cut into chunks of CHUNK elements; a call's chunks are numbered through
-// all tensors and dealt to the blocks in contiguous ranges, so the order of every sum
-// depends on the sizes alone and results are deterministic. Sums are kept in fp64 (a
-// square of any fp32 value fits, and a multiply-add costs what an fp32 one costs);
-// each block leaves one partial sum, and the blocks of the next launch add them all.
-// HBM-bound: one read of the gradients for the norm, a second read and the write for
-// the result.
+// A tensor is cut into units of UNIT elements; a call's units are numbered through all
+// tensors. A first launch sums over them, each block leaving one fp64 partial sum (a
+// square of any fp32 value fits, and a multiply-add costs what an fp32 one costs); a second
+// turns the sum into the factor; a third goes over the units again, last ones first, as the
+// caches still hold those. Which block adds what depends on the sizes alone: results are
+// deterministic. HBM-bound: the gradients are read twice, the result is written once.
 #include <algorithm>
 
 #include "row_ops.hpp"
 
 namespace kfac {
 
-constexpr int CHUNK = 16384;       // elements of a work item
-constexpr int MAX_BLOCKS = 2048;   // 8 blocks of 4 waves for each of 256 compute units
+constexpr int UNIT = 4096;         // elements of a unit
+constexpr int MAX_BLOCKS = 2048;   // partial sums: 8 blocks of 4 waves for each of 256 compute units
 constexpr int GT = 256;            // threads per block
+constexpr int ONE_THREADS = 1024;  // of the block that does a small call alone
 
 struct GradDesc {
-  const void* grad;  // NULL: the Fisher is diagonal, g = P (fisher + shift)
-  const float* fisher;
+  const void* grad;      // or the diagonal Fisher
   const float* precond;
-  void* out;         // clipped gradient, or the weights of the update
-  int64_t numel;
-  int32_t grad_dtype, out_dtype;
+  void* out;             // clipped gradient, or the weights of the update
+  int64_t info;          // numel, and above it the types
+  static constexpr int kType = 48, kWide = 50, kDiagonal = 51;
+  __host__ __device__ int64_t numel() const { return info & ((int64_t(1) << kType) - 1); }
+  __host__ __device__ int type() const { return static_cast<int>(info >> kType) & 3; }
+  __host__ __device__ bool wide() const { return info >> kWide & 1; }  // out is fp32
+  __host__ __device__ bool diagonal() const { return info >> kDiagonal & 1; }
 };
 
+// The tables of a call: in the workspace, or where they fit in the kernel's arguments
+// themselves, which saves the launches that send them.
+struct SentTables {
+  const GradDesc* desc;
+  const int32_t* begin;  // first unit of each tensor
+};
+constexpr int INLINE = 108;  // tensors whose tables stay below 4 KB of arguments
+struct InlineTables {
+  GradDesc desc[INLINE];
+  int32_t begin[INLINE];
+};
+
+// The tensor that unit c lies in: 64 begins a step, one a lane.
+template <class TB>
+__device__ inline int find_tensor(const TB& tb, int count, int c) {
+  const int lane = threadIdx.x & 63;
+  int p = -1;
+  for (int k = 0; k < count; k += 64) {
+    const bool below = k + lane < count && tb.begin[k + lane] <= c;
+    const int n = __popcll(__ballot(below));
+    p += n;
+    if (n < 64) break;
+  }
+  return __builtin_amdgcn_readfirstlane(p);
+}
+
+// f(type tag) with the type of a code.
+template <class F>
+__device__ inline void with_type(int code, F f) {
+  if (code == KFAC_F32) f(float{});
+  else if (code == KFAC_BF16) f(__bf16{});
+  else f(_Float16{});
+}
+
+// N elements at any address that is a multiple of an element's size.
+template <class T, int N>
+struct Pack {
+  typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+};
+
+// The elements [0, n) of a unit over NT threads in groups of EV: load(i, u) for all groups of
+// a thread first, so that they are in flight together (a store could alias what is loaded next),
+// then use(i, u); one(i) for the last n % EV elements.
+template <int NT, int EV, class L, class U, class O>
+__device__ inline void over_unit(int n, L load, U use, O one) {
+  constexpr int trips = (UNIT + NT * EV - 1) / (NT * EV);
+  const int tid = threadIdx.x;
+  const int full = n == UNIT ? UNIT : n / EV * EV;
+#pragma unroll
+  for (int u = 0; u < trips; ++u)
+    if ((u * NT + tid) * EV < full) load((u * NT + tid) * EV, u);
+#pragma unroll
+  for (int u = 0; u < trips; ++u)
+    if ((u * NT + tid) * EV < full) use((u * NT + tid) * EV, u);
+  if (full + tid < n) one(full + tid);
+}
+template <int NT, int EV>
+constexpr int kTrips = (UNIT + NT * EV - 1) / (NT * EV);
+
+template <int NT>
+__device__ inline void add_squares(const GradDesc& d, int64_t e0, int n, double& acc) {
+  with_type(d.type(), [&](auto tag) {
+    using T = decltype(tag);
+    constexpr int EV = Chunk16<T>::ev;
+    using V = typename Chunk16<T>::vec;
+    const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
+    V v[kTrips<NT, EV>];
+    over_unit<NT, EV>(
+        n, [&](int i, int u) { v[u] = *reinterpret_cast<const KG V*>(g + i); },
+        [&](int, int u) {
+#pragma unroll
+          for (int k = 0; k < EV; ++k) {
+            const double x = static_cast<float>(v[u][k]);
+            acc = fma(x, x, acc);
+          }
+        },
+        [&](int i) {
+          const double x = static_cast<float>(g[i]);
+          acc = fma(x, x, acc);
+        });
+  });
+}
+
+// out = coef * grad, coef in fp32, the product rounded once to the type of out.
+template <int NT>
+__device__ inline void scale_unit(const GradDesc& d, int64_t e0, int n, float coef) {
+  with_type(d.type(), [&](auto tag) {
+    using T = decltype(tag);
+    constexpr int EV = Chunk16<T>::ev;
+    using V = typename Chunk16<T>::vec;
+    const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
+    const auto scale = [&](auto otag) {
+      using O = decltype(otag);
+      using W = typename Pack<O, EV>::vec;
+      KG O* o = gp(static_cast<O*>(d.out)) + e0;
+      V v[kTrips<NT, EV>];
+      over_unit<NT, EV>(
+          n, [&](int i, int u) { v[u] = *reinterpret_cast<const KG V*>(g + i); },
+          [&](int i, int u) {
+            W w;
+#pragma unroll
+            for (int k = 0; k < EV; ++k) w[k] = static_cast<O>(static_cast<float>(v[u][k]) * coef);
+            *reinterpret_cast<KG W*>(o + i) = w;
+          },
+          [&](int i) { o[i] = static_cast<O>(static_cast<float>(g[i]) * coef); });
+    };
+    if (d.wide()) scale(float{});
+    else scale(T{});
+  });
+}
+
+// P * g, the preconditioned gradient against the gradient it came from.
+template <int NT>
+__device__ inline void add_products(const GradDesc& d, int64_t e0, int n, float shift, double& acc) {
+  const bool diagonal = d.diagonal();
+  with_type(d.type(), [&](auto tag) {
+    using T = decltype(tag);
+    using V = Pack<float, 4>::vec;
+    using W = typename Pack<T, 4>::vec;
+    const KG float* p = gp(d.precond) + e0;
+    const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
+    V v[kTrips<NT, 4>];
+    W w[kTrips<NT, 4>];
+    const auto add = [&](float x, float y) {
+      const double a = x, b = y;
+      acc = fma(a, diagonal ? a * (b + shift) : b, acc);
+    };
+    over_unit<NT, 4>(
+        n,
+        [&](int i, int u) {
+          v[u] = *reinterpret_cast<const KG V*>(p + i);
+          w[u] = *reinterpret_cast<const KG W*>(g + i);
+        },
+        [&](int, int u) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) add(v[u][k], static_cast<float>(w[u][k]));
+        },
+        [&](int i) { add(p[i], static_cast<float>(g[i])); });
+  });
+}
+
+// w -= step * P.
+template <int NT>
+__device__ inline void apply_unit(const GradDesc& d, int64_t e0, int n, float step) {
+  using V = Pack<float, 4>::vec;
+  const KG float* p = gp(d.precond) + e0;
+  KG float* w = gp(static_cast<float*>(d.out)) + e0;
+  V v[kTrips<NT, 4>], x[kTrips<NT, 4>];
+  over_unit<NT, 4>(
+      n,
+      [&](int i, int u) {
+        v[u] = *reinterpret_cast<const KG V*>(p + i);
+        x[u] = *reinterpret_cast<const KG V*>(w + i);
+      },
+      [&](int i, int u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[u][k] = fmaf(-step, v[u][k], x[u][k]);
+        *reinterpret_cast<KG V*>(w + i) = x[u];
+      },
+      [&](int i) { w[i] = fmaf(-step, p[i], w[i]); });
+}
+
+// What a call does with its sum: the norm alone, clipping by it, or the bounded update.
+enum Work { NORM, CLIP, TRUST };
+struct WorkArgs {
+  float* result;  // norm; or step and q
+  float a, b;     // max_norm; or lr and delta
+  float shift;
+};
+
+// The factor of the second pass from the sum; `shown` writes the results.
+template <int W>
+__device__ inline float factor(double sum, const WorkArgs& k, bool shown) {
+  if constexpr (W == TRUST) {
+    float step = 0.f;  // a sum that is not finite: no update
+    if (sum - sum == 0) step = fmin(static_cast<double>(k.a), sqrt(2.0 * k.b / fabs(sum)));
+    if (shown) {
+      gp(k.result)[0] = step;
+      gp(k.result)[1] = static_cast<float>(sum);
+    }
+    return step;
+  } else {
+    const double root = sqrt(sum);
+    const float norm = static_cast<float>(root);
+    if (shown) gp(k.result)[0] = norm;
+    // a norm that is no finite float: the gradients as they are
+    return W == CLIP && norm > k.a && norm <= 3.402823466e38f ? static_cast<float>(k.a / root) : 1.f;
+  }
+}
+
+template <int W, int NT>
+__device__ inline void sum_unit(const GradDesc& d, int64_t e0, int n, float shift, double& acc) {
+  if constexpr (W == TRUST) add_products<NT>(d, e0, n, shift, acc);
+  else add_squares<NT>(d, e0, n, acc);
+}
+template <int W, int NT>
+__device__ inline void second_unit(const GradDesc& d, int64_t e0, int n, float f) {
+  if constexpr (W == TRUST) {
+    if (f != 0.f) apply_unit<NT>(d, e0, n, f);
+  } else if constexpr (W == CLIP) {
+    if (f != 1.f || d.out != d.grad) scale_unit<NT>(d, e0, n, f);
+  }
+}
+
 // Sum of a block's per-thread values, in every thread (fixed order).
+template <int NT>
 __device__ inline double block_sum(double v, double* s) {
 #pragma unroll
   for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
@@ -35,183 +243,69 @@ __device__ inline double block_sum(double v, double* s) {
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
   double t = 0;
-  for (int i = 0; i < GT / 64; ++i) t += s[i];
+  for (int i = 0; i < NT / 64; ++i) t += s[i];
   return t;
 }
 
-__device__ inline double partial_total(const double* partial, int n, double* s) {
+// First pass: the block's units b, b + grid, ...
+template <int W, class TB>
+__global__ void __launch_bounds__(GT) grads_sum_kernel(TB tb, int count, int units, WorkArgs k,
+                                                       double* __restrict__ partial) {
+  __shared__ double s[GT / 64];
+  double acc = 0;
+  int p = find_tensor(tb, count, blockIdx.x);
+  for (int c = blockIdx.x; c < units; c += gridDim.x) {
+    while (p + 1 < count && tb.begin[p + 1] <= c) ++p;
+    const GradDesc d = tb.desc[p];
+    const int64_t e0 = int64_t(c - tb.begin[p]) * UNIT;
+    sum_unit<W, GT>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
+  }
+  acc = block_sum<GT>(acc, s);
+  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
+}
+
+template <int W>
+__global__ void __launch_bounds__(ONE_THREADS) grads_factor_kernel(const double* __restrict__ partial, int n,
+                                                                   WorkArgs k, float* __restrict__ out) {
+  __shared__ double s[ONE_THREADS / 64];
   double v = 0;
-  for (int i = threadIdx.x; i < n; i += GT) v += gp(partial)[i];
-  return block_sum(v, s);
+  for (int i = threadIdx.x; i < n; i += ONE_THREADS) v += partial[i];
+  v = block_sum<ONE_THREADS>(v, s);
+  const float f = factor<W>(v, k, threadIdx.x == 0);
+  if (threadIdx.x == 0) out[0] = f;
 }
 
-// f(tensor, first element, one past the last) for each of this block's chunks.
-template <class F>
-__device__ inline void for_chunks(const GradDesc* desc, const int32_t* begin, int count, int total, bool reverse, F f) {
-  const int b = reverse ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-  const int c0 = static_cast<int>(int64_t(total) * b / gridDim.x);
-  const int c1 = static_cast<int>(int64_t(total) * (b + 1) / gridDim.x);
-  if (c0 >= c1) return;
-  int p = find_problem(begin, count, c0);
-  for (int c = c0; c < c1; ++c) {
-    while (p + 1 < count && begin[p + 1] <= c) ++p;
-    const GradDesc d = desc[p];
-    const int64_t e0 = int64_t(c - begin[p]) * CHUNK;
-    f(d, e0, min(d.numel, e0 + CHUNK));
-  }
+template <int W, class TB>
+__global__ void __launch_bounds__(GT) grads_apply_kernel(TB tb, int count, int units, const float* __restrict__ f) {
+  const int c = units - 1 - static_cast<int>(blockIdx.x);
+  const int p = find_tensor(tb, count, c);
+  const GradDesc d = tb.desc[p];
+  const int64_t e0 = int64_t(c - tb.begin[p]) * UNIT;
+  second_unit<W, GT>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), f[0]);
 }
 
-// f(dtype tag) with the type of a code.
-template <class F>
-__device__ inline void with_type(int32_t code, F f) {
-  if (code == KFAC_F32) f(float{});
-  else if (code == KFAC_BF16) f(__bf16{});
-  else f(_Float16{});
-}
-
-__global__ void __launch_bounds__(GT) norm_partial_kernel(const GradDesc* __restrict__ desc,
-                                                          const int32_t* __restrict__ begin, int count, int total,
-                                                          double* __restrict__ partial) {
-  __shared__ double s[GT / 64];
+// A small call in one block: both passes, and no launch between them.
+template <int W>
+__global__ void __launch_bounds__(ONE_THREADS) grads_one_kernel(InlineTables tb, int count, WorkArgs k) {
+  __shared__ double s[ONE_THREADS / 64];
   double acc = 0;
-  for_chunks(desc, begin, count, total, false, [&](const GradDesc& d, int64_t e0, int64_t e1) {
-    with_type(d.grad_dtype, [&](auto tag) {
-      using T = decltype(tag);
-      using C = Chunk16<T>;
-      const KG T* g = gp(static_cast<const T*>(d.grad));
-      const int64_t full = e0 + (e1 - e0) / C::ev * C::ev;
-      for (int64_t i = e0 + int64_t(threadIdx.x) * C::ev; i < full; i += GT * C::ev) {
-        const typename C::vec v = *reinterpret_cast<const KG typename C::vec*>(g + i);
-#pragma unroll
-        for (int u = 0; u < C::ev; ++u) {
-          const double x = static_cast<float>(v[u]);
-          acc = fma(x, x, acc);
-        }
-      }
-      const int64_t i = full + threadIdx.x;
-      if (i < e1) {
-        const double x = static_cast<float>(g[i]);
-        acc = fma(x, x, acc);
-      }
-    });
-  });
-  acc = block_sum(acc, s);
-  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
-}
-
-__global__ void __launch_bounds__(GT) norm_finish_kernel(const double* __restrict__ partial, int n, float* norm) {
-  __shared__ double s[GT / 64];
-  const double q = partial_total(partial, n, s);
-  if (threadIdx.x == 0) norm[0] = static_cast<float>(sqrt(q));
-}
-
-// out = coef * grad, coef in fp32, the product rounded once to the type of out.
-__global__ void __launch_bounds__(GT) grad_scale_kernel(const GradDesc* __restrict__ desc,
-                                                        const int32_t* __restrict__ begin, int count, int total,
-                                                        const double* __restrict__ partial, int n, float max_norm,
-                                                        float* norm) {
-  __shared__ double s[GT / 64];
-  const double root = sqrt(partial_total(partial, n, s));
-  const float shown = static_cast<float>(root);
-  const float coef = shown > max_norm && shown <= 3.402823466e38f ? static_cast<float>(max_norm / root) : 1.f;
-  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = shown;
-  for_chunks(desc, begin, count, total, true, [&](const GradDesc& d, int64_t e0, int64_t e1) {
-    if (coef == 1.f && d.out == d.grad) return;
-    with_type(d.grad_dtype, [&](auto tag) {
-      using T = decltype(tag);
-      const auto scale = [&](auto otag) {
-        using O = decltype(otag);
-        constexpr int ev = Chunk16<T>::ev;
-        typedef O ovec __attribute__((ext_vector_type(ev), aligned(sizeof(O))));
-        using V = typename Chunk16<T>::vec;
-        const KG T* g = gp(static_cast<const T*>(d.grad));
-        KG O* o = gp(static_cast<O*>(d.out));
-        const int64_t full = e0 + (e1 - e0) / ev * ev;
-        for (int64_t i = e0 + int64_t(threadIdx.x) * ev; i < full; i += GT * ev) {
-          const V v = *reinterpret_cast<const KG V*>(g + i);
-          ovec w;
-#pragma unroll
-          for (int u = 0; u < ev; ++u) w[u] = static_cast<O>(static_cast<float>(v[u]) * coef);
-          *reinterpret_cast<KG ovec*>(o + i) = w;
-        }
-        const int64_t i = full + threadIdx.x;
-        if (i < e1) o[i] = static_cast<O>(static_cast<float>(g[i]) * coef);
-      };
-      if (d.out_dtype == KFAC_F32) scale(float{});
-      else scale(T{});
-    });
-  });
-}
-
-// q = sum of P * g, the preconditioned gradient against the gradient it came from.
-__global__ void __launch_bounds__(GT) trust_partial_kernel(const GradDesc* __restrict__ desc,
-                                                           const int32_t* __restrict__ begin, int count, int total,
-                                                           float shift, double* __restrict__ partial) {
-  __shared__ double s[GT / 64];
-  double acc = 0;
-  for_chunks(desc, begin, count, total, false, [&](const GradDesc& d, int64_t e0, int64_t e1) {
-    const KG float* p = gp(d.precond);
-    if (!d.grad) {
-      for (int64_t i = e0 + threadIdx.x; i < e1; i += GT) {
-        const double x = p[i];
-        acc = fma(x * x, static_cast<double>(gp(d.fisher)[i]) + shift, acc);
-      }
-      return;
-    }
-    with_type(d.grad_dtype, [&](auto tag) {
-      using T = decltype(tag);
-      typedef T gvec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-      using V = Chunk16<float>::vec;
-      const KG T* g = gp(static_cast<const T*>(d.grad));
-      const int64_t full = e0 + (e1 - e0) / 4 * 4;
-      for (int64_t i = e0 + int64_t(threadIdx.x) * 4; i < full; i += GT * 4) {
-        const V v = *reinterpret_cast<const KG V*>(p + i);
-        const gvec w = *reinterpret_cast<const KG gvec*>(g + i);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) acc = fma(static_cast<double>(v[u]), static_cast<double>(static_cast<float>(w[u])), acc);
-      }
-      const int64_t i = full + threadIdx.x;
-      if (i < e1) acc = fma(static_cast<double>(p[i]), static_cast<double>(static_cast<float>(g[i])), acc);
-    });
-  });
-  acc = block_sum(acc, s);
-  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
-}
-
-// w -= step * P, step = min(lr, sqrt(2 delta / |q|)).
-__global__ void __launch_bounds__(GT) trust_apply_kernel(const GradDesc* __restrict__ desc,
-                                                         const int32_t* __restrict__ begin, int count, int total,
-                                                         const double* __restrict__ partial, int n, float lr,
-                                                         float delta, float* step_out) {
-  __shared__ double s[GT / 64];
-  const double q = partial_total(partial, n, s);
-  float step = 0.f;  // q not finite: no update
-  if (q - q == 0) step = fmin(static_cast<double>(lr), sqrt(2.0 * delta / fabs(q)));
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    step_out[0] = step;
-    step_out[1] = static_cast<float>(q);
+  for (int p = 0; p < count; ++p) {
+    const GradDesc d = tb.desc[p];
+    for (int64_t e0 = 0; e0 < d.numel(); e0 += UNIT)
+      sum_unit<W, ONE_THREADS>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
   }
-  if (step == 0.f) return;
-  for_chunks(desc, begin, count, total, true, [&](const GradDesc& d, int64_t e0, int64_t e1) {
-    using V = Chunk16<float>::vec;
-    const KG float* p = gp(d.precond);
-    KG float* w = gp(static_cast<float*>(d.out));
-    const int64_t full = e0 + (e1 - e0) / 4 * 4;
-    for (int64_t i = e0 + int64_t(threadIdx.x) * 4; i < full; i += GT * 4) {
-      const V v = *reinterpret_cast<const KG V*>(p + i);
-      V x = *reinterpret_cast<const KG V*>(w + i);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) x[u] = fmaf(-step, v[u], x[u]);
-      *reinterpret_cast<KG V*>(w + i) = x;
+  const float f = factor<W>(block_sum<ONE_THREADS>(acc, s), k, threadIdx.x == 0);
+  if constexpr (W != NORM)
+    for (int p = 0; p < count; ++p) {
+      const GradDesc d = tb.desc[p];
+      for (int64_t e0 = 0; e0 < d.numel(); e0 += UNIT)
+        second_unit<W, ONE_THREADS>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), f);
     }
-    const int64_t i = full + threadIdx.x;
-    if (i < e1) w[i] = fmaf(-step, p[i], w[i]);
-  });
 }
 
 static size_t grads_need(int count) {
   return align256(sizeof(GradDesc) * size_t(count)) + align256(sizeof(int32_t) * size_t(count)) +
-         align256(sizeof(double) * MAX_BLOCKS);
+         align256(sizeof(double) * MAX_BLOCKS) + 256;
 }
 
 }  // namespace kfac
@@ -224,13 +318,13 @@ static int dtype_size(kfac_dtype t) { return t == KFAC_F32 ? 4 : 2; }
 static kfac_status sizes_validate(int32_t count, const int64_t* numel) {
   if (count < 0) return fail(KFAC_ERR_INVALID, "count must be >= 0");
   if (count > 0 && !numel) return fail(KFAC_ERR_INVALID, "numel is NULL");
-  int64_t chunks = 0;
+  int64_t units = 0;
   for (int i = 0; i < count; ++i) {
     if (numel[i] < 0 || numel[i] > (int64_t(1) << 40))
       return fail(KFAC_ERR_INVALID, "numel[%d] = %lld out of range", i, static_cast<long long>(numel[i]));
-    chunks += (numel[i] + CHUNK - 1) / CHUNK;
+    units += (numel[i] + UNIT - 1) / UNIT;
   }
-  if (chunks >= (int64_t(1) << 31)) return fail(KFAC_ERR_UNSUPPORTED, "too many elements in one call");
+  if (units >= (int64_t(1) << 31)) return fail(KFAC_ERR_UNSUPPORTED, "too many elements in one call");
   return KFAC_OK;
 }
 
@@ -274,13 +368,16 @@ struct GradCall {
   std::vector<GradDesc> desc;
   std::vector<int32_t> begin;
   Spans spans;
-  int total = 0;  // chunks
+  int units = 0;
   void add(const GradDesc& d) {
     desc.push_back(d);
-    begin.push_back(total);
-    total += static_cast<int>((d.numel + CHUNK - 1) / CHUNK);
+    begin.push_back(units);
+    units += static_cast<int>((d.numel() + UNIT - 1) / UNIT);
   }
-  int blocks() const { return total < 1 ? 1 : total < MAX_BLOCKS ? total : MAX_BLOCKS; }
+  static int64_t pack(int64_t numel, int type, bool wide, bool diagonal) {
+    return numel | int64_t(type) << GradDesc::kType | int64_t(wide) << GradDesc::kWide |
+           int64_t(diagonal) << GradDesc::kDiagonal;
+  }
 };
 
 static kfac_status check_pointer(const void* p, int size, int i, const char* what) {
@@ -289,26 +386,54 @@ static kfac_status check_pointer(const void* p, int size, int i, const char* wha
   return KFAC_OK;
 }
 
-struct GradTables {
-  GradDesc* desc;
-  int32_t* begin;
-  double* partial;
-};
+// Calls of at most this many units go to one block: it takes about what the two launches it
+// saves take.
+constexpr int ONE_UNITS = 8;
 
-static kfac_status send_tables(const GradCall& call, int32_t count, void* workspace, size_t ws_bytes, hipStream_t s,
-                               GradTables* t) {
+template <int W, class TB>
+static kfac_status launch_passes(const TB& tb, const GradCall& call, const WorkArgs& k, double* partial, float* f,
+                                 hipStream_t s) {
+  const int n = static_cast<int>(call.desc.size()), blocks = std::max(1, std::min(call.units, MAX_BLOCKS));
+  KFAC_LAUNCH(W == TRUST ? K_TRUST_SUM : K_NORM_SUM, (grads_sum_kernel<W == CLIP ? NORM : W, TB>), dim3(blocks),
+              dim3(GT), 0, s, tb, n, call.units, k, partial);
+  KFAC_CHECK_LAUNCH("grads_sum_kernel");
+  KFAC_LAUNCH(K_GRADS_FACTOR, grads_factor_kernel<W>, dim3(1), dim3(ONE_THREADS), 0, s, partial, blocks, k, f);
+  KFAC_CHECK_LAUNCH("grads_factor_kernel");
+  if constexpr (W != NORM) {
+    KFAC_LAUNCH(W == TRUST ? K_TRUST_APPLY : K_GRAD_SCALE, (grads_apply_kernel<W, TB>), dim3(call.units), dim3(GT), 0,
+                s, tb, n, call.units, f);
+    KFAC_CHECK_LAUNCH("grads_apply_kernel");
+  }
+  return KFAC_OK;
+}
+
+template <int W>
+static kfac_status launch_grads(const GradCall& call, int32_t count, const WorkArgs& k, void* workspace,
+                                size_t ws_bytes, hipStream_t s) {
   kfac_status st = check_device();
   if (st) return st;
   st = check_workspace(workspace, ws_bytes, grads_need(count));
   if (st) return st;
+  const int n = static_cast<int>(call.desc.size());
   Carver cv(workspace);
-  t->desc = cv.take<GradDesc>(count);
-  t->begin = cv.take<int32_t>(count);
-  t->partial = cv.take<double>(MAX_BLOCKS);
+  GradDesc* desc = cv.take<GradDesc>(count);
+  int32_t* begin = cv.take<int32_t>(count);
+  double* partial = cv.take<double>(MAX_BLOCKS);
+  float* f = cv.take<float>(1);
+  if (n <= INLINE) {
+    InlineTables tb;
+    std::copy(call.desc.begin(), call.desc.end(), tb.desc);
+    std::copy(call.begin.begin(), call.begin.end(), tb.begin);
+    if (call.units > ONE_UNITS) return launch_passes<W>(tb, call, k, partial, f, s);
+    KFAC_LAUNCH(K_GRADS_ONE, grads_one_kernel<W>, dim3(1), dim3(ONE_THREADS), 0, s, tb, n, k);
+    KFAC_CHECK_LAUNCH("grads_one_kernel");
+    return KFAC_OK;
+  }
   TableUpload tu;
-  tu.add(t->desc, call.desc.data(), sizeof(GradDesc) * call.desc.size());
-  tu.add(t->begin, call.begin.data(), sizeof(int32_t) * call.begin.size());
-  return tu.flush(s);
+  tu.add(desc, call.desc.data(), sizeof(GradDesc) * n);
+  tu.add(begin, call.begin.data(), sizeof(int32_t) * n);
+  if ((st = tu.flush(s))) return st;
+  return launch_passes<W>(SentTables{desc, begin}, call, k, partial, f, s);
 }
 
 extern "C" kfac_status kfac_grad_norm_workspace(int32_t count, const int64_t* numel, size_t* bytes) {
@@ -335,13 +460,12 @@ static kfac_status grad_impl(int32_t count, const int64_t* numel, const kfac_dty
       return fail(KFAC_ERR_UNSUPPORTED, "tensor %d: out must have the gradient's type or fp32", i);
     if (numel[i] == 0) continue;
     if ((st = check_pointer(grad[i], dtype_size(dtype[i]), i, "grad"))) return st;
-    GradDesc d = {grad[i], nullptr, nullptr, nullptr, numel[i], dtype[i], dtype[i]};
+    GradDesc d = {grad[i], nullptr, nullptr, GradCall::pack(numel[i], dtype[i], clip && out_dtype[i] == KFAC_F32, false)};
     if (clip) {
       if ((st = check_pointer(out[i], dtype_size(out_dtype[i]), i, "out"))) return st;
       d.out = out[i];
-      d.out_dtype = out_dtype[i];
-      call.spans.write(d.out, d.numel * dtype_size(d.out_dtype), i);
-      call.spans.read(d.grad, d.numel * dtype_size(d.grad_dtype), i, d.out_dtype == d.grad_dtype);
+      call.spans.write(out[i], numel[i] * dtype_size(out_dtype[i]), i);
+      call.spans.read(grad[i], numel[i] * dtype_size(dtype[i]), i, out_dtype[i] == dtype[i]);
     }
     call.add(d);
   }
@@ -349,22 +473,10 @@ static kfac_status grad_impl(int32_t count, const int64_t* numel, const kfac_dty
     call.spans.write(norm, 4, -1);
     if ((st = call.spans.check())) return st;
   }
-  GradTables t;
+  const WorkArgs k = {norm, max_norm, 0.f, 0.f};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if ((st = send_tables(call, count, workspace, ws_bytes, s, &t))) return st;
-  const int n = static_cast<int>(call.desc.size()), blocks = call.blocks();
-  KFAC_LAUNCH(K_NORM_PARTIAL, norm_partial_kernel, dim3(blocks), dim3(GT), 0, s, t.desc, t.begin, n, call.total,
-              t.partial);
-  KFAC_CHECK_LAUNCH("norm_partial_kernel");
-  if (clip) {
-    KFAC_LAUNCH(K_GRAD_SCALE, grad_scale_kernel, dim3(blocks), dim3(GT), 0, s, t.desc, t.begin, n, call.total,
-                t.partial, blocks, max_norm, norm);
-    KFAC_CHECK_LAUNCH("grad_scale_kernel");
-  } else {
-    KFAC_LAUNCH(K_NORM_FINISH, norm_finish_kernel, dim3(1), dim3(GT), 0, s, t.partial, blocks, norm);
-    KFAC_CHECK_LAUNCH("norm_finish_kernel");
-  }
-  return KFAC_OK;
+  return clip ? launch_grads<CLIP>(call, count, k, workspace, ws_bytes, s)
+              : launch_grads<NORM>(call, count, k, workspace, ws_bytes, s);
 }
 
 static kfac_status trust_impl(int32_t count, const int64_t* numel, const float* const* precond,
@@ -383,14 +495,15 @@ static kfac_status trust_impl(int32_t count, const int64_t* numel, const float* 
     if (numel[i] == 0) continue;
     if ((st = check_pointer(precond[i], 4, i, "precond"))) return st;
     if ((st = check_pointer(w[i], 4, i, "w"))) return st;
-    GradDesc d = {grad[i], nullptr, precond[i], w[i], numel[i], grad_dtype[i], KFAC_F32};
+    GradDesc d = {grad[i], precond[i], w[i], GradCall::pack(numel[i], grad_dtype[i] & 3, true, false)};
     if (grad[i]) {
       if (!known_dtype(grad_dtype[i])) return fail(KFAC_ERR_UNSUPPORTED, "tensor %d: dtype %d", i, grad_dtype[i]);
       if ((st = check_pointer(grad[i], dtype_size(grad_dtype[i]), i, "grad"))) return st;
       call.spans.read(grad[i], dtype_size(grad_dtype[i]) * numel[i], i, false);
     } else {
       if ((st = check_pointer(fisher ? fisher[i] : nullptr, 4, i, "fisher (and grad)"))) return st;
-      d.fisher = fisher[i];
+      d.grad = fisher[i];
+      d.info = GradCall::pack(numel[i], KFAC_F32, true, true);
       call.spans.read(fisher[i], 4 * numel[i], i, false);
     }
     call.spans.read(precond[i], 4 * numel[i], i, false);
@@ -399,17 +512,8 @@ static kfac_status trust_impl(int32_t count, const int64_t* numel, const float* 
   }
   call.spans.write(step, 8, -1);
   if ((st = call.spans.check())) return st;
-  GradTables t;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  if ((st = send_tables(call, count, workspace, ws_bytes, s, &t))) return st;
-  const int n = static_cast<int>(call.desc.size()), blocks = call.blocks();
-  KFAC_LAUNCH(K_TRUST_PARTIAL, trust_partial_kernel, dim3(blocks), dim3(GT), 0, s, t.desc, t.begin, n, call.total,
-              shift, t.partial);
-  KFAC_CHECK_LAUNCH("trust_partial_kernel");
-  KFAC_LAUNCH(K_TRUST_APPLY, trust_apply_kernel, dim3(blocks), dim3(GT), 0, s, t.desc, t.begin, n, call.total,
-              t.partial, blocks, lr, delta, step);
-  KFAC_CHECK_LAUNCH("trust_apply_kernel");
-  return KFAC_OK;
+  return launch_grads<TRUST>(call, count, WorkArgs{step, lr, delta, shift}, workspace, ws_bytes,
+                             static_cast<hipStream_t>(stream));
 }
 
 extern "C" kfac_status kfac_grad_norm(int32_t count, const int64_t* numel, const kfac_dtype* dtype,

@@ -9,11 +9,12 @@
 namespace kfac {
 
 enum RowKernelId {
-  K_NORM_PARTIAL = K_COUNT,
-  K_NORM_FINISH,
-  K_GRAD_SCALE,
-  K_TRUST_PARTIAL,
-  K_TRUST_APPLY,
+  K_NORM_SUM = K_COUNT,  // grads_sum_kernel of the norm and the clipping
+  K_TRUST_SUM,           // grads_sum_kernel of the bounded update
+  K_GRADS_FACTOR,
+  K_GRAD_SCALE,          // grads_apply_kernel of the clipping
+  K_TRUST_APPLY,         // grads_apply_kernel of the bounded update
+  K_GRADS_ONE,
   K_LOSS_COUNT,
   K_POLICY_ROWS,
   K_POLICY_FINISH,
