@@ -14,7 +14,8 @@
 namespace kfac {
 
 constexpr int UNIT = 4096;         // elements of a unit
-constexpr int MAX_BLOCKS = 2048;   // partial sums: 8 blocks of 4 waves for each of 256 compute units
+constexpr int PART = 2048;         // of a unit that one block of the second pass takes
+constexpr int MAX_BLOCKS = 1024;   // partial sums
 constexpr int GT = 256;            // threads per block
 constexpr int ONE_THREADS = 1024;  // of the block that does a small call alone
 
@@ -70,35 +71,41 @@ struct Pack {
   typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
 
-// The elements [0, n) of a unit over NT threads in groups of EV: load(i, u) for all groups of
-// a thread first, so that they are in flight together (a store could alias what is loaded next),
-// then use(i, u); one(i) for the last n % EV elements.
-template <int NT, int EV, class L, class U, class O>
-__device__ inline void over_unit(int n, L load, U use, O one) {
-  constexpr int trips = (UNIT + NT * EV - 1) / (NT * EV);
-  const int tid = threadIdx.x;
-  const int full = n == UNIT ? UNIT : n / EV * EV;
+// n <= SIZE elements over NT threads in groups of EV: load(i, u) for all groups of a thread first,
+// so that they are in flight together (a store could alias what is loaded next), one(i) for the
+// last n % EV elements, use(i, u) for the groups. The groups come last: what runs behind a store
+// and needs its registers waits until the store is done.
+template <int SIZE, int NT, int EV>
+constexpr int kTrips = (SIZE + NT * EV - 1) / (NT * EV);
+template <int SIZE, int NT, int EV, class L, class U, class O>
+__device__ inline void over(int n, L load, U use, O one) {
+  const int tid = threadIdx.x, full = n / EV * EV;
 #pragma unroll
-  for (int u = 0; u < trips; ++u)
+  for (int u = 0; u < kTrips<SIZE, NT, EV>; ++u)
     if ((u * NT + tid) * EV < full) load((u * NT + tid) * EV, u);
-#pragma unroll
-  for (int u = 0; u < trips; ++u)
-    if ((u * NT + tid) * EV < full) use((u * NT + tid) * EV, u);
   if (full + tid < n) one(full + tid);
+#pragma unroll
+  for (int u = 0; u < kTrips<SIZE, NT, EV>; ++u)
+    if ((u * NT + tid) * EV < full) use((u * NT + tid) * EV, u);
 }
-template <int NT, int EV>
-constexpr int kTrips = (UNIT + NT * EV - 1) / (NT * EV);
 
-template <int NT>
+// A 16-byte group; LAST: nothing reads it again before the caches have turned over.
+template <bool LAST, class V, class P>
+__device__ inline V read(const KG P* p) {
+  if constexpr (LAST) return __builtin_nontemporal_load(reinterpret_cast<const KG V*>(p));
+  else return *reinterpret_cast<const KG V*>(p);
+}
+
+template <int NT, bool LAST>
 __device__ inline void add_squares(const GradDesc& d, int64_t e0, int n, double& acc) {
   with_type(d.type(), [&](auto tag) {
     using T = decltype(tag);
     constexpr int EV = Chunk16<T>::ev;
     using V = typename Chunk16<T>::vec;
     const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
-    V v[kTrips<NT, EV>];
-    over_unit<NT, EV>(
-        n, [&](int i, int u) { v[u] = *reinterpret_cast<const KG V*>(g + i); },
+    V v[kTrips<UNIT, NT, EV>];
+    over<UNIT, NT, EV>(
+        n, [&](int i, int u) { v[u] = read<LAST, V>(g + i); },
         [&](int, int u) {
 #pragma unroll
           for (int k = 0; k < EV; ++k) {
@@ -114,25 +121,25 @@ __device__ inline void add_squares(const GradDesc& d, int64_t e0, int n, double&
 }
 
 // out = coef * grad, coef in fp32, the product rounded once to the type of out.
-template <int NT>
-__device__ inline void scale_unit(const GradDesc& d, int64_t e0, int n, float coef) {
+template <int SIZE, int NT>
+__device__ inline void scale_part(const GradDesc& d, int64_t e0, int n, float coef) {
   with_type(d.type(), [&](auto tag) {
     using T = decltype(tag);
-    constexpr int EV = Chunk16<T>::ev;
-    using V = typename Chunk16<T>::vec;
     const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
     const auto scale = [&](auto otag) {
       using O = decltype(otag);
+      constexpr int EV = Chunk16<O>::ev;  // a store of 16 bytes a lane, side by side
+      using V = typename Pack<T, EV>::vec;
       using W = typename Pack<O, EV>::vec;
       KG O* o = gp(static_cast<O*>(d.out)) + e0;
-      V v[kTrips<NT, EV>];
-      over_unit<NT, EV>(
-          n, [&](int i, int u) { v[u] = *reinterpret_cast<const KG V*>(g + i); },
+      V v[kTrips<SIZE, NT, EV>];
+      over<SIZE, NT, EV>(
+          n, [&](int i, int u) { v[u] = read<true, V>(g + i); },
           [&](int i, int u) {
             W w;
 #pragma unroll
             for (int k = 0; k < EV; ++k) w[k] = static_cast<O>(static_cast<float>(v[u][k]) * coef);
-            *reinterpret_cast<KG W*>(o + i) = w;
+            __builtin_nontemporal_store(w, reinterpret_cast<KG W*>(o + i));
           },
           [&](int i) { o[i] = static_cast<O>(static_cast<float>(g[i]) * coef); });
     };
@@ -142,7 +149,7 @@ __device__ inline void scale_unit(const GradDesc& d, int64_t e0, int n, float co
 }
 
 // P * g, the preconditioned gradient against the gradient it came from.
-template <int NT>
+template <int NT, bool LAST>
 __device__ inline void add_products(const GradDesc& d, int64_t e0, int n, float shift, double& acc) {
   const bool diagonal = d.diagonal();
   with_type(d.type(), [&](auto tag) {
@@ -151,17 +158,17 @@ __device__ inline void add_products(const GradDesc& d, int64_t e0, int n, float 
     using W = typename Pack<T, 4>::vec;
     const KG float* p = gp(d.precond) + e0;
     const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
-    V v[kTrips<NT, 4>];
-    W w[kTrips<NT, 4>];
+    V v[kTrips<UNIT, NT, 4>];
+    W w[kTrips<UNIT, NT, 4>];
     const auto add = [&](float x, float y) {
       const double a = x, b = y;
       acc = fma(a, diagonal ? a * (b + shift) : b, acc);
     };
-    over_unit<NT, 4>(
+    over<UNIT, NT, 4>(
         n,
         [&](int i, int u) {
-          v[u] = *reinterpret_cast<const KG V*>(p + i);
-          w[u] = *reinterpret_cast<const KG W*>(g + i);
+          v[u] = read<LAST, V>(p + i);
+          w[u] = read<true, W>(g + i);
         },
         [&](int, int u) {
 #pragma unroll
@@ -172,22 +179,22 @@ __device__ inline void add_products(const GradDesc& d, int64_t e0, int n, float 
 }
 
 // w -= step * P.
-template <int NT>
-__device__ inline void apply_unit(const GradDesc& d, int64_t e0, int n, float step) {
+template <int SIZE, int NT>
+__device__ inline void apply_part(const GradDesc& d, int64_t e0, int n, float step) {
   using V = Pack<float, 4>::vec;
   const KG float* p = gp(d.precond) + e0;
   KG float* w = gp(static_cast<float*>(d.out)) + e0;
-  V v[kTrips<NT, 4>], x[kTrips<NT, 4>];
-  over_unit<NT, 4>(
+  V v[kTrips<SIZE, NT, 4>], x[kTrips<SIZE, NT, 4>];
+  over<SIZE, NT, 4>(
       n,
       [&](int i, int u) {
-        v[u] = *reinterpret_cast<const KG V*>(p + i);
-        x[u] = *reinterpret_cast<const KG V*>(w + i);
+        v[u] = read<true, V>(p + i);
+        x[u] = read<true, V>(w + i);
       },
       [&](int i, int u) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[u][k] = fmaf(-step, v[u][k], x[u][k]);
-        *reinterpret_cast<KG V*>(w + i) = x[u];
+        __builtin_nontemporal_store(x[u], reinterpret_cast<KG V*>(w + i));
       },
       [&](int i) { w[i] = fmaf(-step, p[i], w[i]); });
 }
@@ -220,17 +227,17 @@ __device__ inline float factor(double sum, const WorkArgs& k, bool shown) {
   }
 }
 
-template <int W, int NT>
+template <int W, int NT, bool LAST>
 __device__ inline void sum_unit(const GradDesc& d, int64_t e0, int n, float shift, double& acc) {
-  if constexpr (W == TRUST) add_products<NT>(d, e0, n, shift, acc);
-  else add_squares<NT>(d, e0, n, acc);
+  if constexpr (W == TRUST) add_products<NT, LAST>(d, e0, n, shift, acc);
+  else add_squares<NT, LAST>(d, e0, n, acc);
 }
-template <int W, int NT>
-__device__ inline void second_unit(const GradDesc& d, int64_t e0, int n, float f) {
+template <int W, int SIZE, int NT>
+__device__ inline void second_part(const GradDesc& d, int64_t e0, int n, float f) {
   if constexpr (W == TRUST) {
-    if (f != 0.f) apply_unit<NT>(d, e0, n, f);
+    if (f != 0.f) apply_part<SIZE, NT>(d, e0, n, f);
   } else if constexpr (W == CLIP) {
-    if (f != 1.f || d.out != d.grad) scale_unit<NT>(d, e0, n, f);
+    if (f != 1.f || d.out != d.grad) scale_part<SIZE, NT>(d, e0, n, f);
   }
 }
 
@@ -248,7 +255,7 @@ __device__ inline double block_sum(double v, double* s) {
 }
 
 // First pass: the block's units b, b + grid, ...
-template <int W, class TB>
+template <int W, bool LAST, class TB>
 __global__ void __launch_bounds__(GT) grads_sum_kernel(TB tb, int count, int units, WorkArgs k,
                                                        double* __restrict__ partial) {
   __shared__ double s[GT / 64];
@@ -258,30 +265,35 @@ __global__ void __launch_bounds__(GT) grads_sum_kernel(TB tb, int count, int uni
     while (p + 1 < count && tb.begin[p + 1] <= c) ++p;
     const GradDesc d = tb.desc[p];
     const int64_t e0 = int64_t(c - tb.begin[p]) * UNIT;
-    sum_unit<W, GT>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
+    sum_unit<W, GT, LAST>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
   }
   acc = block_sum<GT>(acc, s);
   if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
 
 template <int W>
-__global__ void __launch_bounds__(ONE_THREADS) grads_factor_kernel(const double* __restrict__ partial, int n,
-                                                                   WorkArgs k, float* __restrict__ out) {
-  __shared__ double s[ONE_THREADS / 64];
+__global__ void __launch_bounds__(GT) grads_factor_kernel(const double* __restrict__ partial, int n, WorkArgs k,
+                                                          float* __restrict__ out) {
+  __shared__ double s[GT / 64];
   double v = 0;
-  for (int i = threadIdx.x; i < n; i += ONE_THREADS) v += partial[i];
-  v = block_sum<ONE_THREADS>(v, s);
-  const float f = factor<W>(v, k, threadIdx.x == 0);
+  for (int i = threadIdx.x; i < n; i += GT) v += gp(partial)[i];
+  const float f = factor<W>(block_sum<GT>(v, s), k, threadIdx.x == 0);
   if (threadIdx.x == 0) out[0] = f;
 }
 
+// Second pass, a part of a unit a block, the last first: `parts` of them up to the part `end`. No
+// loop, and so no wait for a block's stores.
+constexpr int PARTS = UNIT / PART;
 template <int W, class TB>
-__global__ void __launch_bounds__(GT) grads_apply_kernel(TB tb, int count, int units, const float* __restrict__ f) {
-  const int c = units - 1 - static_cast<int>(blockIdx.x);
+__global__ void __launch_bounds__(GT) grads_apply_kernel(TB tb, int count, int64_t end,
+                                                         const float* __restrict__ f) {
+  const int64_t at = end - 1 - blockIdx.x;
+  const int c = static_cast<int>(at / PARTS);
   const int p = find_tensor(tb, count, c);
   const GradDesc d = tb.desc[p];
-  const int64_t e0 = int64_t(c - tb.begin[p]) * UNIT;
-  second_unit<W, GT>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), f[0]);
+  const int64_t e0 = int64_t(c - tb.begin[p]) * UNIT + at % PARTS * PART;
+  const int64_t n = min(d.numel() - e0, int64_t(PART));
+  if (n > 0) second_part<W, PART, GT>(d, e0, static_cast<int>(n), f[0]);
 }
 
 // A small call in one block: both passes, and no launch between them.
@@ -292,14 +304,14 @@ __global__ void __launch_bounds__(ONE_THREADS) grads_one_kernel(InlineTables tb,
   for (int p = 0; p < count; ++p) {
     const GradDesc d = tb.desc[p];
     for (int64_t e0 = 0; e0 < d.numel(); e0 += UNIT)
-      sum_unit<W, ONE_THREADS>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
+      sum_unit<W, ONE_THREADS, false>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
   }
   const float f = factor<W>(block_sum<ONE_THREADS>(acc, s), k, threadIdx.x == 0);
   if constexpr (W != NORM)
     for (int p = 0; p < count; ++p) {
       const GradDesc d = tb.desc[p];
       for (int64_t e0 = 0; e0 < d.numel(); e0 += UNIT)
-        second_unit<W, ONE_THREADS>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), f);
+        second_part<W, UNIT, ONE_THREADS>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), f);
     }
 }
 
@@ -369,7 +381,9 @@ struct GradCall {
   std::vector<int32_t> begin;
   Spans spans;
   int units = 0;
-  void add(const GradDesc& d) {
+  int64_t read_bytes = 0;  // what the second pass reads again
+  void add(const GradDesc& d, int64_t bytes) {
+    read_bytes += bytes;
     desc.push_back(d);
     begin.push_back(units);
     units += static_cast<int>((d.numel() + UNIT - 1) / UNIT);
@@ -388,21 +402,32 @@ static kfac_status check_pointer(const void* p, int size, int i, const char* wha
 
 // Calls of at most this many units go to one block: it takes about what the two launches it
 // saves take.
-constexpr int ONE_UNITS = 8;
+constexpr int ONE_UNITS = 16;
+// The second pass finds what the first has read in the 256 MB last-level cache, if it fits; beyond
+// that the first pass does not keep it.
+constexpr int64_t CACHE_BYTES = int64_t(256) << 20;
 
 template <int W, class TB>
 static kfac_status launch_passes(const TB& tb, const GradCall& call, const WorkArgs& k, double* partial, float* f,
                                  hipStream_t s) {
   const int n = static_cast<int>(call.desc.size()), blocks = std::max(1, std::min(call.units, MAX_BLOCKS));
-  KFAC_LAUNCH(W == TRUST ? K_TRUST_SUM : K_NORM_SUM, (grads_sum_kernel<W == CLIP ? NORM : W, TB>), dim3(blocks),
-              dim3(GT), 0, s, tb, n, call.units, k, partial);
+  constexpr int S = W == CLIP ? NORM : W;  // the same sum
+  const int id = W == TRUST ? K_TRUST_SUM : K_NORM_SUM;
+  if (call.read_bytes > CACHE_BYTES) {
+    KFAC_LAUNCH(id, (grads_sum_kernel<S, true, TB>), dim3(blocks), dim3(GT), 0, s, tb, n, call.units, k, partial);
+  } else {
+    KFAC_LAUNCH(id, (grads_sum_kernel<S, false, TB>), dim3(blocks), dim3(GT), 0, s, tb, n, call.units, k, partial);
+  }
   KFAC_CHECK_LAUNCH("grads_sum_kernel");
-  KFAC_LAUNCH(K_GRADS_FACTOR, grads_factor_kernel<W>, dim3(1), dim3(ONE_THREADS), 0, s, partial, blocks, k, f);
+  KFAC_LAUNCH(K_GRADS_FACTOR, grads_factor_kernel<W>, dim3(1), dim3(GT), 0, s, partial, blocks, k, f);
   KFAC_CHECK_LAUNCH("grads_factor_kernel");
   if constexpr (W != NORM) {
-    KFAC_LAUNCH(W == TRUST ? K_TRUST_APPLY : K_GRAD_SCALE, (grads_apply_kernel<W, TB>), dim3(call.units), dim3(GT), 0,
-                s, tb, n, call.units, f);
-    KFAC_CHECK_LAUNCH("grads_apply_kernel");
+    constexpr int64_t grid = int64_t(1) << 23;  // 2^31 threads
+    for (int64_t end = int64_t(call.units) * PARTS; end > 0; end -= grid) {
+      KFAC_LAUNCH(W == TRUST ? K_TRUST_APPLY : K_GRAD_SCALE, (grads_apply_kernel<W, TB>),
+                  dim3(static_cast<unsigned>(std::min(end, grid))), dim3(GT), 0, s, tb, n, end, f);
+      KFAC_CHECK_LAUNCH("grads_apply_kernel");
+    }
   }
   return KFAC_OK;
 }
@@ -467,7 +492,7 @@ static kfac_status grad_impl(int32_t count, const int64_t* numel, const kfac_dty
       call.spans.write(out[i], numel[i] * dtype_size(out_dtype[i]), i);
       call.spans.read(grad[i], numel[i] * dtype_size(dtype[i]), i, out_dtype[i] == dtype[i]);
     }
-    call.add(d);
+    call.add(d, numel[i] * dtype_size(dtype[i]));
   }
   if (clip) {
     call.spans.write(norm, 4, -1);
@@ -508,7 +533,7 @@ static kfac_status trust_impl(int32_t count, const int64_t* numel, const float* 
     }
     call.spans.read(precond[i], 4 * numel[i], i, false);
     call.spans.write(w[i], 4 * numel[i], i);
-    call.add(d);
+    call.add(d, numel[i] * 4);
   }
   call.spans.write(step, 8, -1);
   if ((st = call.spans.check())) return st;
