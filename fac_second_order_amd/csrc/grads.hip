@@ -65,12 +65,6 @@ __device__ inline void with_type(int code, F f) {
   else f(_Float16{});
 }
 
-// N elements at any address that is a multiple of an element's size.
-template <class T, int N>
-struct Pack {
-  typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
-};
-
 // n <= SIZE elements over NT threads in groups of EV: load(i, u) for all groups of a thread first,
 // so that they are in flight together (a store could alias what is loaded next), one(i) for the
 // last n % EV elements, use(i, u) for the groups. The groups come last: what runs behind a store
@@ -89,23 +83,16 @@ __device__ inline void over(int n, L load, U use, O one) {
     if ((u * NT + tid) * EV < full) use((u * NT + tid) * EV, u);
 }
 
-// A 16-byte group; LAST: nothing reads it again before the caches have turned over.
-template <bool LAST, class V, class P>
-__device__ inline V read(const KG P* p) {
-  if constexpr (LAST) return __builtin_nontemporal_load(reinterpret_cast<const KG V*>(p));
-  else return *reinterpret_cast<const KG V*>(p);
-}
-
 template <int NT, bool LAST>
 __device__ inline void add_squares(const GradDesc& d, int64_t e0, int n, double& acc) {
   with_type(d.type(), [&](auto tag) {
     using T = decltype(tag);
-    constexpr int EV = Chunk16<T>::ev;
-    using V = typename Chunk16<T>::vec;
+    constexpr int EV = Pack<T>::n;
+    using V = typename Pack<T>::vec;
     const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
     V v[kTrips<UNIT, NT, EV>];
     over<UNIT, NT, EV>(
-        n, [&](int i, int u) { v[u] = read<LAST, V>(g + i); },
+        n, [&](int i, int u) { v[u] = load_pack<LAST, T>(g + i); },
         [&](int, int u) {
 #pragma unroll
           for (int k = 0; k < EV; ++k) {
@@ -128,18 +115,18 @@ __device__ inline void scale_part(const GradDesc& d, int64_t e0, int n, float co
     const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
     const auto scale = [&](auto otag) {
       using O = decltype(otag);
-      constexpr int EV = Chunk16<O>::ev;  // a store of 16 bytes a lane, side by side
+      constexpr int EV = Pack<O>::n;  // a store of 16 bytes a lane, side by side
       using V = typename Pack<T, EV>::vec;
       using W = typename Pack<O, EV>::vec;
       KG O* o = gp(static_cast<O*>(d.out)) + e0;
       V v[kTrips<SIZE, NT, EV>];
       over<SIZE, NT, EV>(
-          n, [&](int i, int u) { v[u] = read<true, V>(g + i); },
+          n, [&](int i, int u) { v[u] = load_pack<true, T, EV>(g + i); },
           [&](int i, int u) {
             W w;
 #pragma unroll
             for (int k = 0; k < EV; ++k) w[k] = static_cast<O>(static_cast<float>(v[u][k]) * coef);
-            __builtin_nontemporal_store(w, reinterpret_cast<KG W*>(o + i));
+            store_pack<true, O>(o + i, w);
           },
           [&](int i) { o[i] = static_cast<O>(static_cast<float>(g[i]) * coef); });
     };
@@ -167,8 +154,8 @@ __device__ inline void add_products(const GradDesc& d, int64_t e0, int n, float 
     over<UNIT, NT, 4>(
         n,
         [&](int i, int u) {
-          v[u] = read<LAST, V>(p + i);
-          w[u] = read<true, W>(g + i);
+          v[u] = load_pack<LAST, float>(p + i);
+          w[u] = load_pack<true, T, 4>(g + i);
         },
         [&](int, int u) {
 #pragma unroll
@@ -188,13 +175,13 @@ __device__ inline void apply_part(const GradDesc& d, int64_t e0, int n, float st
   over<SIZE, NT, 4>(
       n,
       [&](int i, int u) {
-        v[u] = read<true, V>(p + i);
-        x[u] = read<true, V>(w + i);
+        v[u] = load_pack<true, float>(p + i);
+        x[u] = load_pack<true, float>(w + i);
       },
       [&](int i, int u) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[u][k] = fmaf(-step, v[u][k], x[u][k]);
-        __builtin_nontemporal_store(x[u], reinterpret_cast<KG V*>(w + i));
+        store_pack<true, float>(w + i, x[u]);
       },
       [&](int i) { w[i] = fmaf(-step, p[i], w[i]); });
 }

@@ -9,11 +9,14 @@
 // The softmax is taken about a maximum in fp32. What is formed once per row or per
 // sequence (the sum over the waves, l, the ratio, the sums of l) is formed in fp64: l is
 // a difference of numbers much larger than the error that a ratio near its bound may carry.
+#include <algorithm>
+
 #include "row_ops.hpp"
 
 namespace kfac {
 
 constexpr int LT = 256;    // threads of the blocks that hold no row
+constexpr int ONE = 1024;  // of a block that is alone
 constexpr float LOG2E = 1.44269504088896340736f;
 // What rounding log2(e) to fp32 leaves off. Without it the exponential of d is off by
 // 1.3e-8 d of itself, always to the same side, which a sum of l over a long sequence shows.
@@ -39,9 +42,9 @@ __device__ inline void seq_range(const LossRows& a, int s0, int s1, int& r0, int
 
 // A row counts if its mask is set and its token lies in the vocabulary.
 __device__ inline bool row_counts(const LossRows& a, int t) {
-  if (a.mask && !gp(a.mask)[t]) return false;
   const int64_t y = gp(a.token)[t];
-  return y >= 0 && y < a.vocab;
+  const bool kept = a.mask ? gp(a.mask)[t] != 0 : true;
+  return kept & (y >= 0) & (y < a.vocab);
 }
 
 // exp(z - m), the argument off by its rounding alone.
@@ -89,8 +92,8 @@ __device__ inline MaxSum join_lanes(MaxSum v) {
 // Gradient of a row, coef (one-hot(y) - softmax): -coef softmax(z) everywhere but at y.
 template <class T>
 struct GradRow {
-  typedef typename Chunk16<T>::vec V;
-  static constexpr int EV = Chunk16<T>::ev;
+  typedef typename Pack<T>::vec V;
+  static constexpr int EV = Pack<T>::n;
   float m, scale;  // 16-bit types: log2(|coef| / sum); fp32: -coef / sum
   float at_y;
   int y;
@@ -127,14 +130,15 @@ struct GradRow {
 // A row over NT threads, C groups of 16 bytes in each thread's registers: all loads are in
 // flight at once and the row is read from memory once. Groups past the row hold -inf, which
 // weighs nothing; the last vocab % EV logits, one a thread, are `rest`. A group index that no
-// thread reaches is skipped by all. C = 0: the row stays in memory, read twice.
+// thread reaches is skipped by all. C = 0: the row stays in memory and is read again for its gradient.
 template <class T, int NT, int C>
 struct Row {
-  typedef typename Chunk16<T>::vec V;
-  static constexpr int EV = Chunk16<T>::ev;
+  typedef typename Pack<T>::vec V;
+  static constexpr int EV = Pack<T>::n;
   V v[C ? C : 1];
   float rest;
 
+  template <bool PAST>
   __device__ inline void load(const KG T* z, int vocab, int tid) {
     const int full = vocab / EV;
 #pragma unroll
@@ -142,7 +146,7 @@ struct Row {
       if (c * NT < full) {
 #pragma unroll
         for (int u = 0; u < EV; ++u) v[c][u] = static_cast<T>(NEG_INF);
-        if (c * NT + tid < full) v[c] = *reinterpret_cast<const KG V*>(z + (c * NT + tid) * EV);
+        if (c * NT + tid < full) v[c] = load_pack<PAST, T>(z + (c * NT + tid) * EV);
       }
     rest = full * EV + tid < vocab ? static_cast<float>(z[full * EV + tid]) : NEG_INF;
   }
@@ -173,53 +177,69 @@ struct Row {
           s += e;
         }
       return {m, wave_add(static_cast<double>(s))};
-    } else {  // a running maximum in each thread, the sum about it in fp64
+    } else {  // BATCH groups at a time; a running maximum in each thread, the sum about it in fp64
+      constexpr int BATCH = 8;
       float m = rest;
       double s = rest == NEG_INF ? 0.0 : exp_about(rest, rest);
-      for (int g = tid; g < full; g += NT) {
-        const V x = *reinterpret_cast<const KG V*>(z + int64_t(g) * EV);
+      for (int g0 = tid; g0 < full; g0 += NT * BATCH) {
+        V x[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+#pragma unroll
+          for (int u = 0; u < EV; ++u) x[b][u] = static_cast<T>(NEG_INF);
+          if (g0 + b * NT < full) x[b] = load_pack<false, T>(z + int64_t(g0 + b * NT) * EV);
+        }
         float top = m;
 #pragma unroll
-        for (int u = 0; u < EV; ++u) top = fmaxf(top, static_cast<float>(x[u]));
-        const float at = top == NEG_INF ? 0.f : top;
-        if (top != m) s *= exp(static_cast<double>(m) - at);
-        m = top;
-        float e = 0;
+        for (int b = 0; b < BATCH; ++b)
 #pragma unroll
-        for (int u = 0; u < EV; ++u) e += exp_about(static_cast<float>(x[u]), at);
-        s += e;
+          for (int u = 0; u < EV; ++u) top = fmaxf(top, static_cast<float>(x[b][u]));
+        const float at = top == NEG_INF ? 0.f : top;
+        if (top != m) s *= exp_about(m, at);
+        m = top;
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          v4u raw = __builtin_bit_cast(v4u, x[b]);
+          asm("" : "+v"(raw));  // widened again, as above
+          const V w = __builtin_bit_cast(V, raw);
+          float e = 0;
+#pragma unroll
+          for (int u = 0; u < EV; ++u) e += exp_about(static_cast<float>(w[u]), at);
+          s += e;
+        }
       }
       return join_lanes({m, s});
     }
   }
 
   // An element is read and written by one thread: d may be z.
+  template <bool PAST>
   __device__ inline void gradient(const GradRow<T>& k, const KG T* z, KG T* d, int vocab, int tid) const {
     const int full = vocab / EV;
+    if (full * EV + tid < vocab) d[full * EV + tid] = k.one(rest, full * EV + tid);
     if constexpr (C > 0) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
         if (c * NT + tid < full) {
           const int g = c * NT + tid;
-          *reinterpret_cast<KG V*>(d + g * EV) = k.group(v[c], g);
+          store_pack<PAST, T>(d + g * EV, k.group(v[c], g));
         }
     } else {
       for (int g = tid; g < full; g += NT) {
-        const V x = *reinterpret_cast<const KG V*>(z + int64_t(g) * EV);
-        *reinterpret_cast<KG V*>(d + int64_t(g) * EV) = k.group(x, g);
+        const V x = load_pack<false, T>(z + int64_t(g) * EV);
+        store_pack<PAST, T>(d + int64_t(g) * EV, k.group(x, g));
       }
     }
-    if (full * EV + tid < vocab) d[full * EV + tid] = k.one(rest, full * EV + tid);
   }
 };
 
-template <class T, int NT>
+template <class T, int NT, bool PAST>
 __device__ inline void row_zero(KG T* d, int vocab, int tid) {
-  typedef typename Chunk16<T>::vec V;
-  constexpr int EV = Chunk16<T>::ev;
+  typedef typename Pack<T>::vec V;
+  constexpr int EV = Pack<T>::n;
   const int full = vocab / EV;
   const V w = {};
-  for (int g = tid; g < full; g += NT) *reinterpret_cast<KG V*>(d + int64_t(g) * EV) = w;
+  for (int g = tid; g < full; g += NT) store_pack<PAST, T>(d + int64_t(g) * EV, w);
   if (full * EV + tid < vocab) d[full * EV + tid] = static_cast<T>(0.f);
 }
 
@@ -229,41 +249,50 @@ constexpr int kRowsPerBlock = NT == 64 ? 4 : 1;
 template <int NT>
 constexpr int kRowThreads = NT == 64 ? 256 : NT;
 
-// The waves' statistics as the row's, in the row's first wave.
+// What a wave knows of its row: statistics of its part, and a share of the rows that count.
+struct WavePart {
+  MaxSum v;
+  int n;
+};
+
+// The waves' parts as the row's, in the row's first wave.
 template <int NT>
-__device__ inline MaxSum join_waves(MaxSum v, MaxSum* lds) {
+__device__ inline WavePart join_waves(WavePart w, WavePart* lds) {
   if constexpr (NT > 64) {
     const int lane = threadIdx.x & 63;
-    if (lane == 0) lds[threadIdx.x >> 6] = v;
+    if (lane == 0) lds[threadIdx.x >> 6] = w;
     __syncthreads();
     if (threadIdx.x < 64) {
-      v = lane < NT / 64 ? lds[lane] : MaxSum{NEG_INF, 0.0};
-      v = join_lanes(v);
+      w = lane < NT / 64 ? lds[lane] : WavePart{{NEG_INF, 0.0}, 0};
+      w.v = join_lanes(w.v);
+      w.n = wave_add(w.n);
     }
   }
-  return v;
+  return w;
 }
 
-// Sequence q in `slices` parts: how many rows of each count; per row: its sequence, -1
-// where it does not count and -2 outside every sequence.
+// Rows that count, in gridDim.y slices. By sequence (row_seq given): of each sequence, and per
+// row its sequence, -1 where the row does not count; rows outside every sequence get -2. Else: of
+// all sequences together.
 __global__ void __launch_bounds__(LT) loss_count_kernel(LossRows a, int32_t* __restrict__ row_seq,
                                                         int32_t* __restrict__ count) {
   __shared__ int s[LT / 64];
   const int q = blockIdx.x, slice = blockIdx.y, slices = gridDim.y;
   int r0, r1, n = 0;
-  seq_range(a, q, q + 1, r0, r1);
+  if (row_seq) seq_range(a, q, q + 1, r0, r1);
+  else seq_range(a, 0, a.seqs, r0, r1);
   const int per = (r1 - r0 + slices - 1) / slices;
   const int b0 = min(r0 + slice * per, r1), b1 = min(b0 + per, r1);
   for (int t = b0 + threadIdx.x; t < b1; t += LT) {
     const bool counts = row_counts(a, t);
-    row_seq[t] = counts ? q : -1;
+    if (row_seq) row_seq[t] = counts ? q : -1;
     n += counts;
   }
   n = block_add<LT>(n, s);
   if (threadIdx.x == 0) count[q * slices + slice] = n;
-  if (q == 0 && slice == 0)
+  if (row_seq && q == 0 && slice == 0)
     for (int t = threadIdx.x; t < r0; t += LT) row_seq[t] = -2;
-  if (q == a.seqs - 1 && slice == 0)
+  if (row_seq && q == a.seqs - 1 && slice == 0)
     for (int t = r1 + threadIdx.x; t < a.rows; t += LT) row_seq[t] = -2;
 }
 
@@ -273,78 +302,110 @@ struct PolicyArgs {
   const float* advantage;
   float* logp;
   float low, high, kl_coef, grad_scale;
-  int32_t by_seq;
+  // what loss_count_kernel left; by sequence both, over all rows `count` alone, and neither where
+  // the blocks count for themselves
+  const int32_t* row_seq;
+  const int32_t* count;
+  int32_t slices;
 };
 
+// Weighted surrogate loss, KL and clipped share of a row.
 struct PolicyTerms {
-  double part, kl, over;  // weighted surrogate loss, KL and clipped share of a row
+  double part, kl, over;
 };
 
-// Rows that count: all of them, or with by_seq the sequences that have one; a wave's work.
-__device__ inline int counted_total(const int32_t* count, int seqs, int slices, bool by_seq) {
-  int n = 0;
-  for (int i = threadIdx.x & 63; i < (by_seq ? seqs : seqs * slices); i += 64) {
-    if (by_seq) {
-      int k = 0;
-      for (int j = 0; j < slices; ++j) k |= count[i * slices + j];
-      n += k != 0;
-    } else {
-      n += count[i];
-    }
+enum Place { OUTSIDE, IDLE, COUNTS };  // of a row: in no sequence; in one, not counting; counting
+
+// Place of row t, and its sequence where rows weigh by sequence.
+__device__ inline Place row_place(const LossRows& a, const int32_t* row_seq, int t, int& q) {
+  const bool counts = row_counts(a, t);
+  if (row_seq) {  // offsets that decrease leave rows that no sequence wrote: q may be anything
+    q = row_seq[t];
+    return q < -1 || q >= a.seqs ? OUTSIDE : q >= 0 && counts ? COUNTS : IDLE;
   }
-  return wave_add(n);
+  int r0, r1;
+  seq_range(a, 0, a.seqs, r0, r1);
+  return t < r0 || t >= r1 ? OUTSIDE : counts ? COUNTS : IDLE;
 }
 
-template <class T, int NT, int C>
+// A thread's share of the rows that count, for a block that counts for itself.
+__device__ inline int own_count(const LossRows& a, int tid, int threads) {
+  int r0, r1, n = 0;
+  seq_range(a, 0, a.seqs, r0, r1);
+  for (int t = r0 + tid; t < r1; t += threads) n += row_counts(a, t);
+  return n;
+}
+
+// 1 / weight of the rows of sequence q; n: the rows that count, of a block that counted. A wave's work.
+__device__ inline double inverse_weight(const LossRows& a, const PolicyArgs& p, int q, int n) {
+  const int lane = threadIdx.x & 63;
+  if (!p.count) return n;
+  if (!p.row_seq) return wave_add(lane < p.slices ? p.count[lane] : 0);
+  int own = 0;
+  n = 0;
+  for (int j = 0; j < p.slices; ++j) own += p.count[q * p.slices + j];
+  for (int i = lane; i < a.seqs; i += 64) {
+    int k = 0;
+    for (int j = 0; j < p.slices; ++j) k |= p.count[i * p.slices + j];
+    n += k != 0;
+  }
+  return static_cast<double>(wave_add(n)) * own;
+}
+
+// Loss of row t from its softmax, and the coefficient of its gradient; `shown` writes l.
+__device__ inline float policy_row(const PolicyArgs& p, int t, float z_y, MaxSum r, double weight, bool shown,
+                                   PolicyTerms& out) {
+  const double l = static_cast<double>(z_y) - r.m - log(r.s);
+  const double ratio = exp(l - gp(p.old_logp)[t]);
+  const double adv = gp(p.advantage)[t];
+  // NaN goes through: a comparison with it is false
+  const double bounded = ratio < 1.0 - p.low ? 1.0 - p.low : ratio > 1.0 + p.high ? 1.0 + p.high : ratio;
+  const double free = ratio * adv, held = bounded * adv;
+  const bool over = free > held;
+  double slope = over ? 0.0 : -free, kl = 0;
+  if (p.ref_logp) {
+    const double x = gp(p.ref_logp)[t] - l, e = expm1(x);
+    kl = e - x;
+    if (p.kl_coef != 0.f) slope -= p.kl_coef * e;
+  }
+  if (shown) gp(p.logp)[t] = static_cast<float>(l);
+  out = {weight * -(over ? held : free), weight * kl, over ? weight : 0.0};
+  return static_cast<float>(p.grad_scale * weight * slope);
+}
+
+template <class T, int NT, int C, bool PAST>
 __global__ void __launch_bounds__(kRowThreads<NT>) policy_rows_kernel(LossRows a, PolicyArgs p,
-                                                                      const int32_t* __restrict__ row_seq,
-                                                                      const int32_t* __restrict__ count, int slices,
                                                                       PolicyTerms* __restrict__ terms) {
-  __shared__ MaxSum lds[NT / 64];
+  __shared__ WavePart lds[NT / 64];
   __shared__ struct { double s; float m, coef; } row_s;
   const int tid = threadIdx.x & (NT - 1);
   const int t = blockIdx.x * kRowsPerBlock<NT> + (NT == 64 ? threadIdx.x >> 6 : 0);
   if (t >= a.rows) return;
-  int q = row_seq[t];
-  if (q >= 0 && (q >= a.seqs || !row_counts(a, t))) q = -2;  // offsets that decrease: no sequence wrote this row
+  int q = 0;
+  const Place place = row_place(a, p.row_seq, t, q);
   KG T* d = a.dlogits ? gp(static_cast<T*>(a.dlogits)) + t * a.ld_grad : nullptr;
-  if (q < 0) {  // outside (left as it is) or not counted (no gradient)
+  if (place != COUNTS) {
     if (tid == 0) {
       terms[t] = {0, 0, 0};
-      if (q == -1) gp(p.logp)[t] = 0.f;
+      if (place == IDLE) gp(p.logp)[t] = 0.f;
     }
-    if (q == -1 && d) row_zero<T, NT>(d, a.vocab, tid);
+    if (place == IDLE && d) row_zero<T, NT, PAST>(d, a.vocab, tid);
     return;
   }
   const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
   const int y = static_cast<int>(gp(a.token)[t]);
   const float z_y = static_cast<float>(z[y]);
   Row<T, NT, C> row;
-  row.load(z, a.vocab, tid);
-  MaxSum r = join_waves<NT>(row.wave_stats(z, a.vocab, tid), lds);
+  row.template load<PAST>(z, a.vocab, tid);
+  const int mine = p.count ? 0 : wave_add(own_count(a, tid, NT));
+  const WavePart w = join_waves<NT>({row.wave_stats(z, a.vocab, tid), mine}, lds);
+  MaxSum r = w.v;
   float coef = 0;
   if (tid < 64) {
-    const int n = counted_total(count, a.seqs, slices, p.by_seq);
-    int own = 0;
-    for (int j = 0; j < slices; ++j) own += count[q * slices + j];
-    const double weight = p.by_seq ? 1.0 / (static_cast<double>(n) * own) : 1.0 / n;
-    const double l = static_cast<double>(z_y) - r.m - log(r.s);
-    const double ratio = exp(l - gp(p.old_logp)[t]);
-    const double adv = gp(p.advantage)[t];
-    // NaN goes through: a comparison with it is false
-    const double bounded = ratio < 1.0 - p.low ? 1.0 - p.low : ratio > 1.0 + p.high ? 1.0 + p.high : ratio;
-    const double free = ratio * adv, held = bounded * adv;
-    const bool over = free > held;
-    double slope = over ? 0.0 : -free, kl = 0;
-    if (p.ref_logp) {
-      const double x = gp(p.ref_logp)[t] - l, e = expm1(x);
-      kl = e - x;
-      if (p.kl_coef != 0.f) slope -= p.kl_coef * e;
-    }
-    coef = static_cast<float>(p.grad_scale * weight * slope);
+    PolicyTerms out;
+    coef = policy_row(p, t, z_y, r, 1.0 / inverse_weight(a, p, q, w.n), tid == 0, out);
     if (tid == 0) {
-      gp(p.logp)[t] = static_cast<float>(l);
-      terms[t] = {weight * -(over ? held : free), weight * kl, over ? weight : 0.0};
+      terms[t] = out;
       row_s.s = r.s;
       row_s.m = r.m;
       row_s.coef = coef;
@@ -357,29 +418,33 @@ __global__ void __launch_bounds__(kRowThreads<NT>) policy_rows_kernel(LossRows a
     r.s = row_s.s;
     coef = row_s.coef;
   }
-  row.gradient(GradRow<T>(r.m, r.s, y, z_y, coef), z, d, a.vocab, tid);
+  row.template gradient<PAST>(GradRow<T>(r.m, r.s, y, z_y, coef), z, d, a.vocab, tid);
 }
 
-// stats: loss, its surrogate part, the mean KL, the clipped share.
-constexpr int FT = 1024;
-__global__ void __launch_bounds__(FT) policy_finish_kernel(const PolicyTerms* __restrict__ terms, int rows,
-                                                           float kl_coef, float* stats) {
-  __shared__ double s[FT / 64];
-  double part = 0, kl = 0, over = 0;
-  for (int t = threadIdx.x; t < rows; t += FT) {
-    part += terms[t].part;
-    kl += terms[t].kl;
-    over += terms[t].over;
-  }
-  part = block_add<FT>(part, s);
-  kl = block_add<FT>(kl, s);
-  over = block_add<FT>(over, s);
+// stats from the waves' sums of terms: loss, its surrogate part, the mean KL, the clipped share.
+template <int NT>
+__device__ inline void policy_stats(PolicyTerms v, float kl_coef, float* stats) {
+  __shared__ PolicyTerms lds[NT / 64];
+  v = {wave_add(v.part), wave_add(v.kl), wave_add(v.over)};
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
   if (threadIdx.x == 0) {
-    stats[0] = static_cast<float>(kl_coef != 0.f ? part + kl_coef * kl : part);
-    stats[1] = static_cast<float>(part);
-    stats[2] = static_cast<float>(kl);
-    stats[3] = static_cast<float>(over);
+    for (int i = 1; i < NT / 64; ++i) v = {v.part + lds[i].part, v.kl + lds[i].kl, v.over + lds[i].over};
+    gp(stats)[0] = static_cast<float>(kl_coef != 0.f ? v.part + kl_coef * v.kl : v.part);
+    gp(stats)[1] = static_cast<float>(v.part);
+    gp(stats)[2] = static_cast<float>(v.kl);
+    gp(stats)[3] = static_cast<float>(v.over);
   }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NT) policy_finish_kernel(const PolicyTerms* __restrict__ terms, int rows,
+                                                           float kl_coef, float* stats) {
+  PolicyTerms v = {0, 0, 0};
+#pragma unroll 4
+  for (int t = threadIdx.x; t < rows; t += NT)
+    v = {v.part + terms[t].part, v.kl + terms[t].kl, v.over + terms[t].over};
+  policy_stats<NT>(v, kl_coef, stats);
 }
 
 // What the gradient of a row needs of its softmax.
@@ -392,22 +457,20 @@ struct RowStat {
 template <class T, int NT, int C>
 __global__ void __launch_bounds__(kRowThreads<NT>) pref_rows_kernel(LossRows a, RowStat* __restrict__ row_stat,
                                                                     double* __restrict__ row_logp) {
-  __shared__ MaxSum lds[NT / 64];
+  __shared__ WavePart lds[NT / 64];
   const int tid = threadIdx.x & (NT - 1);
   const int t = blockIdx.x * kRowsPerBlock<NT> + (NT == 64 ? threadIdx.x >> 6 : 0);
-  if (t >= a.rows) return;
-  int r0, r1;
-  seq_range(a, 0, a.seqs, r0, r1);
-  if (t < r0 || t >= r1) return;
-  if (!row_counts(a, t)) {
-    if (tid == 0) row_logp[t] = 0;
+  int q;
+  const Place place = t < a.rows ? row_place(a, nullptr, t, q) : OUTSIDE;
+  if (place != COUNTS) {
+    if (place == IDLE && tid == 0) row_logp[t] = 0;
     return;
   }
   const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
   const float z_y = static_cast<float>(z[gp(a.token)[t]]);
   Row<T, NT, C> row;
-  row.load(z, a.vocab, tid);
-  const MaxSum r = join_waves<NT>(row.wave_stats(z, a.vocab, tid), lds);
+  row.template load<false>(z, a.vocab, tid);
+  const MaxSum r = join_waves<NT>({row.wave_stats(z, a.vocab, tid), 0}, lds).v;
   if (tid == 0) {
     row_stat[t] = {r.m, z_y, r.s};
     row_logp[t] = static_cast<double>(z_y) - r.m - log(r.s);
@@ -423,41 +486,53 @@ struct PrefArgs {
   int32_t pairs;
 };
 
-// log(1 + exp(x))
-__device__ inline double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+// Pair i from its sequences' sums of l: the margin, its share of the loss, and what its gradient
+// takes: the coefficient of a row of the preferred sequence. `shown` writes the results.
+__device__ inline float pref_pair(const PrefArgs& p, int i, double chosen, double other, bool shown, double& loss) {
+  const double rc = p.ref_logp ? gp(p.ref_logp)[i] : 0.f, rr = p.ref_logp ? gp(p.ref_logp)[i + p.pairs] : 0.f;
+  const double x = p.beta * ((chosen - rc) - (other - rr)), e = p.smooth;
+  const double t = exp(-fabs(x));
+  const double below = fmax(-x, 0.0) + log1p(t);            // log(1 + exp(-x)); log(1 + exp(x)) is x more
+  const double miss = (x > 0 ? t : 1.0) / (1.0 + t);        // 1 / (1 + exp(x))
+  loss = (e != 0 ? below + e * x : below) / p.pairs;
+  if (shown) {
+    gp(p.margin)[i] = static_cast<float>(x);
+    gp(p.seq_logp)[i] = static_cast<float>(chosen);
+    gp(p.seq_logp)[i + p.pairs] = static_cast<float>(other);
+  }
+  return static_cast<float>(p.grad_scale * (e - miss) * p.beta / p.pairs);
+}
 
-// A block takes PAIRS pairs, a wave each of their sequences: the sums of l, the margins, the
-// loss, and for each row the coefficient of its gradient. part: a block's share of the loss.
-constexpr int PAIRS = 8;
-constexpr int PT = 2 * PAIRS * 64;
-__global__ void __launch_bounds__(PT) pref_pairs_kernel(LossRows a, PrefArgs p, const double* __restrict__ row_logp,
-                                                        float* __restrict__ row_coef, double* __restrict__ part) {
+// Sum of l over a sequence by one wave.
+__device__ inline double sequence_sum(const LossRows& a, int q, const double* row_logp) {
+  int r0, r1;
+  seq_range(a, q, q + 1, r0, r1);
+  double v = 0;
+  for (int t = r0 + static_cast<int>(threadIdx.x & 63); t < r1; t += 64) v += gp(row_logp)[t];
+  return wave_add(v);
+}
+
+// A block takes PAIRS pairs, a wave each of their sequences: the sums of l, the pair's results,
+// and for each row the coefficient of its gradient. part: a block's share of the loss.
+constexpr int PAIRS = ONE / 128;
+__global__ void __launch_bounds__(ONE) pref_pairs_kernel(LossRows a, PrefArgs p, const double* __restrict__ row_logp,
+                                                         float* __restrict__ row_coef, double* __restrict__ part) {
   __shared__ double sum_s[2 * PAIRS], loss_s[PAIRS];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int local = wave >> 1, side = wave & 1;  // side 1: the other of the pair
   const int i = blockIdx.x * PAIRS + local;
   const bool here = i < p.pairs;
-  int r0 = 0, r1 = 0;
-  if (here) seq_range(a, i + side * p.pairs, i + side * p.pairs + 1, r0, r1);
-  double v = 0;
-  for (int t = r0 + lane; t < r1; t += 64) v += row_logp[t];
-  v = wave_add(v);
-  if (lane == 0) sum_s[wave] = v;
+  if (here) {
+    const double v = sequence_sum(a, i + side * p.pairs, row_logp);
+    if (lane == 0) sum_s[wave] = v;
+  }
   __syncthreads();
   double loss = 0;
   if (here) {
-    const double chosen = sum_s[2 * local], other = sum_s[2 * local + 1];
-    const double rc = p.ref_logp ? gp(p.ref_logp)[i] : 0.f, rr = p.ref_logp ? gp(p.ref_logp)[i + p.pairs] : 0.f;
-    const double x = p.beta * ((chosen - rc) - (other - rr)), e = p.smooth;
-    const double below = softplus(-x), above = softplus(x);  // -log sig(x), -log sig(-x)
-    loss = (e != 0 ? (1 - e) * below + e * above : below) / p.pairs;
-    const double slope = (e - exp(-above)) * p.beta / p.pairs;
-    if (lane == 0) {
-      if (side == 0) gp(p.margin)[i] = static_cast<float>(x);
-      gp(p.seq_logp)[i + side * p.pairs] = static_cast<float>(v);
-    }
-    const float c = static_cast<float>(p.grad_scale * (side ? -slope : slope));
-    for (int t = r0 + lane; t < r1; t += 64) row_coef[t] = c;
+    const float c = pref_pair(p, i, sum_s[2 * local], sum_s[2 * local + 1], side == 0 && lane == 0, loss);
+    int r0, r1;
+    seq_range(a, i + side * p.pairs, i + side * p.pairs + 1, r0, r1);
+    for (int t = r0 + lane; t < r1; t += 64) row_coef[t] = side ? -c : c;
   }
   if (lane == 0 && side == 0) loss_s[local] = loss;
   __syncthreads();
@@ -477,43 +552,99 @@ __global__ void __launch_bounds__(LT) pref_finish_kernel(const double* __restric
   if (threadIdx.x == 0) loss[0] = static_cast<float>(v);
 }
 
-// Elementwise over the rows, last rows first: what pref_rows_kernel read last is what the
-// caches still hold. A block takes LT * GRAD_U groups of 16 bytes of a row.
-constexpr int GRAD_U = 2;
-template <class T>
-__global__ void __launch_bounds__(LT) pref_grad_kernel(LossRows a, const RowStat* __restrict__ row_stat,
-                                                       const float* __restrict__ row_coef) {
-  typedef typename Chunk16<T>::vec V;
-  constexpr int EV = Chunk16<T>::ev;
-  int r0, r1;
-  seq_range(a, 0, a.seqs, r0, r1);
-  const int full = a.vocab / EV, g0 = blockIdx.x * LT * GRAD_U + threadIdx.x;
-  const bool last = blockIdx.x == 0 && full * EV + static_cast<int>(threadIdx.x) < a.vocab;
-  for (int t = r1 - 1 - static_cast<int>(blockIdx.y); t >= r0; t -= gridDim.y) {
-    const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
-    KG T* d = gp(static_cast<T*>(a.dlogits)) + t * a.ld_grad;
-    if (!row_counts(a, t)) {
-      const V none = {};
-#pragma unroll
-      for (int u = 0; u < GRAD_U; ++u)
-        if (g0 + u * LT < full) *reinterpret_cast<KG V*>(d + int64_t(g0 + u * LT) * EV) = none;
-      if (last) d[full * EV + threadIdx.x] = static_cast<T>(0.f);
-      continue;
-    }
-    const RowStat r = row_stat[t];
-    V v[GRAD_U];
-#pragma unroll
-    for (int u = 0; u < GRAD_U; ++u)
-      if (g0 + u * LT < full) v[u] = *reinterpret_cast<const KG V*>(z + int64_t(g0 + u * LT) * EV);
-    const GradRow<T> k(r.m, r.s, static_cast<int>(gp(a.token)[t]), r.z_y, row_coef[t]);
-#pragma unroll
-    for (int u = 0; u < GRAD_U; ++u)
-      if (g0 + u * LT < full) *reinterpret_cast<KG V*>(d + int64_t(g0 + u * LT) * EV) = k.group(v[u], g0 + u * LT);
-    if (last) {
-      const int j = full * EV + threadIdx.x;
-      d[j] = k.one(static_cast<float>(z[j]), j);
-    }
+// Coefficient of row t's gradient, formed by the block that needs it (at most 32 sequences).
+__device__ inline float row_coefficient(const LossRows& a, const PrefArgs& p, int t, const double* row_logp) {
+  __shared__ double s[2][LT / 64];
+  const int lane = threadIdx.x & 63;
+  // the last sequence that begins at or before t
+  const int q = __popcll(__ballot(lane > 0 && lane < a.seqs && gp(a.begin)[lane] <= t));
+  const int side = q >= p.pairs, i = q - side * p.pairs;
+  double v[2];
+  for (int k = 0; k < 2; ++k) {
+    int r0, r1;
+    seq_range(a, i + k * p.pairs, i + k * p.pairs + 1, r0, r1);
+    v[k] = 0;
+    for (int u = r0 + static_cast<int>(threadIdx.x); u < r1; u += LT) v[k] += gp(row_logp)[u];
+    v[k] = wave_add(v[k]);
+    if (lane == 0) s[k][threadIdx.x >> 6] = v[k];
   }
+  __syncthreads();
+  for (int k = 0; k < 2; ++k) {
+    v[k] = 0;
+    for (int w = 0; w < LT / 64; ++w) v[k] += s[k][w];
+  }
+  double loss;
+  const float c = pref_pair(p, i, v[0], v[1], false, loss);
+  return side ? -c : c;
+}
+
+// The results of all pairs by one block, a wave a pair.
+__device__ inline void pair_results(const LossRows& a, const PrefArgs& p, const double* row_logp) {
+  __shared__ double loss_s[LT / 64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  double loss = 0;
+  for (int i = wave; i < p.pairs; i += LT / 64) {
+    double share;
+    const double chosen = sequence_sum(a, i, row_logp), other = sequence_sum(a, i + p.pairs, row_logp);
+    pref_pair(p, i, chosen, other, lane == 0, share);
+    loss += share;
+  }
+  if (lane == 0) loss_s[wave] = loss;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < LT / 64; ++w) loss += loss_s[w];
+    gp(p.loss)[0] = static_cast<float>(loss);
+  }
+}
+
+// Elementwise over the rows below `end`, last rows first: what pref_rows_kernel read last is what the
+// caches still hold. A block takes LT * GRAD_U groups of 16 bytes of a row and ends with its stores: no
+// loop over rows, which would wait for them. ALONE: no pref_pairs_kernel came before; every block
+// forms its row's coefficient, and one more in y the pairs' results.
+constexpr int GRAD_U = 2;
+template <class T, bool PAST, bool ALONE>
+__global__ void __launch_bounds__(LT) pref_grad_kernel(LossRows a, PrefArgs p, const RowStat* __restrict__ row_stat,
+                                                       const float* __restrict__ row_coef,
+                                                       const double* __restrict__ row_logp, int end) {
+  typedef typename Pack<T>::vec V;
+  constexpr int EV = Pack<T>::n;
+  int y = blockIdx.y;
+  if constexpr (ALONE) {
+    if (y == 0) {
+      if (blockIdx.x == 0) pair_results(a, p, row_logp);
+      return;
+    }
+    --y;
+  }
+  const int t = end - 1 - y;
+  int q;
+  const Place place = row_place(a, nullptr, t, q);
+  if (place == OUTSIDE) return;
+  const int full = a.vocab / EV, g0 = blockIdx.x * LT * GRAD_U + threadIdx.x;
+  const int j = full * EV + threadIdx.x;
+  const bool last = blockIdx.x == 0 && j < a.vocab;
+  const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
+  KG T* d = gp(static_cast<T*>(a.dlogits)) + t * a.ld_grad;
+  if (place == IDLE) {
+    const V none = {};
+    if (last) d[j] = static_cast<T>(0.f);
+#pragma unroll
+    for (int u = 0; u < GRAD_U; ++u)
+      if (g0 + u * LT < full) store_pack<PAST, T>(d + int64_t(g0 + u * LT) * EV, none);
+    return;
+  }
+  V v[GRAD_U];
+#pragma unroll
+  for (int u = 0; u < GRAD_U; ++u)
+    if (g0 + u * LT < full) v[u] = load_pack<true, T>(z + int64_t(g0 + u * LT) * EV);
+  const float rest = last ? static_cast<float>(z[j]) : 0.f;
+  const RowStat r = row_stat[t];
+  const float coef = ALONE ? row_coefficient(a, p, t, row_logp) : row_coef[t];
+  const GradRow<T> k(r.m, r.s, static_cast<int>(gp(a.token)[t]), r.z_y, coef);
+  if (last) d[j] = k.one(rest, j);
+#pragma unroll
+  for (int u = 0; u < GRAD_U; ++u)
+    if (g0 + u * LT < full) store_pack<PAST, T>(d + int64_t(g0 + u * LT) * EV, k.group(v[u], g0 + u * LT));
 }
 
 }  // namespace kfac
@@ -572,21 +703,28 @@ static bool finite(float x) { return x - x == 0.f; }
 // block. Longer rows stay in memory.
 #define KFAC_BY_ROW(T, vocab, LAUNCH)                     \
   do {                                                    \
-    const int groups_ = (vocab) / Chunk16<T>::ev;         \
+    const int groups_ = (vocab) / Pack<T>::n;         \
     if (groups_ <= 64 * 4) { LAUNCH(T, 64, 4) }           \
     else if (groups_ <= 256 * 4) { LAUNCH(T, 256, 4) }    \
     else if (groups_ <= 256 * 8) { LAUNCH(T, 256, 8) }    \
     else if (groups_ <= 512 * 8) { LAUNCH(T, 512, 8) }    \
-    else if (groups_ <= 1024 * 8) { LAUNCH(T, 1024, 8) }  \
+    else if (groups_ <= 512 * 16) { LAUNCH(T, 512, 16) }  \
     else if (groups_ <= 1024 * 16) { LAUNCH(T, 1024, 16) } \
     else if (groups_ <= 1024 * 20) { LAUNCH(T, 1024, 20) } \
     else { LAUNCH(T, 1024, 0) }                           \
   } while (0)
 
-// Parts of a sequence that are counted side by side.
-static int count_slices(int32_t rows, int32_t seqs) {
-  const int64_t n = rows / (int64_t(seqs) * 1024);
-  return n < 1 ? 1 : n > 16 ? 16 : static_cast<int>(n);
+static int64_t row_bytes(int32_t rows, int32_t vocab, kfac_dtype dtype) {
+  return int64_t(rows) * vocab * (dtype == KFAC_F32 ? 4 : 2);
+}
+// Rows of more than this pass the caches by where they are read or written once. What is dirty in
+// the 256 MB last-level cache is written back later at the expense of what is read then.
+constexpr int64_t STORE_PAST = int64_t(64) << 20;
+
+// A count of rows: by sequence in 256-row slices, up to 16; over all rows in up to 64.
+static int count_slices(int32_t rows, int32_t seqs, bool by_seq) {
+  const int64_t n = rows / (int64_t(by_seq ? seqs : 1) * LT), most = by_seq ? 16 : 64;
+  return n < 1 ? 1 : n > most ? static_cast<int>(most) : static_cast<int>(n);
 }
 
 struct PolicyWs {
@@ -598,7 +736,7 @@ static PolicyWs policy_ws(void* ws, int32_t rows, int32_t seqs) {
   Carver cv(ws);
   PolicyWs w;
   w.row_seq = cv.take<int32_t>(rows);
-  w.count = cv.take<int32_t>(size_t(seqs ? seqs : 1) * count_slices(rows, seqs ? seqs : 1));
+  w.count = cv.take<int32_t>(std::max<size_t>(64, size_t(seqs) * (seqs ? count_slices(rows, seqs, true) : 0)));
   w.terms = cv.take<PolicyTerms>(rows);
   w.bytes = cv.used;
   return w;
@@ -609,6 +747,16 @@ extern "C" kfac_status kfac_policy_loss_workspace(int32_t rows, int32_t vocab, i
   kfac_status st = rows_validate(rows, vocab, seqs);
   if (st) return st;
   *bytes = policy_ws(nullptr, rows, seqs).bytes;
+  return KFAC_OK;
+}
+
+static kfac_status launch_finish(const PolicyTerms* terms, int32_t rows, float kl_coef, float* stats, hipStream_t s) {
+  if (rows <= 4 * LT) {
+    KFAC_LAUNCH(K_POLICY_FINISH, policy_finish_kernel<LT>, dim3(1), dim3(LT), 0, s, terms, rows, kl_coef, stats);
+  } else {
+    KFAC_LAUNCH(K_POLICY_FINISH, policy_finish_kernel<ONE>, dim3(1), dim3(ONE), 0, s, terms, rows, kl_coef, stats);
+  }
+  KFAC_CHECK_LAUNCH("policy_finish_kernel");
   return KFAC_OK;
 }
 
@@ -639,24 +787,46 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
   const PolicyWs w = policy_ws(workspace, rows, seqs);
   if ((st = check_workspace(workspace, ws_bytes, w.bytes))) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (rows > 0) {
-    const PolicyArgs p = {old_logp, ref_logp, advantage, logp, clip_low, clip_high, kl_coef, grad_scale, by_sequence};
-    const int slices = count_slices(rows, a.seqs);
-    KFAC_LAUNCH(K_LOSS_COUNT, loss_count_kernel, dim3(a.seqs, slices), dim3(LT), 0, s, a, w.row_seq, w.count);
+  PolicyArgs p = {old_logp, ref_logp, advantage, logp, clip_low, clip_high, kl_coef, grad_scale, nullptr, nullptr, 0};
+  const bool by_seq = by_sequence && seqs > 1;  // the mean over one sequence is the mean over its rows
+  if (rows == 0) return launch_finish(w.terms, rows, kl_coef, stats, s);
+  // Where a row's threads have one row each to look at (a wave up to four) they count for themselves,
+  // behind the loads of their own row; with four each, 4096 rows of 131072 took 387 us instead of 360.
+  int row_threads = 0;
+#define KFAC_THREADS(T, NT, C) row_threads = NT;
+#define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, KFAC_THREADS);
+  KFAC_BY_TYPE(dtype, KFAC_TYPED);
+#undef KFAC_TYPED
+#undef KFAC_THREADS
+  if (by_seq || rows > std::max(row_threads, 256)) {
+    p.row_seq = by_seq ? w.row_seq : nullptr;
+    p.count = w.count;
+    p.slices = count_slices(rows, seqs, by_seq);
+    KFAC_LAUNCH(K_LOSS_COUNT, loss_count_kernel, dim3(by_seq ? seqs : 1, p.slices), dim3(LT), 0, s, a,
+                by_seq ? w.row_seq : nullptr, w.count);
     KFAC_CHECK_LAUNCH("loss_count_kernel");
+  }
+  const bool past = row_bytes(rows, vocab, dtype) > STORE_PAST;
 #define KFAC_ROWS(T, NT, C)                                                                                      \
-  KFAC_LAUNCH(K_POLICY_ROWS, (policy_rows_kernel<T, NT, C>), dim3((rows - 1) / kRowsPerBlock<NT> + 1),           \
-              dim3(kRowThreads<NT>), 0, s, a, p, w.row_seq, w.count, slices, w.terms);
+  const unsigned grid = (rows - 1) / kRowsPerBlock<NT> + 1;                                                      \
+  if (past) {                                                                                                    \
+    KFAC_LAUNCH(K_POLICY_ROWS, (policy_rows_kernel<T, NT, C, true>), dim3(grid), dim3(kRowThreads<NT>), 0, s, a, \
+                p, w.terms);                                                                                     \
+  } else {                                                                                                       \
+    KFAC_LAUNCH(K_POLICY_ROWS, (policy_rows_kernel<T, NT, C, false>), dim3(grid), dim3(kRowThreads<NT>), 0, s, a, \
+                p, w.terms);                                                                                     \
+  }
 #define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, KFAC_ROWS);
-    KFAC_BY_TYPE(dtype, KFAC_TYPED);
+  KFAC_BY_TYPE(dtype, KFAC_TYPED);
 #undef KFAC_TYPED
 #undef KFAC_ROWS
-    KFAC_CHECK_LAUNCH("policy_rows_kernel");
-  }
-  KFAC_LAUNCH(K_POLICY_FINISH, policy_finish_kernel, dim3(1), dim3(FT), 0, s, w.terms, rows, kl_coef, stats);
-  KFAC_CHECK_LAUNCH("policy_finish_kernel");
-  return KFAC_OK;
+  KFAC_CHECK_LAUNCH("policy_rows_kernel");
+  return launch_finish(w.terms, rows, kl_coef, stats, s);
 }
+
+// Up to here the gradient's blocks wait less for their sums than the launch of pref_pairs_kernel takes
+// (1000 rows of 1000 in fp32: 14.6 against 16.8 us; 300 of 32000: 25.2 against 23.5).
+constexpr int64_t ALONE_BYTES = int64_t(8) << 20;
 
 struct PrefWs {
   RowStat* stat;
@@ -712,9 +882,10 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
   hipStream_t s = static_cast<hipStream_t>(stream);
   const PrefArgs p = {ref_logp, seq_logp, margin, loss, beta, label_smoothing, grad_scale, pairs};
   const bool any = rows > 0 && pairs > 0;
+  const bool store_past = row_bytes(rows, vocab, dtype) > STORE_PAST;
   if (any) {
-#define KFAC_ROWS(T, NT, C)                                                                                 \
-  KFAC_LAUNCH(K_PREF_ROWS, (pref_rows_kernel<T, NT, C>), dim3((rows - 1) / kRowsPerBlock<NT> + 1),          \
+#define KFAC_ROWS(T, NT, C)                                                                        \
+  KFAC_LAUNCH(K_PREF_ROWS, (pref_rows_kernel<T, NT, C>), dim3((rows - 1) / kRowsPerBlock<NT> + 1), \
               dim3(kRowThreads<NT>), 0, s, a, w.stat, w.logp);
 #define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, KFAC_ROWS);
     KFAC_BY_TYPE(dtype, KFAC_TYPED);
@@ -722,21 +893,35 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
 #undef KFAC_ROWS
     KFAC_CHECK_LAUNCH("pref_rows_kernel");
   }
-  const int blocks = pair_blocks(pairs);
-  KFAC_LAUNCH(K_PREF_PAIRS, pref_pairs_kernel, dim3(blocks), dim3(PT), 0, s, a, p, w.logp, w.coef, w.part);
-  KFAC_CHECK_LAUNCH("pref_pairs_kernel");
-  if (blocks > 1) {
-    KFAC_LAUNCH(K_PREF_FINISH, pref_finish_kernel, dim3(1), dim3(LT), 0, s, w.part, blocks, loss);
-    KFAC_CHECK_LAUNCH("pref_finish_kernel");
+  // A small call with few pairs: the gradient's blocks form their own coefficients, each from the l of
+  // one pair, and one of them the pairs' results.
+  const bool alone = any && dlogits && pairs <= 16 && row_bytes(rows, vocab, dtype) <= ALONE_BYTES;
+  if (!alone) {
+    const int blocks = pair_blocks(pairs);
+    KFAC_LAUNCH(K_PREF_PAIRS, pref_pairs_kernel, dim3(blocks), dim3(ONE), 0, s, a, p, w.logp, w.coef, w.part);
+    KFAC_CHECK_LAUNCH("pref_pairs_kernel");
+    if (blocks > 1) {
+      KFAC_LAUNCH(K_PREF_FINISH, pref_finish_kernel, dim3(1), dim3(LT), 0, s, w.part, blocks, loss);
+      KFAC_CHECK_LAUNCH("pref_finish_kernel");
+    }
   }
   if (any && dlogits) {
-    const unsigned y = rows < 65535 ? rows : 65535;
-#define KFAC_TYPED(T)                                                                                             \
-  KFAC_LAUNCH(K_PREF_GRAD, pref_grad_kernel<T>, dim3((vocab / Chunk16<T>::ev) / (LT * GRAD_U) + 1, y), dim3(LT), 0, s, \
-              a, w.stat, w.coef);
-    KFAC_BY_TYPE(dtype, KFAC_TYPED);
+    constexpr int most = 65535;  // of a grid in y
+    for (int32_t end = rows; end > 0; end -= most) {
+      const unsigned y = std::min(end, most);
+#define KFAC_GRAD(T, PAST, ALONE)                                                                                   \
+  KFAC_LAUNCH(K_PREF_GRAD, (pref_grad_kernel<T, PAST, ALONE>),                                                      \
+              dim3((vocab / Pack<T>::n) / (LT * GRAD_U) + 1, ALONE ? y + 1 : y), dim3(LT), 0, s, a, p, w.stat, w.coef, \
+              w.logp, end);
+#define KFAC_TYPED(T)                                   \
+  if (alone) { KFAC_GRAD(T, false, true) }              \
+  else if (store_past) { KFAC_GRAD(T, true, false) }    \
+  else { KFAC_GRAD(T, false, false) }
+      KFAC_BY_TYPE(dtype, KFAC_TYPED);
 #undef KFAC_TYPED
-    KFAC_CHECK_LAUNCH("pref_grad_kernel");
+#undef KFAC_GRAD
+      KFAC_CHECK_LAUNCH("pref_grad_kernel");
+    }
   }
   return KFAC_OK;
 }

@@ -25,13 +25,30 @@ enum RowKernelId {
   K_TOTAL
 };
 
-// 16 bytes of T at any address that is a multiple of its size: global memory takes them
-// as one access, aligned or not.
-template <class T>
-struct Chunk16 {
-  static constexpr int ev = 16 / sizeof(T);
-  typedef T vec __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+// N elements at any address that is a multiple of an element's size: global memory takes up to
+// 16 bytes as one access, aligned or not.
+template <class T, int N = 16 / sizeof(T)>
+struct Pack {
+  static constexpr int n = N;
+  typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
+
+// Loads and stores of a pack; PAST: nothing looks at it again before the caches have turned over,
+// so it passes them by. (The element type and the length are named, not the vector: a template
+// argument would lose its alignment. PAST is no run-time choice: the compiler would make one
+// plain access of both.)
+template <bool PAST, class T, int N = 16 / sizeof(T)>
+__device__ inline typename Pack<T, N>::vec load_pack(const KG T* p) {
+  const auto from = reinterpret_cast<const KG typename Pack<T, N>::vec*>(p);
+  if constexpr (PAST) return __builtin_nontemporal_load(from);
+  else return *from;
+}
+template <bool PAST, class T, int N = 16 / sizeof(T)>
+__device__ inline void store_pack(KG T* p, typename Pack<T, N>::vec v) {
+  const auto to = reinterpret_cast<KG typename Pack<T, N>::vec*>(p);
+  if constexpr (PAST) __builtin_nontemporal_store(v, to);
+  else *to = v;
+}
 
 // Host tables are vectors: a failed allocation leaves an entry point as a status, not as
 // an exception.
