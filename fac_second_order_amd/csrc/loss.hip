@@ -89,6 +89,23 @@ __device__ inline MaxSum join_lanes(MaxSum v) {
   return {m, wave_add(s)};
 }
 
+// A row of any address as groups of 16 bytes: `head` elements up to the first aligned group, `full`
+// groups, and the elements behind them. (Groups across two lines cost a tenth of the rate on rows of
+// 50001 fp16 elements.) The elements outside the groups, fewer than 2 EV, go one to a thread.
+template <class T>
+struct Cut {
+  static constexpr int EV = Pack<T>::n;
+  int head, full, vocab;
+  __device__ inline Cut(const KG T* z, int vocab_) : vocab(vocab_) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) / sizeof(T)) & (EV - 1);
+    head = min(vocab, (EV - off) & (EV - 1));
+    full = (vocab - head) / EV;
+  }
+  __device__ inline int64_t group(int g) const { return head + int64_t(g) * EV; }
+  __device__ inline bool has_single(int i) const { return i < vocab - full * EV; }
+  __device__ inline int single(int i) const { return i < head ? i : full * EV + i; }
+};
+
 // Gradient of a row, coef (one-hot(y) - softmax): -coef softmax(z) everywhere but at y.
 template <class T>
 struct GradRow {
@@ -96,9 +113,11 @@ struct GradRow {
   static constexpr int EV = Pack<T>::n;
   float m, scale;  // 16-bit types: log2(|coef| / sum); fp32: -coef / sum
   float at_y;
-  int y;
-  unsigned sign;   // flips the signs of two 16-bit results
-  __device__ inline GradRow(float m_, double sum, int y_, float z_y, float coef) : m(m_), y(y_) {
+  int y, group_y, place_y;  // the token; its group and place there
+  unsigned sign;            // flips the signs of two 16-bit results
+  __device__ inline GradRow(const Cut<T>& cut, float m_, double sum, int y_, float z_y, float coef) : m(m_), y(y_) {
+    group_y = y < cut.head ? -1 : (y - cut.head) / EV;
+    place_y = (y - cut.head) & (EV - 1);
     const float inv = static_cast<float>(1.0 / sum);
     at_y = coef * (1.f - exp_about(z_y, m) * inv);
     scale = sizeof(T) == 2 ? __builtin_amdgcn_logf(fabsf(coef) * inv) : -coef * inv;
@@ -116,9 +135,9 @@ struct GradRow {
 #pragma unroll
     for (int u = 0; u < EV; ++u) w[u] = static_cast<T>(weight(static_cast<float>(z[u])));
     if constexpr (sizeof(T) == 2) w = __builtin_bit_cast(V, __builtin_bit_cast(v4u, w) ^ sign);
-    if (g == y / EV)
+    if (g == group_y)
 #pragma unroll
-      for (int u = 0; u < EV; ++u) w[u] = u == y % EV ? static_cast<T>(at_y) : w[u];
+      for (int u = 0; u < EV; ++u) w[u] = u == place_y ? static_cast<T>(at_y) : w[u];
     return w;
   }
   __device__ inline T one(float z, int j) const {
@@ -129,8 +148,8 @@ struct GradRow {
 
 // A row over NT threads, C groups of 16 bytes in each thread's registers: all loads are in
 // flight at once and the row is read from memory once. Groups past the row hold -inf, which
-// weighs nothing; the last vocab % EV logits, one a thread, are `rest`. A group index that no
-// thread reaches is skipped by all. C = 0: the row stays in memory and is read again for its gradient.
+// weighs nothing; `rest` is the thread's element outside the groups. A group index that no thread
+// reaches is skipped by all. C = 0: the row stays in memory and is read again for its gradient.
 template <class T, int NT, int C>
 struct Row {
   typedef typename Pack<T>::vec V;
@@ -139,21 +158,21 @@ struct Row {
   float rest;
 
   template <bool PAST>
-  __device__ inline void load(const KG T* z, int vocab, int tid) {
-    const int full = vocab / EV;
+  __device__ inline void load(const Cut<T>& cut, const KG T* z, int tid) {
+    const int full = cut.full;
 #pragma unroll
     for (int c = 0; c < C; ++c)
       if (c * NT < full) {
 #pragma unroll
         for (int u = 0; u < EV; ++u) v[c][u] = static_cast<T>(NEG_INF);
-        if (c * NT + tid < full) v[c] = load_pack<PAST, T>(z + (c * NT + tid) * EV);
+        if (c * NT + tid < full) v[c] = load_pack<PAST, T>(z + cut.group(c * NT + tid));
       }
-    rest = full * EV + tid < vocab ? static_cast<float>(z[full * EV + tid]) : NEG_INF;
+    rest = cut.has_single(tid) ? static_cast<float>(z[cut.single(tid)]) : NEG_INF;
   }
 
   // Of the wave's part of the row, in every lane.
-  __device__ inline MaxSum wave_stats(const KG T* z, int vocab, int tid) const {
-    const int full = vocab / EV;
+  __device__ inline MaxSum wave_stats(const Cut<T>& cut, const KG T* z, int tid) const {
+    const int full = cut.full;
     if constexpr (C > 0) {
       float m = rest;
 #pragma unroll
@@ -187,7 +206,7 @@ struct Row {
         for (int b = 0; b < BATCH; ++b) {
 #pragma unroll
           for (int u = 0; u < EV; ++u) x[b][u] = static_cast<T>(NEG_INF);
-          if (g0 + b * NT < full) x[b] = load_pack<false, T>(z + int64_t(g0 + b * NT) * EV);
+          if (g0 + b * NT < full) x[b] = load_pack<false, T>(z + cut.group(g0 + b * NT));
         }
         float top = m;
 #pragma unroll
@@ -214,20 +233,20 @@ struct Row {
 
   // An element is read and written by one thread: d may be z.
   template <bool PAST>
-  __device__ inline void gradient(const GradRow<T>& k, const KG T* z, KG T* d, int vocab, int tid) const {
-    const int full = vocab / EV;
-    if (full * EV + tid < vocab) d[full * EV + tid] = k.one(rest, full * EV + tid);
+  __device__ inline void gradient(const Cut<T>& cut, const GradRow<T>& k, const KG T* z, KG T* d, int tid) const {
+    const int full = cut.full;
+    if (cut.has_single(tid)) d[cut.single(tid)] = k.one(rest, cut.single(tid));
     if constexpr (C > 0) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
         if (c * NT + tid < full) {
           const int g = c * NT + tid;
-          store_pack<PAST, T>(d + g * EV, k.group(v[c], g));
+          store_pack<PAST, T>(d + cut.group(g), k.group(v[c], g));
         }
     } else {
       for (int g = tid; g < full; g += NT) {
-        const V x = load_pack<false, T>(z + int64_t(g) * EV);
-        store_pack<PAST, T>(d + int64_t(g) * EV, k.group(x, g));
+        const V x = load_pack<false, T>(z + cut.group(g));
+        store_pack<PAST, T>(d + cut.group(g), k.group(x, g));
       }
     }
   }
@@ -235,12 +254,10 @@ struct Row {
 
 template <class T, int NT, bool PAST>
 __device__ inline void row_zero(KG T* d, int vocab, int tid) {
-  typedef typename Pack<T>::vec V;
-  constexpr int EV = Pack<T>::n;
-  const int full = vocab / EV;
-  const V w = {};
-  for (int g = tid; g < full; g += NT) store_pack<PAST, T>(d + int64_t(g) * EV, w);
-  if (full * EV + tid < vocab) d[full * EV + tid] = static_cast<T>(0.f);
+  const Cut<T> cut(d, vocab);
+  const typename Pack<T>::vec w = {};
+  if (cut.has_single(tid)) d[cut.single(tid)] = static_cast<T>(0.f);
+  for (int g = tid; g < cut.full; g += NT) store_pack<PAST, T>(d + cut.group(g), w);
 }
 
 // A row's block: a wave for a short row (four rows a block, no barrier), else a block.
@@ -395,10 +412,11 @@ __global__ void __launch_bounds__(kRowThreads<NT>) policy_rows_kernel(LossRows a
   const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
   const int y = static_cast<int>(gp(a.token)[t]);
   const float z_y = static_cast<float>(z[y]);
+  const Cut<T> cut(z, a.vocab);
   Row<T, NT, C> row;
-  row.template load<PAST>(z, a.vocab, tid);
+  row.template load<PAST>(cut, z, tid);
   const int mine = p.count ? 0 : wave_add(own_count(a, tid, NT));
-  const WavePart w = join_waves<NT>({row.wave_stats(z, a.vocab, tid), mine}, lds);
+  const WavePart w = join_waves<NT>({row.wave_stats(cut, z, tid), mine}, lds);
   MaxSum r = w.v;
   float coef = 0;
   if (tid < 64) {
@@ -418,33 +436,45 @@ __global__ void __launch_bounds__(kRowThreads<NT>) policy_rows_kernel(LossRows a
     r.s = row_s.s;
     coef = row_s.coef;
   }
-  row.template gradient<PAST>(GradRow<T>(r.m, r.s, y, z_y, coef), z, d, a.vocab, tid);
+  row.template gradient<PAST>(cut, GradRow<T>(cut, r.m, r.s, y, z_y, coef), z, d, tid);
 }
 
-// stats from the waves' sums of terms: loss, its surrogate part, the mean KL, the clipped share.
+// A block's sum of terms, in its first thread.
 template <int NT>
-__device__ inline void policy_stats(PolicyTerms v, float kl_coef, float* stats) {
+__device__ inline PolicyTerms block_terms(const PolicyTerms* terms, int r0, int r1) {
   __shared__ PolicyTerms lds[NT / 64];
+  PolicyTerms v = {0, 0, 0};
+#pragma unroll 4
+  for (int t = r0 + threadIdx.x; t < r1; t += NT)
+    v = {v.part + terms[t].part, v.kl + terms[t].kl, v.over + terms[t].over};
   v = {wave_add(v.part), wave_add(v.kl), wave_add(v.over)};
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
+  for (int i = 1; i < NT / 64; ++i)
+    if (threadIdx.x == 0) v = {v.part + lds[i].part, v.kl + lds[i].kl, v.over + lds[i].over};
+  return v;
+}
+
+// Many rows: TERMS of them to one.
+constexpr int TERMS = 2048;
+__global__ void __launch_bounds__(LT) policy_terms_kernel(const PolicyTerms* __restrict__ terms, int rows,
+                                                          PolicyTerms* __restrict__ out) {
+  const int r0 = blockIdx.x * TERMS;
+  const PolicyTerms v = block_terms<LT>(terms, r0, min(rows, r0 + TERMS));
+  if (threadIdx.x == 0) out[blockIdx.x] = v;
+}
+
+// stats: loss, its surrogate part, the mean KL, the clipped share.
+template <int NT>
+__global__ void __launch_bounds__(NT) policy_finish_kernel(const PolicyTerms* __restrict__ terms, int rows,
+                                                           float kl_coef, float* stats) {
+  const PolicyTerms v = block_terms<NT>(terms, 0, rows);
   if (threadIdx.x == 0) {
-    for (int i = 1; i < NT / 64; ++i) v = {v.part + lds[i].part, v.kl + lds[i].kl, v.over + lds[i].over};
     gp(stats)[0] = static_cast<float>(kl_coef != 0.f ? v.part + kl_coef * v.kl : v.part);
     gp(stats)[1] = static_cast<float>(v.part);
     gp(stats)[2] = static_cast<float>(v.kl);
     gp(stats)[3] = static_cast<float>(v.over);
   }
-}
-
-template <int NT>
-__global__ void __launch_bounds__(NT) policy_finish_kernel(const PolicyTerms* __restrict__ terms, int rows,
-                                                           float kl_coef, float* stats) {
-  PolicyTerms v = {0, 0, 0};
-#pragma unroll 4
-  for (int t = threadIdx.x; t < rows; t += NT)
-    v = {v.part + terms[t].part, v.kl + terms[t].kl, v.over + terms[t].over};
-  policy_stats<NT>(v, kl_coef, stats);
 }
 
 // What the gradient of a row needs of its softmax.
@@ -468,9 +498,10 @@ __global__ void __launch_bounds__(kRowThreads<NT>) pref_rows_kernel(LossRows a, 
   }
   const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
   const float z_y = static_cast<float>(z[gp(a.token)[t]]);
+  const Cut<T> cut(z, a.vocab);
   Row<T, NT, C> row;
-  row.template load<false>(z, a.vocab, tid);
-  const MaxSum r = join_waves<NT>({row.wave_stats(z, a.vocab, tid), 0}, lds).v;
+  row.template load<false>(cut, z, tid);
+  const MaxSum r = join_waves<NT>({row.wave_stats(cut, z, tid), 0}, lds).v;
   if (tid == 0) {
     row_stat[t] = {r.m, z_y, r.s};
     row_logp[t] = static_cast<double>(z_y) - r.m - log(r.s);
@@ -503,42 +534,47 @@ __device__ inline float pref_pair(const PrefArgs& p, int i, double chosen, doubl
   return static_cast<float>(p.grad_scale * (e - miss) * p.beta / p.pairs);
 }
 
-// Sum of l over a sequence by one wave.
-__device__ inline double sequence_sum(const LossRows& a, int q, const double* row_logp) {
+// Sum of l over a sequence by one wave, the `part`th of `parts`.
+__device__ inline double sequence_sum(const LossRows& a, int q, const double* row_logp, int part = 0, int parts = 1) {
   int r0, r1;
   seq_range(a, q, q + 1, r0, r1);
   double v = 0;
-  for (int t = r0 + static_cast<int>(threadIdx.x & 63); t < r1; t += 64) v += gp(row_logp)[t];
+#pragma unroll 4
+  for (int t = r0 + 64 * part + static_cast<int>(threadIdx.x & 63); t < r1; t += 64 * parts) v += gp(row_logp)[t];
   return wave_add(v);
 }
 
-// A block takes PAIRS pairs, a wave each of their sequences: the sums of l, the pair's results,
-// and for each row the coefficient of its gradient. part: a block's share of the loss.
-constexpr int PAIRS = ONE / 128;
+// W waves a sequence, so PAIRS = 8 / W pairs a block: the sums of l, the pair's results, and for
+// each row the coefficient of its gradient. part: a block's share of the loss.
+constexpr int PAIR_WAVES = ONE / 64;
 __global__ void __launch_bounds__(ONE) pref_pairs_kernel(LossRows a, PrefArgs p, const double* __restrict__ row_logp,
-                                                         float* __restrict__ row_coef, double* __restrict__ part) {
-  __shared__ double sum_s[2 * PAIRS], loss_s[PAIRS];
+                                                         float* __restrict__ row_coef, double* __restrict__ part, int W) {
+  __shared__ double sum_s[PAIR_WAVES], loss_s[PAIR_WAVES];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int local = wave >> 1, side = wave & 1;  // side 1: the other of the pair
-  const int i = blockIdx.x * PAIRS + local;
+  const int seq = wave / W, share = wave % W;  // of the block's sequences; of the sequence's waves
+  const int local = seq >> 1, side = seq & 1;  // side 1: the other of the pair
+  const int i = blockIdx.x * (PAIR_WAVES / 2 / W) + local;
   const bool here = i < p.pairs;
   if (here) {
-    const double v = sequence_sum(a, i + side * p.pairs, row_logp);
+    const double v = sequence_sum(a, i + side * p.pairs, row_logp, share, W);
     if (lane == 0) sum_s[wave] = v;
   }
   __syncthreads();
   double loss = 0;
   if (here) {
-    const float c = pref_pair(p, i, sum_s[2 * local], sum_s[2 * local + 1], side == 0 && lane == 0, loss);
+    double sum[2] = {0, 0};
+    for (int k = 0; k < 2; ++k)
+      for (int w = 0; w < W; ++w) sum[k] += sum_s[(2 * local + k) * W + w];
+    const float c = pref_pair(p, i, sum[0], sum[1], side == 0 && share == 0 && lane == 0, loss);
     int r0, r1;
     seq_range(a, i + side * p.pairs, i + side * p.pairs + 1, r0, r1);
-    for (int t = r0 + lane; t < r1; t += 64) row_coef[t] = side ? -c : c;
+    for (int t = r0 + 64 * share + lane; t < r1; t += 64 * W) row_coef[t] = side ? -c : c;
   }
-  if (lane == 0 && side == 0) loss_s[local] = loss;
+  if (lane == 0) loss_s[wave] = side == 0 && share == 0 ? loss : 0.0;
   __syncthreads();
   if (threadIdx.x == 0) {
     double total = 0;
-    for (int k = 0; k < PAIRS; ++k) total += loss_s[k];
+    for (int k = 0; k < PAIR_WAVES; ++k) total += loss_s[k];
     if (gridDim.x == 1) gp(p.loss)[0] = static_cast<float>(total);
     else part[blockIdx.x] = total;
   }
@@ -552,29 +588,15 @@ __global__ void __launch_bounds__(LT) pref_finish_kernel(const double* __restric
   if (threadIdx.x == 0) loss[0] = static_cast<float>(v);
 }
 
-// Coefficient of row t's gradient, formed by the block that needs it (at most 32 sequences).
+// Coefficient of row t's gradient, formed by the wave that needs it (at most 32 sequences).
 __device__ inline float row_coefficient(const LossRows& a, const PrefArgs& p, int t, const double* row_logp) {
-  __shared__ double s[2][LT / 64];
   const int lane = threadIdx.x & 63;
   // the last sequence that begins at or before t
   const int q = __popcll(__ballot(lane > 0 && lane < a.seqs && gp(a.begin)[lane] <= t));
   const int side = q >= p.pairs, i = q - side * p.pairs;
-  double v[2];
-  for (int k = 0; k < 2; ++k) {
-    int r0, r1;
-    seq_range(a, i + k * p.pairs, i + k * p.pairs + 1, r0, r1);
-    v[k] = 0;
-    for (int u = r0 + static_cast<int>(threadIdx.x); u < r1; u += LT) v[k] += gp(row_logp)[u];
-    v[k] = wave_add(v[k]);
-    if (lane == 0) s[k][threadIdx.x >> 6] = v[k];
-  }
-  __syncthreads();
-  for (int k = 0; k < 2; ++k) {
-    v[k] = 0;
-    for (int w = 0; w < LT / 64; ++w) v[k] += s[k][w];
-  }
   double loss;
-  const float c = pref_pair(p, i, v[0], v[1], false, loss);
+  const float c =
+      pref_pair(p, i, sequence_sum(a, i, row_logp), sequence_sum(a, i + p.pairs, row_logp), false, loss);
   return side ? -c : c;
 }
 
@@ -598,53 +620,51 @@ __device__ inline void pair_results(const LossRows& a, const PrefArgs& p, const 
 }
 
 // Elementwise over the rows below `end`, last rows first: what pref_rows_kernel read last is what the
-// caches still hold. A block takes LT * GRAD_U groups of 16 bytes of a row and ends with its stores: no
-// loop over rows, which would wait for them. ALONE: no pref_pairs_kernel came before; every block
-// forms its row's coefficient, and one more in y the pairs' results.
-constexpr int GRAD_U = 2;
-template <class T, bool PAST, bool ALONE>
+// caches still hold. NT threads take a row, or U groups of 16 bytes each of a longer one (a wave a short
+// row, four rows a block), and end with their stores: no loop over rows, which would wait for them.
+// ALONE: no pref_pairs_kernel came before; every row's coefficient is formed here, and by one block
+// more in y the pairs' results.
+template <class T, int NT, int U, bool PAST, bool ALONE>
 __global__ void __launch_bounds__(LT) pref_grad_kernel(LossRows a, PrefArgs p, const RowStat* __restrict__ row_stat,
                                                        const float* __restrict__ row_coef,
                                                        const double* __restrict__ row_logp, int end) {
-  typedef typename Pack<T>::vec V;
-  constexpr int EV = Pack<T>::n;
-  int y = blockIdx.y;
+  int by = blockIdx.y;
   if constexpr (ALONE) {
-    if (y == 0) {
+    if (by == 0) {
       if (blockIdx.x == 0) pair_results(a, p, row_logp);
       return;
     }
-    --y;
+    --by;
   }
-  const int t = end - 1 - y;
+  const int tid = threadIdx.x & (NT - 1);
+  const int t = end - 1 - (by * kRowsPerBlock<NT> + (NT == 64 ? threadIdx.x >> 6 : 0));
   int q;
-  const Place place = row_place(a, nullptr, t, q);
+  const Place place = t >= 0 ? row_place(a, nullptr, t, q) : OUTSIDE;
   if (place == OUTSIDE) return;
-  const int full = a.vocab / EV, g0 = blockIdx.x * LT * GRAD_U + threadIdx.x;
-  const int j = full * EV + threadIdx.x;
-  const bool last = blockIdx.x == 0 && j < a.vocab;
   const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
   KG T* d = gp(static_cast<T*>(a.dlogits)) + t * a.ld_grad;
+  const Cut<T> cut(z, a.vocab);
+  const int g0 = blockIdx.x * NT * U + tid;
+  const bool single = blockIdx.x == 0 && cut.has_single(tid);
+  typename Pack<T>::vec v[U];
   if (place == IDLE) {
-    const V none = {};
-    if (last) d[j] = static_cast<T>(0.f);
+    if (single) d[cut.single(tid)] = static_cast<T>(0.f);
 #pragma unroll
-    for (int u = 0; u < GRAD_U; ++u)
-      if (g0 + u * LT < full) store_pack<PAST, T>(d + int64_t(g0 + u * LT) * EV, none);
+    for (int u = 0; u < U; ++u)
+      if (g0 + u * NT < cut.full) store_pack<PAST, T>(d + cut.group(g0 + u * NT), typename Pack<T>::vec{});
     return;
   }
-  V v[GRAD_U];
 #pragma unroll
-  for (int u = 0; u < GRAD_U; ++u)
-    if (g0 + u * LT < full) v[u] = load_pack<true, T>(z + int64_t(g0 + u * LT) * EV);
-  const float rest = last ? static_cast<float>(z[j]) : 0.f;
+  for (int u = 0; u < U; ++u)
+    if (g0 + u * NT < cut.full) v[u] = load_pack<true, T>(z + cut.group(g0 + u * NT));
+  const float rest = single ? static_cast<float>(z[cut.single(tid)]) : 0.f;
   const RowStat r = row_stat[t];
   const float coef = ALONE ? row_coefficient(a, p, t, row_logp) : row_coef[t];
-  const GradRow<T> k(r.m, r.s, static_cast<int>(gp(a.token)[t]), r.z_y, coef);
-  if (last) d[j] = k.one(rest, j);
+  const GradRow<T> k(cut, r.m, r.s, static_cast<int>(gp(a.token)[t]), r.z_y, coef);
+  if (single) d[cut.single(tid)] = k.one(rest, cut.single(tid));
 #pragma unroll
-  for (int u = 0; u < GRAD_U; ++u)
-    if (g0 + u * LT < full) store_pack<PAST, T>(d + int64_t(g0 + u * LT) * EV, k.group(v[u], g0 + u * LT));
+  for (int u = 0; u < U; ++u)
+    if (g0 + u * NT < cut.full) store_pack<PAST, T>(d + cut.group(g0 + u * NT), k.group(v[u], g0 + u * NT));
 }
 
 }  // namespace kfac
@@ -710,7 +730,7 @@ static bool finite(float x) { return x - x == 0.f; }
     else if (groups_ <= 512 * 8) { LAUNCH(T, 512, 8) }    \
     else if (groups_ <= 512 * 16) { LAUNCH(T, 512, 16) }  \
     else if (groups_ <= 1024 * 16) { LAUNCH(T, 1024, 16) } \
-    else if (groups_ <= 1024 * 20) { LAUNCH(T, 1024, 20) } \
+    else if (groups_ <= 1024 * 19) { LAUNCH(T, 1024, 19) } \
     else { LAUNCH(T, 1024, 0) }                           \
   } while (0)
 
@@ -729,7 +749,7 @@ static int count_slices(int32_t rows, int32_t seqs, bool by_seq) {
 
 struct PolicyWs {
   int32_t *row_seq, *count;
-  PolicyTerms* terms;
+  PolicyTerms *terms, *sums;
   size_t bytes;
 };
 static PolicyWs policy_ws(void* ws, int32_t rows, int32_t seqs) {
@@ -738,6 +758,7 @@ static PolicyWs policy_ws(void* ws, int32_t rows, int32_t seqs) {
   w.row_seq = cv.take<int32_t>(rows);
   w.count = cv.take<int32_t>(std::max<size_t>(64, size_t(seqs) * (seqs ? count_slices(rows, seqs, true) : 0)));
   w.terms = cv.take<PolicyTerms>(rows);
+  w.sums = cv.take<PolicyTerms>(rows / TERMS + 1);
   w.bytes = cv.used;
   return w;
 }
@@ -750,7 +771,15 @@ extern "C" kfac_status kfac_policy_loss_workspace(int32_t rows, int32_t vocab, i
   return KFAC_OK;
 }
 
-static kfac_status launch_finish(const PolicyTerms* terms, int32_t rows, float kl_coef, float* stats, hipStream_t s) {
+static kfac_status launch_finish(const PolicyWs& w, int32_t rows, float kl_coef, float* stats, hipStream_t s) {
+  const PolicyTerms* terms = w.terms;
+  if (rows > 2 * TERMS) {
+    const int blocks = (rows - 1) / TERMS + 1;
+    KFAC_LAUNCH(K_POLICY_TERMS, policy_terms_kernel, dim3(blocks), dim3(LT), 0, s, w.terms, rows, w.sums);
+    KFAC_CHECK_LAUNCH("policy_terms_kernel");
+    terms = w.sums;
+    rows = blocks;
+  }
   if (rows <= 4 * LT) {
     KFAC_LAUNCH(K_POLICY_FINISH, policy_finish_kernel<LT>, dim3(1), dim3(LT), 0, s, terms, rows, kl_coef, stats);
   } else {
@@ -789,7 +818,7 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
   hipStream_t s = static_cast<hipStream_t>(stream);
   PolicyArgs p = {old_logp, ref_logp, advantage, logp, clip_low, clip_high, kl_coef, grad_scale, nullptr, nullptr, 0};
   const bool by_seq = by_sequence && seqs > 1;  // the mean over one sequence is the mean over its rows
-  if (rows == 0) return launch_finish(w.terms, rows, kl_coef, stats, s);
+  if (rows == 0) return launch_finish(w, rows, kl_coef, stats, s);
   // Where a row's threads have one row each to look at (a wave up to four) they count for themselves,
   // behind the loads of their own row; with four each, 4096 rows of 131072 took 387 us instead of 360.
   int row_threads = 0;
@@ -821,7 +850,7 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
 #undef KFAC_TYPED
 #undef KFAC_ROWS
   KFAC_CHECK_LAUNCH("policy_rows_kernel");
-  return launch_finish(w.terms, rows, kl_coef, stats, s);
+  return launch_finish(w, rows, kl_coef, stats, s);
 }
 
 // Up to here the gradient's blocks wait less for their sums than the launch of pref_pairs_kernel takes
@@ -834,14 +863,25 @@ struct PrefWs {
   float* coef;
   size_t bytes;
 };
-static int pair_blocks(int32_t pairs) { return pairs < 1 ? 1 : (pairs - 1) / PAIRS + 1; }
+// Waves of a sequence: about four rows a lane, while the pairs fit in one block; with more pairs
+// than that, or sequences longer than 16 rows a lane, several blocks and a launch to add their losses.
+static int sequence_waves(int32_t rows, int32_t pairs) {
+  const int64_t per = pairs < 1 ? 1 : rows / (2 * int64_t(pairs)) + 1;
+  int w = 1;
+  while (w < PAIR_WAVES / 2 && per > 256 * w && (pairs * w < PAIR_WAVES / 2 || per > 1024 * w)) w *= 2;
+  return w;
+}
+static int pair_blocks(int32_t rows, int32_t pairs) {
+  const int each = PAIR_WAVES / 2 / sequence_waves(rows, pairs);
+  return pairs < 1 ? 1 : (pairs - 1) / each + 1;
+}
 
 static PrefWs pref_ws(void* ws, int32_t rows, int32_t pairs) {
   Carver cv(ws);
   PrefWs w;
   w.stat = cv.take<RowStat>(rows);
   w.logp = cv.take<double>(rows);
-  w.part = cv.take<double>(pair_blocks(pairs));
+  w.part = cv.take<double>(pair_blocks(rows, pairs));
   w.coef = cv.take<float>(rows);
   w.bytes = cv.used;
   return w;
@@ -897,8 +937,9 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
   // one pair, and one of them the pairs' results.
   const bool alone = any && dlogits && pairs <= 16 && row_bytes(rows, vocab, dtype) <= ALONE_BYTES;
   if (!alone) {
-    const int blocks = pair_blocks(pairs);
-    KFAC_LAUNCH(K_PREF_PAIRS, pref_pairs_kernel, dim3(blocks), dim3(ONE), 0, s, a, p, w.logp, w.coef, w.part);
+    const int blocks = pair_blocks(rows, pairs);
+    KFAC_LAUNCH(K_PREF_PAIRS, pref_pairs_kernel, dim3(blocks), dim3(ONE), 0, s, a, p, w.logp, w.coef, w.part,
+                sequence_waves(rows, pairs));
     KFAC_CHECK_LAUNCH("pref_pairs_kernel");
     if (blocks > 1) {
       KFAC_LAUNCH(K_PREF_FINISH, pref_finish_kernel, dim3(1), dim3(LT), 0, s, w.part, blocks, loss);
@@ -906,19 +947,24 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
     }
   }
   if (any && dlogits) {
-    constexpr int most = 65535;  // of a grid in y
+    const bool waves = vocab / (dtype == KFAC_F32 ? 4 : 8) <= 64 * 4;  // a wave holds a row
+    const int most = 65534 * (waves ? 4 : 1);                         // rows of a grid
     for (int32_t end = rows; end > 0; end -= most) {
-      const unsigned y = std::min(end, most);
-#define KFAC_GRAD(T, PAST, ALONE)                                                                                   \
-  KFAC_LAUNCH(K_PREF_GRAD, (pref_grad_kernel<T, PAST, ALONE>),                                                      \
-              dim3((vocab / Pack<T>::n) / (LT * GRAD_U) + 1, ALONE ? y + 1 : y), dim3(LT), 0, s, a, p, w.stat, w.coef, \
-              w.logp, end);
-#define KFAC_TYPED(T)                                   \
-  if (alone) { KFAC_GRAD(T, false, true) }              \
-  else if (store_past) { KFAC_GRAD(T, true, false) }    \
-  else { KFAC_GRAD(T, false, false) }
+      const unsigned blocks = (std::min(end, most) - 1) / (waves ? 4 : 1) + 1;
+#define KFAC_GRAD(T, NT, U, PAST, ALONE)                                                                              \
+  KFAC_LAUNCH(K_PREF_GRAD, (pref_grad_kernel<T, NT, U, PAST, ALONE>),                                                 \
+              dim3((vocab / Pack<T>::n) / (NT * U) + 1, ALONE ? blocks + 1 : blocks), dim3(LT), 0, s, a, p, w.stat,   \
+              w.coef, w.logp, end);
+#define KFAC_ROWS(T, NT, U)                                    \
+  if (alone) { KFAC_GRAD(T, NT, U, false, true) }              \
+  else if (store_past) { KFAC_GRAD(T, NT, U, true, false) }    \
+  else { KFAC_GRAD(T, NT, U, false, false) }
+#define KFAC_TYPED(T)                     \
+  if (waves) { KFAC_ROWS(T, 64, 4) }      \
+  else { KFAC_ROWS(T, 256, 2) }
       KFAC_BY_TYPE(dtype, KFAC_TYPED);
 #undef KFAC_TYPED
+#undef KFAC_ROWS
 #undef KFAC_GRAD
       KFAC_CHECK_LAUNCH("pref_grad_kernel");
     }

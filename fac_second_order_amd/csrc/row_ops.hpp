@@ -17,6 +17,7 @@ enum RowKernelId {
   K_GRADS_ONE,
   K_LOSS_COUNT,
   K_POLICY_ROWS,
+  K_POLICY_TERMS,
   K_POLICY_FINISH,
   K_PREF_ROWS,
   K_PREF_PAIRS,
