@@ -450,8 +450,10 @@ __device__ inline PolicyTerms block_terms(const PolicyTerms* terms, int r0, int 
   v = {wave_add(v.part), wave_add(v.kl), wave_add(v.over)};
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  for (int i = 1; i < NT / 64; ++i)
-    if (threadIdx.x == 0) v = {v.part + lds[i].part, v.kl + lds[i].kl, v.over + lds[i].over};
+  if (threadIdx.x < 64) {
+    v = threadIdx.x < NT / 64 ? lds[threadIdx.x] : PolicyTerms{0, 0, 0};
+    v = {wave_add(v.part), wave_add(v.kl), wave_add(v.over)};
+  }
   return v;
 }
 
