@@ -43,16 +43,16 @@ struct InlineTables {
   int32_t begin[INLINE];
 };
 
-// The tensor that unit c lies in: 64 begins a step, one a lane.
+// The tensor that unit c lies in, 64 begins a step, one a lane: one load for up to 64 tensors, two
+// for 4096. Every tensor here has units, so the begins increase.
 template <class TB>
 __device__ inline int find_tensor(const TB& tb, int count, int c) {
   const int lane = threadIdx.x & 63;
-  int p = -1;
-  for (int k = 0; k < count; k += 64) {
-    const bool below = k + lane < count && tb.begin[k + lane] <= c;
-    const int n = __popcll(__ballot(below));
-    p += n;
-    if (n < 64) break;
+  int step = 1, p = 0;
+  while (step < (count + 63) / 64) step *= 64;
+  for (; step > 0; step /= 64) {
+    const int i = p + lane * step;
+    p += (__popcll(__ballot(i < count && tb.begin[i] <= c)) - 1) * step;
   }
   return __builtin_amdgcn_readfirstlane(p);
 }
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(GT) grads_sum_kernel(TB tb, int count, int uni
   double acc = 0;
   int p = find_tensor(tb, count, blockIdx.x);
   for (int c = blockIdx.x; c < units; c += gridDim.x) {
-    while (p + 1 < count && tb.begin[p + 1] <= c) ++p;
+    if (p + 1 < count && tb.begin[p + 1] <= c) p = find_tensor(tb, count, c);
     const GradDesc d = tb.desc[p];
     const int64_t e0 = int64_t(c - tb.begin[p]) * UNIT;
     sum_unit<W, GT, LAST>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);

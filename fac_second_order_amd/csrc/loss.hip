@@ -323,6 +323,7 @@ struct PolicyArgs {
   // the blocks count for themselves
   const int32_t* row_seq;
   const int32_t* count;
+  const int32_t* nonempty;  // the sequences that have a row that counts; NULL: a wave counts them
   int32_t slices;
 };
 
@@ -353,20 +354,33 @@ __device__ inline int own_count(const LossRows& a, int tid, int threads) {
   return n;
 }
 
+// A lane's share of the sequences that have a row that counts.
+__device__ inline int nonempty_share(const int32_t* count, int seqs, int slices, int lane, int lanes) {
+  int n = 0;
+  for (int i = lane; i < seqs; i += lanes) {
+    int k = 0;
+    for (int j = 0; j < slices; ++j) k |= count[i * slices + j];
+    n += k != 0;
+  }
+  return n;
+}
+// Of many sequences, for all rows.
+__global__ void __launch_bounds__(ONE) loss_nonempty_kernel(const int32_t* __restrict__ count, int seqs, int slices,
+                                                            int32_t* __restrict__ out) {
+  __shared__ int s[ONE / 64];
+  const int n = block_add<ONE>(nonempty_share(count, seqs, slices, threadIdx.x, ONE), s);
+  if (threadIdx.x == 0) out[0] = n;
+}
+
 // 1 / weight of the rows of sequence q; n: the rows that count, of a block that counted. A wave's work.
 __device__ inline double inverse_weight(const LossRows& a, const PolicyArgs& p, int q, int n) {
   const int lane = threadIdx.x & 63;
   if (!p.count) return n;
   if (!p.row_seq) return wave_add(lane < p.slices ? p.count[lane] : 0);
   int own = 0;
-  n = 0;
   for (int j = 0; j < p.slices; ++j) own += p.count[q * p.slices + j];
-  for (int i = lane; i < a.seqs; i += 64) {
-    int k = 0;
-    for (int j = 0; j < p.slices; ++j) k |= p.count[i * p.slices + j];
-    n += k != 0;
-  }
-  return static_cast<double>(wave_add(n)) * own;
+  const int full = p.nonempty ? p.nonempty[0] : wave_add(nonempty_share(p.count, a.seqs, p.slices, lane, 64));
+  return static_cast<double>(full) * own;
 }
 
 // Loss of row t from its softmax, and the coefficient of its gradient; `shown` writes l.
@@ -424,9 +438,11 @@ __global__ void __launch_bounds__(kRowThreads<NT>) policy_rows_kernel(LossRows a
     coef = policy_row(p, t, z_y, r, 1.0 / inverse_weight(a, p, q, w.n), tid == 0, out);
     if (tid == 0) {
       terms[t] = out;
-      row_s.s = r.s;
-      row_s.m = r.m;
-      row_s.coef = coef;
+      if constexpr (NT > 64) {
+        row_s.s = r.s;
+        row_s.m = r.m;
+        row_s.coef = coef;
+      }
     }
   }
   if (!d) return;
@@ -675,8 +691,10 @@ using namespace kfac;
 
 static kfac_status rows_validate(int32_t rows, int32_t vocab, int32_t seqs) {
   if (rows < 0) return fail(KFAC_ERR_INVALID, "rows must be >= 0");
+  // a launch may have 2^32 threads, and a row 1024 of them
+  if (rows >= (1 << 22)) return fail(KFAC_ERR_UNSUPPORTED, "%d rows: more than one call takes", rows);
   if (vocab < 1 || vocab > (1 << 30)) return fail(KFAC_ERR_INVALID, "vocab = %d out of range", vocab);
-  if (seqs < 0 || seqs > (1 << 24)) return fail(KFAC_ERR_INVALID, "%d sequences: out of range", seqs);
+  if (seqs < 0 || seqs > (1 << 22)) return fail(KFAC_ERR_INVALID, "%d sequences: out of range", seqs);
   return KFAC_OK;
 }
 
@@ -750,7 +768,7 @@ static int count_slices(int32_t rows, int32_t seqs, bool by_seq) {
 }
 
 struct PolicyWs {
-  int32_t *row_seq, *count;
+  int32_t *row_seq, *count, *nonempty;
   PolicyTerms *terms, *sums;
   size_t bytes;
 };
@@ -759,6 +777,7 @@ static PolicyWs policy_ws(void* ws, int32_t rows, int32_t seqs) {
   PolicyWs w;
   w.row_seq = cv.take<int32_t>(rows);
   w.count = cv.take<int32_t>(std::max<size_t>(64, size_t(seqs) * (seqs ? count_slices(rows, seqs, true) : 0)));
+  w.nonempty = cv.take<int32_t>(1);
   w.terms = cv.take<PolicyTerms>(rows);
   w.sums = cv.take<PolicyTerms>(rows / TERMS + 1);
   w.bytes = cv.used;
@@ -818,7 +837,7 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
   const PolicyWs w = policy_ws(workspace, rows, seqs);
   if ((st = check_workspace(workspace, ws_bytes, w.bytes))) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  PolicyArgs p = {old_logp, ref_logp, advantage, logp, clip_low, clip_high, kl_coef, grad_scale, nullptr, nullptr, 0};
+  PolicyArgs p = {old_logp, ref_logp, advantage, logp, clip_low, clip_high, kl_coef, grad_scale, nullptr, nullptr, nullptr, 0};
   const bool by_seq = by_sequence && seqs > 1;  // the mean over one sequence is the mean over its rows
   if (rows == 0) return launch_finish(w, rows, kl_coef, stats, s);
   // Where a row's threads have one row each to look at (a wave up to four) they count for themselves,
@@ -836,6 +855,11 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
     KFAC_LAUNCH(K_LOSS_COUNT, loss_count_kernel, dim3(by_seq ? seqs : 1, p.slices), dim3(LT), 0, s, a,
                 by_seq ? w.row_seq : nullptr, w.count);
     KFAC_CHECK_LAUNCH("loss_count_kernel");
+    if (by_seq && seqs > 256) {  // more than four looks a lane for every row
+      p.nonempty = w.nonempty;
+      KFAC_LAUNCH(K_LOSS_NONEMPTY, loss_nonempty_kernel, dim3(1), dim3(ONE), 0, s, w.count, seqs, p.slices, w.nonempty);
+      KFAC_CHECK_LAUNCH("loss_nonempty_kernel");
+    }
   }
   const bool past = row_bytes(rows, vocab, dtype) > STORE_PAST;
 #define KFAC_ROWS(T, NT, C)                                                                                      \
@@ -891,7 +915,7 @@ static PrefWs pref_ws(void* ws, int32_t rows, int32_t pairs) {
 
 extern "C" kfac_status kfac_preference_loss_workspace(int32_t rows, int32_t vocab, int32_t pairs, size_t* bytes) {
   if (!bytes) return fail(KFAC_ERR_INVALID, "bytes is NULL");
-  if (pairs < 0 || pairs > (1 << 23)) return fail(KFAC_ERR_INVALID, "%d pairs: out of range", pairs);
+  if (pairs < 0 || pairs > (1 << 21)) return fail(KFAC_ERR_INVALID, "%d pairs: out of range", pairs);
   kfac_status st = rows_validate(rows, vocab, 2 * pairs);
   if (st) return st;
   *bytes = pref_ws(nullptr, rows, pairs).bytes;
@@ -904,7 +928,7 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
                                             float label_smoothing, float grad_scale, float* seq_logp, float* margin,
                                             float* loss, void* dlogits, int64_t ld_grad, void* workspace,
                                             size_t ws_bytes, void* stream) {
-  if (pairs < 0 || pairs > (1 << 23)) return fail(KFAC_ERR_INVALID, "%d pairs: out of range", pairs);
+  if (pairs < 0 || pairs > (1 << 21)) return fail(KFAC_ERR_INVALID, "%d pairs: out of range", pairs);
   kfac_status st = rows_validate(rows, vocab, 2 * pairs);
   if (st) return st;
   if (!finite(beta) || !finite(grad_scale)) return fail(KFAC_ERR_INVALID, "beta and grad_scale must be finite");

@@ -16,6 +16,7 @@ enum RowKernelId {
   K_TRUST_APPLY,         // grads_apply_kernel of the bounded update
   K_GRADS_ONE,
   K_LOSS_COUNT,
+  K_LOSS_NONEMPTY,
   K_POLICY_ROWS,
   K_POLICY_TERMS,
   K_POLICY_FINISH,

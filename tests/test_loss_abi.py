@@ -120,6 +120,8 @@ def test_policy_loss_refusals(lib):
     for rows, vocab, seqs in ((-1, 4, 0), (4, 0, 0), (4, -3, 0), (4, (1 << 30) + 1, 0), (4, 4, -1)):
         assert so.kfac_policy_loss_workspace(rows, vocab, seqs, c.byref(sz)) == -1
     assert so.kfac_policy_loss_workspace(4, 4, 0, None) == -1
+    assert so.kfac_policy_loss_workspace(1 << 22, 4, 0, c.byref(sz)) == -2          # rows of a call
+    assert so.kfac_policy_loss_workspace((1 << 22) - 1, 4, 0, c.byref(sz)) == 0
     past = policy(so)
     assert past not in (0, -1)
     assert policy(so, dt=F64) == -2 and policy(so, dt=9) == -2
