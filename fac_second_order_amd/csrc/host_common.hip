@@ -142,7 +142,8 @@ static const char* const kKernelNames[K_TOTAL] = {
     "refine_residual_gemm_tn64_kernel",         "refine_correction_gemm_tn_kernel",
     "shift_assemble_kernel", "norm_sum_kernel",    "trust_sum_kernel",    "grads_factor_kernel",
     "grad_scale_kernel",  "trust_apply_kernel",  "grads_one_kernel",   "loss_count_kernel",
-    "loss_nonempty_kernel", "policy_rows_kernel", "policy_terms_kernel", "policy_finish_kernel", "pref_rows_kernel",
+    "loss_nonempty_kernel", "policy_rows_kernel", "policy_terms_kernel", "policy_finish_kernel", "policy_part_kernel",
+    "policy_join_kernel", "pref_rows_kernel",
     "pref_pairs_kernel",  "pref_finish_kernel",  "pref_grad_kernel"};
 
 }  // namespace kfac

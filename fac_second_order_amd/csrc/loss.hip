@@ -81,6 +81,11 @@ struct MaxSum {
   double s;
 };
 
+__device__ inline MaxSum join(MaxSum a, MaxSum b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == NEG_INF) return {m, a.s + b.s};  // as below
+  return {m, a.s * exp(static_cast<double>(a.m) - m) + b.s * exp(static_cast<double>(b.m) - m)};
+}
 // The lanes' sets as one, in every lane.
 __device__ inline MaxSum join_lanes(MaxSum v) {
   const float m = wave_max(v.m);
@@ -95,15 +100,26 @@ __device__ inline MaxSum join_lanes(MaxSum v) {
 template <class T>
 struct Cut {
   static constexpr int EV = Pack<T>::n;
-  int head, full, vocab;
-  __device__ inline Cut(const KG T* z, int vocab_) : vocab(vocab_) {
+  int first, full;            // element of the first group, groups
+  int head, singles, behind;  // elements before the groups, elements outside them, elements in them
+  __device__ inline Cut(const KG T* z, int vocab) {
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) / sizeof(T)) & (EV - 1);
-    head = min(vocab, (EV - off) & (EV - 1));
+    first = head = min(vocab, (EV - off) & (EV - 1));
     full = (vocab - head) / EV;
+    behind = full * EV;
+    singles = vocab - behind;
   }
-  __device__ inline int64_t group(int g) const { return head + int64_t(g) * EV; }
-  __device__ inline bool has_single(int i) const { return i < vocab - full * EV; }
-  __device__ inline int single(int i) const { return i < head ? i : full * EV + i; }
+  // The groups [b n, b n + n) alone; with the first of them the elements outside the groups.
+  __device__ inline Cut part(int b, int n) const {
+    Cut c = *this;
+    c.first += b * n * EV;
+    c.full = max(0, min(full - b * n, n));
+    if (b) c.singles = 0;
+    return c;
+  }
+  __device__ inline int64_t group(int g) const { return first + int64_t(g) * EV; }
+  __device__ inline bool has_single(int i) const { return i < singles; }
+  __device__ inline int single(int i) const { return i < head ? i : behind + i; }
 };
 
 // Gradient of a row, coef (one-hot(y) - softmax): -coef softmax(z) everywhere but at y.
@@ -116,8 +132,8 @@ struct GradRow {
   int y, group_y, place_y;  // the token; its group and place there
   unsigned sign;            // flips the signs of two 16-bit results
   __device__ inline GradRow(const Cut<T>& cut, float m_, double sum, int y_, float z_y, float coef) : m(m_), y(y_) {
-    group_y = y < cut.head ? -1 : (y - cut.head) / EV;
-    place_y = (y - cut.head) & (EV - 1);
+    group_y = y < cut.first ? -1 : (y - cut.first) / EV;
+    place_y = (y - cut.first) & (EV - 1);
     const float inv = static_cast<float>(1.0 / sum);
     at_y = coef * (1.f - exp_about(z_y, m) * inv);
     scale = sizeof(T) == 2 ? __builtin_amdgcn_logf(fabsf(coef) * inv) : -coef * inv;
@@ -253,8 +269,7 @@ struct Row {
 };
 
 template <class T, int NT, bool PAST>
-__device__ inline void row_zero(KG T* d, int vocab, int tid) {
-  const Cut<T> cut(d, vocab);
+__device__ inline void row_zero(const Cut<T>& cut, KG T* d, int tid) {
   const typename Pack<T>::vec w = {};
   if (cut.has_single(tid)) d[cut.single(tid)] = static_cast<T>(0.f);
   for (int g = tid; g < cut.full; g += NT) store_pack<PAST, T>(d + cut.group(g), w);
@@ -420,7 +435,7 @@ __global__ void __launch_bounds__(kRowThreads<NT>) policy_rows_kernel(LossRows a
       terms[t] = {0, 0, 0};
       if (place == IDLE) gp(p.logp)[t] = 0.f;
     }
-    if (place == IDLE && d) row_zero<T, NT, PAST>(d, a.vocab, tid);
+    if (place == IDLE && d) row_zero<T, NT, PAST>(Cut<T>(d, a.vocab), d, tid);
     return;
   }
   const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
@@ -482,17 +497,81 @@ __global__ void __launch_bounds__(LT) policy_terms_kernel(const PolicyTerms* __r
   if (threadIdx.x == 0) out[blockIdx.x] = v;
 }
 
-// stats: loss, its surrogate part, the mean KL, the clipped share.
+// The loss, its surrogate part, the mean KL, the clipped share.
+__device__ inline void policy_stats(PolicyTerms v, float kl_coef, float* stats) {
+  gp(stats)[0] = static_cast<float>(kl_coef != 0.f ? v.part + kl_coef * v.kl : v.part);
+  gp(stats)[1] = static_cast<float>(v.part);
+  gp(stats)[2] = static_cast<float>(v.kl);
+  gp(stats)[3] = static_cast<float>(v.over);
+}
+
 template <int NT>
 __global__ void __launch_bounds__(NT) policy_finish_kernel(const PolicyTerms* __restrict__ terms, int rows,
                                                            float kl_coef, float* stats) {
   const PolicyTerms v = block_terms<NT>(terms, 0, rows);
-  if (threadIdx.x == 0) {
-    gp(stats)[0] = static_cast<float>(kl_coef != 0.f ? v.part + kl_coef * v.kl : v.part);
-    gp(stats)[1] = static_cast<float>(v.part);
-    gp(stats)[2] = static_cast<float>(v.kl);
-    gp(stats)[3] = static_cast<float>(v.over);
+  if (threadIdx.x == 0) policy_stats(v, kl_coef, stats);
+}
+
+// Few long rows, which would leave most of the chip idle: blocks for the parts of a row, then blocks
+// that join the parts, each for the gradient of a piece of its row, and one for all rows' results. A
+// call has at most 64 rows, a row at most 64 parts: a lane each.
+constexpr int SPLIT = 64, SPLIT_C = 4, SPLIT_GROUPS = LT * SPLIT_C;
+
+template <class T>
+__global__ void __launch_bounds__(LT) policy_part_kernel(LossRows a, MaxSum* __restrict__ part,
+                                                         float* __restrict__ row_z) {
+  __shared__ WavePart lds[LT / 64];
+  const int t = blockIdx.y;
+  int q;
+  if (row_place(a, nullptr, t, q) != COUNTS) return;
+  const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
+  const Cut<T> cut = Cut<T>(z, a.vocab).part(blockIdx.x, SPLIT_GROUPS);
+  Row<T, LT, SPLIT_C> row;
+  row.template load<false>(cut, z, threadIdx.x);
+  const WavePart w = join_waves<LT>({row.wave_stats(cut, z, threadIdx.x), 0}, lds);
+  if (threadIdx.x == 0) part[t * gridDim.x + blockIdx.x] = w.v;
+  // the token's logit, which the gradient may overwrite before every block has read it
+  if (threadIdx.x == 0 && blockIdx.x == 0) row_z[t] = static_cast<float>(z[gp(a.token)[t]]);
+}
+
+template <class T>
+__global__ void __launch_bounds__(LT) policy_join_kernel(LossRows a, PolicyArgs p, const MaxSum* __restrict__ part,
+                                                         const float* __restrict__ row_z, int parts, float* stats) {
+  const int lane = threadIdx.x & 63;
+  const double weight = 1.0 / wave_add(own_count(a, lane, 64));
+  int q;
+  if (blockIdx.y == 0) {  // the results, a lane a row
+    if (blockIdx.x || threadIdx.x >= 64) return;
+    PolicyTerms v = {0, 0, 0};
+    const Place place = lane < a.rows ? row_place(a, nullptr, lane, q) : OUTSIDE;
+    if (place == IDLE) gp(p.logp)[lane] = 0.f;
+    if (place == COUNTS) {
+      MaxSum r = part[lane * parts];
+      for (int i = 1; i < parts; ++i) r = join(r, part[lane * parts + i]);
+      policy_row(p, lane, row_z[lane], r, weight, true, v);
+    }
+    v = {wave_add(v.part), wave_add(v.kl), wave_add(v.over)};
+    if (lane == 0) policy_stats(v, p.kl_coef, stats);
+    return;
   }
+  const int t = blockIdx.y - 1;
+  const Place place = row_place(a, nullptr, t, q);
+  if (place == OUTSIDE) return;
+  const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
+  KG T* d = gp(static_cast<T*>(a.dlogits)) + t * a.ld_grad;
+  const Cut<T> cut = Cut<T>(z, a.vocab).part(blockIdx.x, SPLIT_GROUPS);
+  if (place == IDLE) {
+    row_zero<T, LT, false>(cut, d, threadIdx.x);
+    return;
+  }
+  const int y = static_cast<int>(gp(a.token)[t]);
+  const float z_y = row_z[t];
+  Row<T, LT, SPLIT_C> row;
+  row.template load<false>(cut, z, threadIdx.x);
+  const MaxSum r = join_lanes(lane < parts ? part[t * parts + lane] : MaxSum{NEG_INF, 0.0});
+  PolicyTerms unused;
+  const float coef = policy_row(p, t, z_y, r, weight, false, unused);
+  row.template gradient<false>(cut, GradRow<T>(cut, r.m, r.s, y, z_y, coef), z, d, threadIdx.x);
 }
 
 // What the gradient of a row needs of its softmax.
@@ -661,28 +740,17 @@ __global__ void __launch_bounds__(LT) pref_grad_kernel(LossRows a, PrefArgs p, c
   if (place == OUTSIDE) return;
   const KG T* z = gp(static_cast<const T*>(a.logits)) + t * a.ld;
   KG T* d = gp(static_cast<T*>(a.dlogits)) + t * a.ld_grad;
-  const Cut<T> cut(z, a.vocab);
-  const int g0 = blockIdx.x * NT * U + tid;
-  const bool single = blockIdx.x == 0 && cut.has_single(tid);
-  typename Pack<T>::vec v[U];
+  const Cut<T> cut = Cut<T>(z, a.vocab).part(blockIdx.x, NT * U);
   if (place == IDLE) {
-    if (single) d[cut.single(tid)] = static_cast<T>(0.f);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (g0 + u * NT < cut.full) store_pack<PAST, T>(d + cut.group(g0 + u * NT), typename Pack<T>::vec{});
+    row_zero<T, NT, PAST>(cut, d, tid);
     return;
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (g0 + u * NT < cut.full) v[u] = load_pack<true, T>(z + cut.group(g0 + u * NT));
-  const float rest = single ? static_cast<float>(z[cut.single(tid)]) : 0.f;
+  Row<T, NT, U> row;
+  row.template load<true>(cut, z, tid);
   const RowStat r = row_stat[t];
   const float coef = ALONE ? row_coefficient(a, p, t, row_logp) : row_coef[t];
   const GradRow<T> k(cut, r.m, r.s, static_cast<int>(gp(a.token)[t]), r.z_y, coef);
-  if (single) d[cut.single(tid)] = k.one(rest, cut.single(tid));
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (g0 + u * NT < cut.full) store_pack<PAST, T>(d + cut.group(g0 + u * NT), k.group(v[u], g0 + u * NT));
+  row.template gradient<PAST>(cut, k, z, d, tid);
 }
 
 }  // namespace kfac
@@ -767,9 +835,14 @@ static int count_slices(int32_t rows, int32_t seqs, bool by_seq) {
   return n < 1 ? 1 : n > most ? static_cast<int>(most) : static_cast<int>(n);
 }
 
+// Rows of more groups than this are cut into parts where they are few.
+constexpr int SPLIT_FROM = 1024;
+
 struct PolicyWs {
   int32_t *row_seq, *count, *nonempty;
   PolicyTerms *terms, *sums;
+  MaxSum* part;
+  float* row_z;
   size_t bytes;
 };
 static PolicyWs policy_ws(void* ws, int32_t rows, int32_t seqs) {
@@ -780,6 +853,8 @@ static PolicyWs policy_ws(void* ws, int32_t rows, int32_t seqs) {
   w.nonempty = cv.take<int32_t>(1);
   w.terms = cv.take<PolicyTerms>(rows);
   w.sums = cv.take<PolicyTerms>(rows / TERMS + 1);
+  w.part = cv.take<MaxSum>(size_t(std::min(rows, SPLIT)) * SPLIT);
+  w.row_z = cv.take<float>(SPLIT);
   w.bytes = cv.used;
   return w;
 }
@@ -840,6 +915,18 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
   PolicyArgs p = {old_logp, ref_logp, advantage, logp, clip_low, clip_high, kl_coef, grad_scale, nullptr, nullptr, nullptr, 0};
   const bool by_seq = by_sequence && seqs > 1;  // the mean over one sequence is the mean over its rows
   if (rows == 0) return launch_finish(w, rows, kl_coef, stats, s);
+  const int64_t groups = vocab / (dtype == KFAC_F32 ? 4 : 8), parts = groups / SPLIT_GROUPS + 1;
+  if (!by_seq && rows <= SPLIT && parts <= SPLIT && groups > SPLIT_FROM) {
+#define KFAC_TYPED(T)                                                                                            \
+  KFAC_LAUNCH(K_POLICY_PART, policy_part_kernel<T>, dim3(parts, rows), dim3(LT), 0, s, a, w.part, w.row_z);      \
+  KFAC_CHECK_LAUNCH("policy_part_kernel");                                                                       \
+  KFAC_LAUNCH(K_POLICY_JOIN, policy_join_kernel<T>, dlogits ? dim3(parts, rows + 1) : dim3(1, 1), dim3(LT), 0, s, a, \
+              p, w.part, w.row_z, static_cast<int>(parts), stats);
+    KFAC_BY_TYPE(dtype, KFAC_TYPED);
+#undef KFAC_TYPED
+    KFAC_CHECK_LAUNCH("policy_join_kernel");
+    return KFAC_OK;
+  }
   // Where a row's threads have one row each to look at (a wave up to four) they count for themselves,
   // behind the loads of their own row; with four each, 4096 rows of 131072 took 387 us instead of 360.
   int row_threads = 0;

@@ -20,6 +20,8 @@ enum RowKernelId {
   K_POLICY_ROWS,
   K_POLICY_TERMS,
   K_POLICY_FINISH,
+  K_POLICY_PART,
+  K_POLICY_JOIN,
   K_PREF_ROWS,
   K_PREF_PAIRS,
   K_PREF_FINISH,

@@ -25,17 +25,61 @@ EDGES = [256, 1024, 2048, 4096, 8192, 16384, 19456]
 @pytest.mark.parametrize("offset", [0, 1])
 def test_rows_on_both_sides_of_an_edge(kfac_gpu, dtype, groups, offset):
     """Rows of exactly that many groups, one element fewer and a whole group more; offset 1: no row
-    begins at a multiple of 16 bytes. The rows are few, so pass the numbers of rows at which blocks
-    count for themselves as well (test_counts)."""
+    begins at a multiple of 16 bytes. By sequence: the rows are then held whole; otherwise so few
+    are cut into parts."""
     ev = 4 if dtype == F32 else 8
     for vocab in (groups * ev - 1, groups * ev, groups * ev + ev):
         z, token, old, adv, ref = _policy_inputs(vocab + offset, 2, vocab, dtype, 0, offset)
         token[1] = vocab - 1
         old[1] = lo.row_logp(host64(z[1]), vocab - 1)[0] + 0.1
-        kw = dict(ref=ref, kl_coef=0.1, grad_scale=2.0)
-        _check_policy(_policy(kfac_gpu, z, token, old, adv, **kw), z, token, old, adv, **kw)
+        for by in (dict(), dict(begin=_offsets(0, 1, 2), by_sequence=True)):
+            kw = dict(ref=ref, kl_coef=0.1, grad_scale=2.0, **by)
+            _check_policy(_policy(kfac_gpu, z, token, old, adv, **kw), z, token, old, adv, **kw)
         kw = dict(beta=0.3, grad_scale=2.0)
         _check_prefer(_prefer(kfac_gpu, z, token, _offsets(0, 1, 2), **kw), z, token, _offsets(0, 1, 2), **kw)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 63, 64, 65])
+@pytest.mark.parametrize("dtype,vocab", [(F32, 4097), (F32, 4100), (F32, 8191), (F32, 8193), (BF16, 8199), (BF16, 8200),
+                                         (F16, 16385), (BF16, 50001), (F32, 262143), (F32, 262144)])
+def test_few_long_rows(kfac_gpu, rows, dtype, vocab):
+    """Rows in parts of 1024 groups, up to 64 parts and one more; up to 64 rows and one more."""
+    if rows > 3 and vocab > 60000:
+        rows = {63: 4, 64: 5, 65: 6}[rows]
+    z, token, old, adv, ref = _policy_inputs(rows + vocab, rows, vocab, dtype, 0, 1)
+    mask = torch.arange(rows) % 5 != 3
+    begin = None if rows < 60 else _offsets(2, 30, rows - 1)
+    kw = dict(ref=ref, kl_coef=0.1, grad_scale=float(rows), mask=mask.cuda(), begin=begin)
+    z0 = z.clone()
+    got = _policy(kfac_gpu, z, token, old, adv, **kw)
+    _check_policy(got, z0, token, old, adv, **kw)
+    alone = _policy(kfac_gpu, z, token, old, adv, grad=False, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got[:2], alone[:2]))
+    again = _policy(kfac_gpu, z, token, old, adv, dlogits=z, **kw)
+    inside = torch.arange(rows, device="cuda") >= 0 if begin is None else \
+        (torch.arange(rows, device="cuda") >= 2) & (torch.arange(rows, device="cuda") < rows - 1)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[2][inside], again[2][inside])
+    assert torch.equal(again[2][~inside], z0[~inside])
+
+
+@pytest.mark.parametrize("by_sequence", [False, True])
+def test_long_rows_of_masked_and_bad_values(kfac_gpu, by_sequence):
+    """Whole parts of -inf or of the lowest value, rows of nothing else, NaN and +inf in one part."""
+    low = torch.finfo(F32).min
+    begin = _offsets(0, 3, 8) if by_sequence else None
+    z, token, old, adv, ref = _policy_inputs(3, 8, 20000, F32)
+    z[0, :9000] = float("-inf")
+    z[1, 4096:] = low
+    z[2] = low
+    z[3, :19999] = float("-inf")
+    token[:4] = torch.tensor([19999, 5, 12345, 19999], device="cuda")
+    old = torch.tensor([lo.row_logp(a, b)[0] for a, b in zip(host64(z), token.tolist())]).float().cuda() + 0.05
+    kw = dict(begin=begin, by_sequence=by_sequence, grad_scale=8.0)
+    _check_policy(_policy(kfac_gpu, z, token, old, adv, **kw), z, token, old, adv, **kw)
+    z[4, 17000], z[5, 3], z[6] = float("nan"), float("inf"), float("-inf")
+    stats, logp, d = _policy(kfac_gpu, z, token, old, adv, **kw)
+    assert logp[4:7].isnan().all() and logp[[0, 1, 2, 3, 7]].isfinite().all()
+    assert d[4:7].isnan().all() and d[[0, 1, 2, 3, 7]].isfinite().all() and stats[0].isnan()
 
 
 @pytest.mark.parametrize("place", [0, 1, 6, 7, 8, 9, 1022, 1023, 1024, 1029])
