@@ -505,10 +505,10 @@ __device__ inline void policy_stats(PolicyTerms v, float kl_coef, float* stats) 
   gp(stats)[3] = static_cast<float>(v.over);
 }
 
-template <int NT>
-__global__ void __launch_bounds__(NT) policy_finish_kernel(const PolicyTerms* __restrict__ terms, int rows,
+constexpr int FT = 512;
+__global__ void __launch_bounds__(FT) policy_finish_kernel(const PolicyTerms* __restrict__ terms, int rows,
                                                            float kl_coef, float* stats) {
-  const PolicyTerms v = block_terms<NT>(terms, 0, rows);
+  const PolicyTerms v = block_terms<FT>(terms, 0, rows);
   if (threadIdx.x == 0) policy_stats(v, kl_coef, stats);
 }
 
@@ -876,11 +876,7 @@ static kfac_status launch_finish(const PolicyWs& w, int32_t rows, float kl_coef,
     terms = w.sums;
     rows = blocks;
   }
-  if (rows <= 4 * LT) {
-    KFAC_LAUNCH(K_POLICY_FINISH, policy_finish_kernel<LT>, dim3(1), dim3(LT), 0, s, terms, rows, kl_coef, stats);
-  } else {
-    KFAC_LAUNCH(K_POLICY_FINISH, policy_finish_kernel<ONE>, dim3(1), dim3(ONE), 0, s, terms, rows, kl_coef, stats);
-  }
+  KFAC_LAUNCH(K_POLICY_FINISH, policy_finish_kernel, dim3(1), dim3(FT), 0, s, terms, rows, kl_coef, stats);
   KFAC_CHECK_LAUNCH("policy_finish_kernel");
   return KFAC_OK;
 }
