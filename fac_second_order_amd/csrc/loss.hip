@@ -10,6 +10,7 @@
 // sequence (the sum over the waves, l, the ratio, the sums of l) is formed in fp64: l is
 // a difference of numbers much larger than the error that a ratio near its bound may carry.
 #include <algorithm>
+#include <initializer_list>
 
 #include "row_ops.hpp"
 
@@ -797,6 +798,25 @@ static kfac_status rows_check(const LossRows& a, kfac_dtype dtype) {
 
 static bool finite(float x) { return x - x == 0.f; }
 
+// Bytes of a call's buffer; none where it is NULL.
+struct Bytes {
+  const void* p;
+  int64_t n;
+};
+// No result may share bytes with an input: blocks that write it and blocks that read it run at
+// once. (The gradient and the logits are rows_check's.)
+static kfac_status check_apart(std::initializer_list<Bytes> results, std::initializer_list<Bytes> inputs) {
+  for (const Bytes& r : results)
+    for (const Bytes& i : inputs) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(r.p), y = reinterpret_cast<uintptr_t>(i.p);
+      if (x && y && r.n && i.n && x < y + i.n && y < x + r.n) return fail(KFAC_ERR_INVALID, "a result overlaps an input");
+    }
+  return KFAC_OK;
+}
+static Bytes rows_of(const void* p, const LossRows& a, int64_t ld, kfac_dtype dtype) {
+  return {p, a.rows ? ((a.rows - 1) * ld + a.vocab) * (dtype == KFAC_F32 ? 4 : 2) : 0};
+}
+
 // LAUNCH(type) for the type of a code.
 #define KFAC_BY_TYPE(dtype, LAUNCH)              \
   do {                                           \
@@ -903,6 +923,14 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
         (st = check_array(logp, 4, "logp")))
       return st;
     if (ref_logp && (st = check_array(ref_logp, 4, "ref_logp"))) return st;
+    const int64_t n = rows;
+    const Bytes in_z = rows_of(logits, a, ld, dtype), in_token = {token, 8 * n}, in_mask = {mask, n},
+                in_begin = {seq_begin, 4 * (int64_t(seqs) + 1)}, in_old = {old_logp, 4 * n},
+                in_ref = {ref_logp, 4 * n}, in_adv = {advantage, 4 * n};
+    if ((st = check_apart({{logp, 4 * n}, {stats, 16}}, {in_z, in_token, in_mask, in_begin, in_old, in_ref, in_adv})) ||
+        (st = check_apart({rows_of(dlogits, a, ld_grad, dtype)},
+                          {in_token, in_mask, in_begin, in_old, in_ref, in_adv})))
+      return st;
   }
   if ((st = check_device())) return st;
   const PolicyWs w = policy_ws(workspace, rows, seqs);
@@ -1024,6 +1052,13 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
         (st = check_array(margin, 4, "margin")))
       return st;
     if (ref_logp && (st = check_array(ref_logp, 4, "ref_logp"))) return st;
+    const int64_t n = rows, seqs = 2 * int64_t(pairs);
+    const Bytes in_z = rows_of(logits, a, ld, dtype), in_token = {token, 8 * n}, in_mask = {mask, n},
+                in_begin = {seq_begin, 4 * (seqs + 1)}, in_ref = {ref_logp, 4 * seqs};
+    if ((st = check_apart({{seq_logp, 4 * seqs}, {margin, 2 * seqs}, {loss, 4}},
+                          {in_z, in_token, in_mask, in_begin, in_ref})) ||
+        (st = check_apart({rows_of(dlogits, a, ld_grad, dtype)}, {in_token, in_mask, in_begin, in_ref})))
+      return st;
   }
   if ((st = check_device())) return st;
   const PrefWs w = pref_ws(workspace, rows, pairs);

@@ -365,8 +365,9 @@ kfac_status kfac_trust_update(int32_t count, const int64_t* numel, const float* 
  * grad_scale times the gradient of the loss in the logits, in their type, rounded once
  * from fp32, at the pitch ld_grad >= vocab: zeros in the rows of a sequence that do not
  * count. Rows outside every sequence are left as they were, in every output. dlogits may
- * be logits with ld_grad = ld; otherwise they must not overlap. A call takes fewer than 2^22
- * rows (KFAC_ERR_UNSUPPORTED). A logit may be -inf;
+ * be logits with ld_grad = ld; otherwise they must not overlap. No other result may share
+ * bytes with an input (old_logp and logp are two buffers), and none with another result. A call
+ * takes fewer than 2^22 rows (KFAC_ERR_UNSUPPORTED). A logit may be -inf;
  * +inf, NaN or a row of nothing but -inf makes that row's results NaN.
  * Results are deterministic.
  *

@@ -163,6 +163,35 @@ def test_preference_loss_refusals(lib):
     assert prefer(so, d=A + 16, ldd=8) == -1 and prefer(so, d=A, ldd=8) == past
 
 
+def test_results_lie_apart_from_inputs(lib):
+    """A result that shares bytes with an input is refused: its writer and the input's readers run at
+    the same time. Rows 2, vocab 8, float32: 64 bytes of logits, 8 of a float for each row."""
+    so = lib._lib
+    mine = dict(stats=0x500000, logp=0x600000, old=0x700000, ref=0x800000, adv=0x900000, mask=0xa00000, seqs=2, begin=0xb00000,
+                d=0xc00000, ldd=8)
+    past = policy(so, **mine)
+    assert past not in (0, -1)
+    for name in ("logp", "stats"):
+        for what in ("old", "ref", "adv", "mask", "begin"):
+            assert policy(so, **{**mine, name: mine[what]}) == -1 and b"overlaps an input" in so.kfac_last_error()
+        assert policy(so, **{**mine, name: A + 60}) == -1 and policy(so, **{**mine, name: B + 12}) == -1
+    assert policy(so, **{**mine, "logp": 0x700004}) == -1 and policy(so, **{**mine, "logp": 0x6ffffc}) == -1
+    assert policy(so, **{**mine, "logp": 0x700008}) == past and policy(so, **{**mine, "logp": 0x6ffff8}) == past
+    assert policy(so, **{**mine, "stats": 0x6ffff4}) == -1 and policy(so, **{**mine, "logp": 0xb00008}) == -1
+    for what in ("old", "ref", "adv", "mask", "begin"):
+        assert policy(so, **{**mine, "d": mine[what]}) == -1
+    assert policy(so, **{**mine, "d": 0x6fffc4}) == -1 and policy(so, **{**mine, "d": 0x6fffc0}) == past
+    pair = dict(seq=0x500000, margin=0x600000, loss=0x700000, ref=0x800000, mask=0xa00000, begin=0xb00000, d=0xc00000, ldd=8)
+    past = prefer(so, **pair)
+    assert past not in (0, -1)
+    for name in ("seq", "margin", "loss", "d"):
+        for what in ("ref", "mask", "begin"):
+            assert prefer(so, **{**pair, name: pair[what]}) == -1 and b"overlaps an input" in so.kfac_last_error()
+        assert prefer(so, **{**pair, name: B + 8}) == -1                     # the last token
+    assert prefer(so, **{**pair, "seq": 0x7ffffc}) == -1 and prefer(so, **{**pair, "seq": 0x7ffff8}) == past
+    assert prefer(so, **{**pair, "margin": 0x7ffffc}) == past
+
+
 def test_binding_refuses_other_devices(lib):
     """Tensors that are not on the current device, here on the CPU, are refused before their
     addresses reach the library."""
