@@ -412,7 +412,7 @@ __device__ inline float policy_row(const PolicyArgs& p, int t, float z_y, MaxSum
   double slope = over ? 0.0 : -free, kl = 0;
   if (p.ref_logp) {
     const double x = gp(p.ref_logp)[t] - l, e = expm1(x);
-    kl = e - x;
+    kl = e < __builtin_huge_val() ? e - x : e;  // l of -inf: infinite, not inf - inf
     if (p.kl_coef != 0.f) slope -= p.kl_coef * e;
   }
   if (shown) gp(p.logp)[t] = static_cast<float>(l);
@@ -620,10 +620,11 @@ struct PrefArgs {
 __device__ inline float pref_pair(const PrefArgs& p, int i, double chosen, double other, bool shown, double& loss) {
   const double rc = p.ref_logp ? gp(p.ref_logp)[i] : 0.f, rr = p.ref_logp ? gp(p.ref_logp)[i + p.pairs] : 0.f;
   const double x = p.beta * ((chosen - rc) - (other - rr)), e = p.smooth;
-  const double t = exp(-fabs(x));
-  const double below = fmax(-x, 0.0) + log1p(t);            // log(1 + exp(-x)); log(1 + exp(x)) is x more
-  const double miss = (x > 0 ? t : 1.0) / (1.0 + t);        // 1 / (1 + exp(x))
-  loss = (e != 0 ? below + e * x : below) / p.pairs;
+  const double t = exp(-fabs(x)), both = log1p(t);
+  const double below = fmax(-x, 0.0) + both, above = fmax(x, 0.0) + both;  // log(1 + exp(-x)), log(1 + exp(x))
+  const double miss = (x > 0 ? t : 1.0) / (1.0 + t);                       // 1 / (1 + exp(x))
+  // either may be infinite, and has no part in the loss where its share is 0
+  loss = ((e < 1 ? (1 - e) * below : 0.0) + (e > 0 ? e * above : 0.0)) / p.pairs;
   if (shown) {
     gp(p.margin)[i] = static_cast<float>(x);
     gp(p.seq_logp)[i] = static_cast<float>(chosen);

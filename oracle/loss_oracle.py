@@ -54,13 +54,13 @@ def policy_loss(z, token, old, adv, ref=None, mask=None, begin=None, by_sequence
             over += weight if r * A > held else 0.0
             if ref is not None:
                 d = float(ref[t]) - l
-                kl += weight * (math.expm1(d) - d)
-                slope -= kl_coef * math.expm1(d)
+                kl += weight * (math.expm1(d) - d if d < math.inf else d)
+                slope -= kl_coef * math.expm1(d) if kl_coef else 0.0
             logp[t] = l
             one = np.zeros(vocab)
             one[token[t]] = 1.0
             grad[t] = scale * weight * slope * (one - p)
-    return np.array([part + kl_coef * kl, part, kl, over]), logp, grad
+    return np.array([part + (kl_coef * kl if kl_coef else 0.0), part, kl, over]), logp, grad
 
 
 def _softplus(x):
@@ -84,7 +84,8 @@ def preference_loss(z, token, begin, ref=None, mask=None, beta=0.1, smooth=0.0, 
         sums.append(math.fsum(ls))
     ref = [0.0] * (2 * pairs) if ref is None else [float(v) for v in ref]
     x = [beta * ((sums[i] - ref[i]) - (sums[pairs + i] - ref[pairs + i])) for i in range(pairs)]
-    loss = sum((1 - smooth) * _softplus(-v) + smooth * _softplus(v) for v in x) / pairs if pairs else 0.0
+    loss = sum(share * _softplus(v) for x_i in x for share, v in ((1 - smooth, -x_i), (smooth, x_i)) if share)
+    loss = loss / pairs if pairs else 0.0
     for i in range(pairs):
         slope = (smooth - math.exp(-_softplus(x[i]))) * beta / pairs
         for s, sign in ((i, 1.0), (pairs + i, -1.0)):

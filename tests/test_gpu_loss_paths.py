@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from gpu_helpers import say
-from loss_cases import U, host64, logits
+from loss_cases import U, grad_bound, host64, logits, row_errors
 from oracle import loss_oracle as lo
 from test_gpu_grads import _check_clip, _check_trust, _clip, _norm, _tensors, _trust
 from test_gpu_loss import BF16, F16, F32, _check_policy, _check_prefer, _offsets, _policy, _policy_inputs, _prefer, _vec
@@ -274,3 +274,46 @@ def test_workspaces_hold_anything_before_a_call(kfac_gpu):
         got = [logp, stats, d, seq, margin, loss, d2, norm, *outs]
         assert want is None or all(torch.equal(a, b) for a, b in zip(got, want))
         want = got
+
+
+def _unlikely(dtype, vocab):
+    """Two rows, the first with a logit of -inf at its token."""
+    z, token, old, adv, ref = _policy_inputs(77, 2, vocab, dtype)
+    z[0, int(token[0])] = float("-inf")
+    return z, token, old, adv, ref
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("vocab", [24, 3000])
+@pytest.mark.parametrize("smooth", [0.0, 0.25, 1.0])
+@pytest.mark.parametrize("first", [True, False])
+def test_prefer_a_token_without_probability(kfac_gpu, dtype, vocab, smooth, first):
+    """l of -inf: a margin of -inf or +inf, a loss that is infinite or has none of it, and a gradient
+    whose sigmoid is 0 or 1: with no error but the row's own, the rounding of the coefficient (1 u)
+    and those of grad_bound."""
+    z, token, *_ = _unlikely(dtype, vocab)
+    if not first:
+        z, token = z.flip(0), token.flip(0)
+    loss, margin, seq, d = _prefer(kfac_gpu, z, token, _offsets(0, 1, 2), beta=0.5, label_smoothing=smooth)
+    zz, tok = host64(z), token.cpu().numpy()
+    want, x, sums, want_d = lo.preference_loss(zz, tok, [0, 1, 2], beta=0.5, smooth=smooth)
+    assert float(loss) == want and float(margin) == x[0] and host64(seq)[0 if first else 1] == -np.inf
+    coef = np.array([1.0, -1.0]) * (smooth - (1.0 if first else 0.0)) * 0.5
+    bound = grad_bound(want_d, zz, tok, coef, np.abs(coef) * U, row_errors(zz), dtype)
+    assert (np.abs(host64(d) - want_d) <= bound).all()
+
+
+@pytest.mark.parametrize("vocab", [24, 3000, 4100])
+def test_policy_a_token_without_probability(kfac_gpu, vocab):
+    """l of -inf: the ratio is 0, the KL infinite, and without a KL term the row has no gradient."""
+    z, token, old, adv, ref = _unlikely(F32, vocab)
+    adv = adv.abs()
+    stats, logp, d = (host64(t) for t in _policy(kfac_gpu, z, token, old, adv, ref=ref))
+    want, want_l, want_d = lo.policy_loss(host64(z), token.cpu().numpy(), host64(old), host64(adv), host64(ref))
+    assert logp[0] == -np.inf and stats[2] == np.inf == want[2] and not d[0].any() and not want_d[0].any()
+    # |error| of l, and of the ratio of row 1 relative to it, weighted by 1/2
+    err = row_errors(host64(z))[1]
+    ratio = np.exp(want_l[1] - host64(old)[1])
+    assert abs(logp[1] - want_l[1]) <= err + 1.01 * U * abs(want_l[1])
+    assert np.abs(stats[:2] - want[:2]).max() <= 0.5 * ratio * host64(adv)[1] * err + 1.01 * U * abs(want[1])
+    assert stats[3] == np.float32(want[3])

@@ -116,3 +116,19 @@ def test_clip_and_trust_closed_forms():
     d = np.abs(rng.standard_normal(6))
     assert lo.trust_step([P], [None], 1.0, 1e-2, [d], 0.5) == lo.trust_step([P], [P * (d + 0.5)], 1.0, 1e-2)
     assert lo.trust_step([np.zeros(3)], [np.ones(3)], 0.3, 1e-2) == (0.3, 0.0)
+
+
+def test_a_token_without_probability():
+    """A logit of -inf at the token: the loss of its pair, or its KL, is infinite, and 0 where it has no share."""
+    z = np.array([[0.0, -np.inf, 0.0], [1.0, 0.0, 0.0]])
+    token = np.array([1, 0])
+    for smooth in (0.0, 0.25, 1.0):
+        loss, margin, sums, grad = lo.preference_loss(z, token, [0, 1, 2], beta=0.5, smooth=smooth)
+        assert margin[0] == -np.inf and sums[0] == -np.inf and loss == (0.0 if smooth == 1 else np.inf)
+        assert np.isfinite(grad).all() and grad[0, 1] == pytest.approx((smooth - 1) * 0.5)
+        loss, margin, _, grad = lo.preference_loss(z[::-1], token[::-1], [0, 1, 2], beta=0.5, smooth=smooth)
+        assert margin[0] == np.inf and loss == (0.0 if smooth == 0 else np.inf)
+        assert grad[1, 1] == pytest.approx(-smooth * 0.5)
+    stats, logp, grad = lo.policy_loss(z, token, np.array([-1.0, -1.0]), np.array([1.0, 1.0]),
+                                       ref=np.array([-1.0, -1.0]))
+    assert logp[0] == -np.inf and stats[2] == np.inf and np.isfinite(stats[:2]).all() and not grad[0].any()
