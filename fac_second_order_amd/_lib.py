@@ -409,7 +409,10 @@ def _call_ws(workspace, query, sizes, device, stream):
     """Aligned address and bytes of the call's workspace, and the tensor behind it, to be held
     until the call has been made. Without one from the caller, query(*sizes) bytes are
     allocated on the stream that the call runs on: their memory is free there, and goes to
-    nothing else before the call's kernels are done."""
+    nothing else before the call's kernels are done. A stream of another device would run
+    the call there."""
+    if stream is not None and stream.device != device:
+        raise ValueError("stream must be of the current HIP device")
     if workspace is None:
         with torch.cuda.stream(stream):
             workspace = torch.empty(query(*sizes) + 256, dtype=torch.uint8, device=device)

@@ -333,7 +333,8 @@ static kfac_status sizes_validate(int32_t count, const int64_t* numel) {
       return fail(KFAC_ERR_INVALID, "numel[%d] = %lld out of range", i, static_cast<long long>(numel[i]));
     units += (numel[i] + UNIT - 1) / UNIT;
   }
-  if (units >= (int64_t(1) << 31)) return fail(KFAC_ERR_UNSUPPORTED, "too many elements in one call");
+  // a block's last step leads up to MAX_BLOCKS past them
+  if (units > INT32_MAX - MAX_BLOCKS) return fail(KFAC_ERR_UNSUPPORTED, "too many elements in one call");
   return KFAC_OK;
 }
 

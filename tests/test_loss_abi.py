@@ -1,6 +1,7 @@
 """Refusals of the losses, the clipping and the bounded update that need no GPU: every bad
 argument is refused before the device is touched, in C and in the binding."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -54,6 +55,14 @@ def test_grad_norm_refusals(lib):
     assert norm(so, g=ptrs(None)) == -1 and norm(so, g=ptrs(B + 2)) == -1
     assert norm(so, dt=i32(BF16), g=ptrs(B + 1)) == -1
     assert norm(so, n=i64(0), g=ptrs(None)) not in (-1, 0)      # nothing to read: past the arguments
+
+
+def test_units_of_a_call_stay_countable(lib):
+    """4096 elements a unit, and unit numbers that stay below 2^31 with a grid of 1024 added."""
+    so, sz = lib._lib, c.c_size_t()
+    most = ((1 << 31) - 1 - 1024) * 4096 - 7 * (1 << 40)
+    assert so.kfac_grad_norm_workspace(8, i64(*[1 << 40] * 7, most), c.byref(sz)) == 0
+    assert so.kfac_grad_norm_workspace(8, i64(*[1 << 40] * 7, most + 1), c.byref(sz)) == -2
 
 
 def clip(so, n=(4, 4), dt=(F32, F32), g=(A, B), odt=(F32, F32), out=(C, D), top=1.0, norm_at=0x500000):
@@ -280,3 +289,10 @@ def test_a_workspace_smaller_than_its_alignment_has_no_bytes(lib):
     at = (-big.data_ptr()) % 256 + 1                     # one byte past an aligned address
     assert lib._ws(big[at:at + 8], 100, "cpu")[1] == 0
     assert lib._ws(big[at:at + 300], 100, "cpu")[1] == 45
+
+
+def test_a_stream_of_another_device_is_refused(lib):
+    there = SimpleNamespace(device=torch.device("cuda", 1))
+    for workspace in (None, torch.zeros(8)):
+        with pytest.raises(ValueError, match="stream"):
+            lib._call_ws(workspace, None, (), torch.device("cuda", 0), there)
