@@ -418,7 +418,9 @@ def _call_ws(workspace, query, sizes, device, stream):
             workspace = torch.empty(query(*sizes) + 256, dtype=torch.uint8, device=device)
     elif workspace.device != device:
         raise ValueError("workspace must be on the current HIP device")
-    return *_ws(workspace, 1, device), workspace
+    at = workspace.data_ptr()
+    pad = -at % 256
+    return at + pad, max(0, workspace.numel() * workspace.element_size() - pad), workspace
 
 
 def kfac_grad_norm_workspace(numel):
@@ -510,28 +512,35 @@ def _vector(t, dtype, n, what):
     return t.data_ptr()
 
 
+def _pitch(t, rows, vocab, what):
+    apart, within = t.stride()
+    if (vocab > 1 and within != 1) or (rows > 1 and apart < vocab):
+        raise TypeError(f"the rows of {what} must be contiguous and apart")
+    return apart if rows > 1 else vocab
+
+
 def _logit_rows(logits, dlogits, token, mask, others):
     """Checks the rows of a loss; (rows, vocab, dtype code, logits pointer and pitch,
-    token, mask, dlogits pointer and pitch)."""
-    if logits.dim() != 2 or logits.dtype not in _ANY_CODE:
+    token, mask, dlogits pointer and pitch). Small calls wait for the host, so each tensor
+    is asked once for what is needed of it."""
+    dtype = logits.dtype
+    if logits.dim() != 2 or dtype not in _ANY_CODE:
         raise TypeError("logits must be [rows, vocab] in float16, bfloat16 or float32")
-    rows, vocab = logits.shape
-    given = [t for t in (logits, token, mask, dlogits, *others) if t is not None]
-    _on_device(given, "every tensor of the call")
-
-    def pitch(t, what):
-        if (vocab > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < vocab):
-            raise TypeError(f"the rows of {what} must be contiguous and apart")
-        return t.stride(0) if rows > 1 else vocab
-
-    if dlogits is not None and (dlogits.shape != logits.shape or dlogits.dtype != logits.dtype):
-        raise TypeError("dlogits must have the shape and type of logits")
-    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
-        raise TypeError("mask must be bool or uint8")
-    return (rows, vocab, _ANY_CODE[logits.dtype], logits.data_ptr(), pitch(logits, "logits"),
-            _vector(token, torch.int64, rows, "token"),
-            None if mask is None else _vector(mask, mask.dtype, rows, "mask"),
-            None if dlogits is None else dlogits.data_ptr(), 0 if dlogits is None else pitch(dlogits, "dlogits"))
+    rows, vocab = shape = logits.shape
+    _on_device([t for t in (logits, token, mask, dlogits, *others) if t is not None], "every tensor of the call")
+    d = msk = None
+    ldd = 0
+    ld = _pitch(logits, rows, vocab, "logits")
+    if dlogits is not None:
+        if dlogits.shape != shape or dlogits.dtype != dtype:
+            raise TypeError("dlogits must have the shape and type of logits")
+        d, ldd = dlogits.data_ptr(), _pitch(dlogits, rows, vocab, "dlogits")
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("mask must be bool or uint8")
+        msk = _vector(mask, mask.dtype, rows, "mask")
+    return (rows, vocab, _ANY_CODE[dtype], logits.data_ptr(), ld, _vector(token, torch.int64, rows, "token"), msk, d,
+            ldd)
 
 
 def kfac_policy_loss(logits, token, old_logp, advantage, logp, stats, dlogits=None, ref_logp=None, mask=None,
