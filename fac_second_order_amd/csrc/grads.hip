@@ -7,14 +7,22 @@
 // turns the sum into the factor; a third goes over the units again, last ones first, as the
 // caches still hold those. Which block adds what depends on the sizes alone: results are
 // deterministic. HBM-bound: the gradients are read twice, the result is written once.
+//
+// Measured: 54 fp32 tensors of ResNet-50 (102 MB) clipped in 52.8 us: 20.4 for the sum (5.0 TB/s),
+// 4.6 for the factor, 29.7 for the second pass (6.9 TB/s, its reads from the last-level cache). A
+// 111-tensor decoder, 1.7 GB in bf16 to fp32: 1.13 ms, 6.2 TB/s over both passes. The bounded update
+// of ResNet-50 (409 MB moved): 82.7 us. (A copy kernel's best here is 6.15 TB/s, with one group of
+// 16 bytes a thread in address order; a library copy does 4.95.)
 #include <algorithm>
 
 #include "row_ops.hpp"
 
 namespace kfac {
 
-constexpr int UNIT = 4096;         // elements of a unit
-constexpr int PART = 2048;         // of a unit that one block of the second pass takes
+// Elements of a unit, and of the part of one that a block of the second pass takes: two groups of 16
+// bytes a thread. A thread with one group copies fastest (6.15 TB/s, with four 5.7), but then finds
+// its tensor for half as much.
+constexpr int UNIT = 4096, PART = 2048;
 constexpr int MAX_BLOCKS = 1024;   // partial sums
 constexpr int GT = 256;            // threads per block
 constexpr int ONE_THREADS = 1024;  // of the block that does a small call alone
@@ -278,8 +286,10 @@ __global__ void __launch_bounds__(GT) grads_factor_kernel(const double* __restri
   if (threadIdx.x == 0) out[0] = f;
 }
 
-// Second pass, a part of a unit a block, the last first: `parts` of them up to the part `end`. No
-// loop, and so no wait for a block's stores.
+// Second pass, a part of a unit a block, the last first, up to the part `end`. No loop, and so no
+// wait for a block's stores: with one the decoder's pass took 1137 us, without 857. Each part's block
+// reads the factor that a launch of its own has formed: with the partial sums added up in every block
+// the clipping of ResNet-50 took 55.5 us instead of 53.7.
 constexpr int PARTS = UNIT / PART;
 template <int W, class TB>
 __global__ void __launch_bounds__(GT) grads_apply_kernel(TB tb, int count, int64_t end,
@@ -398,11 +408,14 @@ static kfac_status check_pointer(const void* p, int size, int i, const char* wha
   return KFAC_OK;
 }
 
-// Calls of at most this many units go to one block: it takes about what the two launches it
-// saves take.
+// Calls of at most this many units go to one block, which takes less than the launches it saves: at
+// 65536 elements the norm takes 11.1 us against 13.8, the clipping 14.2 against 19.9, the bounded
+// update 17.3 against 22.9; at 131072 the clipping takes 25.5 against 20.6.
 constexpr int ONE_UNITS = 16;
-// The second pass finds what the first has read in the 256 MB last-level cache, if it fits; beyond
-// that the first pass does not keep it.
+// The second pass finds what the first has read in the 256 MB last-level cache, if it fits (ResNet-50's
+// 102 MB: second pass 29.7 us); beyond that the first pass does not keep it, and reads past the caches
+// (streams of 2 GB: 7.2 TB/s against 6.4). The second pass always does, and writes past them too: lines
+// left dirty there made the next call's sum take 36 us instead of 20.
 constexpr int64_t CACHE_BYTES = int64_t(256) << 20;
 
 template <int W, class TB>

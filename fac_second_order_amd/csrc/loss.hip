@@ -4,7 +4,13 @@
 // A row of logits z predicts one token y: l = z[y] - log sum_j exp(z_j). Both losses
 // are functions of the rows' l, so the gradient of a row is one coefficient times
 // (one-hot(y) - softmax(z)). Per element that is two exponentials against four to
-// eight bytes moved: HBM-bound.
+// eight bytes moved: HBM-bound (without any exponential 4096 rows of 131072 bf16 take 343 us instead
+// of 360).
+//
+// The policy loss reads a row once, keeps it in registers and writes its gradient: 2048 rows of 32000
+// bf16 take 49.9 us (rows 44.6 of them, 4.8 TB/s), 4096 of 131072 357 us (354, 5.1 TB/s). The gradient
+// of the preference loss needs its whole sequence first, so rows are read twice: 2048 rows of 32000
+// take 54.6 us (statistics 19.6, pairs 6, gradient 28.9), 4096 of 50001 fp16 159 us (61 and 97).
 //
 // The softmax is taken about a maximum in fp32. What is formed once per row or per
 // sequence (the sum over the waves, l, the ratio, the sums of l) is formed in fp64: l is
@@ -489,8 +495,9 @@ __device__ inline PolicyTerms block_terms(const PolicyTerms* terms, int r0, int 
   return v;
 }
 
-// Many rows: TERMS of them to one.
-constexpr int TERMS = 2048;
+// Many rows, beyond FEW_TERMS: TERMS of them to one. (A call of 6000 rows of 200 takes 16.5 us without
+// this launch and 18.8 with it, 20000 rows 31.5 and 29.7, 200000 rows of 64 216 and 172.)
+constexpr int TERMS = 2048, FEW_TERMS = 16384;
 __global__ void __launch_bounds__(LT) policy_terms_kernel(const PolicyTerms* __restrict__ terms, int rows,
                                                           PolicyTerms* __restrict__ out) {
   const int r0 = blockIdx.x * TERMS;
@@ -506,6 +513,7 @@ __device__ inline void policy_stats(PolicyTerms v, float kl_coef, float* stats) 
   gp(stats)[3] = static_cast<float>(v.over);
 }
 
+// One block; of 2048 rows it takes 4.5 us, about the launch.
 constexpr int FT = 512;
 __global__ void __launch_bounds__(FT) policy_finish_kernel(const PolicyTerms* __restrict__ terms, int rows,
                                                            float kl_coef, float* stats) {
@@ -515,7 +523,8 @@ __global__ void __launch_bounds__(FT) policy_finish_kernel(const PolicyTerms* __
 
 // Few long rows, which would leave most of the chip idle: blocks for the parts of a row, then blocks
 // that join the parts, each for the gradient of a piece of its row, and one for all rows' results. A
-// call has at most 64 rows, a row at most 64 parts: a lane each.
+// call has at most 64 rows, a row at most 64 parts: a lane each. Latency-bound: 4 rows of 50001 fp16
+// take 4.2 and 5.0 us in the kernels, 11.7 a call.
 constexpr int SPLIT = 64, SPLIT_C = 4, SPLIT_GROUPS = LT * SPLIT_C;
 
 template <class T>
@@ -720,7 +729,9 @@ __device__ inline void pair_results(const LossRows& a, const PrefArgs& p, const 
 
 // Elementwise over the rows below `end`, last rows first: what pref_rows_kernel read last is what the
 // caches still hold. NT threads take a row, or U groups of 16 bytes each of a longer one (a wave a short
-// row, four rows a block), and end with their stores: no loop over rows, which would wait for them.
+// row, four rows a block: 32768 rows of 250 groups take 63.3 us a call so and 73.0 with a block each; U
+// of 2: 2048 rows of 4000 groups 57.0 us, with 4 58.0), and end with their stores: no loop over rows,
+// which would wait for them.
 // ALONE: no pref_pairs_kernel came before; every row's coefficient is formed here, and by one block
 // more in y the pairs' results.
 template <class T, int NT, int U, bool PAST, bool ALONE>
@@ -826,9 +837,14 @@ static Bytes rows_of(const void* p, const LossRows& a, int64_t ld, kfac_dtype dt
     else { LAUNCH(_Float16) }                    \
   } while (0)
 
-// LAUNCH(T, NT, C) for a row length: as few threads as hold the row in at most 8 groups of
-// 16 bytes each (32 registers, eight waves of a SIMD's 16 stay resident), at most 1024; 20
-// groups a thread are the most that leave no spills under the 128 registers of a 1024-thread
+// LAUNCH(T, NT, C) for a row length: C groups of 16 bytes, four registers each, in NT threads. Policy
+// calls, in us:
+//    250 groups, 32768 rows:  58.5 in   64 x 4 (four rows a block, no barrier),  99.5 in  256 x 4
+//   1000 groups, 16384 rows: 103   in  256 x 4,                                 107   in  256 x 8
+//   2000 groups,  8192 rows: 102   in  256 x 8,                                 108   in  512 x 8
+//   4000 groups,  2048 rows:  50.3 in  512 x 8,       52.4 in 256 x 16,  51.9 in 1024 x 4
+//   6250 groups,  4096 rows: 173   in 512 x 16,                                 192   in 1024 x 8
+// 19 groups a thread are the most that leave no spills under the 128 registers of a 1024-thread
 // block. Longer rows stay in memory.
 #define KFAC_BY_ROW(T, vocab, LAUNCH)                     \
   do {                                                    \
@@ -847,7 +863,9 @@ static int64_t row_bytes(int32_t rows, int32_t vocab, kfac_dtype dtype) {
   return int64_t(rows) * vocab * (dtype == KFAC_F32 ? 4 : 2);
 }
 // Rows of more than this pass the caches by where they are read or written once. What is dirty in
-// the 256 MB last-level cache is written back later at the expense of what is read then.
+// the 256 MB last-level cache is written back later at the expense of what is read then: 131 MB of
+// rows take 50 us instead of 56 (policy) and 53.7 instead of 63.6 (preference). The first pass of the
+// preference loss stays in the caches for the second: 410 MB take 166 us instead of 186.
 constexpr int64_t STORE_PAST = int64_t(64) << 20;
 
 // A count of rows: by sequence in 256-row slices, up to 16; over all rows in up to 64.
@@ -856,7 +874,9 @@ static int count_slices(int32_t rows, int32_t seqs, bool by_seq) {
   return n < 1 ? 1 : n > most ? static_cast<int>(most) : static_cast<int>(n);
 }
 
-// Rows of more groups than this are cut into parts where they are few.
+// Rows of more groups than this are cut into parts where they are few: one row of 131072 bf16 takes
+// 11.9 us against 20.4 whole, 16 rows of 32000 25.1 against 27.5 when the caller waits, 64 rows of 131072
+// 18.4 against 24.0; at 9000 elements, 1125 groups, both take the same.
 constexpr int SPLIT_FROM = 1024;
 
 struct PolicyWs {
@@ -890,7 +910,7 @@ extern "C" kfac_status kfac_policy_loss_workspace(int32_t rows, int32_t vocab, i
 
 static kfac_status launch_finish(const PolicyWs& w, int32_t rows, float kl_coef, float* stats, hipStream_t s) {
   const PolicyTerms* terms = w.terms;
-  if (rows > 2 * TERMS) {
+  if (rows > FEW_TERMS) {
     const int blocks = (rows - 1) / TERMS + 1;
     KFAC_LAUNCH(K_POLICY_TERMS, policy_terms_kernel, dim3(blocks), dim3(LT), 0, s, w.terms, rows, w.sums);
     KFAC_CHECK_LAUNCH("policy_terms_kernel");
@@ -953,7 +973,8 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
     return KFAC_OK;
   }
   // Where a row's threads have one row each to look at (a wave up to four) they count for themselves,
-  // behind the loads of their own row; with four each, 4096 rows of 131072 took 387 us instead of 360.
+  // behind the loads of their own row, which saves the launch (4.6 us); with four each, 4096 rows of
+  // 131072 took 387 us instead of 360.
   int row_threads = 0;
 #define KFAC_THREADS(T, NT, C) row_threads = NT;
 #define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, KFAC_THREADS);
@@ -967,7 +988,9 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
     KFAC_LAUNCH(K_LOSS_COUNT, loss_count_kernel, dim3(by_seq ? seqs : 1, p.slices), dim3(LT), 0, s, a,
                 by_seq ? w.row_seq : nullptr, w.count);
     KFAC_CHECK_LAUNCH("loss_count_kernel");
-    if (by_seq && seqs > 256) {  // more than four looks a lane for every row
+    // A wave looks for a row's sequences itself, or many are counted before: 300 sequences over 8192 rows
+    // of 1000 take 22.1 us without this launch and 23.2 with it, 2000 sequences 26.7 and 24.6.
+    if (by_seq && seqs > 1024) {
       p.nonempty = w.nonempty;
       KFAC_LAUNCH(K_LOSS_NONEMPTY, loss_nonempty_kernel, dim3(1), dim3(ONE), 0, s, w.count, seqs, p.slices, w.nonempty);
       KFAC_CHECK_LAUNCH("loss_nonempty_kernel");
@@ -1003,6 +1026,8 @@ struct PrefWs {
 };
 // Waves of a sequence: about four rows a lane, while the pairs fit in one block; with more pairs
 // than that, or sequences longer than 16 rows a lane, several blocks and a launch to add their losses.
+// (One wave each: two sequences over 8192 rows of 1000 take 27.2 us a call instead of 21.3, eight over
+// 60000 rows of 200 71.9 instead of 53.3.)
 static int sequence_waves(int32_t rows, int32_t pairs) {
   const int64_t per = pairs < 1 ? 1 : rows / (2 * int64_t(pairs)) + 1;
   int w = 1;

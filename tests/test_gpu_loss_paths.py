@@ -112,6 +112,13 @@ def test_counts(kfac_gpu, rows, layout):
     _check_policy(_policy(kfac_gpu, z, token, old, adv, **kw), z, token, old, adv, **kw)
 
 
+@pytest.mark.parametrize("rows,layout", [(16384, "none"), (16385, "none"), (7168, "many by sequence"),
+                                         (7175, "many by sequence")])
+def test_counts_on_both_sides_of_an_edge(kfac_gpu, rows, layout):
+    """The last rows that are summed in one step; 1024 sequences and one more."""
+    test_counts(kfac_gpu, rows, layout)
+
+
 @pytest.mark.parametrize("rows,pairs", [(300, 1), (5000, 1), (9000, 1), (9000, 2), (9000, 4), (9000, 8), (9000, 9),
                                         (20000, 16), (3000, 40), (2000, 500)])
 def test_pairs(kfac_gpu, rows, pairs):
