@@ -220,7 +220,7 @@ struct Row {
         }
       return {m, wave_add(static_cast<double>(s))};
     } else {  // BATCH groups at a time; a running maximum in each thread, the sum about it in fp64
-      constexpr int BATCH = 8;
+      constexpr int BATCH = 4;  // with 8 within 2% of it
       float m = rest;
       double s = rest == NEG_INF ? 0.0 : exp_about(rest, rest);
       for (int g0 = tid; g0 < full; g0 += NT * BATCH) {
@@ -844,19 +844,30 @@ static Bytes rows_of(const void* p, const LossRows& a, int64_t ld, kfac_dtype dt
 //   2000 groups,  8192 rows: 102   in  256 x 8,                                 108   in  512 x 8
 //   4000 groups,  2048 rows:  50.3 in  512 x 8,       52.4 in 256 x 16,  51.9 in 1024 x 4
 //   6250 groups,  4096 rows: 173   in 512 x 16,                                 192   in 1024 x 8
-// 19 groups a thread are the most that leave no spills under the 128 registers of a 1024-thread
-// block. Longer rows stay in memory.
-#define KFAC_BY_ROW(T, vocab, LAUNCH)                     \
-  do {                                                    \
-    const int groups_ = (vocab) / Pack<T>::n;         \
-    if (groups_ <= 64 * 4) { LAUNCH(T, 64, 4) }           \
-    else if (groups_ <= 256 * 4) { LAUNCH(T, 256, 4) }    \
-    else if (groups_ <= 256 * 8) { LAUNCH(T, 256, 8) }    \
-    else if (groups_ <= 512 * 8) { LAUNCH(T, 512, 8) }    \
-    else if (groups_ <= 512 * 16) { LAUNCH(T, 512, 16) }  \
-    else if (groups_ <= 1024 * 16) { LAUNCH(T, 1024, 16) } \
-    else if (groups_ <= 1024 * 19) { LAUNCH(T, 1024, 19) } \
-    else { LAUNCH(T, 1024, 0) }                           \
+// A row that waits in its registers for its gradient (`keep`) may have 19 groups a thread, the most that
+// leave no spills under the 128 registers of a 1024-thread block: 4096 rows of 16384 groups take 429 us
+// so, 470 if they stay in memory (no row masked). Rows without a gradient stay there from 8192 groups on,
+// two blocks on a CU instead of one: 1453 rows of 11803 groups 63.9 us instead of 83.4, 1453 of 16384
+// 78.3 instead of 96.9; in blocks of 512 threads 62.7 and 81.5. Longer rows stay in memory.
+#define KFAC_SHORT_ROWS(T, LAUNCH)                         \
+  if (groups_ <= 64 * 4) { LAUNCH(T, 64, 4) }             \
+  else if (groups_ <= 256 * 4) { LAUNCH(T, 256, 4) }      \
+  else if (groups_ <= 256 * 8) { LAUNCH(T, 256, 8) }      \
+  else if (groups_ <= 512 * 8) { LAUNCH(T, 512, 8) }      \
+  else if (groups_ <= 512 * 16) { LAUNCH(T, 512, 16) }
+#define KFAC_BY_ROW(T, vocab, keep, LAUNCH)                         \
+  do {                                                              \
+    const int groups_ = (vocab) / Pack<T>::n;                       \
+    KFAC_SHORT_ROWS(T, LAUNCH)                                      \
+    else if ((keep) && groups_ <= 1024 * 16) { LAUNCH(T, 1024, 16) } \
+    else if ((keep) && groups_ <= 1024 * 19) { LAUNCH(T, 1024, 19) } \
+    else { LAUNCH(T, 1024, 0) }                                      \
+  } while (0)
+#define KFAC_BY_STATS(T, vocab, LAUNCH)       \
+  do {                                        \
+    const int groups_ = (vocab) / Pack<T>::n; \
+    KFAC_SHORT_ROWS(T, LAUNCH)                \
+    else { LAUNCH(T, 1024, 0) }                \
   } while (0)
 
 static int64_t row_bytes(int32_t rows, int32_t vocab, kfac_dtype dtype) {
@@ -977,7 +988,7 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
   // 131072 took 387 us instead of 360.
   int row_threads = 0;
 #define KFAC_THREADS(T, NT, C) row_threads = NT;
-#define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, KFAC_THREADS);
+#define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, dlogits, KFAC_THREADS);
   KFAC_BY_TYPE(dtype, KFAC_TYPED);
 #undef KFAC_TYPED
 #undef KFAC_THREADS
@@ -1006,7 +1017,7 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
     KFAC_LAUNCH(K_POLICY_ROWS, (policy_rows_kernel<T, NT, C, false>), dim3(grid), dim3(kRowThreads<NT>), 0, s, a, \
                 p, w.terms);                                                                                     \
   }
-#define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, KFAC_ROWS);
+#define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, dlogits, KFAC_ROWS);
   KFAC_BY_TYPE(dtype, KFAC_TYPED);
 #undef KFAC_TYPED
 #undef KFAC_ROWS
@@ -1097,7 +1108,7 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
 #define KFAC_ROWS(T, NT, C)                                                                        \
   KFAC_LAUNCH(K_PREF_ROWS, (pref_rows_kernel<T, NT, C>), dim3((rows - 1) / kRowsPerBlock<NT> + 1), \
               dim3(kRowThreads<NT>), 0, s, a, w.stat, w.logp);
-#define KFAC_TYPED(T) KFAC_BY_ROW(T, vocab, KFAC_ROWS);
+#define KFAC_TYPED(T) KFAC_BY_STATS(T, vocab, KFAC_ROWS);
     KFAC_BY_TYPE(dtype, KFAC_TYPED);
 #undef KFAC_TYPED
 #undef KFAC_ROWS

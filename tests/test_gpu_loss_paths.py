@@ -39,6 +39,26 @@ def test_rows_on_both_sides_of_an_edge(kfac_gpu, dtype, groups, offset):
         _check_prefer(_prefer(kfac_gpu, z, token, _offsets(0, 1, 2), **kw), z, token, _offsets(0, 1, 2), **kw)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("groups", [4096, 8192, 19456])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_rows_without_a_gradient(kfac_gpu, dtype, groups, offset):
+    """Rows of which nothing but l is wanted, at the lengths where they stay in memory; -inf in whole
+    groups, and the maximum in the first, a middle and the last element."""
+    ev = 4 if dtype == F32 else 8
+    for vocab in (groups * ev - 1, groups * ev, groups * ev + ev):
+        z, token, old, adv, ref = _policy_inputs(vocab + offset + 1, 3, vocab, dtype, 0, offset)
+        for t, j in enumerate((0, vocab // 2, vocab - 1)):
+            z[t, vocab // 4: vocab // 4 + 5000] = float("-inf")
+            z[t, j] = 14.0
+            token[t] = j
+            old[t] = lo.row_logp(host64(z[t]), j)[0] + 0.1
+        kw = dict(ref=ref, kl_coef=0.1, begin=_offsets(0, 1, 3), by_sequence=True)
+        _check_policy(_policy(kfac_gpu, z, token, old, adv, grad=False, **kw), z, token, old, adv, **kw)
+        kw = dict(ref=_vec(torch.Generator().manual_seed(1), 2), beta=0.3)
+        _check_prefer(_prefer(kfac_gpu, z, token, _offsets(0, 1, 3), grad=False, **kw), z, token, _offsets(0, 1, 3), **kw)
+
+
 @pytest.mark.parametrize("rows", [1, 3, 63, 64, 65])
 @pytest.mark.parametrize("dtype,vocab", [(F32, 4097), (F32, 4100), (F32, 8191), (F32, 8193), (BF16, 8199), (BF16, 8200),
                                          (F16, 16385), (BF16, 50001), (F32, 262143), (F32, 262144)])
