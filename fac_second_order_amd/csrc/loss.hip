@@ -844,21 +844,22 @@ static Bytes rows_of(const void* p, const LossRows& a, int64_t ld, kfac_dtype dt
 //   2000 groups,  8192 rows: 102   in  256 x 8,                                 108   in  512 x 8
 //   4000 groups,  2048 rows:  50.3 in  512 x 8,       52.4 in 256 x 16,  51.9 in 1024 x 4
 //   6250 groups,  4096 rows: 173   in 512 x 16,                                 192   in 1024 x 8
+//  16384 groups,  4096 rows: 433.5 in 1024 x 16,                                435.3 in 1024 x 19
 // A row that waits in its registers for its gradient (`keep`) may have 19 groups a thread, the most that
 // leave no spills under the 128 registers of a 1024-thread block: 4096 rows of 16384 groups take 429 us
 // so, 470 if they stay in memory (no row masked). Rows without a gradient stay there from 8192 groups on,
 // two blocks on a CU instead of one: 1453 rows of 11803 groups 63.9 us instead of 83.4, 1453 of 16384
 // 78.3 instead of 96.9; in blocks of 512 threads 62.7 and 81.5. Longer rows stay in memory.
-#define KFAC_SHORT_ROWS(T, LAUNCH)                         \
-  if (groups_ <= 64 * 4) { LAUNCH(T, 64, 4) }             \
-  else if (groups_ <= 256 * 4) { LAUNCH(T, 256, 4) }      \
-  else if (groups_ <= 256 * 8) { LAUNCH(T, 256, 8) }      \
-  else if (groups_ <= 512 * 8) { LAUNCH(T, 512, 8) }      \
+#define KFAC_SHORT_ROWS(T, LAUNCH)                   \
+  if (groups_ <= 64 * 4) { LAUNCH(T, 64, 4) }        \
+  else if (groups_ <= 256 * 4) { LAUNCH(T, 256, 4) } \
+  else if (groups_ <= 256 * 8) { LAUNCH(T, 256, 8) } \
+  else if (groups_ <= 512 * 8) { LAUNCH(T, 512, 8) } \
   else if (groups_ <= 512 * 16) { LAUNCH(T, 512, 16) }
-#define KFAC_BY_ROW(T, vocab, keep, LAUNCH)                         \
-  do {                                                              \
-    const int groups_ = (vocab) / Pack<T>::n;                       \
-    KFAC_SHORT_ROWS(T, LAUNCH)                                      \
+#define KFAC_BY_ROW(T, vocab, keep, LAUNCH)                          \
+  do {                                                               \
+    const int groups_ = (vocab) / Pack<T>::n;                        \
+    KFAC_SHORT_ROWS(T, LAUNCH)                                       \
     else if ((keep) && groups_ <= 1024 * 16) { LAUNCH(T, 1024, 16) } \
     else if ((keep) && groups_ <= 1024 * 19) { LAUNCH(T, 1024, 19) } \
     else { LAUNCH(T, 1024, 0) }                                      \
@@ -867,7 +868,7 @@ static Bytes rows_of(const void* p, const LossRows& a, int64_t ld, kfac_dtype dt
   do {                                        \
     const int groups_ = (vocab) / Pack<T>::n; \
     KFAC_SHORT_ROWS(T, LAUNCH)                \
-    else { LAUNCH(T, 1024, 0) }                \
+    else { LAUNCH(T, 1024, 0) }               \
   } while (0)
 
 static int64_t row_bytes(int32_t rows, int32_t vocab, kfac_dtype dtype) {
