@@ -460,23 +460,21 @@ def kfac_trust_update(precond, grad, w, lr, delta, step, fisher=None, shift=0.0,
     """w[i] <- w[i] - s * precond[i], s = min(lr, sqrt(2 delta / |q|)), q = sum of
     <precond[i], grad[i]>; step[:2] <- s, q. Where grad[i] is None, fisher[i] (diagonal)
     and shift give the gradient (see kfac.h)."""
-    numel, codes, p_at = _listed(precond, "precond")
-    w_numel, w_codes, w_at = _listed(w, "w")
-    f32 = [KFAC_F32] * len(codes)
-    if codes != f32 or w_codes != [KFAC_F32] * len(w_codes):
-        raise TypeError("precond and w must be float32")
-    if len(grad) != len(numel) or (fisher is not None and len(fisher) != len(numel)):
+    n = len(precond)
+    if len(grad) != n or len(w) != n or (fisher is not None and len(fisher) != n):
         raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
-    diagonal = [i for i, g in enumerate(grad) if g is None]
     given = list(grad)  # an entry's gradient, or else its Fisher
+    diagonal = [i for i, g in enumerate(given) if g is None]
     for i in diagonal:
         if fisher is None or fisher[i] is None:
             raise ValueError("an entry without a gradient needs its fisher")
         given[i] = fisher[i]
-    s_numel, s_codes, g_at = _listed(given, "grad and fisher")
-    if s_numel != numel or w_numel != numel:
+    numel, codes, at = _listed([*precond, *w, *given], "precond, grad, fisher and w")
+    if codes[:2 * n] != [KFAC_F32] * (2 * n):
+        raise TypeError("precond and w must be float32")
+    if numel[n:2 * n] != numel[:n] or numel[2 * n:] != numel[:n]:
         raise ValueError("precond, grad, fisher and w must have one tensor of one size for each entry")
-    f_at = [0] * len(numel)
+    numel, s_codes, p_at, w_at, g_at, f_at = numel[:n], codes[2 * n:], at[:n], at[n:2 * n], at[2 * n:], [0] * n
     for i in diagonal:
         if s_codes[i] != KFAC_F32:
             raise TypeError("fisher must be float32")
@@ -484,9 +482,9 @@ def kfac_trust_update(precond, grad, w, lr, delta, step, fisher=None, shift=0.0,
     _on_device([step], "step")
     step_at = _scalar_out(step, 2, "step")
     ws, wsb, held = _call_ws(workspace, kfac_grad_norm_workspace, (numel,), step.device, stream)
-    n, c, p, ww = _words(numel), _halfwords(s_codes), _words(p_at), _words(w_at)
+    counts, c, p, ww = _words(numel), _halfwords(s_codes), _words(p_at), _words(w_at)
     g, f = _words(g_at), _words(f_at)
-    _check(_lib.kfac_trust_update(len(numel), _at(n), _at(p), _at(c), _at(g), _at(f), float(shift), _at(ww), float(lr),
+    _check(_lib.kfac_trust_update(n, _at(counts), _at(p), _at(c), _at(g), _at(f), float(shift), _at(ww), float(lr),
                                   float(delta), step_at, ws, wsb, _stream(stream)), "kfac_trust_update")
 
 
