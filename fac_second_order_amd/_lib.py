@@ -418,6 +418,8 @@ def _call_ws(workspace, query, sizes, device, stream):
             workspace = torch.empty(query(*sizes) + 256, dtype=torch.uint8, device=device)
     elif workspace.device != device:
         raise ValueError("workspace must be on the current HIP device")
+    elif not workspace.is_contiguous():  # numel would count bytes that are not there
+        raise TypeError("workspace must be contiguous")
     at = workspace.data_ptr()
     pad = -at % 256
     return at + pad, max(0, workspace.numel() * workspace.element_size() - pad), workspace

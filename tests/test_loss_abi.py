@@ -296,3 +296,9 @@ def test_a_stream_of_another_device_is_refused(lib):
     for workspace in (None, torch.zeros(8)):
         with pytest.raises(ValueError, match="stream"):
             lib._call_ws(workspace, None, (), torch.device("cuda", 0), there)
+
+
+def test_a_workspace_of_repeated_bytes_is_refused(lib):
+    """An expanded tensor has more elements than bytes."""
+    with pytest.raises(TypeError, match="contiguous"):
+        lib._call_ws(torch.zeros(1).expand(1 << 20), None, (), torch.device("cpu"), None)
