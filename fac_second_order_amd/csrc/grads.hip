@@ -14,6 +14,7 @@
 // of ResNet-50 (409 MB moved): 82.7 us. (A copy kernel's best here is 6.15 TB/s, with one group of
 // 16 bytes a thread in address order; a library copy does 4.95.)
 #include <algorithm>
+#include <type_traits>
 
 #include "row_ops.hpp"
 
@@ -27,28 +28,40 @@ constexpr int MAX_BLOCKS = 1024;   // partial sums
 constexpr int GT = 256;            // threads per block
 constexpr int ONE_THREADS = 1024;  // of the block that does a small call alone
 
-struct GradDesc {
-  const void* grad;      // or the diagonal Fisher
-  const float* precond;
-  void* out;             // clipped gradient, or the weights of the update
-  int64_t info;          // numel, and above it the types
+// What a call does with its sum: the norm alone, clipping by it, or the bounded update.
+enum Work { NORM, CLIP, TRUST };
+
+// A tensor of a call: what the norm takes, and what the others need beside.
+struct NormDesc {
+  const void* grad;  // or the diagonal Fisher
+  int64_t info;      // numel, and above it the types
   static constexpr int kType = 48, kWide = 50, kDiagonal = 51;
   __host__ __device__ int64_t numel() const { return info & ((int64_t(1) << kType) - 1); }
   __host__ __device__ int type() const { return static_cast<int>(info >> kType) & 3; }
   __host__ __device__ bool wide() const { return info >> kWide & 1; }  // out is fp32
   __host__ __device__ bool diagonal() const { return info >> kDiagonal & 1; }
 };
+struct ClipDesc : NormDesc {
+  void* out;  // clipped gradient, or the weights of the update
+};
+struct TrustDesc : ClipDesc {
+  const float* precond;
+};
+template <int W>
+using DescOf = std::conditional_t<W == NORM, NormDesc, std::conditional_t<W == CLIP, ClipDesc, TrustDesc>>;
 
 // The tables of a call: in the workspace, or where they fit in the kernel's arguments
-// themselves, which saves the launches that send them.
+// themselves, which saves the launches that send them (4.6 us each).
+template <class D>
 struct SentTables {
-  const GradDesc* desc;
+  const D* desc;
   const int32_t* begin;  // first unit of each tensor
 };
-constexpr int INLINE = 108;  // tensors whose tables stay below 4 KB of arguments
+template <class D>
 struct InlineTables {
-  GradDesc desc[INLINE];
-  int32_t begin[INLINE];
+  static constexpr int most = 3888 / (sizeof(D) + 4);  // 194, 138 or 108: all arguments stay below 4 KB
+  D desc[most];
+  int32_t begin[most];
 };
 
 // The tensor that unit c lies in, by 64 begins at a time, one a lane: two loads side by side for up to
@@ -102,7 +115,7 @@ __device__ inline void over(int n, L load, U use, O one) {
 }
 
 template <int NT, bool LAST>
-__device__ inline void add_squares(const GradDesc& d, int64_t e0, int n, double& acc) {
+__device__ inline void add_squares(const NormDesc& d, int64_t e0, int n, double& acc) {
   with_type(d.type(), [&](auto tag) {
     using T = decltype(tag);
     constexpr int EV = Pack<T>::n;
@@ -127,7 +140,7 @@ __device__ inline void add_squares(const GradDesc& d, int64_t e0, int n, double&
 
 // out = coef * grad, coef in fp32, the product rounded once to the type of out.
 template <int SIZE, int NT>
-__device__ inline void scale_part(const GradDesc& d, int64_t e0, int n, float coef) {
+__device__ inline void scale_part(const ClipDesc& d, int64_t e0, int n, float coef) {
   with_type(d.type(), [&](auto tag) {
     using T = decltype(tag);
     const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
@@ -155,7 +168,7 @@ __device__ inline void scale_part(const GradDesc& d, int64_t e0, int n, float co
 
 // P * g, the preconditioned gradient against the gradient it came from.
 template <int NT, bool LAST>
-__device__ inline void add_products(const GradDesc& d, int64_t e0, int n, float shift, double& acc) {
+__device__ inline void add_products(const TrustDesc& d, int64_t e0, int n, float shift, double& acc) {
   const bool diagonal = d.diagonal();
   with_type(d.type(), [&](auto tag) {
     using T = decltype(tag);
@@ -185,7 +198,7 @@ __device__ inline void add_products(const GradDesc& d, int64_t e0, int n, float 
 
 // w -= step * P.
 template <int SIZE, int NT>
-__device__ inline void apply_part(const GradDesc& d, int64_t e0, int n, float step) {
+__device__ inline void apply_part(const TrustDesc& d, int64_t e0, int n, float step) {
   using V = Pack<float, 4>::vec;
   const KG float* p = gp(d.precond) + e0;
   KG float* w = gp(static_cast<float*>(d.out)) + e0;
@@ -204,8 +217,6 @@ __device__ inline void apply_part(const GradDesc& d, int64_t e0, int n, float st
       [&](int i) { w[i] = fmaf(-step, p[i], w[i]); });
 }
 
-// What a call does with its sum: the norm alone, clipping by it, or the bounded update.
-enum Work { NORM, CLIP, TRUST };
 struct WorkArgs {
   float* result;  // norm; or step and q
   float a, b;     // max_norm; or lr and delta
@@ -232,13 +243,13 @@ __device__ inline float factor(double sum, const WorkArgs& k, bool shown) {
   }
 }
 
-template <int W, int NT, bool LAST>
-__device__ inline void sum_unit(const GradDesc& d, int64_t e0, int n, float shift, double& acc) {
+template <int W, int NT, bool LAST, class D>
+__device__ inline void sum_unit(const D& d, int64_t e0, int n, float shift, double& acc) {
   if constexpr (W == TRUST) add_products<NT, LAST>(d, e0, n, shift, acc);
   else add_squares<NT, LAST>(d, e0, n, acc);
 }
-template <int W, int SIZE, int NT>
-__device__ inline void second_part(const GradDesc& d, int64_t e0, int n, float f) {
+template <int W, int SIZE, int NT, class D>
+__device__ inline void second_part(const D& d, int64_t e0, int n, float f) {
   if constexpr (W == TRUST) {
     if (f != 0.f) apply_part<SIZE, NT>(d, e0, n, f);
   } else if constexpr (W == CLIP) {
@@ -268,7 +279,7 @@ __global__ void __launch_bounds__(GT) grads_sum_kernel(TB tb, int count, int uni
   int p = find_tensor(tb, count, blockIdx.x);
   for (int c = blockIdx.x; c < units; c += gridDim.x) {
     if (p + 1 < count && tb.begin[p + 1] <= c) p = find_tensor(tb, count, c);
-    const GradDesc d = tb.desc[p];
+    const auto d = tb.desc[p];
     const int64_t e0 = int64_t(c - tb.begin[p]) * UNIT;
     sum_unit<W, GT, LAST>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
   }
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(GT) grads_apply_kernel(TB tb, int count, int64
   const int64_t at = end - 1 - blockIdx.x;
   const int c = static_cast<int>(at / PARTS);
   const int p = find_tensor(tb, count, c);
-  const GradDesc d = tb.desc[p];
+  const auto d = tb.desc[p];
   const int64_t e0 = int64_t(c - tb.begin[p]) * UNIT + at % PARTS * PART;
   const int64_t n = min(d.numel() - e0, int64_t(PART));
   if (n > 0) second_part<W, PART, GT>(d, e0, static_cast<int>(n), f[0]);
@@ -305,25 +316,26 @@ __global__ void __launch_bounds__(GT) grads_apply_kernel(TB tb, int count, int64
 
 // A small call in one block: both passes, and no launch between them.
 template <int W>
-__global__ void __launch_bounds__(ONE_THREADS) grads_one_kernel(InlineTables tb, int count, WorkArgs k) {
+__global__ void __launch_bounds__(ONE_THREADS) grads_one_kernel(InlineTables<DescOf<W>> tb, int count,
+                                                              WorkArgs k) {
   __shared__ double s[ONE_THREADS / 64];
   double acc = 0;
   for (int p = 0; p < count; ++p) {
-    const GradDesc d = tb.desc[p];
+    const auto d = tb.desc[p];
     for (int64_t e0 = 0; e0 < d.numel(); e0 += UNIT)
       sum_unit<W, ONE_THREADS, false>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
   }
   const float f = factor<W>(block_sum<ONE_THREADS>(acc, s), k, threadIdx.x == 0);
   if constexpr (W != NORM)
     for (int p = 0; p < count; ++p) {
-      const GradDesc d = tb.desc[p];
+      const auto d = tb.desc[p];
       for (int64_t e0 = 0; e0 < d.numel(); e0 += UNIT)
         second_part<W, UNIT, ONE_THREADS>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), f);
     }
 }
 
 static size_t grads_need(int count) {
-  return align256(sizeof(GradDesc) * size_t(count)) + align256(sizeof(int32_t) * size_t(count)) +
+  return align256(sizeof(TrustDesc) * size_t(count)) + align256(sizeof(int32_t) * size_t(count)) +
          align256(sizeof(double) * MAX_BLOCKS) + 256;
 }
 
@@ -385,20 +397,20 @@ struct Spans {
 
 // The tensors that hold elements, as descriptors.
 struct GradCall {
-  std::vector<GradDesc> desc;
+  std::vector<TrustDesc> desc;
   std::vector<int32_t> begin;
   Spans spans;
   int units = 0;
   int64_t read_bytes = 0;  // what the second pass reads again
-  void add(const GradDesc& d, int64_t bytes) {
+  void add(const TrustDesc& d, int64_t bytes) {
     read_bytes += bytes;
     desc.push_back(d);
     begin.push_back(units);
     units += static_cast<int>((d.numel() + UNIT - 1) / UNIT);
   }
   static int64_t pack(int64_t numel, int type, bool wide, bool diagonal) {
-    return numel | int64_t(type) << GradDesc::kType | int64_t(wide) << GradDesc::kWide |
-           int64_t(diagonal) << GradDesc::kDiagonal;
+    return numel | int64_t(type) << NormDesc::kType | int64_t(wide) << NormDesc::kWide |
+           int64_t(diagonal) << NormDesc::kDiagonal;
   }
 };
 
@@ -451,13 +463,14 @@ static kfac_status launch_grads(const GradCall& call, int32_t count, const WorkA
   st = check_workspace(workspace, ws_bytes, grads_need(count));
   if (st) return st;
   const int n = static_cast<int>(call.desc.size());
+  using D = DescOf<W>;
   Carver cv(workspace);
-  GradDesc* desc = cv.take<GradDesc>(count);
+  D* desc = cv.take<D>(count);
   int32_t* begin = cv.take<int32_t>(count);
   double* partial = cv.take<double>(MAX_BLOCKS);
   float* f = cv.take<float>(1);
-  if (n <= INLINE) {
-    InlineTables tb;
+  if (n <= InlineTables<D>::most) {
+    InlineTables<D> tb;
     std::copy(call.desc.begin(), call.desc.end(), tb.desc);
     std::copy(call.begin.begin(), call.begin.end(), tb.begin);
     if (call.units > ONE_UNITS) return launch_passes<W>(tb, call, k, partial, f, s);
@@ -465,11 +478,12 @@ static kfac_status launch_grads(const GradCall& call, int32_t count, const WorkA
     KFAC_CHECK_LAUNCH("grads_one_kernel");
     return KFAC_OK;
   }
+  const std::vector<D> sent(call.desc.begin(), call.desc.end());
   TableUpload tu;
-  tu.add(desc, call.desc.data(), sizeof(GradDesc) * n);
+  tu.add(desc, sent.data(), sizeof(D) * n);
   tu.add(begin, call.begin.data(), sizeof(int32_t) * n);
   if ((st = tu.flush(s))) return st;
-  return launch_passes<W>(SentTables{desc, begin}, call, k, partial, f, s);
+  return launch_passes<W>(SentTables<D>{desc, begin}, call, k, partial, f, s);
 }
 
 extern "C" kfac_status kfac_grad_norm_workspace(int32_t count, const int64_t* numel, size_t* bytes) {
@@ -496,7 +510,9 @@ static kfac_status grad_impl(int32_t count, const int64_t* numel, const kfac_dty
       return fail(KFAC_ERR_UNSUPPORTED, "tensor %d: out must have the gradient's type or fp32", i);
     if (numel[i] == 0) continue;
     if ((st = check_pointer(grad[i], dtype_size(dtype[i]), i, "grad"))) return st;
-    GradDesc d = {grad[i], nullptr, nullptr, GradCall::pack(numel[i], dtype[i], clip && out_dtype[i] == KFAC_F32, false)};
+    TrustDesc d = {};
+    d.grad = grad[i];
+    d.info = GradCall::pack(numel[i], dtype[i], clip && out_dtype[i] == KFAC_F32, false);
     if (clip) {
       if ((st = check_pointer(out[i], dtype_size(out_dtype[i]), i, "out"))) return st;
       d.out = out[i];
@@ -531,7 +547,11 @@ static kfac_status trust_impl(int32_t count, const int64_t* numel, const float* 
     if (numel[i] == 0) continue;
     if ((st = check_pointer(precond[i], 4, i, "precond"))) return st;
     if ((st = check_pointer(w[i], 4, i, "w"))) return st;
-    GradDesc d = {grad[i], precond[i], w[i], GradCall::pack(numel[i], grad_dtype[i] & 3, true, false)};
+    TrustDesc d = {};
+    d.grad = grad[i];
+    d.precond = precond[i];
+    d.out = w[i];
+    d.info = GradCall::pack(numel[i], grad_dtype[i] & 3, true, false);
     if (grad[i]) {
       if (!known_dtype(grad_dtype[i])) return fail(KFAC_ERR_UNSUPPORTED, "tensor %d: dtype %d", i, grad_dtype[i]);
       if ((st = check_pointer(grad[i], dtype_size(grad_dtype[i]), i, "grad"))) return st;

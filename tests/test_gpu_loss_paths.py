@@ -236,7 +236,7 @@ def test_offsets_that_decrease_stay_inside(kfac_gpu):
 @pytest.mark.parametrize("count,size", [(108, 5000), (109, 5000), (150, 1 << 20), (64, 4097), (65, 4096), (4100, 50),
                                         (300, 1)])
 def test_tables_of_tensors(kfac_gpu, count, size):
-    """Tables in the arguments (to 108 tensors) and sent ahead; 150 MB and 600 MB of gradients, found
+    """Tables in the arguments (of an update, to 108 tensors) and sent ahead; 150 MB and 600 MB of gradients, found
     in the caches again and not; one to three steps of the search for a unit's tensor."""
     sizes = [size + i % 3 for i in range(count)]
     grads = _tensors(count, sizes, [F32, BF16] if size < 1 << 20 else [F32])
@@ -254,6 +254,12 @@ def test_tables_of_tensors(kfac_gpu, count, size):
     c = 0.5 / want
     for o, t in zip(outs, grads):
         assert ((o.double() - t.double() * c).abs() <= 2.02 * U * (t.double() * c).abs()).all()
+
+
+@pytest.mark.parametrize("count", [138, 139, 194, 195])
+def test_tables_on_both_sides_of_an_edge(kfac_gpu, count):
+    """The most tensors whose tables the clipping and the norm take in their arguments, and one more."""
+    test_tables_of_tensors(kfac_gpu, count, 5000)
 
 
 def test_a_call_of_one_block_and_of_more(kfac_gpu):
