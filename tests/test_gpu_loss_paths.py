@@ -199,6 +199,33 @@ def test_many_rows_of_a_gradient_launch(kfac_gpu):
         say("preference gradient over", rows, "rows")
 
 
+@pytest.mark.parametrize("rows,vocab,pairs", [(262200, 3, 12), (1500, 40, 9), (1500, 40, 40)])
+def test_the_loss_of_several_shares(kfac_gpu, rows, vocab, pairs):
+    """More pairs than one block takes: their shares are added by the gradient's launch, the first of two
+    where the rows are many, or by one of their own without a gradient, to the same bits."""
+    z, token, g = logits(rows + pairs, rows, vocab, F32, std=1.0)
+    cuts = torch.linspace(2, rows - 3, 2 * pairs + 1).int().tolist()
+    begin = _offsets(*cuts)
+    d = torch.full((rows, vocab), 7.0, device="cuda")
+    kw = dict(beta=1e-3, grad_scale=float(rows))
+    loss, margin, seq, _ = _prefer(kfac_gpu, z, token, begin, dlogits=d, **kw)
+    alone = _prefer(kfac_gpu, z, token, begin, grad=False, **kw)
+    assert torch.equal(loss, alone[0]) and torch.equal(margin, alone[1]) and torch.equal(seq, alone[2])
+    x = host64(margin)
+    # the loss moves by at most as much as a margin, which is off by half a step as it stands
+    assert abs(float(loss) - np.logaddexp(0, -x).mean()) <= U * (np.abs(x).mean() + 1.01 * float(loss)) + 1e-14
+    assert (d[:cuts[0]] == 7).all() and (d[cuts[-1]:] == 7).all()
+    one = torch.nn.functional.one_hot(token, vocab).double()
+    side = np.repeat([1.0, -1.0], pairs)
+    slope = np.tile(-rows * 1e-3 / (1 + np.exp(x)) / pairs, 2) * side
+    coef = torch.from_numpy(np.repeat(slope, np.diff(cuts))).cuda()[:, None]
+    want = coef * (one - z.double().softmax(1))[cuts[0]:cuts[-1]]
+    # l of a row is off by less than 1e-5, a softmax of 40 elements by 2e-5 of itself; the coefficient by
+    # a quarter of its margin's half step and its own
+    err = 2e-5 + U * (float(np.abs(x).max()) / 4 + 2)
+    assert ((d[cuts[0]:cuts[-1]] - want).abs() <= err * coef.abs()).all()
+
+
 def test_losses_without_rows(kfac_gpu):
     e = torch.empty(0, device="cuda")
     z = torch.empty(0, 5, device="cuda")
