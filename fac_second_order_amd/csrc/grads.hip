@@ -227,11 +227,12 @@ struct WorkArgs {
 template <int W>
 __device__ inline float factor(double sum, const WorkArgs& k, bool shown) {
   if constexpr (W == TRUST) {
-    float step = 0.f;  // a sum that is not finite: no update
-    if (sum - sum == 0) step = fmin(static_cast<double>(k.a), sqrt(2.0 * k.b / fabs(sum)));
+    const float q = static_cast<float>(sum);
+    float step = 0.f;  // a q that is no finite float: no update, and q shows why
+    if (q - q == 0) step = fmin(static_cast<double>(k.a), sqrt(2.0 * k.b / fabs(sum)));
     if (shown) {
       gp(k.result)[0] = step;
-      gp(k.result)[1] = static_cast<float>(sum);
+      gp(k.result)[1] = q;
     }
     return step;
   } else {

@@ -343,8 +343,8 @@ kfac_status kfac_grad_clip(int32_t count, const int64_t* numel, const kfac_dtype
  * (KFAC_F16, KFAC_BF16 or KFAC_F32). Where grad[i] is NULL the Fisher is diagonal and
  * fisher[i] (fp32; kfac_bn_diag's, with its shift) gives g = P (fisher + shift);
  * fisher may be NULL if every grad[i] is given. step (device, two floats) receives s and
- * q. q is summed in fp64 in a fixed order. Where q is not finite s is 0 and w is left
- * alone. w must not share bytes with any other buffer of the call; lr must be finite and
+ * q. q is summed in fp64 in a fixed order. Where q, as a float, is not finite s is 0 and w
+ * is left alone. w must not share bytes with any other buffer of the call; lr must be finite and
  * >= 0, delta positive and finite. Workspace: kfac_grad_norm_workspace.
  * ------------------------------------------------------------------------- */
 kfac_status kfac_trust_update(int32_t count, const int64_t* numel, const float* const* precond,

@@ -260,3 +260,19 @@ def test_calls_in_a_graph(kfac_gpu):
         calls()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(have, (*outs, *w, norm, step))), k
+
+
+@pytest.mark.parametrize("n", [300, 70001])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_trust_leaves_alone_what_a_float_does_not_hold(kfac_gpu, n, sign):
+    """P and g finite, and q finite in fp64 (n 1e40) but no float: the step is 0, w stays and q
+    shows it; one launch and several."""
+    P, g = [torch.full((n,), 1e20, device="cuda")], [torch.full((n,), sign * 1e20, device="cuda")]
+    w = _tensors(17, [n], [F32])
+    w0 = w[0].clone()
+    assert _trust(kfac_gpu, P, g, w, 0.25, 1.0).tolist() == [0.0, sign * math.inf]
+    assert torch.equal(w[0], w0)
+    # n 1e32 is one
+    P, g = [torch.full((n,), 1e16, device="cuda")], [torch.full((n,), sign * 1e16, device="cuda")]
+    step = _trust(kfac_gpu, P, g, w, 0.25, 1e30)
+    assert step[0] > 0 and step[1].isfinite() and not torch.equal(w[0], w0)
