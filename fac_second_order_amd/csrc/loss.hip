@@ -838,6 +838,27 @@ static Bytes rows_of(const void* p, const LossRows& a, int64_t ld, kfac_dtype dt
   return {p, a.rows ? ((a.rows - 1) * ld + a.vocab) * (dtype == KFAC_F32 ? 4 : 2) : 0};
 }
 
+// Nor with another result or the workspace, which are written at once too; `written` holds all of
+// them but the gradient, of which its rows count and not what lies between them.
+static kfac_status check_written(const LossRows& a, kfac_dtype dtype, std::initializer_list<Bytes> written) {
+  const int64_t size = dtype == KFAC_F32 ? 4 : 2, pitch = a.ld_grad * size, width = a.vocab * size;
+  const uintptr_t d = reinterpret_cast<uintptr_t>(a.dlogits);
+  for (auto x = written.begin(); x != written.end(); ++x) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(x->p), e = b + x->n;
+    if (!b || !x->n) continue;
+    for (auto y = written.begin(); y != x; ++y) {
+      const uintptr_t o = reinterpret_cast<uintptr_t>(y->p);
+      if (o && y->n && b < o + y->n && o < e) return fail(KFAC_ERR_INVALID, "results overlap each other or the workspace");
+    }
+    if (!d || !a.rows || e <= d) continue;
+    const uintptr_t row = b > d ? (b - d) / pitch : 0;  // the first that may hold one of its bytes, or the next
+    for (uintptr_t r = row; r < uintptr_t(a.rows) && r <= row + 1; ++r)
+      if (b < d + r * pitch + width && d + r * pitch < e)
+        return fail(KFAC_ERR_INVALID, "dlogits overlaps a result or the workspace");
+  }
+  return KFAC_OK;
+}
+
 // LAUNCH(type) for the type of a code.
 #define KFAC_BY_TYPE(dtype, LAUNCH)              \
   do {                                           \
@@ -977,6 +998,7 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
   if ((st = check_device())) return st;
   const PolicyWs w = policy_ws(workspace, rows, seqs);
   if ((st = check_workspace(workspace, ws_bytes, w.bytes))) return st;
+  if ((st = check_written(a, dtype, {{logp, 4 * int64_t(rows)}, {stats, 16}, {workspace, int64_t(w.bytes)}}))) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   PolicyArgs p = {old_logp, ref_logp, advantage, logp, clip_low, clip_high, kl_coef, grad_scale, nullptr, nullptr, nullptr, 0};
   const bool by_seq = by_sequence && seqs > 1;  // the mean over one sequence is the mean over its rows
@@ -1110,6 +1132,9 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
   if ((st = check_device())) return st;
   const PrefWs w = pref_ws(workspace, rows, pairs);
   if ((st = check_workspace(workspace, ws_bytes, w.bytes))) return st;
+  const int64_t n = pairs;
+  if ((st = check_written(a, dtype, {{seq_logp, 8 * n}, {margin, 4 * n}, {loss, 4}, {workspace, int64_t(w.bytes)}})))
+    return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const PrefArgs p = {ref_logp, seq_logp, margin, loss, beta, label_smoothing, grad_scale, pairs};
   const bool any = rows > 0 && pairs > 0;

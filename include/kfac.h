@@ -366,7 +366,8 @@ kfac_status kfac_trust_update(int32_t count, const int64_t* numel, const float* 
  * from fp32, at the pitch ld_grad >= vocab: zeros in the rows of a sequence that do not
  * count. Rows outside every sequence are left as they were, in every output. dlogits may
  * be logits with ld_grad = ld; otherwise they must not overlap. No other result may share
- * bytes with an input (old_logp and logp are two buffers), and none with another result. A call
+ * bytes with an input (old_logp and logp are two buffers), and none with another result or
+ * the workspace (KFAC_ERR_INVALID; what lies between the rows of dlogits is not theirs). A call
  * takes fewer than 2^22 rows (KFAC_ERR_UNSUPPORTED). A logit may be -inf;
  * +inf, NaN or a row of nothing but -inf makes that row's results NaN.
  * Results are deterministic.

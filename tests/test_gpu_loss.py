@@ -509,6 +509,60 @@ def test_two_calls_at_once(kfac_gpu):
         assert torch.equal(stats, w[0]) and torch.equal(logp, w[1]) and torch.equal(d, w[2])
 
 
+def _refused(kfac, call, **kw):
+    with pytest.raises(kfac.KfacError, match="overlap"):
+        call(**kw)
+
+
+def test_results_lie_apart_from_each_other(kfac_gpu):
+    """A result inside another one or the workspace is refused, before any launch; one between the
+    rows of the gradient is not."""
+    rows, vocab = 6, 10
+    z, token, old, adv, ref = _policy_inputs(60, rows, vocab, F32)
+    buf = torch.zeros(rows * 24 + 64, device="cuda")
+    wide = buf[:rows * 24].view(rows, 24)
+    d = wide[:, :vocab]
+
+    def policy(**kw):
+        own = dict(logp=torch.zeros(rows, device="cuda"), stats=torch.zeros(4, device="cuda"), dlogits=d)
+        kfac_gpu.kfac_policy_loss(z, token, old, adv, **{**own, **kw})
+
+    one = torch.zeros(rows + 4, device="cuda")
+    _refused(kfac_gpu, policy, logp=one[:rows], stats=one[rows - 1:rows + 3])
+    _refused(kfac_gpu, policy, stats=wide[0, 9:13])              # the last element of the first row
+    _refused(kfac_gpu, policy, stats=wide[1, :4])
+    _refused(kfac_gpu, policy, stats=buf[22:26])                 # past the first row's end, into the second
+    _refused(kfac_gpu, policy, logp=wide[rows - 1, 9:9 + rows])  # the last element of all
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    _refused(kfac_gpu, policy, stats=ws[1024:1040].view(F32), workspace=ws)
+    _refused(kfac_gpu, policy, workspace=ws, dlogits=ws[512:512 + rows * vocab * 4].view(F32).view(rows, vocab))
+    assert not buf.any() and not one.any() and not ws.any()
+    want = _policy(kfac_gpu, z, token, old, adv)
+    for at in (10, 20):                                          # right behind a row, right before the next
+        policy(stats=wide[2, at:at + 4])
+        assert torch.equal(wide[2, at:at + 4], want[0]) and torch.equal(d, want[2])
+    policy(logp=wide[rows - 1, 10:10 + rows])
+    assert torch.equal(wide[rows - 1, 10:10 + rows], want[1]) and torch.equal(d, want[2])
+    begin = _offsets(0, 2, 6)
+    buf.zero_()
+
+    def prefer(**kw):
+        own = dict(seq_logp=torch.zeros(2, device="cuda"), margin=torch.zeros(1, device="cuda"),
+                   loss=torch.zeros(1, device="cuda"), dlogits=d)
+        kfac_gpu.kfac_preference_loss(z, token, begin, **{**own, **kw})
+
+    _refused(kfac_gpu, prefer, seq_logp=one[:2], margin=one[1:2])
+    _refused(kfac_gpu, prefer, margin=one[:1], loss=one[:1])
+    _refused(kfac_gpu, prefer, loss=wide[3, 2:3])
+    _refused(kfac_gpu, prefer, seq_logp=wide[3, 9:11])
+    _refused(kfac_gpu, prefer, loss=ws[:4].view(F32), workspace=ws)
+    assert not buf.any() and not one.any()
+    prefer(seq_logp=one[:2], margin=one[2:3], loss=wide[0, 10:11])
+    torch.cuda.synchronize()
+    got = _prefer(kfac_gpu, z, token, begin)
+    assert torch.equal(wide[0, 10:11], got[0]) and torch.equal(one[2:3], got[1]) and torch.equal(d, got[3])
+
+
 def test_bounds_are_the_types_own():
     for t in (F32, F16, BF16):
         assert HALF_STEP[t] == torch.finfo(t).eps / 2
