@@ -1058,8 +1058,13 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
 }
 
 // Up to here the gradient's blocks wait less for their sums than the launch of pref_pairs_kernel takes
-// (1000 rows of 1000 in fp32: 14.6 against 16.8 us; 300 of 32000: 25.2 against 23.5).
+// (1000 rows of 1000 in fp32: 14.6 against 16.8 us; 300 of 32000: 25.2 against 23.5). Each row's wave adds up
+// its whole pair, however the pairs share the rows, so their number is bounded too: rows of 2 to 100
+// elements in one pair take 12.6 against 15.7 us at 2000 rows, 13.7 against 15.7 at 3000, 17.3 against 16.5 at
+// 4000, 55 against 18 at 10000; in 16 pairs of which one has nearly all rows 15.0 against 16.0 at 3000, 18.6
+// against 18.6 at 4000, 57 against 32 at 10000.
 constexpr int64_t ALONE_BYTES = int64_t(8) << 20;
+constexpr int ALONE_ROWS = 3000;
 
 struct PrefWs {
   RowStat* stat;
@@ -1151,7 +1156,8 @@ extern "C" kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dt
   }
   // A small call with few pairs: the gradient's blocks form their own coefficients, each from the l of
   // one pair, and one of them the pairs' results.
-  const bool alone = any && dlogits && pairs <= 16 && row_bytes(rows, vocab, dtype) <= ALONE_BYTES;
+  const bool alone =
+      any && dlogits && pairs <= 16 && rows <= ALONE_ROWS && row_bytes(rows, vocab, dtype) <= ALONE_BYTES;
   int parts = 0;  // of the loss, where several blocks have a share each
   if (!alone) {
     const int blocks = pair_blocks(rows, pairs);

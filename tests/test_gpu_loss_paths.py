@@ -377,3 +377,29 @@ def test_policy_a_token_without_probability(kfac_gpu, vocab):
     assert abs(logp[1] - want_l[1]) <= err + 1.01 * U * abs(want_l[1])
     assert np.abs(stats[:2] - want[:2]).max() <= 0.5 * ratio * host64(adv)[1] * err + 1.01 * U * abs(want[1])
     assert stats[3] == np.float32(want[3])
+
+
+def _launches(kfac, call):
+    """Kernel launches of a call by name."""
+    kfac.kfac_timing_reset()
+    kfac.kfac_timing_enable(True)
+    try:
+        call()
+    finally:
+        kfac.kfac_timing_enable(False)
+    counts = {kfac.kfac_kernel_name(i): kfac.kfac_timing_read(i)[1] for i in range(kfac.kfac_timing_kernels())}
+    kfac.kfac_timing_reset()
+    return {k: n for k, n in counts.items() if n}
+
+
+@pytest.mark.parametrize("rows,vocab,pairs,own", [(3000, 64, 1, True), (3001, 64, 1, False), (20000, 100, 1, False),
+                                                  (3001, 2, 16, False), (65536, 16, 4, False), (1000, 1000, 4, True)])
+def test_rows_that_form_their_own_coefficient(kfac_gpu, rows, vocab, pairs, own):
+    """A row's wave adds up its whole pair, which is quadratic in the rows: above 3000 of them, however few
+    bytes they have, each sequence is added up once, by a kernel of its own."""
+    z, token, g = logits(rows + pairs, rows, vocab, F32 if rows * vocab < 1 << 21 else BF16, std=1.0)
+    begin = _offsets(*[rows * i // (2 * pairs) for i in range(2 * pairs)], rows)
+    got = []
+    launched = _launches(kfac_gpu, lambda: got.extend(_prefer(kfac_gpu, z, token, begin, beta=1e-3, grad_scale=float(rows))))
+    assert ("pref_pairs_kernel" in launched) != own and launched["pref_grad_kernel"] == 1
+    _check_prefer(got, z, token, begin, beta=1e-3, grad_scale=float(rows))
