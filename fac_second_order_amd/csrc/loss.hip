@@ -916,6 +916,9 @@ static int count_slices(int32_t rows, int32_t seqs, bool by_seq) {
   return n < 1 ? 1 : n > most ? static_cast<int>(most) : static_cast<int>(n);
 }
 
+// Steps over counts that the rows of a call by sequence take for themselves.
+constexpr int64_t OWN_STEPS = 200000;
+
 // Rows of more groups than this are cut into parts where they are few: one row of 131072 bf16 takes
 // 11.9 us against 20.4 whole, 16 rows of 32000 25.1 against 27.5 when the caller waits, 64 rows of 131072
 // 18.4 against 24.0; at 9000 elements, 1125 groups, both take the same.
@@ -1031,9 +1034,13 @@ extern "C" kfac_status kfac_policy_loss(int32_t rows, int32_t vocab, kfac_dtype 
     KFAC_LAUNCH(K_LOSS_COUNT, loss_count_kernel, dim3(by_seq ? seqs : 1, p.slices), dim3(LT), 0, s, a,
                 by_seq ? w.row_seq : nullptr, w.count);
     KFAC_CHECK_LAUNCH("loss_count_kernel");
-    // A wave looks for a row's sequences itself, or many are counted before: 300 sequences over 8192 rows
-    // of 1000 take 22.1 us without this launch and 23.2 with it, 2000 sequences 26.7 and 24.6.
-    if (by_seq && seqs > 1024) {
+    // A wave looks for the sequences that hold its row's weight itself, `steps` counts behind one another, or they
+    // are counted before: 300 sequences over 8192 rows of 1000 take 22.1 us without this launch and 23.2 with
+    // it, 2000 sequences 26.7 and 24.6. Every row repeats the steps: rows of 64 bf16 take 28.4 us without it and
+    // 29.5 with it at 20000 rows in 16 sequences (4 steps), 35.3 and 29.0 in 1000 (16 steps), 72.2 and 66.0 at 60000
+    // rows in two (16 steps), 3657 and 894 at 10^6 in 300 (65 steps).
+    const int64_t steps = int64_t((seqs + 63) / 64) * p.slices;
+    if (by_seq && (seqs > 1024 || rows * steps > OWN_STEPS)) {
       p.nonempty = w.nonempty;
       KFAC_LAUNCH(K_LOSS_NONEMPTY, loss_nonempty_kernel, dim3(1), dim3(ONE), 0, s, w.count, seqs, p.slices, w.nonempty);
       KFAC_CHECK_LAUNCH("loss_nonempty_kernel");

@@ -403,3 +403,29 @@ def test_rows_that_form_their_own_coefficient(kfac_gpu, rows, vocab, pairs, own)
     launched = _launches(kfac_gpu, lambda: got.extend(_prefer(kfac_gpu, z, token, begin, beta=1e-3, grad_scale=float(rows))))
     assert ("pref_pairs_kernel" in launched) != own and launched["pref_grad_kernel"] == 1
     _check_prefer(got, z, token, begin, beta=1e-3, grad_scale=float(rows))
+
+
+@pytest.mark.parametrize("rows,seqs,own", [(12500, 2, True), (12501, 2, False), (12500, 1000, True), (12501, 1000, False),
+                                           (40000, 300, True), (40001, 300, False), (100000, 16, False)])
+def test_rows_that_count_the_sequences(kfac_gpu, rows, seqs, own):
+    """Every row's wave looks through the counts of all sequences, up to 200000 steps of 64 of them over all
+    rows; beyond that they are counted once. Slices of a sequence count each: 16 at 12500 rows in two."""
+    vocab = 5
+    z, token, g = logits(rows + seqs, rows, vocab, F32)
+    cuts = [rows * i // seqs for i in range(seqs)] + [rows]
+    cuts[1] = cuts[0]                                         # an empty one
+    begin = _offsets(*cuts)
+    l = torch.log_softmax(z.double(), 1).gather(1, token[:, None])[:, 0]
+    got = []
+    launched = _launches(kfac_gpu, lambda: got.extend(_policy(kfac_gpu, z, token, l.float(), torch.ones_like(l).float(),
+                                                               begin=begin, by_sequence=True, grad_scale=float(rows))))
+    assert ("loss_nonempty_kernel" in launched) != own
+    # ratios of 1 and advantages of 1: the rows' weights, which add up to 1, are the slopes
+    lengths = np.diff(cuts)
+    weight = np.repeat(1.0 / ((lengths > 0).sum() * np.maximum(lengths, 1)), lengths)
+    stats, logp, d = got
+    err = row_errors(host64(z)).max() + U * float(l.abs().max())
+    assert abs(float(stats[1]) + 1.0) <= 2 * err + U
+    want = (z.double().softmax(1) - torch.nn.functional.one_hot(token, vocab)) * torch.from_numpy(weight * rows).cuda()[:, None]
+    bound = torch.from_numpy(weight * rows).cuda()[:, None] * (4 * err + 6 * U)
+    assert ((d.double() - want).abs() <= bound).all()
