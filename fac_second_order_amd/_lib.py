@@ -376,6 +376,7 @@ def _on_device(tensors, what):
 
 def _listed(tensors, what):
     """(numel, dtype code, addresses) of contiguous tensors on the current device."""
+    tensors = list(tensors)  # looked through several times: a generator would be empty after the first
     _on_device(tensors, what)
     if not all(map(torch.Tensor.is_contiguous, tensors)):
         raise TypeError(f"{what} must be contiguous")

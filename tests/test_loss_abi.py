@@ -283,6 +283,18 @@ def test_binding_checks(anywhere):
             L.kfac_preference_loss(**{**fine, **bad})
 
 
+def test_tensors_of_a_generator_are_looked_at(anywhere):
+    """Tensors may come from anything that is iterable: none gets lost to the first look."""
+    L = anywhere
+    bad = [torch.zeros(4, dtype=torch.float64)]
+    one = torch.zeros(1)
+    with pytest.raises(TypeError, match="dtype"):
+        L.kfac_grad_norm((t for t in bad), one)
+    with pytest.raises(TypeError, match="dtype"):
+        L.kfac_grad_clip((t for t in bad), (t for t in bad), 1.0, one)
+    assert L._listed((t for t in [torch.zeros(3), torch.zeros(5)]), "grad")[0] == [3, 5]
+
+
 def test_a_workspace_smaller_than_its_alignment_has_no_bytes(lib):
     """The bytes behind the aligned address of a tiny workspace are none, not a wrapped count."""
     big = torch.zeros(600, dtype=torch.uint8)
