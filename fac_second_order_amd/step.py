@@ -27,6 +27,13 @@ def side_split(n_all, min_order=1024):
     return long_
 
 
+def _bound(v, what):
+    """v, None or a number whose float32 is positive and finite."""
+    if v is not None and not 0.0 < float(torch.tensor(float(v), dtype=torch.float32)) < math.inf:
+        raise ValueError(f"{what} must be positive and finite")
+    return v
+
+
 class KfacStep:
     """Buffers for `layers` (objects with the kfac_layer fields) and `bn_layers`
     (objects with n, hw, c). Tikhonov damping gamma puts sqrt(gamma) on each
@@ -85,7 +92,8 @@ class KfacStep:
         self.out = [torch.empty(g, a, dtype=f32, device=dev) for g, a in zip(self.d_g, self.d_a)]
         self.refine = bool(refine_inverse)
         self.factor_full = [torch.empty(d, d, dtype=f32, device=dev) for d in self.n_all] if self.refine else []
-        self.max_grad_norm, self.trust_radius = max_grad_norm, trust_radius
+        self.max_grad_norm = _bound(max_grad_norm, "max_grad_norm")
+        self.trust_radius = _bound(trust_radius, "trust_radius")
         self.grad_norm = self.trust = None
         self.clipped = []
         if max_grad_norm is not None:
@@ -277,6 +285,9 @@ class KfacStep:
         kept, the gradients are preconditioned with them, and BN divides its fresh
         gradient by the stored Fisher (decay 1 keeps it). Given weights and/or
         bn_params, those are updated in place with learning rate lr."""
+        # refused here, before the factors and the Fisher have taken the batch in
+        if self.trust_radius is not None and not 0.0 <= lr < math.inf:
+            raise ValueError("lr must be finite and >= 0")
         grads = self.clip(grads, stream)
         if self.trust_radius is not None:
             self._step(act, gout, grads, xhat, bn_gout, ema_decay, refresh, None, None, lr, stream)

@@ -1,5 +1,7 @@
 """Host logic of KfacStep's two-stream schedule (no GPU): which inverses go to the
-second stream, and the groups of layers of the caller's stream's calls."""
+second stream, and the groups of layers of the caller's stream's calls; the bounds it refuses."""
+import pytest
+
 import synth
 from fac_second_order_amd.step import KfacStep, side_split
 
@@ -42,3 +44,26 @@ def test_main_stream_call_groups():
                 share = sum(cost(i) for i in idx) / parts
                 assert all(sum(cost(i) for i in g) <= share + max(cost(i) for i in g) for g in groups)
     assert len(KfacStep._groups(list(range(10)), lambda i: 1.0, 4)) == 4
+
+
+SMALL = [synth.Layer("fc", 4, 1, 1, 6, 1, 1, 3, 1, 1, 1, 1, 0, 0, 1)]
+
+
+@pytest.mark.parametrize("bad", [0.0, -1.0, float("inf"), float("nan"), 1e-60, 1e39])
+def test_bounds_are_refused_before_a_step(bad):
+    for kw in (dict(max_grad_norm=bad), dict(trust_radius=bad)):
+        with pytest.raises(ValueError, match="positive and finite"):
+            KfacStep(SMALL, device="cpu", **kw)
+
+
+@pytest.mark.parametrize("lr", [-0.1, float("inf"), float("nan")])
+def test_a_rate_is_refused_before_anything_is_done(lr, monkeypatch):
+    st = KfacStep(SMALL, device="cpu", max_grad_norm=1.0, trust_radius=1.0)
+    done = []
+    for name in ("clip", "_step", "_bounded_update"):
+        monkeypatch.setattr(st, name, lambda *a, name=name: done.append(name))
+    with pytest.raises(ValueError, match="lr"):
+        st.step([], [], [], lr=lr)
+    assert not done
+    st.step([], [], [], lr=0.1)
+    assert done == ["clip", "_step", "_bounded_update"]
