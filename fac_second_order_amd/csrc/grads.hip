@@ -138,9 +138,16 @@ __device__ inline void add_squares(const NormDesc& d, int64_t e0, int n, double&
   });
 }
 
+// What the second pass multiplies by, in two factors: their product may be too small for a float, as
+// of a norm near the largest one, while its products with the gradients are not.
+struct Factor {
+  float f, pre;  // pre is 1 or a power of two
+};
+
 // out = coef * grad, coef in fp32, the product rounded once to the type of out.
 template <int SIZE, int NT>
-__device__ inline void scale_part(const ClipDesc& d, int64_t e0, int n, float coef) {
+__device__ inline void scale_part(const ClipDesc& d, int64_t e0, int n, Factor c) {
+  const auto times = [c](float g) { return g * c.pre * c.f; };
   with_type(d.type(), [&](auto tag) {
     using T = decltype(tag);
     const KG T* g = gp(static_cast<const T*>(d.grad)) + e0;
@@ -156,10 +163,10 @@ __device__ inline void scale_part(const ClipDesc& d, int64_t e0, int n, float co
           [&](int i, int u) {
             W w;
 #pragma unroll
-            for (int k = 0; k < EV; ++k) w[k] = static_cast<O>(static_cast<float>(v[u][k]) * coef);
+            for (int k = 0; k < EV; ++k) w[k] = static_cast<O>(times(static_cast<float>(v[u][k])));
             store_pack<true, O>(o + i, w);
           },
-          [&](int i) { o[i] = static_cast<O>(static_cast<float>(g[i]) * coef); });
+          [&](int i) { o[i] = static_cast<O>(times(static_cast<float>(g[i]))); });
     };
     if (d.wide()) scale(float{});
     else scale(T{});
@@ -225,7 +232,7 @@ struct WorkArgs {
 
 // The factor of the second pass from the sum; `shown` writes the results.
 template <int W>
-__device__ inline float factor(double sum, const WorkArgs& k, bool shown) {
+__device__ inline Factor factor(double sum, const WorkArgs& k, bool shown) {
   if constexpr (W == TRUST) {
     const float q = static_cast<float>(sum);
     float step = 0.f;  // a q that is no finite float: no update, and q shows why
@@ -234,13 +241,15 @@ __device__ inline float factor(double sum, const WorkArgs& k, bool shown) {
       gp(k.result)[0] = step;
       gp(k.result)[1] = q;
     }
-    return step;
+    return {step, 1.f};
   } else {
     const double root = sqrt(sum);
     const float norm = static_cast<float>(root);
     if (shown) gp(k.result)[0] = norm;
     // a norm that is no finite float: the gradients as they are
-    return W == CLIP && norm > k.a && norm <= 3.402823466e38f ? static_cast<float>(k.a / root) : 1.f;
+    if (W != CLIP || !(norm > k.a && norm <= 3.402823466e38f)) return {1.f, 1.f};
+    const double c = k.a / root;
+    return c >= 0x1p-126 ? Factor{static_cast<float>(c), 1.f} : Factor{static_cast<float>(c * 0x1p126), 0x1p-126f};
   }
 }
 
@@ -250,11 +259,11 @@ __device__ inline void sum_unit(const D& d, int64_t e0, int n, float shift, doub
   else add_squares<NT, LAST>(d, e0, n, acc);
 }
 template <int W, int SIZE, int NT, class D>
-__device__ inline void second_part(const D& d, int64_t e0, int n, float f) {
+__device__ inline void second_part(const D& d, int64_t e0, int n, Factor f) {
   if constexpr (W == TRUST) {
-    if (f != 0.f) apply_part<SIZE, NT>(d, e0, n, f);
+    if (f.f != 0.f) apply_part<SIZE, NT>(d, e0, n, f.f);
   } else if constexpr (W == CLIP) {
-    if (f != 1.f || d.out != d.grad) scale_part<SIZE, NT>(d, e0, n, f);
+    if (f.f != 1.f || d.out != d.grad) scale_part<SIZE, NT>(d, e0, n, f);
   }
 }
 
@@ -290,11 +299,11 @@ __global__ void __launch_bounds__(GT) grads_sum_kernel(TB tb, int count, int uni
 
 template <int W>
 __global__ void __launch_bounds__(GT) grads_factor_kernel(const double* __restrict__ partial, int n, WorkArgs k,
-                                                          float* __restrict__ out) {
+                                                          Factor* __restrict__ out) {
   __shared__ double s[GT / 64];
   double v = 0;
   for (int i = threadIdx.x; i < n; i += GT) v += gp(partial)[i];
-  const float f = factor<W>(block_sum<GT>(v, s), k, threadIdx.x == 0);
+  const Factor f = factor<W>(block_sum<GT>(v, s), k, threadIdx.x == 0);
   if (threadIdx.x == 0) out[0] = f;
 }
 
@@ -305,7 +314,7 @@ __global__ void __launch_bounds__(GT) grads_factor_kernel(const double* __restri
 constexpr int PARTS = UNIT / PART;
 template <int W, class TB>
 __global__ void __launch_bounds__(GT) grads_apply_kernel(TB tb, int count, int64_t end,
-                                                         const float* __restrict__ f) {
+                                                         const Factor* __restrict__ f) {
   const int64_t at = end - 1 - blockIdx.x;
   const int c = static_cast<int>(at / PARTS);
   const int p = find_tensor(tb, count, c);
@@ -326,7 +335,7 @@ __global__ void __launch_bounds__(ONE_THREADS) grads_one_kernel(InlineTables<Des
     for (int64_t e0 = 0; e0 < d.numel(); e0 += UNIT)
       sum_unit<W, ONE_THREADS, false>(d, e0, static_cast<int>(min(d.numel() - e0, int64_t(UNIT))), k.shift, acc);
   }
-  const float f = factor<W>(block_sum<ONE_THREADS>(acc, s), k, threadIdx.x == 0);
+  const Factor f = factor<W>(block_sum<ONE_THREADS>(acc, s), k, threadIdx.x == 0);
   if constexpr (W != NORM)
     for (int p = 0; p < count; ++p) {
       const auto d = tb.desc[p];
@@ -432,7 +441,7 @@ constexpr int ONE_UNITS = 16;
 constexpr int64_t CACHE_BYTES = int64_t(256) << 20;
 
 template <int W, class TB>
-static kfac_status launch_passes(const TB& tb, const GradCall& call, const WorkArgs& k, double* partial, float* f,
+static kfac_status launch_passes(const TB& tb, const GradCall& call, const WorkArgs& k, double* partial, Factor* f,
                                  hipStream_t s) {
   const int n = static_cast<int>(call.desc.size()), blocks = std::max(1, std::min(call.units, MAX_BLOCKS));
   constexpr int S = W == CLIP ? NORM : W;  // the same sum
@@ -469,7 +478,7 @@ static kfac_status launch_grads(const GradCall& call, int32_t count, const WorkA
   D* desc = cv.take<D>(count);
   int32_t* begin = cv.take<int32_t>(count);
   double* partial = cv.take<double>(MAX_BLOCKS);
-  float* f = cv.take<float>(1);
+  Factor* f = cv.take<Factor>(1);
   if (n <= InlineTables<D>::most) {
     InlineTables<D> tb;
     std::copy(call.desc.begin(), call.desc.end(), tb.desc);

@@ -118,6 +118,20 @@ def test_clip_leaves_what_is_not_finite(kfac_gpu, bad):
     assert norm == math.inf and torch.equal(outs[0], huge[0])
 
 
+@pytest.mark.parametrize("dtypes", [[F32], [BF16], [F32, BF16]])
+@pytest.mark.parametrize("n,scale", [(1000, 5e36), (70001, 5e35)])
+@pytest.mark.parametrize("max_norm", [1e-3, 1e-9, 1e-30])
+@pytest.mark.parametrize("widen", [False, True])
+def test_clip_by_a_factor_below_the_smallest_float(kfac_gpu, dtypes, n, scale, max_norm, widen):
+    """A norm of 1e38 and a small bound: their quotient is no normal float (6e-42, with 12 bits) or none at
+    all, the clipped gradients are ordinary numbers."""
+    grads = _tensors(6, [n] * len(dtypes), dtypes, scale=scale)
+    outs, norm = _clip(kfac_gpu, grads, max_norm, widen)
+    assert math.isfinite(norm) and max_norm / norm < 2.0 ** -126
+    _check_clip(outs, norm, grads, max_norm)
+    assert all(o.any() for o in outs)
+
+
 def test_norm_past_32_bit_offsets(kfac_gpu):
     """One tensor of more than 2^31 elements and 2^32 bytes, values at its ends and about 2^31."""
     n = (1 << 31) + 70001
