@@ -210,6 +210,9 @@ class KfacCapture:
     # geometry and parameter layouts -------------------------------------------
     def _geometry(self):
         layers = []
+        for a, g in (*zip(self.act, self.gout), *zip(self.xhat, self.bgout)):
+            if a.shape[0] != g.shape[0]:
+                raise RuntimeError("the last forward and the last backward pass are of different batches")
         for (m, _), a, g in zip(self.pairs, self.act, self.gout):
             if isinstance(m, nn.Conv2d):
                 n, h, w, c_in = a.shape
@@ -288,8 +291,8 @@ class KfacCapture:
         if any(a is None for a in self.act) or any(g is None for g in self.gout):
             raise RuntimeError("step() needs one forward and backward pass with the hooks in place")
         dev = self.act[0].device
+        layers, bns = self._geometry()
         if self.kstep is None:
-            layers, bns = self._geometry()
             self.kstep = KfacStep(layers, bns, dev, damping=self.damping, precond_accum=self.precond_accum,
                                   refine_inverse=self.refine_inverse, max_grad_norm=self.max_grad_norm,
                                   trust_radius=self.trust_radius)
@@ -300,7 +303,7 @@ class KfacCapture:
         refresh = self.calls % self.refresh_every == 0
         decay = 0.0 if self.calls == 0 else self.ema_decay
         self.kstep.step(self.act, self.gout, grads, self.xhat, self.bgout, ema_decay=decay, refresh=refresh,
-                        weights=self.master, bn_params=self.bn_master, lr=lr)
+                        weights=self.master, bn_params=self.bn_master, lr=lr, layers=layers, bn_layers=bns)
         self.calls += 1
         for (m, _), mat in zip(self.pairs, self.master):
             self._from_matrix(m, mat)

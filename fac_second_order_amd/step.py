@@ -34,6 +34,16 @@ def _bound(v, what):
     return v
 
 
+def _same_but_samples(given, made, fields, what):
+    """`given`, layers that differ from `made` in n alone; `made` where it is None."""
+    if given is None:
+        return made
+    names = [f for f, _ in fields if f != "n"]
+    if len(given) != len(made) or any(getattr(a, f) != getattr(b, f) for a, b in zip(given, made) for f in names):
+        raise ValueError(f"{what} may differ in n alone from those the step was made for")
+    return given
+
+
 class KfacStep:
     """Buffers for `layers` (objects with the kfac_layer fields) and `bn_layers`
     (objects with n, hw, c). Tikhonov damping gamma puts sqrt(gamma) on each
@@ -103,8 +113,8 @@ class KfacStep:
             self.trust = torch.zeros(2, dtype=f32, device=dev)
         self.fisher = [torch.zeros(2, b.c, dtype=f32, device=dev) for b in self.bn_layers]
         self.bn_pre = [torch.empty(2, b.c, dtype=f32, device=dev) for b in self.bn_layers]
-        code = K.KFAC_F16 if in_dtype == torch.float16 else K.KFAC_F32
-        sizes = [K.kfac_factors_workspace(self.layers, code),
+        self.in_code = K.KFAC_F16 if in_dtype == torch.float16 else K.KFAC_F32
+        sizes = [K.kfac_factors_workspace(self.layers, self.in_code),
                  K.kfac_pack_sym_workspace(self.n_all),
                  K.kfac_invert_workspace(self.n_all),
                  K.kfac_precondition_workspace(self.d_g, self.d_a)]
@@ -149,11 +159,22 @@ class KfacStep:
         K.kfac_factors(self.layers, act, gout, self.A_packed, self.G_packed, ema_decay,
                        self.workspace, stream)
 
-    def _factors_full(self, act, gout, ema_decay, stream):
+    def _make_room(self, layers, bn_layers, stream):
+        """A workspace that also serves these layers, where they are not those of the step."""
+        need = 0 if layers is self.layers else K.kfac_factors_workspace(layers, self.in_code)
+        if bn_layers is not self.bn_layers and bn_layers:
+            need = max(need, K.kfac_bn_diag_workspace(bn_layers))
+        if self.workspace.numel() < need + 256:
+            on = torch.cuda.current_stream(self.device) if stream is None else stream
+            self.workspace.record_stream(on)  # calls in flight there use the old one
+            with torch.cuda.stream(on):
+                self.workspace = torch.empty(need + 256, dtype=torch.uint8, device=self.device)
+
+    def _factors_full(self, layers, act, gout, ema_decay, stream):
         # the packed factors (the stored state) and the upper triangles that kfac_invert
         # reads, from the same kernels: no separate unpack pass
         L = len(self.layers)
-        K.kfac_factors_full(self.layers, act, gout, self.A_packed, self.G_packed, self.full[:L], self.full[L:],
+        K.kfac_factors_full(layers, act, gout, self.A_packed, self.G_packed, self.full[:L], self.full[L:],
                             ema_decay, self.workspace, stream)
 
     # With the second stream, the caller's stream forms its factors in 2 calls,
@@ -247,17 +268,17 @@ class KfacStep:
     def bn(self, xhat, bn_gout, ema_decay=0.0, bn_params=None, lr=0.0, stream=None):
         """BN Fisher and preconditioned gradients; with bn_params (fp32 [2, c]: gamma,
         beta) also bn_params -= lr * self.bn_pre."""
-        self._bn(list(range(len(self.bn_layers))), xhat, bn_gout, ema_decay, bn_params, lr, stream)
+        self._bn(list(range(len(self.bn_layers))), self.bn_layers, xhat, bn_gout, ema_decay, bn_params, lr, stream)
 
-    def _bn(self, idx, xhat, bn_gout, ema_decay, bn_params, lr, stream):
+    def _bn(self, idx, bn_layers, xhat, bn_gout, ema_decay, bn_params, lr, stream):
         if not idx:
             return
         sub = self._sub
         if bn_params is None:
-            K.kfac_bn_diag(sub(self.bn_layers, idx), sub(xhat, idx), sub(bn_gout, idx), sub(self.fisher, idx),
+            K.kfac_bn_diag(sub(bn_layers, idx), sub(xhat, idx), sub(bn_gout, idx), sub(self.fisher, idx),
                            sub(self.bn_pre, idx), ema_decay, self.bn_shift, self.workspace, stream)
         else:
-            K.kfac_bn_update(sub(self.bn_layers, idx), sub(xhat, idx), sub(bn_gout, idx), sub(self.fisher, idx),
+            K.kfac_bn_update(sub(bn_layers, idx), sub(xhat, idx), sub(bn_gout, idx), sub(self.fisher, idx),
                              sub(self.bn_pre, idx), sub(bn_params, idx), lr, ema_decay, self.bn_shift,
                              self.workspace, stream)
 
@@ -280,32 +301,39 @@ class KfacStep:
         K.kfac_trust_update(P, g, w, lr, self.trust_radius, self.trust, fisher, self.bn_shift, self.workspace, stream)
 
     def step(self, act, gout, grads, xhat=(), bn_gout=(), ema_decay=0.0, refresh=True,
-             weights=None, bn_params=None, lr=0.0, stream=None):
+             weights=None, bn_params=None, lr=0.0, stream=None, layers=None, bn_layers=None):
         """One step. refresh=False is a stale-curvature step: factors and inverses are
         kept, the gradients are preconditioned with them, and BN divides its fresh
         gradient by the stored Fisher (decay 1 keeps it). Given weights and/or
-        bn_params, those are updated in place with learning rate lr."""
+        bn_params, those are updated in place with learning rate lr. layers, bn_layers:
+        those of this call where its tensors have another number of samples, n."""
         # refused here, before the factors and the Fisher have taken the batch in
         if self.trust_radius is not None and not 0.0 <= lr < math.inf:
             raise ValueError("lr must be finite and >= 0")
+        layers = _same_but_samples(layers, self.layers, K.kfac_layer._fields_, "layers")
+        bn_layers = _same_but_samples(bn_layers, self.bn_layers, K.kfac_bn._fields_, "bn_layers")
+        self._make_room(layers, bn_layers, stream)
         grads = self.clip(grads, stream)
+        args = (layers, bn_layers, act, gout, grads, xhat, bn_gout, ema_decay, refresh)
         if self.trust_radius is not None:
-            self._step(act, gout, grads, xhat, bn_gout, ema_decay, refresh, None, None, lr, stream)
+            self._step(*args, None, None, lr, stream)
             self._bounded_update(grads, weights, bn_params, lr, stream)
         else:
-            self._step(act, gout, grads, xhat, bn_gout, ema_decay, refresh, weights, bn_params, lr, stream)
+            self._step(*args, weights, bn_params, lr, stream)
 
-    def _step(self, act, gout, grads, xhat, bn_gout, ema_decay, refresh, weights, bn_params, lr, stream):
+    def _step(self, layers, bn_layers, act, gout, grads, xhat, bn_gout, ema_decay, refresh, weights, bn_params, lr,
+              stream):
+        all_bn = list(range(len(bn_layers)))
         if not refresh:
             self.precondition(grads, weights, lr, stream)
-            self.bn(xhat, bn_gout, 1.0, bn_params, lr, stream)
+            self._bn(all_bn, bn_layers, xhat, bn_gout, 1.0, bn_params, lr, stream)
             return
         if not self.side:
-            self._factors_full(act, gout, ema_decay, stream)
+            self._factors_full(layers, act, gout, ema_decay, stream)
             self._invert(self.main, self._info_main, self.workspace, stream)
             self._refine(stream)
             self.precondition(grads, weights, lr, stream)
-            self.bn(xhat, bn_gout, ema_decay, bn_params, lr, stream)
+            self._bn(all_bn, bn_layers, xhat, bn_gout, ema_decay, bn_params, lr, stream)
             return
         main = torch.cuda.current_stream(self.device) if stream is None else stream
         side = self.stream2
@@ -313,7 +341,7 @@ class KfacStep:
         # factors are formed (a factor call plans its row splits over every layer,
         # whichever inputs it is given: the same bits as one call)
         first, rest = self._factor_inputs(act, gout)
-        self._factors_full(first[0], first[1], ema_decay, main)
+        self._factors_full(layers, first[0], first[1], ema_decay, main)
         formed = torch.cuda.Event()
         formed.record(main)
         side.wait_event(formed)
@@ -322,8 +350,9 @@ class KfacStep:
             lay = [l for l in range(len(self.layers)) if rest[0][l] is not None or rest[1][l] is not None]
             for part in self._groups(lay, self._factor_cost, self.MAIN_CALLS["factors"]):
                 ps = set(part)
-                self._factors_full([a if l in ps else None for l, a in enumerate(rest[0])],
-                                   [g if l in ps else None for l, g in enumerate(rest[1])], ema_decay, main)
+                self._factors_full(layers, [a if l in ps else None for l, a in enumerate(rest[0])],
+                                   [g if l in ps else None for l, g in enumerate(rest[1])], ema_decay,
+                                   main)
             self._invert(self.main, self._info_main, self.workspace, main)
             main_inverses = torch.cuda.Event()
             main_inverses.record(main)
@@ -331,8 +360,8 @@ class KfacStep:
             for part in self._groups(self.main_layers, pcost, self.MAIN_CALLS["precondition"]):
                 self._precondition(part, grads, weights, lr, self.workspace, main)
             bcost = lambda b: self.bn_layers[b].n * self.bn_layers[b].hw * self.bn_layers[b].c  # noqa: E731
-            for part in self._groups(list(range(len(self.bn_layers))), bcost, self.MAIN_CALLS["bn"]):
-                self._bn(part, xhat, bn_gout, ema_decay, bn_params, lr, main)
+            for part in self._groups(all_bn, bcost, self.MAIN_CALLS["bn"]):
+                self._bn(part, bn_layers, xhat, bn_gout, ema_decay, bn_params, lr, main)
             side.wait_event(main_inverses)  # the side layers' other factor
             self._precondition(self.side_layers, grads, weights, lr, self.workspace2, side)
         finally:

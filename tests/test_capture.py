@@ -60,3 +60,34 @@ def test_hooks_record_every_layer():
     p[[0, 1], [1, 7]] -= 1
     assert torch.allclose(cap.gout[-1].float(), p.half().float(), atol=2e-3)
     cap.remove()
+
+
+class Recorder:
+    """Stands in for KfacStep: what a step was given."""
+
+    def __init__(self, layers, bns, dev, **kw):
+        self.made, self.options, self.calls = (layers, bns), kw, []
+
+    def step(self, *args, **kw):
+        self.calls.append((args, kw))
+
+
+def test_a_batch_of_another_size_has_its_own_geometry(monkeypatch):
+    """The step of a smaller or larger batch names that many samples: the library reads what the
+    tensors hold. A backward pass that is missing is refused."""
+    monkeypatch.setattr(cap_mod, "KfacStep", Recorder)
+    torch.manual_seed(4)
+    model = cap_mod.ResNet50(classes=10).to(memory_format=torch.channels_last)
+    cap = cap_mod.KfacCapture(model)
+    for n in (3, 2, 4):
+        F.cross_entropy(model(torch.randn(n, 3, 32, 32)), torch.arange(n)).backward()
+        cap.step(0.1)
+        (act, gout, grads, xhat, bgout), kw = cap.kstep.calls[-1]
+        for L, a, g in zip(kw["layers"], act, gout):
+            assert L.n == n == a.shape[0] == g.shape[0]
+        for B, x, g in zip(kw["bn_layers"], xhat, bgout):
+            assert B.n == n == x.shape[0] == g.shape[0]
+    model(torch.randn(3, 3, 32, 32))
+    with pytest.raises(RuntimeError, match="batches"):
+        cap.step(0.1)
+    cap.remove()

@@ -1,6 +1,7 @@
 """The losses, the clipping and the bounded update as a K-FAC step uses them: KfacStep with
 max_grad_norm and trust_radius, and a policy trained through KfacCapture from the loss over
 its logits to the bounded update of its weights."""
+import dataclasses
 import math
 
 import numpy as np
@@ -105,6 +106,49 @@ def test_step_on_another_stream(kfac_gpu):
         torch.cuda.synchronize()
         got.append(w + p + [st.trust, st.grad_norm])
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("side_stream", [True, False])
+@pytest.mark.parametrize("samples", [1, 2, 5])
+def test_step_of_fewer_and_of_more_samples(kfac_gpu, side_stream, samples):
+    """A step made for one batch size takes another: the bits of a step made for that one."""
+    layers = [dataclasses.replace(l, n=samples) for l in LAYERS]
+    bns = [dataclasses.replace(b, n=samples) for b in BNS]
+    rng = synth.layer_rng(79, 0)
+    to = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    ins = dict(act=[to(synth.relu_normal_f16(rng, l.act_shape)) for l in layers],
+               gout=[to(synth.normal_f16(rng, l.gout_shape, 0.1)) for l in layers],
+               grads=[to(synth.normal_f32(rng, (l.d_g, l.d_a), 0.1)) for l in layers],
+               xhat=[to(synth.normal_f16(rng, b.shape)) for b in bns],
+               bn_gout=[to(synth.normal_f16(rng, b.shape)) for b in bns])
+    got = []
+    for made, kw in ((layers, {}), (LAYERS, dict(layers=layers, bn_layers=bns))):
+        st = kfac_gpu.KfacStep(made, bns if not kw else BNS, "cuda", side_stream=side_stream, trust_radius=1e-3)
+        w, p = _params()
+        st.step(**ins, weights=w, bn_params=p, lr=0.2, **kw)
+        torch.cuda.synchronize()
+        got.append(st.A_packed + st.G_packed + st.fisher + st.out + st.bn_pre + w + p + [st.trust])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_step_whose_workspace_is_too_small(kfac_gpu):
+    """Many more samples than the step was made for: a larger workspace, on the call's stream."""
+    one = [synth.Layer("c3x3", 1, 8, 8, 64, 8, 8, 64, 3, 3, 1, 1, 1, 1, 1)]
+    many = [dataclasses.replace(one[0], n=200)]
+    rng = synth.layer_rng(80, 0)
+    act = torch.from_numpy(synth.relu_normal_f16(rng, many[0].act_shape)).cuda()
+    gout = torch.from_numpy(synth.normal_f16(rng, many[0].gout_shape, 0.1)).cuda()
+    grad = torch.randn(64, many[0].d_a, device="cuda")
+    want = kfac_gpu.KfacStep(many, (), "cuda")
+    st = kfac_gpu.KfacStep(one, (), "cuda")
+    assert kfac_gpu.kfac_factors_workspace(many) + 256 > st.workspace.numel()
+    want.step([act], [gout], [grad])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side, side):
+        st.step([act], [gout], [grad], layers=many, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(st.out[0], want.out[0]) and torch.equal(st.A_packed[0], want.A_packed[0])
 
 
 def _plain_policy(z, token, old, adv, ref, beta):

@@ -1,5 +1,7 @@
 """Host logic of KfacStep's two-stream schedule (no GPU): which inverses go to the
 second stream, and the groups of layers of the caller's stream's calls; the bounds it refuses."""
+import dataclasses
+
 import pytest
 
 import synth
@@ -67,3 +69,16 @@ def test_a_rate_is_refused_before_anything_is_done(lr, monkeypatch):
     assert not done
     st.step([], [], [], lr=0.1)
     assert done == ["clip", "_step", "_bounded_update"]
+
+
+def test_layers_of_a_call_differ_in_samples_alone(monkeypatch):
+    st = KfacStep(SMALL, device="cpu")
+    seen = []
+    monkeypatch.setattr(st, "_step", lambda layers, *a: seen.append(layers))
+    fewer = [dataclasses.replace(SMALL[0], n=3)]
+    st.step([], [], [], layers=fewer)
+    st.step([], [], [])
+    assert seen == [fewer, SMALL]
+    for bad in ([], fewer * 2, [dataclasses.replace(SMALL[0], c_in=7)]):
+        with pytest.raises(ValueError, match="n alone"):
+            st.step([], [], [], layers=bad)
