@@ -244,6 +244,8 @@ class KfacCapture:
         if m.bias is not None:
             m.bias.data.copy_(mat[:, -1])
             mat = mat[:, :-1]
+        elif mat.data_ptr() == m.weight.data_ptr():
+            return  # a weight whose memory has the matrix's order: _to_matrix gave it itself
         if isinstance(m, nn.Conv2d):
             c_out, c_in, kh, kw = m.weight.shape
             m.weight.data.copy_(mat.reshape(c_out, kh, kw, c_in).permute(0, 3, 1, 2))

@@ -91,3 +91,17 @@ def test_a_batch_of_another_size_has_its_own_geometry(monkeypatch):
     with pytest.raises(RuntimeError, match="batches"):
         cap.step(0.1)
     cap.remove()
+
+
+@pytest.mark.parametrize("fmt", [torch.contiguous_format, torch.channels_last])
+def test_matrix_of_a_weight_that_has_its_order(fmt):
+    """A 1x1 convolution's fp32 weight lies in memory as its matrix does, in either format: what the
+    step writes there is the weight."""
+    torch.manual_seed(5)
+    for m in (torch.nn.Conv2d(6, 4, 1, bias=False), torch.nn.Conv2d(6, 4, 3, bias=False), torch.nn.Linear(6, 4, bias=False)):
+        m = m.to(memory_format=fmt)
+        mat = cap_mod.KfacCapture._to_matrix(m)
+        mat.mul_(2.0).add_(1.0)
+        want = mat.clone()
+        cap_mod.KfacCapture._from_matrix(m, mat)
+        assert torch.equal(cap_mod.KfacCapture._to_matrix(m), want)
