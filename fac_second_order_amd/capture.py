@@ -9,7 +9,8 @@ classifier's input and output gradient, and each BatchNorm's normalised input an
 output gradient, to KfacStep in the layouts of include/kfac.h. PyTorch runs the
 network (forward, backward, loss); every K-FAC number is computed by libkfac. For a
 policy, whose rows of logits score the choice that was made, the loss and its gradient
-at the logits are the library's too (policy_backward, preference_backward).
+at the logits are the library's too (policy_backward, preference_backward), and the
+factors are formed from a backward pass of their own.
 
 Layout conventions (the library's):
   * activations and output gradients NHWC fp16; a convolution weight [c_out, c_in,
@@ -17,8 +18,13 @@ Layout conventions (the library's):
     column for the classifier);
   * the loss is a batch mean, so the gradient a hook sees is 1/n of the per-sample
     gradient; it is multiplied by n on capture (the factor G is a per-sample second
-    moment, eq. 5, and the BatchNorm Fisher is over per-sample gradients).
+    moment, eq. 5, and the BatchNorm Fisher is over per-sample gradients);
+  * after policy_backward or preference_backward that does not hold: a row's gradient
+    carries its advantage, its clip and its weight. Their factors take the gradients of
+    log p(y), y drawn from the model at every row that counts (eq. 3, the Fisher), with
+    coefficient 1; rows that do not count are in neither factor.
 """
+import math
 from dataclasses import dataclass
 
 import torch
@@ -144,7 +150,11 @@ class KfacCapture:
     than its order) and the damping small, the preconditioning products cancel and
     amplify the inverses' fp32 error; the two options remove most of it. max_grad_norm
     and trust_radius are passed to KfacStep too: they bound the gradients that are
-    preconditioned and the step that is taken."""
+    preconditioned and the step that is taken. After policy_backward or preference_backward,
+    whose factors are the model's Fisher, trust_radius bounds its predicted KL divergence
+    (the mean over the rows that count, to second order and as far as the Kronecker factors
+    hold); after another loss's backward pass it bounds the quadratic form of that loss's
+    second moment."""
 
     def __init__(self, model, damping=1e-3, ema_decay=0.95, refresh_every=1, precond_accum="f32",
                  refine_inverse=False, max_grad_norm=None, trust_radius=None):
@@ -162,6 +172,11 @@ class KfacCapture:
         self.bns = [bn for _, bn in self.pairs if bn is not None]
         self.xhat = [None] * len(self.bns)
         self.bgout = [None] * len(self.bns)
+        # the gradients of the drawn tokens' log-probabilities, while a pass takes them what it
+        # multiplies them by, and which samples hold one that counts
+        self.score = [None] * len(self.pairs)
+        self.bscore = [None] * len(self.bns)
+        self.score_scale = self.counted = None
         self.kstep = None
         self.calls = 0
         self.hooks = []
@@ -183,11 +198,18 @@ class KfacCapture:
             if torch.is_grad_enabled():
                 self.n = inp[0].shape[0]
                 self.act[i] = _nhwc_half(inp[0])
+                self.score[i] = None
         return hook
 
     def _bwd(self, i):
         def hook(mod, grad_in, grad_out):
-            self.gout[i] = _nhwc_half(grad_out[0] * self.n)
+            g = grad_out[0]
+            if self.score_scale is None:
+                self.gout[i] = _nhwc_half(g * self.n)
+                return
+            # a convolution's Fisher is the sum over its positions, which its factors average
+            places = math.sqrt(g.shape[2] * g.shape[3]) if g.dim() == 4 else 1.0
+            self.score[i] = _nhwc_half(g.float() * (self.score_scale * places))
         return hook
 
     def _bn_fwd(self, i):
@@ -198,22 +220,28 @@ class KfacCapture:
                 xh = (x - mean) * torch.rsqrt(var + mod.eps)
                 self.xhat[i] = xh.permute(0, 2, 3, 1).reshape(x.shape[0], -1, x.shape[1]).to(
                     torch.float16).contiguous()
+                self.bscore[i] = None
         return hook
 
     def _bn_bwd(self, i):
         def hook(mod, grad_in, grad_out):
-            g = grad_out[0] * self.n
-            self.bgout[i] = g.permute(0, 2, 3, 1).reshape(g.shape[0], -1, g.shape[1]).to(
-                torch.float16).contiguous()
+            if self.score_scale is None:
+                to, g = self.bgout, grad_out[0] * self.n
+            else:
+                to, g = self.bscore, grad_out[0].float() * self.score_scale
+            to[i] = g.permute(0, 2, 3, 1).reshape(g.shape[0], -1, g.shape[1]).to(torch.float16).contiguous()
         return hook
 
     # geometry and parameter layouts -------------------------------------------
-    def _geometry(self):
+    def _geometry(self, act=None, gout=None, xhat=None, bgout=None):
+        """Layers of captured tensors, of the last passes' if none are given."""
+        if act is None:
+            act, gout, xhat, bgout = self.act, self.gout, self.xhat, self.bgout
         layers = []
-        for a, g in (*zip(self.act, self.gout), *zip(self.xhat, self.bgout)):
+        for a, g in (*zip(act, gout), *zip(xhat, bgout)):
             if a.shape[0] != g.shape[0]:
                 raise RuntimeError("the last forward and the last backward pass are of different batches")
-        for (m, _), a, g in zip(self.pairs, self.act, self.gout):
+        for (m, _), a, g in zip(self.pairs, act, gout):
             if isinstance(m, nn.Conv2d):
                 n, h, w, c_in = a.shape
                 _, h_out, w_out, c_out = g.shape
@@ -224,7 +252,7 @@ class KfacCapture:
                 n, c_in = a.shape
                 layers.append(LayerGeom(n, 1, 1, c_in, 1, 1, g.shape[1], 1, 1, 1, 1, 0, 0,
                                         1 if m.bias is not None else 0))
-        bns = [BnGeom(x.shape[0], x.shape[1], x.shape[2]) for x in self.xhat]
+        bns = [BnGeom(x.shape[0], x.shape[1], x.shape[2]) for x in xhat]
         return layers, bns
 
     @staticmethod
@@ -261,11 +289,83 @@ class KfacCapture:
             z = z.contiguous()
         return z, torch.zeros(z.shape, dtype=z.dtype, device=z.device)
 
+    @staticmethod
+    def _row_counts(z, token, mask, seq_begin):
+        """Which rows count, as the losses decide it."""
+        token = token.reshape(-1)
+        counts = (token >= 0) & (token < z.shape[1])
+        if mask is not None:
+            counts &= mask.reshape(-1) != 0
+        if seq_begin is not None:
+            at = torch.arange(z.shape[0], device=z.device)
+            counts &= (at >= seq_begin[0]) & (at < seq_begin[-1])
+        return counts
+
+    @staticmethod
+    def _draw(z):
+        """A token for every row from the model's distribution: the largest of z - log e, with
+        exponential numbers e."""
+        e = torch.empty(z.shape, dtype=torch.float32, device=z.device).exponential_().log_()
+        return torch.sub(z, e, out=e).argmax(1)
+
+    @staticmethod
+    def _leaves(out):
+        """The leaves that a backward pass from `out` reaches."""
+        seen, todo, found = set(), [out.grad_fn], []
+        while todo:
+            fn = todo.pop()
+            if fn is None or fn in seen:
+                continue
+            seen.add(fn)
+            if type(fn).__name__ == "AccumulateGrad":
+                found.append(fn.variable)
+            todo.extend(f for f, _ in fn.next_functions)
+        return found
+
+    def _score_pass(self, logits, z, counts):
+        """A backward pass of log p(y) of the rows that count, with coefficient 1 and y drawn from
+        the model: self.score and self.bscore. No leaf's gradient changes."""
+        leaves = self._leaves(logits)
+        if not leaves:
+            return
+        rows = z.shape[0]
+        y, d = self._draw(z), torch.empty(z.shape, dtype=z.dtype, device=z.device)
+        one, logp, unused = (torch.ones(rows, dtype=torch.float32, device=z.device) for _ in range(3))
+        stats = torch.empty(4, dtype=torch.float32, device=z.device)
+        # -1 for the advantage, and l itself for the old log-probability: the loss is -(-r) with r = 1 and
+        # nothing to clip it below, its gradient that of l; rows / counted at a row
+        K.kfac_policy_loss(z, y, one, one, logp, stats, mask=counts)
+        K.kfac_policy_loss(z, y, logp, -one, unused, stats, dlogits=d, mask=counts, clip_low=1.0, clip_high=0.0,
+                           grad_scale=float(rows))
+        # the samples that hold the rows: the model's inputs in their order, or else all of them
+        whole = self.n > 0 and rows % self.n == 0
+        samples = counts.view(self.n, rows // self.n).any(1) if whole else torch.ones(self.n, dtype=torch.bool, device=z.device)
+        # times counted / rows a row's score has coefficient 1; a factor divides by the samples that hold
+        # one that counts, where the mean over the rows divides by the rows
+        scale = (counts.sum() * samples.sum()).float().sqrt() / max(rows, 1)
+        self.counted = (samples.to("cpu", non_blocking=True), torch.cuda.Event() if z.is_cuda else None)
+        if z.is_cuda:
+            self.counted[1].record()
+        self.score_scale = scale
+        try:
+            torch.autograd.grad(logits, leaves, d.view(logits.shape), retain_graph=True)
+        finally:
+            self.score_scale = None
+
+    def _backward(self, logits, z, d, counts):
+        """The backward pass of a loss whose gradient at the logits is d, behind the one that the factors of
+        the next step are formed from, if it forms any."""
+        if self.calls % self.refresh_every == 0:
+            self._score_pass(logits, z, counts)
+        logits.backward(d.view(logits.shape))
+
     def policy_backward(self, logits, token, old_logp, advantage, ref_logp=None, mask=None, seq_begin=None,
                         by_sequence=False, clip_low=0.2, clip_high=0.2, kl_coef=0.0):
         """Backward pass of the clipped policy loss with a KL term (kfac_policy_loss) over
         the model's logits [..., vocab], one token, old log-probability and advantage for
-        each row. Returns (stats, logp): the loss, its surrogate part, the mean KL and
+        each row, the rows those of the model's inputs in their order. The factors of the next
+        step come from a second backward pass through the same graph (torch's generator
+        draws its tokens). Returns (stats, logp): the loss, its surrogate part, the mean KL and
         the clipped share; the rows' log-probabilities."""
         z, d = self._logit_rows(logits)
         logp = torch.zeros(z.shape[0], dtype=torch.float32, device=z.device)
@@ -273,22 +373,41 @@ class KfacCapture:
         K.kfac_policy_loss(z, token, old_logp, advantage, logp, stats, dlogits=d, ref_logp=ref_logp, mask=mask,
                            seq_begin=seq_begin, by_sequence=by_sequence, clip_low=clip_low, clip_high=clip_high,
                            kl_coef=kl_coef)
-        logits.backward(d.view(logits.shape))
+        self._backward(logits, z, d, self._row_counts(z, token, mask, seq_begin))
         return stats, logp
 
     def preference_backward(self, logits, token, seq_begin, ref_logp=None, mask=None, beta=0.1, label_smoothing=0.0):
         """Backward pass of the preference loss (kfac_preference_loss) over the model's
-        logits [..., vocab], whose rows are the preferred sequences and then the others.
-        Returns (loss, margin, seq_logp)."""
+        logits [..., vocab], whose rows are the preferred sequences and then the others, and a
+        second one for the factors, as policy_backward. Returns (loss, margin, seq_logp)."""
         z, d = self._logit_rows(logits)
         pairs = seq_begin.numel() // 2
         seq_logp, margin, loss = (torch.zeros(n, dtype=torch.float32, device=z.device) for n in (2 * pairs, pairs, 1))
         K.kfac_preference_loss(z, token, seq_begin, seq_logp, margin, loss, dlogits=d, ref_logp=ref_logp, mask=mask,
                                beta=beta, label_smoothing=label_smoothing)
-        logits.backward(d.view(logits.shape))
+        self._backward(logits, z, d, self._row_counts(z, token, mask, seq_begin))
         return loss, margin, seq_logp
 
     # the K-FAC step -------------------------------------------------------------
+    def _curvature(self):
+        """What a step forms its factors from, (act, gout, xhat, BatchNorm gout): the score pass's tensors
+        of the samples that count, if there was one, or the loss's; None where no sample counts."""
+        if all(g is None for g in (*self.score, *self.bscore)):
+            return self.act, self.gout, self.xhat, self.bgout
+        if any(g is None for g in (*self.score, *self.bscore)):
+            raise RuntimeError("a layer has no gradient from the model's logits")
+        host, copied = self.counted
+        if copied is not None:
+            copied.synchronize()
+        kept = host.nonzero()[:, 0]
+        taken = (self.act, self.score, self.xhat, self.bscore)
+        if len(kept) == len(host):
+            return taken
+        if not len(kept):
+            return None
+        kept = kept.to(self.act[0].device)
+        return tuple([t.index_select(0, kept) if t.shape[0] == len(host) else t for t in ts] for ts in taken)
+
     def step(self, lr):
         if any(a is None for a in self.act) or any(g is None for g in self.gout):
             raise RuntimeError("step() needs one forward and backward pass with the hooks in place")
@@ -304,8 +423,19 @@ class KfacCapture:
         grads = [self._to_matrix(m, grad=True) for m, _ in self.pairs]
         refresh = self.calls % self.refresh_every == 0
         decay = 0.0 if self.calls == 0 else self.ema_decay
-        self.kstep.step(self.act, self.gout, grads, self.xhat, self.bgout, ema_decay=decay, refresh=refresh,
-                        weights=self.master, bn_params=self.bn_master, lr=lr, layers=layers, bn_layers=bns)
+        act, gout, bn_fisher = self.act, self.gout, None
+        if refresh:
+            taken = self._curvature()
+            if taken is None and self.calls:  # no row counts: there is no curvature in the batch
+                refresh = False
+            else:
+                act, gout, xhat, bscore = taken or (self.act, self.score, self.xhat, self.bscore)
+                layers, fisher_bns = self._geometry(act, gout, xhat, bscore)
+                if self.bns and bscore is not self.bgout:
+                    bn_fisher = (fisher_bns, xhat, bscore)
+        self.kstep.step(act, gout, grads, self.xhat, self.bgout, ema_decay=decay, refresh=refresh,
+                        weights=self.master, bn_params=self.bn_master, lr=lr, layers=layers, bn_layers=bns,
+                        bn_fisher=bn_fisher)
         self.calls += 1
         for (m, _), mat in zip(self.pairs, self.master):
             self._from_matrix(m, mat)

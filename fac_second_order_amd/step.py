@@ -65,8 +65,13 @@ class KfacStep:
     gradients may be float16, bfloat16 or float32. self.grad_norm holds the norm.
 
     trust_radius: step() updates the parameters last and together, by the step s P
-    whose predicted KL divergence s^2/2 <P, gradient> is at most this (kfac_trust_update):
-    s is lr where that is smaller. self.trust holds s and <P, gradient>."""
+    whose quadratic form s^2/2 <P, F P> = s^2/2 <P, gradient> is at most this
+    (kfac_trust_update): s is lr where that is smaller. self.trust holds s and <P, gradient>.
+    F is the damped curvature of the call's own factors. The form predicts the KL
+    divergence of the model's distribution where that is its Fisher: gout (and bn_fisher)
+    the gradients of log-probabilities of outcomes drawn from the model, one sample each, as
+    KfacCapture.policy_backward takes them. Of a loss's own gradients it predicts none: F
+    then scales with the loss."""
 
     def __init__(self, layers, bn_layers=(), device="cuda", damping=1e-3, bn_shift=None,
                  in_dtype=torch.float16, precond_accum="f32", refine_inverse=False, side_stream=True,
@@ -301,28 +306,42 @@ class KfacStep:
         K.kfac_trust_update(P, g, w, lr, self.trust_radius, self.trust, fisher, self.bn_shift, self.workspace, stream)
 
     def step(self, act, gout, grads, xhat=(), bn_gout=(), ema_decay=0.0, refresh=True,
-             weights=None, bn_params=None, lr=0.0, stream=None, layers=None, bn_layers=None):
+             weights=None, bn_params=None, lr=0.0, stream=None, layers=None, bn_layers=None,
+             bn_fisher=None):
         """One step. refresh=False is a stale-curvature step: factors and inverses are
         kept, the gradients are preconditioned with them, and BN divides its fresh
         gradient by the stored Fisher (decay 1 keeps it). Given weights and/or
         bn_params, those are updated in place with learning rate lr. layers, bn_layers:
-        those of this call where its tensors have another number of samples, n."""
+        those of this call where its tensors have another number of samples, n. bn_fisher:
+        (bn_layers, xhat, gout) that the BatchNorm Fisher is formed from where that is not the
+        loss's own gradient; xhat and bn_gout then give the gradient alone."""
         # refused here, before the factors and the Fisher have taken the batch in
         if self.trust_radius is not None and not 0.0 <= lr < math.inf:
             raise ValueError("lr must be finite and >= 0")
         layers = _same_but_samples(layers, self.layers, K.kfac_layer._fields_, "layers")
         bn_layers = _same_but_samples(bn_layers, self.bn_layers, K.kfac_bn._fields_, "bn_layers")
         self._make_room(layers, bn_layers, stream)
+        if bn_fisher is not None:
+            _same_but_samples(bn_fisher[0], self.bn_layers, K.kfac_bn._fields_, "bn_layers")
+            self._make_room(layers, bn_fisher[0], stream)
         grads = self.clip(grads, stream)
-        args = (layers, bn_layers, act, gout, grads, xhat, bn_gout, ema_decay, refresh)
+        args = (layers, bn_layers, act, gout, grads, xhat, bn_gout, bn_fisher, ema_decay, refresh)
         if self.trust_radius is not None:
             self._step(*args, None, None, lr, stream)
             self._bounded_update(grads, weights, bn_params, lr, stream)
         else:
             self._step(*args, weights, bn_params, lr, stream)
 
-    def _step(self, layers, bn_layers, act, gout, grads, xhat, bn_gout, ema_decay, refresh, weights, bn_params, lr,
-              stream):
+    def _bn_groups(self, groups, bn_layers, xhat, bn_gout, bn_fisher, ema_decay, bn_params, lr, stream):
+        if bn_fisher is not None:  # the gradient that this divides is not the loss's: only its Fisher stays
+            for part in groups:
+                self._bn(part, *bn_fisher, ema_decay, None, lr, stream)
+            ema_decay = 1.0
+        for part in groups:
+            self._bn(part, bn_layers, xhat, bn_gout, ema_decay, bn_params, lr, stream)
+
+    def _step(self, layers, bn_layers, act, gout, grads, xhat, bn_gout, bn_fisher, ema_decay, refresh, weights,
+              bn_params, lr, stream):
         all_bn = list(range(len(bn_layers)))
         if not refresh:
             self.precondition(grads, weights, lr, stream)
@@ -333,7 +352,7 @@ class KfacStep:
             self._invert(self.main, self._info_main, self.workspace, stream)
             self._refine(stream)
             self.precondition(grads, weights, lr, stream)
-            self._bn(all_bn, bn_layers, xhat, bn_gout, ema_decay, bn_params, lr, stream)
+            self._bn_groups([all_bn], bn_layers, xhat, bn_gout, bn_fisher, ema_decay, bn_params, lr, stream)
             return
         main = torch.cuda.current_stream(self.device) if stream is None else stream
         side = self.stream2
@@ -360,8 +379,8 @@ class KfacStep:
             for part in self._groups(self.main_layers, pcost, self.MAIN_CALLS["precondition"]):
                 self._precondition(part, grads, weights, lr, self.workspace, main)
             bcost = lambda b: self.bn_layers[b].n * self.bn_layers[b].hw * self.bn_layers[b].c  # noqa: E731
-            for part in self._groups(all_bn, bcost, self.MAIN_CALLS["bn"]):
-                self._bn(part, bn_layers, xhat, bn_gout, ema_decay, bn_params, lr, main)
+            self._bn_groups(self._groups(all_bn, bcost, self.MAIN_CALLS["bn"]), bn_layers, xhat, bn_gout, bn_fisher,
+                            ema_decay, bn_params, lr, main)
             side.wait_event(main_inverses)  # the side layers' other factor
             self._precondition(self.side_layers, grads, weights, lr, self.workspace2, side)
         finally:

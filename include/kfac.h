@@ -332,10 +332,13 @@ kfac_status kfac_grad_clip(int32_t count, const int64_t* numel, const kfac_dtype
                            float max_norm, float* norm, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
- * kfac_trust_update - the update of [OTUNYM] eq. (8) with a bound on its predicted KL
- * divergence. P is a preconditioned gradient and F the damped Fisher that made it from the
- * gradient g (F P = g), so that to second order the step s P changes the model's
- * distribution by s^2/2 <P, F P> = s^2/2 <P, g>. With
+ * kfac_trust_update - the update of [OTUNYM] eq. (8) with a bound on its quadratic form. P is
+ * a preconditioned gradient and F the damped matrix that made it from the gradient g
+ * (F P = g), so that the step s P has s^2/2 <P, F P> = s^2/2 <P, g>. Where F is the model's
+ * Fisher, the second moment of the gradients of log p(y) with y drawn from the model, that
+ * is to second order the KL divergence by which the step changes the model's distribution.
+ * Where F was formed from a loss's own gradients it is not: F then scales with the loss,
+ * the distribution does not. With
  *   q = sum over the tensors of <P_i, g_i>,  s = min(lr, sqrt(2 delta / |q|)),
  * w_i <- w_i - s P_i in fp32 for every tensor.
  *

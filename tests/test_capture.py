@@ -7,6 +7,7 @@ import torch
 import torch.nn.functional as F
 
 import oracle
+from oracle import loss_oracle as lo
 
 cap_mod = pytest.importorskip("fac_second_order_amd.capture")
 
@@ -69,7 +70,7 @@ class Recorder:
         self.made, self.options, self.calls = (layers, bns), kw, []
 
     def step(self, *args, **kw):
-        self.calls.append((args, kw))
+        self.calls.append(([list(a) for a in args], kw))   # the lists are filled again by the next pass
 
 
 def test_a_batch_of_another_size_has_its_own_geometry(monkeypatch):
@@ -105,3 +106,264 @@ def test_matrix_of_a_weight_that_has_its_order(fmt):
         want = mat.clone()
         cap_mod.KfacCapture._from_matrix(m, mat)
         assert torch.equal(cap_mod.KfacCapture._to_matrix(m), want)
+
+
+# ---------------------------------------------------------------------------
+# the backward passes of the losses, the library's calls replaced by the oracle
+# ---------------------------------------------------------------------------
+
+def _np(t):
+    return None if t is None else t.detach().double().numpy() if t.is_floating_point() else t.numpy()
+
+
+def _oracle_policy(z, token, old_logp, advantage, logp, stats, dlogits=None, ref_logp=None, mask=None, seq_begin=None,
+                   by_sequence=False, clip_low=0.2, clip_high=0.2, kl_coef=0.0, grad_scale=1.0):
+    token = token.reshape(-1)
+    begin = None if seq_begin is None else seq_begin.tolist()
+    st, l, d = lo.policy_loss(_np(z), _np(token), _np(old_logp), _np(advantage), _np(ref_logp), _np(mask), begin,
+                              by_sequence, clip_low, clip_high, kl_coef, grad_scale)
+    stats.copy_(torch.from_numpy(st))
+    logp.copy_(torch.from_numpy(np.nan_to_num(l)))
+    if dlogits is not None:
+        dlogits.copy_(torch.from_numpy(np.nan_to_num(d)))
+
+
+def _oracle_preference(z, token, begin, seq_logp, margin, loss, dlogits=None, ref_logp=None, mask=None, beta=0.1,
+                       label_smoothing=0.0, grad_scale=1.0):
+    value, x, sums, d = lo.preference_loss(_np(z), _np(token), begin.tolist(), _np(ref_logp), _np(mask), beta,
+                                           label_smoothing, grad_scale)
+    loss.fill_(value)
+    margin.copy_(torch.from_numpy(x))
+    seq_logp.copy_(torch.tensor(sums))
+    dlogits.copy_(torch.from_numpy(np.nan_to_num(d)))
+
+
+@pytest.fixture
+def passes(monkeypatch):
+    monkeypatch.setattr(cap_mod, "KfacStep", Recorder)
+    monkeypatch.setattr(cap_mod.K, "kfac_policy_loss", _oracle_policy)
+    monkeypatch.setattr(cap_mod.K, "kfac_preference_loss", _oracle_preference)
+
+
+class Net(torch.nn.Module):
+    def __init__(self, per=1):
+        super().__init__()
+        self.a, self.b, self.per = torch.nn.Linear(5, 6), torch.nn.Linear(6, 4 * per), per
+
+    def forward(self, x):
+        return self.b(torch.tanh(self.a(x))).view(x.shape[0] * self.per, 4)
+
+    def kfac_modules(self):
+        return [(self.a, None), (self.b, None)]
+
+
+class ConvNet(torch.nn.Module):
+    def __init__(self):
+        super().__init__()
+        self.c, self.n, self.b = torch.nn.Conv2d(3, 4, 3, 1, 1, bias=False), torch.nn.BatchNorm2d(4), torch.nn.Linear(4, 4)
+
+    def forward(self, x):
+        return self.b(torch.relu(self.n(self.c(x))).mean((2, 3)))
+
+    def kfac_modules(self):
+        return [(self.c, self.n), (self.b, None)]
+
+
+TOL = dict(rtol=2.0 ** -10, atol=2.0 ** -10)      # fp16 tensors of numbers up to 1, and of some up to 3
+
+
+def _score_grads(net, x, y, weights, outs):
+    """Gradients at `outs` (captured by forward hooks) of sum_t weights[t] log p(y_t)."""
+    seen = {}
+    hooks = [m.register_forward_hook(lambda mod, i, o, k=k: seen.__setitem__(k, o)) for k, m in enumerate(outs)]
+    l = torch.log_softmax(net(x), 1).gather(1, y[:, None])[:, 0]
+    got = torch.autograd.grad((l * weights).sum(), [seen[k] for k in range(len(outs))])
+    for h in hooks:
+        h.remove()
+    return got
+
+
+ROWS = 7
+TOKEN = torch.tensor([1, 0, 3, 2, -100, 1, 0])
+DRAWN = torch.tensor([3, 1, 0, 2, 2, 0, 1])
+MASK = torch.tensor([1, 1, 0, 1, 1, 0, 1], dtype=torch.bool)
+BEGIN = torch.tensor([0, 3, 6], dtype=torch.int32)
+COUNTED = torch.tensor([1, 1, 0, 1, 0, 0, 0], dtype=torch.bool)     # 4 has no token, 6 no sequence
+
+
+def _policy_kw():
+    g = torch.Generator().manual_seed(6)
+    return dict(old_logp=-1.4 + 0.1 * torch.randn(ROWS, generator=g), advantage=torch.randn(ROWS, generator=g),
+                ref_logp=torch.full((ROWS,), -1.3), mask=MASK, seq_begin=BEGIN, by_sequence=True, kl_coef=0.2)
+
+
+@pytest.mark.parametrize("loss", ["policy", "preference"])
+def test_factors_take_scores_of_the_rows_that_count(passes, monkeypatch, loss):
+    """gout of the step: d log p(y) at each layer, coefficient 1, of the rows that count alone, whatever the
+    loss weighs them by; the weights' gradients are the loss's and nothing else."""
+    torch.manual_seed(7)
+    net = Net()
+    cap = cap_mod.KfacCapture(net)
+    monkeypatch.setattr(cap, "_draw", lambda z: DRAWN)
+    x = torch.randn(ROWS, 5)
+    net.a.weight.grad = before = torch.ones(6, 5)                     # an earlier pass's
+    logits = net(x)
+    if loss == "policy":
+        cap.policy_backward(logits, TOKEN, **_policy_kw())
+        kw = {k: _np(v) if torch.is_tensor(v) else v for k, v in _policy_kw().items()}
+        want = lo.policy_loss(_np(logits), _np(TOKEN), kw["old_logp"], kw["advantage"], kw["ref_logp"], kw["mask"],
+                              BEGIN.tolist(), True, kl_coef=0.2)[2]
+    else:
+        cap.preference_backward(logits, TOKEN, BEGIN, mask=MASK, beta=0.5)
+        want = lo.preference_loss(_np(logits), _np(TOKEN), BEGIN.tolist(), None, _np(MASK), 0.5)[3]
+    logits = net(x)                                                    # (also: a later forward alone changes no .grad)
+    ref = torch.autograd.grad(logits, list(net.parameters()), torch.from_numpy(np.nan_to_num(want)).float())
+    assert net.a.weight.grad is before
+    for p, w in zip(net.parameters(), ref):
+        assert torch.allclose(p.grad, w + (1.0 if p is net.a.weight else 0.0), rtol=1e-5, atol=1e-6)
+    score = _score_grads(net, x, DRAWN, COUNTED.float(), [net.a, net.b])
+    net.zero_grad()                                                    # the forwards above took the scores away
+    if loss == "policy":
+        cap.policy_backward(net(x), TOKEN, **_policy_kw())
+    else:
+        cap.preference_backward(net(x), TOKEN, BEGIN, mask=MASK, beta=0.5)
+    cap.step(0.1)
+    (act, gout, grads, _, _), kw = cap.kstep.calls[-1]
+    assert torch.equal(act[0], x[COUNTED].half()) and kw["refresh"]
+    assert all(L.n == 3 == a.shape[0] == g.shape[0] for L, a, g in zip(kw["layers"], act, gout))
+    assert all(L.n == ROWS for L in cap.kstep.made[0])
+    for g, s in zip(gout, score):
+        assert torch.allclose(g.float(), s[COUNTED], **TOL) and s[COUNTED].abs().max() > 0.1
+    one_hot = gout[1].float() + torch.softmax(logits.detach()[COUNTED], 1)
+    assert torch.allclose(one_hot, F.one_hot(DRAWN[COUNTED], 4).float(), **TOL)
+    cap.remove()
+
+
+def test_padding_changes_nothing(passes, monkeypatch):
+    """Rows that do not count, in front, between and behind, change neither the factors' tensors nor the
+    weights' gradients; NaN among their logits does not either."""
+    torch.manual_seed(8)
+    net = Net()
+    x, token, drawn = torch.randn(4, 5), torch.tensor([0, 3, 1, 2]), torch.tensor([1, 1, 0, 2])
+    old, adv = torch.full((4,), -1.4), torch.tensor([0.5, -0.3, 1.0, 0.2])
+    at = torch.tensor([1, 2, 4, 5])
+    got = []
+    for padded in (False, True):
+        cap = cap_mod.KfacCapture(net)
+        net.zero_grad()
+        ins = [x, token, old, adv, drawn]
+        mask = None
+        if padded:
+            wide = [torch.full((7, *t.shape[1:]), 9, dtype=t.dtype) for t in ins]
+            for w, t in zip(wide, ins):
+                w[at] = t
+            ins, mask = wide, torch.zeros(7, dtype=torch.bool)
+            mask[at] = True
+        monkeypatch.setattr(cap, "_draw", lambda z, y=ins[4]: y.clamp(max=3))
+        cap.policy_backward(net(ins[0]), ins[1], ins[2], ins[3], mask=mask)
+        cap.step(0.0)
+        (act, gout, grads, _, _), kw = cap.kstep.calls[-1]
+        got.append((*act, *gout, *[torch.tensor(L.n) for L in kw["layers"]]))
+        grads_of = [g.clone() for g in grads]
+        got.append(grads_of)
+        cap.remove()
+    assert all(torch.equal(a, b) for a, b in zip(got[0], got[2]))
+    assert all(torch.allclose(a, b, rtol=1e-5, atol=1e-7) for a, b in zip(got[1], got[3]))
+
+
+def test_several_rows_of_a_sample(passes, monkeypatch):
+    """Three rows a sample: its score is the sum of its rows', times sqrt(samples / rows) of those that count,
+    so that the mean of its square over the samples estimates the mean over the rows."""
+    torch.manual_seed(9)
+    net = Net(per=3)
+    cap = cap_mod.KfacCapture(net)
+    drawn = torch.randint(0, 4, (12,))
+    monkeypatch.setattr(cap, "_draw", lambda z: drawn)
+    x = torch.randn(4, 5)
+    mask = torch.ones(12, dtype=torch.bool)
+    mask[[0, 3, 4, 5, 10]] = False                                     # the second sample has none left
+    cap.policy_backward(net(x), torch.zeros(4, 3, dtype=torch.long), torch.full((12,), -1.4), torch.ones(12), mask=mask)
+    cap.step(0.1)
+    (act, gout, *_), kw = cap.kstep.calls[-1]
+    kept = torch.tensor([0, 2, 3])
+    assert torch.equal(act[0], x[kept].half()) and all(L.n == 3 for L in kw["layers"])
+    score = _score_grads(net, x, drawn, mask.float(), [net.a, net.b])
+    for g, s in zip(gout, score):
+        assert torch.allclose(g.float(), s[kept] * (3 / 7) ** 0.5, **TOL)
+    cap.remove()
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_convolutions_and_batchnorm_take_scores(passes, monkeypatch, masked):
+    """A convolution's score times sqrt(positions), BatchNorm's Fisher from the scores, its gradient from the
+    loss, over all samples."""
+    torch.manual_seed(10)
+    net = ConvNet()
+    cap = cap_mod.KfacCapture(net)
+    drawn = torch.tensor([1, 0, 3, 2, 2])
+    monkeypatch.setattr(cap, "_draw", lambda z: drawn)
+    x = torch.randn(5, 3, 6, 6)
+    mask = torch.tensor([True, True, not masked, True, True])
+    old, adv = torch.full((5,), -1.4), torch.tensor([0.5, -0.3, 1.0, 0.2, 0.1])
+    score = _score_grads(net, x, drawn, mask.float(), [net.c, net.n, net.b])
+    cap.policy_backward(net(x), torch.zeros(5, dtype=torch.long), old, adv, mask=mask)
+    bgout = cap.bgout[0].clone()
+    cap.step(0.1)
+    (act, gout, grads, xhat, bn_gout), kw = cap.kstep.calls[-1]
+    n = 5 - masked
+    assert [L.n for L in kw["layers"]] == [n, n] and [B.n for B in kw["bn_layers"]] == [5]
+    assert torch.allclose(gout[0].float(), 6 * score[0].permute(0, 2, 3, 1)[mask], **TOL)
+    assert torch.allclose(gout[1].float(), score[2][mask], **TOL)
+    assert torch.equal(bn_gout[0], bgout) and xhat[0].shape == (5, 36, 4)
+    bns, fx, fg = kw["bn_fisher"]
+    assert [B.n for B in bns] == [n] and torch.equal(fx[0], cap.xhat[0][mask])
+    assert torch.allclose(fg[0].float(), score[1].permute(0, 2, 3, 1).reshape(5, 36, 4)[mask], **TOL)
+    # the gradient of gamma and beta: the mean over the samples of the captured products
+    s = torch.stack([(bgout.float() * cap.xhat[0].float()).sum(1).mean(0), bgout.float().sum(1).mean(0)])
+    assert torch.allclose(s, torch.stack([net.n.weight.grad, net.n.bias.grad]), rtol=1e-2, atol=1e-3)
+    cap.remove()
+
+
+def test_passes_of_a_stale_step_and_of_another_loss(passes, monkeypatch):
+    """No second pass where the next step keeps its curvature; an ordinary loss behind takes its own
+    gradients; a batch without a row that counts keeps the curvature there is."""
+    torch.manual_seed(11)
+    net = Net()
+    cap = cap_mod.KfacCapture(net, refresh_every=2)
+    drawn = []
+    monkeypatch.setattr(cap, "_draw", lambda z: drawn.append(1) or torch.zeros(z.shape[0], dtype=torch.long))
+    x, one = torch.randn(3, 5), torch.ones(3)
+    call = lambda **kw: cap.policy_backward(net(x), torch.zeros(3, dtype=torch.long), -one, one, **kw)  # noqa: E731
+    for refresh in (True, False, True):
+        call()
+        cap.step(0.1)
+        assert cap.kstep.calls[-1][1]["refresh"] == refresh
+    assert len(drawn) == 2
+    cap.calls = 4
+    F.cross_entropy(net(x), torch.zeros(3, dtype=torch.long)).backward()
+    cap.step(0.1)
+    assert all(a is b for a, b in zip(cap.kstep.calls[-1][0][1], cap.gout)) and len(drawn) == 2
+    assert cap.kstep.calls[-1][1]["bn_fisher"] is None
+    cap.calls = 6
+    call(mask=torch.zeros(3, dtype=torch.bool))
+    cap.step(0.1)
+    assert not cap.kstep.calls[-1][1]["refresh"]
+    cap.calls = 0
+    call(mask=torch.zeros(3, dtype=torch.bool))
+    cap.step(0.1)
+    (act, gout, *_), kw = cap.kstep.calls[-1]
+    assert kw["refresh"] and len(act[0]) == 3 and not any(g.any() for g in gout)
+    cap.remove()
+
+
+def test_drawn_tokens_follow_the_model():
+    """40000 draws of three choices: each share within five standard deviations, 5 sqrt(p (1 - p) / n) <= 0.0125;
+    a choice of no probability is never drawn."""
+    torch.manual_seed(12)
+    p = torch.tensor([0.5, 0.2, 0.0, 0.3])
+    y = cap_mod.KfacCapture._draw(p.log().expand(40000, 4))
+    share = torch.bincount(y, minlength=4) / 40000
+    assert (share - p).abs().max() <= 0.0125 and share[2] == 0
+    assert cap_mod.KfacCapture._draw(torch.zeros(0, 4)).shape == (0,)
+    bad = cap_mod.KfacCapture._draw(torch.full((2, 4), float("nan")))
+    assert ((bad >= 0) & (bad < 4)).all()

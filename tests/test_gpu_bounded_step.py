@@ -230,6 +230,108 @@ def test_preference_training_step(kfac_gpu):
     cap.remove()
 
 
+class Head(torch.nn.Module):
+    """One softmax layer, its logits in a type."""
+
+    def __init__(self, d, choices, dtype=torch.float32, std=0.02):
+        super().__init__()
+        self.fc, self.dtype = torch.nn.Linear(d, choices), dtype
+        with torch.no_grad():
+            self.fc.weight.normal_(0, std)
+            self.fc.bias.normal_(0, std)
+
+    def forward(self, x):
+        return self.fc(x).to(self.dtype)
+
+    def kfac_modules(self):
+        return [(self.fc, None)]
+
+
+@pytest.mark.parametrize("loss", ["policy", "preference"])
+@pytest.mark.parametrize("size", [0.1, 1.0, 10.0])
+@pytest.mark.parametrize("masked", [False, True])
+def test_radius_is_the_kl_of_the_model(kfac_gpu, loss, size, masked):
+    """The KL divergence of the model across a step, measured in fp64 over the rows that count, is the radius
+    it was given, whatever the loss weighs the rows by; rows that do not count, of other inputs, take no part.
+
+    One softmax layer near the uniform distribution: its Fisher is A x (diag p - p p^T) but for p's own
+    spread (logits of 0.08: some percent). G is estimated from 4096 (2048) drawn tokens: for a fixed direction u
+    the square of u . score, whitened, has a mean of 1 and at most 7 as its largest value with 8 choices, so the
+    estimate's deviation is at most sqrt(6 / 2048) = 0.054, and 0.2 is 3.7 of them. To second order: the step
+    moves logits by sqrt(2e-3) = 0.045, and the third order is at most that part of the second. 0.2 + 0.05."""
+    from fac_second_order_amd.capture import KfacCapture
+    torch.manual_seed(41)
+    rows, d, choices, radius = 4096, 16, 8, 1e-3
+    net = Head(d, choices).cuda()
+    cap = KfacCapture(net, damping=1e-6, trust_radius=radius)
+    x = torch.randn(rows, d, device="cuda")
+    token = torch.randint(0, choices, (rows,), device="cuda")
+    mask = None
+    if masked:
+        mask = torch.arange(rows, device="cuda") % 2 == 0
+        x[~mask] *= 20.0
+    with torch.no_grad():
+        before = torch.log_softmax(net(x).double(), 1)
+    old = before.gather(1, token[:, None])[:, 0].float()
+    if loss == "policy":
+        cap.policy_backward(net(x), token, old, size * torch.randn(rows, device="cuda"), mask=mask)
+    else:
+        begin = torch.arange(0, rows + 1, 64, dtype=torch.int32, device="cuda")
+        cap.preference_backward(net(x), token, begin, mask=mask, beta=0.01 * size)
+    cap.step(lr=1e20)
+    with torch.no_grad():
+        after = torch.log_softmax(net(x).double(), 1)
+    kl = (before.exp() * (before - after)).sum(1)
+    kl = float(kl.mean() if mask is None else kl[mask].mean())
+    s, q = (float(v) for v in cap.kstep.trust.double())
+    say(loss, "size", size, "masked", masked, "KL", kl, "predicted", 0.5 * s * s * q)
+    assert abs(0.5 * s * s * q - radius) <= radius * 8 * U
+    assert abs(kl - radius) <= 0.25 * radius
+    cap.remove()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_scores_of_the_factors(kfac_gpu, dtype):
+    """What the factors of a step are formed from, by the library: a one-hot row less the softmax, in the
+    logits' type (half a step of it, one of fp16, and 8 u of fp32) for rows that count, zeros elsewhere; G is
+    their second moment over the rows that count, A that of their inputs."""
+    from fac_second_order_amd.capture import KfacCapture
+    torch.manual_seed(42)
+    rows, d, choices = 300, 24, 11
+    net = Head(d, choices, dtype, std=0.5).cuda()
+    cap = KfacCapture(net, damping=1e-2)
+    x = torch.randn(rows, d, device="cuda")
+    mask = torch.arange(rows, device="cuda") % 3 != 1
+    token = torch.randint(0, choices, (rows,), device="cuda")
+    token[5], mask[6] = -100, True
+    counted = mask & (token >= 0)
+    logits = net(x)
+    cap.policy_backward(logits, token, torch.full((rows,), -2.4, device="cuda"), torch.randn(rows, device="cuda"),
+                        mask=mask)
+    score = host64(cap.score[0])
+    p = np.exp(host64(torch.log_softmax(logits.detach().double(), 1)))
+    on = host64(counted.float()) != 0
+    assert not score[~on].any()
+    m = int(on.sum())
+    # the library's row is rows / counted times the score, rounded to the type, times counted / rows, to fp16
+    drawn = np.abs(score + p - 1.0).argmin(1)
+    one = np.zeros_like(p)
+    one[np.arange(rows), drawn] = 1.0
+    half = torch.finfo(dtype).eps / 2 + 2.0 ** -11 + 8 * U
+    floor = 2.0 ** -25 * (1 + m / rows)                                 # subnormals of fp16
+    assert (np.abs(score - (one - p))[on] <= (np.abs(one - p) * half * 1.01 + 64 * U * p + 4 * U + floor)[on]).all()
+    cap.step(0.0)
+    torch.cuda.synchronize()
+    G = (score[on].T @ score[on]) / m
+    a = np.concatenate([host64(cap.act[0]), np.ones((rows, 1))], 1)[on]
+    A = a.T @ a / m
+    iu = np.triu_indices(choices)
+    assert np.linalg.norm(host64(cap.kstep.G_packed[0]) - G[iu]) <= 1e-5 * np.linalg.norm(G)
+    iu = np.triu_indices(d + 1)
+    assert np.linalg.norm(host64(cap.kstep.A_packed[0]) - A[iu]) <= 1e-5 * np.linalg.norm(A)
+    cap.remove()
+
+
 def test_logits_of_any_layout_reach_the_loss(kfac_gpu):
     """Logits [batch, time, vocab], also as a transposed view: the same loss and gradients."""
     from fac_second_order_amd.capture import KfacCapture
