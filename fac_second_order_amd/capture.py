@@ -177,6 +177,7 @@ class KfacCapture:
         self.score = [None] * len(self.pairs)
         self.bscore = [None] * len(self.bns)
         self.score_scale = self.counted = None
+        self.loss_scale = 1.0  # what the gradients of a running backward pass are multiplied by
         self.kstep = None
         self.calls = 0
         self.hooks = []
@@ -205,7 +206,7 @@ class KfacCapture:
         def hook(mod, grad_in, grad_out):
             g = grad_out[0]
             if self.score_scale is None:
-                self.gout[i] = _nhwc_half(g * self.n)
+                self.gout[i] = _nhwc_half(g * (self.n / self.loss_scale))
                 return
             # a convolution's Fisher is the sum over its positions, which its factors average
             places = math.sqrt(g.shape[2] * g.shape[3]) if g.dim() == 4 else 1.0
@@ -226,7 +227,7 @@ class KfacCapture:
     def _bn_bwd(self, i):
         def hook(mod, grad_in, grad_out):
             if self.score_scale is None:
-                to, g = self.bgout, grad_out[0] * self.n
+                to, g = self.bgout, grad_out[0] * (self.n / self.loss_scale)
             else:
                 to, g = self.bscore, grad_out[0].float() * self.score_scale
             to[i] = g.permute(0, 2, 3, 1).reshape(g.shape[0], -1, g.shape[1]).to(torch.float16).contiguous()
@@ -352,40 +353,71 @@ class KfacCapture:
         finally:
             self.score_scale = None
 
-    def _backward(self, logits, z, d, counts):
-        """The backward pass of a loss whose gradient at the logits is d, behind the one that the factors of
-        the next step are formed from, if it forms any."""
+    @staticmethod
+    def _scale(given, z, x):
+        """grad_scale: the one given, or 1, or for fp16 logits the largest power of two up to x, from 1 to 2^14
+        (a coefficient of 4 times that is still an fp16)."""
+        if given is not None:
+            if not 0.0 < given < math.inf:
+                raise ValueError("grad_scale must be positive and finite")
+            return float(given)
+        return 2.0 ** min(14, math.floor(math.log2(x))) if z.dtype == torch.float16 and x >= 1 else 1.0
+
+    def _backward(self, logits, z, d, counts, scale):
+        """The backward pass of a loss whose gradient at the logits is d / scale, behind the one that the factors
+        of the next step are formed from, if it forms any."""
         if self.calls % self.refresh_every == 0:
             self._score_pass(logits, z, counts)
-        logits.backward(d.view(logits.shape))
+        if scale == 1.0:
+            logits.backward(d.view(logits.shape))
+            return
+        held = [(p, p.grad) for p in self._leaves(logits)]
+        for p, _ in held:
+            p.grad = None
+        self.loss_scale = scale
+        try:
+            logits.backward(d.view(logits.shape))
+        finally:
+            self.loss_scale = 1.0
+            for p, before in held:
+                if p.grad is not None:
+                    p.grad.div_(scale)
+                p.grad = before if p.grad is None else p.grad if before is None else before.add_(p.grad)
 
     def policy_backward(self, logits, token, old_logp, advantage, ref_logp=None, mask=None, seq_begin=None,
-                        by_sequence=False, clip_low=0.2, clip_high=0.2, kl_coef=0.0):
+                        by_sequence=False, clip_low=0.2, clip_high=0.2, kl_coef=0.0, grad_scale=None):
         """Backward pass of the clipped policy loss with a KL term (kfac_policy_loss) over
         the model's logits [..., vocab], one token, old log-probability and advantage for
         each row, the rows those of the model's inputs in their order. The factors of the next
         step come from a second backward pass through the same graph (torch's generator
-        draws its tokens). Returns (stats, logp): the loss, its surrogate part, the mean KL and
-        the clipped share; the rows' log-probabilities."""
+        draws its tokens). The gradients run through the network multiplied by grad_scale, which is
+        divided out of what arrives at the leaves and the hooks: by default 1, and for fp16 logits the rows'
+        number, as a power of two up to 2^14, since a mean over rows leaves most of a softmax below what an
+        fp16 holds. Returns (stats, logp): the loss, its surrogate part, the mean KL and the clipped share; the
+        rows' log-probabilities."""
         z, d = self._logit_rows(logits)
+        scale = self._scale(grad_scale, z, z.shape[0])
         logp = torch.zeros(z.shape[0], dtype=torch.float32, device=z.device)
         stats = torch.zeros(4, dtype=torch.float32, device=z.device)
         K.kfac_policy_loss(z, token, old_logp, advantage, logp, stats, dlogits=d, ref_logp=ref_logp, mask=mask,
                            seq_begin=seq_begin, by_sequence=by_sequence, clip_low=clip_low, clip_high=clip_high,
-                           kl_coef=kl_coef)
-        self._backward(logits, z, d, self._row_counts(z, token, mask, seq_begin))
+                           kl_coef=kl_coef, grad_scale=scale)
+        self._backward(logits, z, d, self._row_counts(z, token, mask, seq_begin), scale)
         return stats, logp
 
-    def preference_backward(self, logits, token, seq_begin, ref_logp=None, mask=None, beta=0.1, label_smoothing=0.0):
+    def preference_backward(self, logits, token, seq_begin, ref_logp=None, mask=None, beta=0.1, label_smoothing=0.0,
+                            grad_scale=None):
         """Backward pass of the preference loss (kfac_preference_loss) over the model's
         logits [..., vocab], whose rows are the preferred sequences and then the others, and a
-        second one for the factors, as policy_backward. Returns (loss, margin, seq_logp)."""
+        second one for the factors; grad_scale as in policy_backward, for fp16 logits about
+        pairs / beta by default, which makes a row's coefficient 1. Returns (loss, margin, seq_logp)."""
         z, d = self._logit_rows(logits)
         pairs = seq_begin.numel() // 2
+        scale = self._scale(grad_scale, z, pairs / abs(beta) if beta else 1.0)
         seq_logp, margin, loss = (torch.zeros(n, dtype=torch.float32, device=z.device) for n in (2 * pairs, pairs, 1))
         K.kfac_preference_loss(z, token, seq_begin, seq_logp, margin, loss, dlogits=d, ref_logp=ref_logp, mask=mask,
-                               beta=beta, label_smoothing=label_smoothing)
-        self._backward(logits, z, d, self._row_counts(z, token, mask, seq_begin))
+                               beta=beta, label_smoothing=label_smoothing, grad_scale=scale)
+        self._backward(logits, z, d, self._row_counts(z, token, mask, seq_begin), scale)
         return loss, margin, seq_logp
 
     # the K-FAC step -------------------------------------------------------------

@@ -367,3 +367,77 @@ def test_drawn_tokens_follow_the_model():
     assert cap_mod.KfacCapture._draw(torch.zeros(0, 4)).shape == (0,)
     bad = cap_mod.KfacCapture._draw(torch.full((2, 4), float("nan")))
     assert ((bad >= 0) & (bad < 4)).all()
+
+
+class HalfHead(torch.nn.Module):
+    def __init__(self, d, choices):
+        super().__init__()
+        self.fc = torch.nn.Linear(d, choices)
+
+    def forward(self, x):
+        return self.fc(x).half()
+
+    def kfac_modules(self):
+        return [(self.fc, None)]
+
+
+@pytest.mark.parametrize("loss", ["policy", "preference"])
+@pytest.mark.parametrize("given", [None, 256.0])
+def test_fp16_logits_keep_the_softmax_of_a_mean(passes, loss, given):
+    """Of 1024 rows of 4096 fp16 logits every softmax entry of the loss's mean is below half the smallest
+    fp16: the weights' gradients hold it all the same, added to what the leaves held; so does what the
+    hooks were handed. An element of the logits' gradient is off by half a step of fp16, 2^-11 of it, or
+    by 2^-25 / scale where it is a subnormal; a sum of 1024 in fp32 by 1024 * 2^-24 of its terms at most."""
+    torch.manual_seed(13)
+    rows, choices, d = 1024, 4096, 3
+    net = HalfHead(d, choices)
+    cap = cap_mod.KfacCapture(net)
+    x, token = torch.randn(rows, d), torch.randint(0, choices, (rows,))
+    logits = net(x)
+    if loss == "policy":
+        old, adv = torch.full((rows,), -8.3), torch.randn(rows)
+        cap.policy_backward(logits, token, old, adv, grad_scale=given)
+        want, scale = lo.policy_loss(_np(logits), _np(token), _np(old), _np(adv))[2], given or 1024.0
+    else:
+        begin = torch.arange(0, rows + 1, 8, dtype=torch.int32)       # 64 pairs
+        net.fc.bias.grad = held = torch.full((choices,), 0.5)
+        cap.preference_backward(logits, token, begin, beta=0.1, grad_scale=given)
+        want, scale = lo.preference_loss(_np(logits), _np(token), begin.tolist(), None, None, 0.1)[3], given or 512.0
+        assert net.fc.bias.grad is held
+        held -= 0.5
+    off = np.abs(want) * (2.0 ** -11 + rows * 2.0 ** -24) + 2.0 ** -25 / scale
+    base = 2.0 ** -24 * (0.5 if loss == "preference" else 0.0)         # beside what was there
+    got = net.fc.bias.grad.double().numpy()
+    assert (np.abs(got - want.sum(0)) <= off.sum(0) * 1.01 + base).all()
+    got = net.fc.weight.grad.double().numpy()
+    xs = np.abs(_np(x))
+    assert (np.abs(got - want.T @ _np(x)) <= (off.T @ xs) * 1.01 + rows * 2.0 ** -24 * (np.abs(want).T @ xs)).all()
+    # n times the gradient, rounded to fp16 once more from fp16
+    seen = cap.gout[0].double().numpy()
+    assert (np.abs(seen - rows * want) <= rows * off * 1.01 + np.abs(rows * want) * 2.0 ** -11 * 1.01 + 2.0 ** -25).all()
+    assert np.abs(want[np.arange(rows), token.numpy()]).max() > 1e-4 > np.abs(np.sort(want, 1)[:, 1:-1]).max()
+    cap.remove()
+
+
+def test_scales_of_other_types_and_refusals(passes):
+    torch.manual_seed(14)
+    net = Net()
+    cap = cap_mod.KfacCapture(net)
+    scale = cap_mod.KfacCapture._scale
+    for z in (torch.zeros(1), torch.zeros(1, dtype=torch.bfloat16)):
+        assert scale(None, z, 4096) == 1.0 and scale(8, z, 4096) == 8.0
+    z = torch.zeros(1, dtype=torch.float16)
+    assert [scale(None, z, x) for x in (0, 0.3, 1, 7, 4096, 1 << 20)] == [1, 1, 1, 4, 4096, 1 << 14]
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(ValueError, match="grad_scale"):
+            cap.policy_backward(net(torch.randn(3, 5)), torch.zeros(3, dtype=torch.long), torch.zeros(3), torch.ones(3),
+                                grad_scale=bad)
+    got = []
+    for s in (None, 64.0):                                             # a power of two: the same bits in fp32
+        net.zero_grad()
+        torch.manual_seed(15)
+        cap.policy_backward(net(torch.randn(3, 5)), torch.zeros(3, dtype=torch.long), -torch.ones(3), torch.ones(3),
+                            grad_scale=s)
+        got.append([p.grad.clone() for p in net.parameters()] + [g.clone() for g in cap.gout])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    cap.remove()

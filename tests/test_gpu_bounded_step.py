@@ -332,6 +332,51 @@ def test_scores_of_the_factors(kfac_gpu, dtype):
     cap.remove()
 
 
+@pytest.mark.parametrize("loss", ["policy", "preference"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_weight_gradients_of_a_mean_over_many_rows(kfac_gpu, loss, dtype):
+    """2048 rows of 20000 choices: a softmax entry of the loss's mean is below the smallest fp16, 2^-24 = 6.0e-8
+    (policy: |advantage| / 2048 / 20000, at most 3.7e-8 on average; preference: beta / (2 pairs) / 20000 = 4.9e-8).
+    The weights' gradients against fp64, off by the rounding of the logits' gradient: half a step of
+    its type and 8 u, or half the smallest subnormal of fp16 over the scale (2048, 512); the row's error of l
+    twice (its softmax and its coefficient, which is below 2 and whose slope is); 2048 u for the sums."""
+    from fac_second_order_amd.capture import KfacCapture
+    torch.manual_seed(43)
+    rows, choices, d = 2048, 20000, 4
+    net = Head(d, choices, dtype, std=0.3).cuda()
+    cap = KfacCapture(net)
+    x = torch.randn(rows, d, device="cuda")
+    token = torch.randint(0, choices, (rows,), device="cuda")
+    logits = net(x)
+    z = logits.detach().double()
+    lp = torch.log_softmax(z, 1)
+    l, one = lp.gather(1, token[:, None])[:, 0], torch.nn.functional.one_hot(token, choices)
+    if loss == "policy":
+        adv = torch.randn(rows, device="cuda").clamp(-1.5, 1.5)
+        cap.policy_backward(logits, token, l.float(), adv)
+        coef, scale = -adv.double() / rows, 2048.0
+    else:
+        begin = torch.arange(0, rows + 1, 16, dtype=torch.int32, device="cuda")   # 64 pairs
+        ref = l.view(-1, 16).sum(1).float()                                       # margins of about 0
+        cap.preference_backward(logits, token, begin, ref_logp=ref, beta=0.125)
+        x_i = 0.125 * ((l.view(-1, 16).sum(1) - ref.double()).view(2, 64))
+        c = -0.125 / 64 / (1 + (x_i[0] - x_i[1]).exp())
+        coef, scale = torch.cat([c, -c]).repeat_interleave(16), 512.0
+    want = coef[:, None] * (one - lp.exp())
+    err = U * (choices / 64 + 40 + 6 * float((z.amax(1) - z.amin(1)).max()))
+    tiny = {torch.float16: 2.0 ** -25 / scale, torch.bfloat16: 2.0 ** -126, torch.float32: 2.0 ** -126}[dtype]
+    # a margin adds up 32 rows' errors, a quarter of which its slope sees
+    bound = want.abs() * (torch.finfo(dtype).eps / 2 + 4 * err + rows * U) + coef.abs()[:, None] * lp.exp() * 4 * err + tiny
+    bound = bound + want.abs() * (8 * err if loss == "preference" else 0.0)
+    assert ((net.fc.bias.grad.double() - want.sum(0)).abs() <= bound.sum(0) * 1.01).all()
+    off = (net.fc.weight.grad.double() - want.T @ x.double()).abs()
+    assert (off <= (bound.T @ x.double().abs()) * 1.01 + rows * U * (want.abs().T @ x.double().abs())).all()
+    entries = want.abs().clone()
+    entries.scatter_(1, token[:, None], 0.0)
+    assert float(entries.median()) < 2.0 ** -24
+    cap.remove()
+
+
 def test_logits_of_any_layout_reach_the_loss(kfac_gpu):
     """Logits [batch, time, vocab], also as a transposed view: the same loss and gradients."""
     from fac_second_order_amd.capture import KfacCapture
