@@ -422,23 +422,26 @@ class KfacCapture:
 
     # the K-FAC step -------------------------------------------------------------
     def _curvature(self):
-        """What a step forms its factors from, (act, gout, xhat, BatchNorm gout): the score pass's tensors
-        of the samples that count, if there was one, or the loss's; None where no sample counts."""
+        """What a step forms its factors from, (act, gout, xhat, BatchNorm gout): of the layers that a score pass
+        reached its tensors of the samples that count, of the others the loss's; None where no sample counts."""
+        taken = tuple(list(ts) for ts in (self.act, self.gout, self.xhat, self.bgout))
         if all(g is None for g in (*self.score, *self.bscore)):
-            return self.act, self.gout, self.xhat, self.bgout
-        if any(g is None for g in (*self.score, *self.bscore)):
-            raise RuntimeError("a layer has no gradient from the model's logits")
+            return taken
         host, copied = self.counted
         if copied is not None:
             copied.synchronize()
         kept = host.nonzero()[:, 0]
-        taken = (self.act, self.score, self.xhat, self.bscore)
-        if len(kept) == len(host):
-            return taken
         if not len(kept):
             return None
-        kept = kept.to(self.act[0].device)
-        return tuple([t.index_select(0, kept) if t.shape[0] == len(host) else t for t in ts] for ts in taken)
+        some = kept.to(self.act[0].device) if len(kept) < len(host) else None
+        for ins, outs, scores in ((taken[0], taken[1], self.score), (taken[2], taken[3], self.bscore)):
+            for i, g in enumerate(scores):
+                if g is None:
+                    continue
+                outs[i] = g
+                if some is not None and len(g) == len(ins[i]) == len(host):
+                    ins[i], outs[i] = ins[i].index_select(0, some), g.index_select(0, some)
+        return taken
 
     def step(self, lr):
         if any(a is None for a in self.act) or any(g is None for g in self.gout):
@@ -460,11 +463,11 @@ class KfacCapture:
             taken = self._curvature()
             if taken is None and self.calls:  # no row counts: there is no curvature in the batch
                 refresh = False
-            else:
-                act, gout, xhat, bscore = taken or (self.act, self.score, self.xhat, self.bscore)
-                layers, fisher_bns = self._geometry(act, gout, xhat, bscore)
-                if self.bns and bscore is not self.bgout:
-                    bn_fisher = (fisher_bns, xhat, bscore)
+            elif taken is not None:
+                act, gout, xhat, bgout = taken
+                layers, fisher_bns = self._geometry(act, gout, xhat, bgout)
+                if any(g is not None for g in self.bscore):
+                    bn_fisher = (fisher_bns, xhat, bgout)
         self.kstep.step(act, gout, grads, self.xhat, self.bgout, ema_decay=decay, refresh=refresh,
                         weights=self.master, bn_params=self.bn_master, lr=lr, layers=layers, bn_layers=bns,
                         bn_fisher=bn_fisher)

@@ -441,3 +441,32 @@ def test_scales_of_other_types_and_refusals(passes):
         got.append([p.grad.clone() for p in net.parameters()] + [g.clone() for g in cap.gout])
     assert all(torch.equal(a, b) for a, b in zip(*got))
     cap.remove()
+
+
+def test_a_layer_that_the_logits_do_not_reach(passes, monkeypatch):
+    """A second head with a loss of its own, in a graph of its own: its factors take that loss's gradients
+    over all samples, beside those of the logits' scores."""
+    class Two(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.policy, self.value = torch.nn.Linear(5, 4), torch.nn.Linear(5, 1)
+
+        def kfac_modules(self):
+            return [(self.policy, None), (self.value, None)]
+
+    torch.manual_seed(16)
+    net = Two()
+    cap = cap_mod.KfacCapture(net)
+    drawn = torch.tensor([0, 1, 2, 3])
+    monkeypatch.setattr(cap, "_draw", lambda z: drawn)
+    x, mask = torch.randn(4, 5), torch.tensor([True, False, True, True])
+    logits, value = net.policy(x), net.value(x)
+    cap.policy_backward(logits, torch.zeros(4, dtype=torch.long), -torch.ones(4), torch.ones(4), mask=mask)
+    value.square().mean().backward()
+    cap.step(0.1)
+    (act, gout, *_), kw = cap.kstep.calls[-1]
+    assert [L.n for L in kw["layers"]] == [3, 4] and kw["refresh"]
+    assert torch.equal(act[0], x[mask].half()) and torch.equal(act[1], x.half())
+    assert torch.allclose(gout[0].float(), (F.one_hot(drawn, 4) - torch.softmax(logits.detach(), 1))[mask], **TOL)
+    assert torch.allclose(gout[1].float(), 2 * value.detach(), **TOL)
+    cap.remove()
