@@ -177,7 +177,8 @@ class KfacCapture:
         self.score = [None] * len(self.pairs)
         self.bscore = [None] * len(self.bns)
         self.score_scale = self.counted = None
-        self.loss_scale = 1.0  # what the gradients of a running backward pass are multiplied by
+        # of a running backward pass: what its gradients are multiplied by, and if it is one behind a score pass
+        self.loss_scale, self.own_loss = 1.0, False
         self.kstep = None
         self.calls = 0
         self.hooks = []
@@ -199,7 +200,6 @@ class KfacCapture:
             if torch.is_grad_enabled():
                 self.n = inp[0].shape[0]
                 self.act[i] = _nhwc_half(inp[0])
-                self.score[i] = None
         return hook
 
     def _bwd(self, i):
@@ -207,6 +207,8 @@ class KfacCapture:
             g = grad_out[0]
             if self.score_scale is None:
                 self.gout[i] = _nhwc_half(g * (self.n / self.loss_scale))
+                if not self.own_loss:
+                    self.score[i] = None
                 return
             # a convolution's Fisher is the sum over its positions, which its factors average
             places = math.sqrt(g.shape[2] * g.shape[3]) if g.dim() == 4 else 1.0
@@ -221,13 +223,14 @@ class KfacCapture:
                 xh = (x - mean) * torch.rsqrt(var + mod.eps)
                 self.xhat[i] = xh.permute(0, 2, 3, 1).reshape(x.shape[0], -1, x.shape[1]).to(
                     torch.float16).contiguous()
-                self.bscore[i] = None
         return hook
 
     def _bn_bwd(self, i):
         def hook(mod, grad_in, grad_out):
             if self.score_scale is None:
                 to, g = self.bgout, grad_out[0] * (self.n / self.loss_scale)
+                if not self.own_loss:
+                    self.bscore[i] = None
             else:
                 to, g = self.bscore, grad_out[0].float() * self.score_scale
             to[i] = g.permute(0, 2, 3, 1).reshape(g.shape[0], -1, g.shape[1]).to(torch.float16).contiguous()
@@ -366,19 +369,17 @@ class KfacCapture:
     def _backward(self, logits, z, d, counts, scale):
         """The backward pass of a loss whose gradient at the logits is d / scale, behind the one that the factors
         of the next step are formed from, if it forms any."""
+        self.score, self.bscore = [None] * len(self.score), [None] * len(self.bscore)
         if self.calls % self.refresh_every == 0:
             self._score_pass(logits, z, counts)
-        if scale == 1.0:
-            logits.backward(d.view(logits.shape))
-            return
-        held = [(p, p.grad) for p in self._leaves(logits)]
+        held = [] if scale == 1.0 else [(p, p.grad) for p in self._leaves(logits)]
         for p, _ in held:
             p.grad = None
-        self.loss_scale = scale
+        self.loss_scale, self.own_loss = scale, True
         try:
             logits.backward(d.view(logits.shape))
         finally:
-            self.loss_scale = 1.0
+            self.loss_scale, self.own_loss = 1.0, False
             for p, before in held:
                 if p.grad is not None:
                     p.grad.div_(scale)

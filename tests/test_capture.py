@@ -222,7 +222,7 @@ def test_factors_take_scores_of_the_rows_that_count(passes, monkeypatch, loss):
     for p, w in zip(net.parameters(), ref):
         assert torch.allclose(p.grad, w + (1.0 if p is net.a.weight else 0.0), rtol=1e-5, atol=1e-6)
     score = _score_grads(net, x, DRAWN, COUNTED.float(), [net.a, net.b])
-    net.zero_grad()                                                    # the forwards above took the scores away
+    net.zero_grad()                                                    # the gradients above took the scores away
     if loss == "policy":
         cap.policy_backward(net(x), TOKEN, **_policy_kw())
     else:
@@ -469,4 +469,21 @@ def test_a_layer_that_the_logits_do_not_reach(passes, monkeypatch):
     assert torch.equal(act[0], x[mask].half()) and torch.equal(act[1], x.half())
     assert torch.allclose(gout[0].float(), (F.one_hot(drawn, 4) - torch.softmax(logits.detach(), 1))[mask], **TOL)
     assert torch.allclose(gout[1].float(), 2 * value.detach(), **TOL)
+    cap.remove()
+
+
+def test_a_forward_before_the_step_leaves_the_scores(passes, monkeypatch):
+    """A forward pass with gradients on between the loss's backward pass and the step, as of an evaluation,
+    does not put the loss's gradients in the scores' place; another loss's backward pass does."""
+    torch.manual_seed(17)
+    net = Net()
+    cap = cap_mod.KfacCapture(net)
+    x, one = torch.randn(3, 5), torch.ones(3)
+    cap.policy_backward(net(x), torch.zeros(3, dtype=torch.long), -one, 0.001 * one)
+    score = [s.clone() for s in cap.score]
+    net(x)
+    cap.step(0.1)
+    assert all(torch.equal(a, b) for a, b in zip(cap.kstep.calls[-1][0][1], score))
+    F.cross_entropy(net(x), torch.zeros(3, dtype=torch.long)).backward()
+    assert cap.score == [None, None]
     cap.remove()
