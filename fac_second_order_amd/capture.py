@@ -237,6 +237,10 @@ class KfacCapture:
         return hook
 
     # geometry and parameter layouts -------------------------------------------
+    def _layers_of(self, *tensors):
+        """Layers of (act, gout, xhat, bgout) for a call; (None, None) where they are those the step was made for."""
+        return (None, None) if [t.shape for ts in tensors for t in ts] == self.shapes else self._geometry(*tensors)
+
     def _geometry(self, act=None, gout=None, xhat=None, bgout=None):
         """Layers of captured tensors, of the last passes' if none are given."""
         if act is None:
@@ -448,8 +452,10 @@ class KfacCapture:
         if any(a is None for a in self.act) or any(g is None for g in self.gout):
             raise RuntimeError("step() needs one forward and backward pass with the hooks in place")
         dev = self.act[0].device
-        layers, bns = self._geometry()
+        passes = self.act, self.gout, self.xhat, self.bgout
         if self.kstep is None:
+            layers, bns = self._geometry()
+            self.shapes = [t.shape for ts in passes for t in ts]
             self.kstep = KfacStep(layers, bns, dev, damping=self.damping, precond_accum=self.precond_accum,
                                   refine_inverse=self.refine_inverse, max_grad_norm=self.max_grad_norm,
                                   trust_radius=self.trust_radius)
@@ -460,13 +466,14 @@ class KfacCapture:
         refresh = self.calls % self.refresh_every == 0
         decay = 0.0 if self.calls == 0 else self.ema_decay
         act, gout, bn_fisher = self.act, self.gout, None
+        layers, bns = self._layers_of(*passes)
         if refresh:
             taken = self._curvature()
             if taken is None and self.calls:  # no row counts: there is no curvature in the batch
                 refresh = False
             elif taken is not None:
                 act, gout, xhat, bgout = taken
-                layers, fisher_bns = self._geometry(act, gout, xhat, bgout)
+                layers, fisher_bns = self._layers_of(*taken)
                 if any(g is not None for g in self.bscore):
                     bn_fisher = (fisher_bns, xhat, bgout)
         self.kstep.step(act, gout, grads, self.xhat, self.bgout, ema_decay=decay, refresh=refresh,

@@ -322,8 +322,9 @@ class KfacStep:
         bn_layers = _same_but_samples(bn_layers, self.bn_layers, K.kfac_bn._fields_, "bn_layers")
         self._make_room(layers, bn_layers, stream)
         if bn_fisher is not None:
-            _same_but_samples(bn_fisher[0], self.bn_layers, K.kfac_bn._fields_, "bn_layers")
-            self._make_room(layers, bn_fisher[0], stream)
+            fisher_layers = _same_but_samples(bn_fisher[0], self.bn_layers, K.kfac_bn._fields_, "bn_layers")
+            self._make_room(layers, fisher_layers, stream)
+            bn_fisher = (fisher_layers, *bn_fisher[1:])
         grads = self.clip(grads, stream)
         args = (layers, bn_layers, act, gout, grads, xhat, bn_gout, bn_fisher, ema_decay, refresh)
         if self.trust_radius is not None:

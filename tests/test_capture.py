@@ -70,6 +70,10 @@ class Recorder:
         self.made, self.options, self.calls = (layers, bns), kw, []
 
     def step(self, *args, **kw):
+        # layers of None: those it was made for
+        kw["layers"], kw["bn_layers"] = kw["layers"] or self.made[0], kw["bn_layers"] or self.made[1]
+        if kw["bn_fisher"] is not None:
+            kw["bn_fisher"] = (kw["bn_fisher"][0] or self.made[1], *kw["bn_fisher"][1:])
         self.calls.append(([list(a) for a in args], kw))   # the lists are filled again by the next pass
 
 
