@@ -149,8 +149,9 @@ class KfacCapture:
     range of its layer's factors, so where a factor is rank-deficient (batch smaller
     than its order) and the damping small, the preconditioning products cancel and
     amplify the inverses' fp32 error; the two options remove most of it. max_grad_norm
-    and trust_radius are passed to KfacStep too: they bound the gradients that are
-    preconditioned and the step that is taken. After policy_backward or preference_backward,
+    and trust_radius are passed to KfacStep too: they bound the layers' weight gradients
+    before those are preconditioned (BatchNorm's are not clipped), and the step that is
+    taken. After policy_backward or preference_backward,
     whose factors are the model's Fisher, trust_radius bounds its predicted KL divergence
     (the mean over the rows that count, to second order and as far as the Kronecker factors
     hold); after another loss's backward pass it bounds the quadratic form of that loss's
@@ -395,7 +396,8 @@ class KfacCapture:
         the model's logits [..., vocab], one token, old log-probability and advantage for
         each row, the rows those of the model's inputs in their order. The factors of the next
         step come from a second backward pass through the same graph (torch's generator
-        draws its tokens). The gradients run through the network multiplied by grad_scale, which is
+        draws its tokens), which the leaves' gradients do not see, but hooks on tensors and retained
+        gradients do. The gradients run through the network multiplied by grad_scale, which is
         divided out of what arrives at the leaves and the hooks: by default 1, and for fp16 logits the rows'
         number, as a power of two up to 2^14, since a mean over rows leaves most of a softmax below what an
         fp16 holds. Returns (stats, logp): the loss, its surrogate part, the mean KL and the clipped share; the
