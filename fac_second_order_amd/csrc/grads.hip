@@ -263,7 +263,7 @@ __device__ inline void second_part(const D& d, int64_t e0, int n, Factor f) {
   if constexpr (W == TRUST) {
     if (f.f != 0.f) apply_part<SIZE, NT>(d, e0, n, f.f);
   } else if constexpr (W == CLIP) {
-    if (f.f != 1.f || d.out != d.grad) scale_part<SIZE, NT>(d, e0, n, f);
+    if (f.f != 1.f || f.pre != 1.f || d.out != d.grad) scale_part<SIZE, NT>(d, e0, n, f);
   }
 }
 

@@ -132,6 +132,17 @@ def test_clip_by_a_factor_below_the_smallest_float(kfac_gpu, dtypes, n, scale, m
     assert all(o.any() for o in outs)
 
 
+@pytest.mark.parametrize("n", [4, 100000])
+def test_clip_in_place_by_a_factor_that_rounds_to_a_power(kfac_gpu, n):
+    """max / norm = 2^-126 (1 - 2^-31): its first part rounds to 1, and the gradients are scaled all the same."""
+    t = torch.zeros(n, device="cuda")
+    t[0], t[1] = 2.0 ** 100, 2.0 ** 85
+    norm = torch.empty(1, device="cuda")
+    kfac_gpu.kfac_grad_clip([t], [t], 2.0 ** -26, norm)
+    torch.cuda.synchronize()
+    assert float(norm) == 2.0 ** 100 and t[:2].tolist() == [2.0 ** -26, 2.0 ** -41]
+
+
 def test_norm_past_32_bit_offsets(kfac_gpu):
     """One tensor of more than 2^31 elements and 2^32 bytes, values at its ends and about 2^31."""
     n = (1 << 31) + 70001
