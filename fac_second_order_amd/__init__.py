@@ -13,6 +13,8 @@ from ._lib import (  # noqa: F401
     kfac_bn_diag_workspace, kfac_bn_diag, kfac_bn_update, kfac_bn_diag_noalloc,
     kfac_grad_norm_workspace, kfac_grad_norm, kfac_grad_clip, kfac_trust_update,
     kfac_policy_loss_workspace, kfac_policy_loss, kfac_preference_loss_workspace, kfac_preference_loss,
+    kfac_quantize_rows, kfac_dequantize_rows, kfac_linear_q8_workspace, kfac_linear_q8,
+    kfac_weight_grad_q8_workspace, kfac_weight_grad_q8, kfac_factors_q8_workspace, kfac_factors_q8,
     kfac_timing_kernels, kfac_kernel_name, kfac_timing_enable, kfac_timing_only, kfac_timing_reset,
     kfac_timing_read,
 )

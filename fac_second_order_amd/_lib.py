@@ -99,6 +99,16 @@ _sig("kfac_policy_loss", _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i32, _vp,
 _sig("kfac_preference_loss_workspace", _i32, _i32, _i32, _i32, _P(_sz))
 _sig("kfac_preference_loss", _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _f32, _f32, _f32, _vp,
      _vp, _vp, _vp, _i64, _vp, _sz, _vp)
+_sig("kfac_quantize_rows", _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp)
+_sig("kfac_dequantize_rows", _i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _vp)
+_sig("kfac_linear_q8_workspace", _i32, _i32, _i32, _i32, _P(_sz))
+_sig("kfac_linear_q8", _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64,
+     _vp, _sz, _vp)
+_sig("kfac_weight_grad_q8_workspace", _i32, _i32, _i32, _i32, _i32, _P(_sz))
+_sig("kfac_weight_grad_q8", _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _i32, _vp,
+     _sz, _vp)
+_sig("kfac_factors_q8_workspace", _i32, _i32, _vp, _vp, _vp, _P(_sz))
+_sig("kfac_factors_q8", _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _sz, _vp)
 _sig("kfac_timing_kernels", _i32)
 _sig("kfac_kernel_name", _c.c_char_p, _i32)
 _sig("kfac_timing_enable", _i32, _i32)
@@ -587,6 +597,153 @@ def kfac_preference_loss(logits, token, seq_begin, seq_logp, margin, loss, dlogi
         float(label_smoothing), float(grad_scale), _vector(seq_logp, f32, 2 * pairs, "seq_logp"),
         _vector(margin, f32, pairs, "margin"), loss_at, d, ldd, ws, wsb, _stream(stream)),
         "kfac_preference_loss")
+
+
+# rows in 8 bits ------------------------------------------------------------------
+
+def _rows(t, what, dtype=None):
+    """(rows, cols, dtype code or None, address, pitch) of a tensor of rows."""
+    if t.dim() != 2 or (t.dtype != dtype if dtype is not None else t.dtype not in _ANY_CODE):
+        raise TypeError(f"{what} must be [rows, cols] in {'float16, bfloat16 or float32' if dtype is None else dtype}")
+    rows, cols = t.shape
+    return rows, cols, _ANY_CODE.get(t.dtype), t.data_ptr(), _pitch(t, rows, cols, what)
+
+
+def _mask_at(mask, rows):
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("mask must be bool or uint8")
+    return _vector(mask, mask.dtype, rows, "mask")
+
+
+def _checkpoint(q, scale, rows=None, cols=None):
+    """(rows, cols, address and pitch of q, address of scale) of a checkpoint."""
+    r, c, _, at, ld = _rows(q, "q", torch.int8)
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"q must be [{rows if rows is not None else r}, {cols if cols is not None else c}]")
+    return r, c, at, ld, _vector(scale, torch.float32, r, "scale")
+
+
+def _here(stream, *tensors):
+    """Refuses tensors, or a stream, of another device than the current one."""
+    tensors = [t for t in tensors if t is not None]
+    _on_device(tensors, "every tensor of the call")
+    if stream is not None and stream.device != tensors[0].device:
+        raise ValueError("stream must be of the current HIP device")
+
+
+def kfac_quantize_rows(x, q, scale, mask=None, pow2=True, stream=None):
+    """q [rows, cols] int8, scale [rows] <- rows of x in 8 bits, scale a power of two or (pow2
+    False) as fine as float32 allows; rows with mask 0 get zeros (see kfac.h)."""
+    rows, cols, code, at, ld = _rows(x, "x")
+    _, _, q_at, q_ld, s_at = _checkpoint(q, scale, rows, cols)
+    m_at = _mask_at(mask, rows)
+    _here(stream, x, q, scale, mask)
+    _check(_lib.kfac_quantize_rows(rows, cols, code, at, ld, m_at, 1 if pow2 else 0, q_at, q_ld, s_at,
+                                   _stream(stream)), "kfac_quantize_rows")
+
+
+def kfac_dequantize_rows(q, scale, x, stream=None):
+    """x <- scale * q (float16, bfloat16 or float32; see kfac.h)."""
+    rows, cols, code, at, ld = _rows(x, "x")
+    _, _, q_at, q_ld, s_at = _checkpoint(q, scale, rows, cols)
+    _here(stream, x, q, scale)
+    _check(_lib.kfac_dequantize_rows(rows, cols, q_at, q_ld, s_at, code, at, ld, _stream(stream)),
+           "kfac_dequantize_rows")
+
+
+def kfac_linear_q8_workspace(rows, c_in, c_out):
+    out = _sz()
+    _check(_lib.kfac_linear_q8_workspace(int(rows), int(c_in), int(c_out), _c.byref(out)), "kfac_linear_q8_workspace")
+    return out.value
+
+
+def kfac_linear_q8(x, q, scale, w, w_scale, y, bias=None, mask=None, workspace=None, stream=None):
+    """y [rows, c_out] <- the product of rows and weights [c_out, c_in] in 8-bit integers, times
+    scale * w_scale, plus bias; q, scale <- x's checkpoint, or with x None the rows themselves
+    (see kfac.h)."""
+    rows, c_out, code, y_at, y_ld = _rows(y, "y")
+    _, c_in, q_at, q_ld, s_at = _checkpoint(q, scale, rows)
+    _, _, w_at, w_ld, ws_at = _checkpoint(w, w_scale, c_out, c_in)
+    x_at = x_ld = 0
+    if x is not None:
+        if x.shape != q.shape or x.dtype != y.dtype:
+            raise TypeError("x must have the shape of q and the type of y")
+        _, _, _, x_at, x_ld = _rows(x, "x")
+    b_at = None if bias is None else _vector(bias, y.dtype, c_out, "bias")
+    m_at = _mask_at(mask, rows)
+    _here(stream, x, q, scale, w, w_scale, y, bias, mask)
+    ws, wsb, held = _call_ws(workspace, kfac_linear_q8_workspace, (rows, c_in, c_out), y.device, stream)
+    _check(_lib.kfac_linear_q8(rows, c_in, c_out, code, x_at or None, x_ld, m_at, q_at, q_ld, s_at, w_at,
+                               w_ld, ws_at, b_at, y_at, y_ld, ws, wsb, _stream(stream)), "kfac_linear_q8")
+
+
+def kfac_weight_grad_q8_workspace(rows, c_in, c_out, dtype=torch.float32):
+    out = _sz()
+    _check(_lib.kfac_weight_grad_q8_workspace(int(rows), int(c_in), int(c_out), _ANY_CODE[dtype], _c.byref(out)),
+           "kfac_weight_grad_q8_workspace")
+    return out.value
+
+
+def kfac_weight_grad_q8(gout, q, scale, dweight, dbias=None, accumulate=False, workspace=None, stream=None):
+    """dweight [c_out, c_in] <- gout^T (scale * q), dbias [c_out] <- the column sums of gout, over
+    the rows whose scale is not 0; with accumulate added to what they hold (see kfac.h)."""
+    rows, c_out, code, g_at, g_ld = _rows(gout, "gout")
+    _, c_in, q_at, q_ld, s_at = _checkpoint(q, scale, rows)
+    _, _, _, w_at, w_ld = _rows(dweight, "dweight", torch.float32)
+    if dweight.shape != (c_out, c_in):
+        raise ValueError(f"dweight must be [{c_out}, {c_in}]")
+    b_at, b_inc = None, 1
+    if dbias is not None:
+        if dbias.dtype != torch.float32 or dbias.shape != (c_out,) or (c_out > 1 and dbias.stride(0) < 1):
+            raise TypeError(f"dbias must be a float32 tensor of {c_out}")
+        b_at, b_inc = dbias.data_ptr(), max(1, dbias.stride(0))
+    _here(stream, gout, q, scale, dweight, dbias)
+    ws, wsb, held = _call_ws(workspace, kfac_weight_grad_q8_workspace, (rows, c_in, c_out, gout.dtype), gout.device,
+                             stream)
+    _check(_lib.kfac_weight_grad_q8(rows, c_in, c_out, code, g_at, g_ld, q_at, q_ld, s_at, w_at, w_ld, b_at, b_inc,
+                                    1 if accumulate else 0, ws, wsb, _stream(stream)), "kfac_weight_grad_q8")
+
+
+def _per_layer(bias, n):
+    bias = [1 if b else 0 for b in bias] if isinstance(bias, (list, tuple)) else [1 if bias else 0] * n
+    if len(bias) != n:
+        raise ValueError("bias needs one entry for each layer")
+    return bias
+
+
+def kfac_factors_q8_workspace(rows, cols, bias):
+    out = _sz()
+    rows, cols = list(rows), list(cols)
+    bias = _per_layer(bias, len(rows))
+    if len(cols) != len(rows):
+        raise ValueError("rows and cols need one entry for each layer")
+    r, c, b = _halfwords(rows), _halfwords(cols), _halfwords(bias)
+    _check(_lib.kfac_factors_q8_workspace(len(rows), _at(r), _at(c), _at(b), _c.byref(out)), "kfac_factors_q8_workspace")
+    return out.value
+
+
+def kfac_factors_q8(q, scale, A_packed, A_full=None, bias=False, ema_decay=0.0, workspace=None, stream=None):
+    """A_packed[l] <- packed factor of layer l from its checkpoint q[l], scale[l], with bias (one
+    for all layers, or a list) the column of ones; A_full[l] as in kfac_factors_full (see kfac.h)."""
+    n = len(q)
+    if len(scale) != n or len(A_packed) != n or (A_full is not None and len(A_full) != n):
+        raise ValueError("q, scale, A_packed and A_full need one entry for each layer")
+    bias = _per_layer(bias, n)
+    full = [None] * n if A_full is None else list(A_full)
+    if n == 0:
+        return
+    rows, cols, q_at, q_ld, s_at = map(list, zip(*map(_checkpoint, q, scale)))
+    orders = [c + b for c, b in zip(cols, bias)]
+    p_at = [_vector(p, torch.float32, d * (d + 1) // 2, "A_packed") for p, d in zip(A_packed, orders)]
+    f_at = [0 if f is None else _vector(f, torch.float32, d * d, "A_full") for f, d in zip(full, orders)]
+    _here(stream, *q, *scale, *A_packed, *full)
+    ws, wsb, held = _call_ws(workspace, kfac_factors_q8_workspace, (rows, cols, bias), q[0].device, stream)
+    r, c, b, qa, ql, sa, pa, fa = (_halfwords(rows), _halfwords(cols), _halfwords(bias), _words(q_at), _words(q_ld),
+                                   _words(s_at), _words(p_at), _words(f_at))
+    _check(_lib.kfac_factors_q8(n, _at(r), _at(c), _at(b), _at(qa), _at(ql), _at(sa), _at(pa), _at(fa), float(ema_decay),
+                                ws, wsb, _stream(stream)), "kfac_factors_q8")
 
 
 # timing -------------------------------------------------------------------

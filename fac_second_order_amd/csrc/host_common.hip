@@ -144,7 +144,8 @@ static const char* const kKernelNames[K_TOTAL] = {
     "grad_scale_kernel",  "trust_apply_kernel",  "grads_one_kernel",   "loss_count_kernel",
     "loss_nonempty_kernel", "policy_rows_kernel", "policy_terms_kernel", "policy_finish_kernel", "policy_part_kernel",
     "policy_join_kernel", "pref_rows_kernel",
-    "pref_pairs_kernel",  "pref_finish_kernel",  "pref_grad_kernel"};
+    "pref_pairs_kernel",  "pref_finish_kernel",  "pref_grad_kernel",  "quantize_rows_kernel", "dequantize_rows_kernel",
+    "linear_q8_kernel",   "grad_q8_kernel",      "grad_q8_join_kernel", "factor_q8_kernel",   "factor_q8_join_kernel"};
 
 }  // namespace kfac
 

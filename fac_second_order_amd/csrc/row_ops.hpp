@@ -26,6 +26,13 @@ enum RowKernelId {
   K_PREF_PAIRS,
   K_PREF_FINISH,
   K_PREF_GRAD,
+  K_QUANTIZE,
+  K_DEQUANTIZE,
+  K_LINEAR_Q8,
+  K_GRAD_Q8,           // q8_tn_kernel of the weight gradient
+  K_GRAD_Q8_JOIN,
+  K_FACTOR_Q8,         // q8_tn_kernel of the factors
+  K_FACTOR_Q8_JOIN,
   K_TOTAL
 };
 

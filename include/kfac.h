@@ -411,6 +411,84 @@ kfac_status kfac_preference_loss(int32_t rows, int32_t vocab, kfac_dtype dtype, 
                                  size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Rows in 8 bits. A layer's input rows x [rows, cols], kept from the forward pass to the
+ * backward pass and the step as a checkpoint: whole numbers q and a scale for each row,
+ * standing for scale[t] * q[t]. Rows lie ld elements apart (ld >= cols); 64-bit offsets.
+ * scale[t] = 0 marks a row that takes no part: in the calls below nothing of it is used, nor
+ * of its gradient, which may hold anything. scale[t] = NaN marks a row that held an infinity
+ * or a NaN: what it takes part in is NaN. rows may be 0. No output may share bytes with
+ * another buffer of the call, nor the workspace with any.
+ *
+ * kfac_quantize_rows - with m = max |x[t]| over the row:
+ *   pow2 = 1: scale[t] = the smallest power of two >= max(m / 127, 2^-126);
+ *   pow2 = 0: scale[t] = max(m / 127 rounded to fp32, 2^-126);
+ *   m = 0: scale[t] = 1. q = x / scale[t], rounded half to even from its exact value, held to
+ *   [-127, 127] (to [-63, 63] at the largest power of two, 2^122, so that scale * q is finite).
+ * A row with mask[t] = 0 (uint8, NULL: all ones) is not read: q and scale get zeros. With an
+ * infinity or a NaN in a row scale is NaN and q zeros. A power of two makes scale * q exact in
+ * bfloat16, and within its range in binary16, for the products below.
+ *
+ * kfac_dequantize_rows - x = scale[t] * q, formed in fp32, rounded to dtype, values beyond the
+ * largest of the type held to it. A scale of 0 gives zeros, one of NaN NaN.
+ * ------------------------------------------------------------------------- */
+kfac_status kfac_quantize_rows(int32_t rows, int32_t cols, kfac_dtype dtype, const void* x, int64_t ld_x,
+                               const uint8_t* mask, int32_t pow2, int8_t* q, int64_t ld_q, float* scale,
+                               void* stream);
+kfac_status kfac_dequantize_rows(int32_t rows, int32_t cols, const int8_t* q, int64_t ld_q, const float* scale,
+                                 kfac_dtype dtype, void* x, int64_t ld_x, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kfac_linear_q8 - a fully connected layer in 8-bit integers, with a scale for each token and
+ * each output channel:
+ *   y[t][o] = fp32(sum_k q[t][k] w[o][k]) * scale[t] * w_scale[o] + bias[o].
+ * w [c_out, c_in] at pitch ld_w and w_scale are kfac_quantize_rows' of the weights (pow2 0 is
+ * the finer one). x [rows, c_in], bias (NULL: none) and y have the type dtype; the sum is
+ * exact in 32 bits, the rest is formed in fp32 and rounded once. With x, q and scale are
+ * outputs: the call first quantises x (pow2 1; mask as there), and they are the checkpoint for
+ * the backward pass. x NULL: q and scale are given (mask NULL). A scale of 0 gives y = bias.
+ * c_in of 2^17 or more gives KFAC_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+kfac_status kfac_linear_q8_workspace(int32_t rows, int32_t c_in, int32_t c_out, size_t* bytes);
+kfac_status kfac_linear_q8(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype, const void* x, int64_t ld_x,
+                           const uint8_t* mask, int8_t* q, int64_t ld_q, float* scale, const int8_t* w, int64_t ld_w,
+                           const float* w_scale, const void* bias, void* y, int64_t ld_y, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kfac_weight_grad_q8 - the weight gradient of a fully connected layer from its checkpoint:
+ *   dweight[o][k] = sum_t gout[t][o] scale[t] q[t][k],  dbias[o] = sum_t gout[t][o]
+ * over the rows with scale[t] != 0. gout [rows, c_out] is fp16, bf16 or fp32 (dtype); dweight
+ * [c_out, c_in] at pitch ld_dw and dbias (NULL: none), inc_db elements apart, are fp32: with
+ * ld_dw = inc_db = c_in + 1 and dbias = dweight + c_in the matrix that kfac_precondition reads.
+ * accumulate = 1 adds to what they hold. With scales that are powers of two the products are
+ * exact (fp16: those of rows whose scale is at least 2^-29 of the largest) and summed in fp32;
+ * with others scale * q is rounded to 16 bits first. Deterministic.
+ * ------------------------------------------------------------------------- */
+kfac_status kfac_weight_grad_q8_workspace(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype, size_t* bytes);
+kfac_status kfac_weight_grad_q8(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype, const void* gout,
+                                int64_t ld_g, const int8_t* q, int64_t ld_q, const float* scale, float* dweight,
+                                int64_t ld_dw, float* dbias, int64_t inc_db, int32_t accumulate, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kfac_factors_q8 - the factors A of `count` fully connected layers ([OTUNYM] eq. (5)) from
+ * their checkpoints: with a_t = scale[t] q[t], and behind it the bias column's 1 where bias[l]
+ * is 1,
+ *   A_l = (1/C) sum_t a_t a_t^T over the C rows with scale[t] != 0,
+ * written like kfac_factors_full's: packed, and where A_full (NULL, or an entry of it NULL) is
+ * given into the upper triangle of a full matrix too; ema_decay as there. A layer without a row
+ * that counts keeps its stored factor, or gets zeros with ema_decay = 0. Host arrays: rows,
+ * cols, bias, q, ld_q, scale, A_packed, A_full. Scales as in kfac_weight_grad_q8 (2^-29 of the
+ * largest). Deterministic.
+ * ------------------------------------------------------------------------- */
+kfac_status kfac_factors_q8_workspace(int32_t count, const int32_t* rows, const int32_t* cols, const int32_t* bias,
+                                      size_t* bytes);
+kfac_status kfac_factors_q8(int32_t count, const int32_t* rows, const int32_t* cols, const int32_t* bias,
+                            const int8_t* const* q, const int64_t* ld_q, const float* const* scale,
+                            float* const* A_packed, float* const* A_full, float ema_decay, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Per-kernel event timing, for measurement. When enabled on a thread, every
  * kernel the library launches from that thread is bracketed by two HIP events on
  * the launch stream. kfac_timing_read synchronises those events and returns, per

@@ -1,0 +1,371 @@
+"""Rows in 8 bits, the integer product, and the gradient and factor formed from them, on the
+GPU against fp64.
+
+Bounds. Codes and scales are equal to the oracle's. A value read back is one fp32 product and one
+rounding to its type. The integer product's sum is exact; its conversion, two products and the
+sum with the bias are four roundings of 2^-24 of |part| + |bias|, and one to the type. Gradients and
+factors are sums of exact products in fp32, whose partial sums never exceed the sum of the
+magnitudes: n terms lose at most n 2^-23 of that (2^-23 where the matrix unit cuts instead of
+rounding), and a few more roundings follow. Inputs whose sums stay whole numbers below 2^24 are
+exact in any order: there the results are equal."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import say
+from loss_cases import FLOOR, HALF_STEP, U, host64
+from oracle import q8_oracle as qo
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+TYPES = [F16, BF16, F32]
+
+
+def host(t):
+    return t.detach().cpu().numpy()
+
+
+def pitched(rows, cols, dtype, pad=0, fill=7):
+    """A [rows, cols] tensor whose rows lie cols + pad apart, and the buffer that it is a part of."""
+    wide = torch.full((rows, cols + pad), fill, dtype=dtype, device="cuda")
+    return wide[:, :cols], wide
+
+
+def rows_of(seed, rows, cols, dtype, pad=0, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(spread * torch.randn(rows, 1, generator=g))
+    out, _ = pitched(rows, cols, dtype, pad)
+    out.copy_(x.to(dtype))
+    return out
+
+
+def quantize(kfac, x, mask=None, pow2=True, pad=0):
+    q, wide = pitched(*x.shape, torch.int8, pad)
+    scale = torch.full((x.shape[0],), 7.0, device="cuda")
+    kfac.kfac_quantize_rows(x, q, scale, mask=mask, pow2=pow2)
+    torch.cuda.synchronize()
+    assert (wide[:, x.shape[1]:] == 7).all()
+    return q, scale
+
+
+def same(a, b):
+    return np.array_equal(np.asarray(a, dtype=np.float64), np.asarray(b, dtype=np.float64), equal_nan=True)
+
+
+COLS = [1, 2, 3, 7, 8, 15, 16, 17, 63, 64, 65, 255, 257, 1001, 1024, 2049, 4096, 4099, 8200, 16400, 40001]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("cols", COLS)
+def test_quantize_rows(kfac_gpu, dtype, cols):
+    for pow2 in (True, False):
+        for pad in (0, 5):
+            rows = 5 if cols > 2000 else 37
+            x = rows_of(cols + pad, rows, cols, dtype, pad, spread=3.0 if dtype != F16 else 0.5)
+            mask = torch.tensor([t % 3 != 1 for t in range(rows)], device="cuda")
+            for m in (None, mask, mask.to(torch.uint8) * 2):
+                q, s = quantize(kfac_gpu, x, m, pow2, pad)
+                want, scale = qo.quantize_rows(host64(x), None if m is None else host(m), pow2)
+                assert same(host(s), scale) and same(host(q), want), (cols, pow2, pad)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_every_half(kfac_gpu, dtype):
+    """Quotients at, just below and just above every half step."""
+    top = 127.0
+    for s in (1.0, 2.0 ** -9):
+        halves = torch.arange(-126, 127, dtype=torch.float64) + 0.5
+        near = torch.cat([halves, halves * (1 + 2.0 ** -20), halves * (1 - 2.0 ** -20), torch.tensor([top, -top])]) * s
+        x = near.to(dtype).cuda().repeat(3, 1).contiguous()
+        for pow2 in (True, False):
+            q, scale = quantize(kfac_gpu, x, None, pow2)
+            want, ws = qo.quantize_rows(host64(x), None, pow2)
+            assert same(host(scale), ws) and same(host(q), want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("cols", [1, 9, 300, 5000])
+def test_quantize_special_rows(kfac_gpu, dtype, cols):
+    inf, nan, big = float("inf"), float("nan"), torch.finfo(dtype).max
+    rows = [inf, -inf, nan, 0.0, -0.0, big, -big, torch.finfo(dtype).smallest_normal, torch.finfo(dtype).tiny / 4, 1.0]
+    x = torch.zeros(len(rows), cols)
+    x[:, cols // 2] = torch.tensor(rows)
+    x[-1, 0] = 1.0
+    x = x.to(dtype).cuda()
+    for mask in (None, torch.tensor([0, 1] * 5, device="cuda", dtype=torch.uint8)):
+        for pow2 in (True, False):
+            q, s = quantize(kfac_gpu, x, mask, pow2)
+            want, scale = qo.quantize_rows(host64(x), None if mask is None else host(mask), pow2)
+            assert same(host(s), scale) and same(host(q), want)
+            out = torch.full_like(x, 7.0)
+            kfac_gpu.kfac_dequantize_rows(q, s, out)
+            v = qo.row_values(want, scale)
+            assert (host64(out)[np.isnan(scale)] != host64(out)[np.isnan(scale)]).all()
+            fine = ~np.isnan(scale)
+            assert np.isfinite(host64(out)[fine]).all()
+            if pow2:
+                assert same(host64(out)[fine], np.clip(v[fine], -big, big))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (3, 7, 2), (65, 129, 0), (33, 1001, 7), (17, 4096, 0), (2, 20003, 1)])
+def test_dequantize_rows(kfac_gpu, dtype, rows, cols, pad):
+    g = torch.Generator().manual_seed(rows)
+    for pow2 in (True, False):
+        q, _ = pitched(rows, cols, torch.int8, pad)
+        q.copy_(torch.randint(-128, 128, (rows, cols), generator=g))
+        s = torch.exp2(torch.randint(-9, 9, (rows,), generator=g).float()) if pow2 else torch.rand(rows, generator=g) + 0.1
+        out, wide = pitched(rows, cols, dtype, pad)
+        kfac_gpu.kfac_dequantize_rows(q, s.cuda(), out)
+        v = qo.row_values(host(q), s.numpy())
+        err = np.abs(host64(out) - v)
+        if pow2:
+            assert not err.any()
+        else:
+            assert (err <= np.abs(v) * (U + (HALF_STEP[dtype] if dtype != F32 else 0)) * 1.01).all()
+        assert (wide[:, cols:] == 7).all()
+
+
+def codes(seed, rows, cols, pad=0, most=127):
+    g = torch.Generator().manual_seed(seed)
+    q, _ = pitched(rows, cols, torch.int8, pad)
+    q.copy_(torch.randint(-most, most + 1, (rows, cols), generator=g))
+    return q
+
+
+LINEAR = [(1, 1, 1), (1, 64, 5), (1, 1000, 1001), (2, 4096, 64), (3, 17, 33), (5, 4099, 130), (8, 256, 256), (16, 512, 100),
+          (17, 96, 257), (31, 2048, 1000), (64, 128, 64), (65, 65, 65), (128, 4096, 128), (200, 333, 777), (257, 1024, 512),
+          (513, 160, 300), (1024, 64, 1024), (1000, 2500, 260)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,c_in,c_out", LINEAR)
+def test_linear(kfac_gpu, dtype, rows, c_in, c_out):
+    for pad, biased, given in ((0, True, False), (3, False, True)):
+        x = rows_of(rows + pad, rows, c_in, dtype, pad)
+        w, v = codes(c_in, c_out, c_in, pad), torch.rand(c_out, device="cuda") * 0.01 + 0.001
+        b = torch.randn(c_out, device="cuda").to(dtype) if biased else None
+        mask = torch.tensor([t % 5 != 3 for t in range(rows)], device="cuda") if pad else None
+        q, q_wide = pitched(rows, c_in, torch.int8, pad)
+        s = torch.full((rows,), 7.0, device="cuda")
+        y, wide = pitched(rows, c_out, dtype, pad)
+        if given:
+            kfac_gpu.kfac_quantize_rows(x, q, s, mask=mask)
+            kfac_gpu.kfac_linear_q8(None, q, s, w, v, y, bias=b)
+        else:
+            kfac_gpu.kfac_linear_q8(x, q, s, w, v, y, bias=b, mask=mask)
+        want_q, want_s = qo.quantize_rows(host64(x), None if mask is None else host(mask))
+        assert same(host(q), want_q) and same(host(s), want_s)
+        want, size = qo.linear(want_q, want_s, host(w), host64(v), None if b is None else host64(b))
+        bound = 4 * U * size * 1.01 + (HALF_STEP[dtype] * np.abs(want) * 1.01 if dtype != F32 else 0) + FLOOR[dtype]
+        assert (np.abs(host64(y) - want) <= bound).all()
+        assert (wide[:, c_out:] == 7).all() and (q_wide[:, c_in:] == 7).all()
+
+
+def test_linear_sums_are_exact(kfac_gpu):
+    """Every code at its largest, sums up to 2^31: no int32 overflows, none is rounded before its end."""
+    c_in = 131071
+    q = torch.full((3, c_in), -128, dtype=torch.int8, device="cuda")
+    q[1] = 127
+    w = torch.full((2, c_in), -128, dtype=torch.int8, device="cuda")
+    w[1, ::2] = 127
+    one = torch.ones(3, device="cuda")
+    y = torch.zeros(3, 2, device="cuda")
+    kfac_gpu.kfac_linear_q8(None, q, one, w, one[:2].contiguous(), y)
+    want = host(q).astype(np.int64) @ host(w).astype(np.int64).T
+    assert same(host(y), want.astype(np.float32))
+
+
+def grads_of(seed, rows, cols, dtype, pad=0, whole=False):
+    g = torch.Generator().manual_seed(seed)
+    out, _ = pitched(rows, cols, dtype, pad)
+    out.copy_(torch.randint(-3, 4, (rows, cols), generator=g) if whole else torch.randn(rows, cols, generator=g) * 0.01)
+    return out
+
+
+def scales_of(seed, rows, zeros=True):
+    g = torch.Generator().manual_seed(seed)
+    s = torch.exp2(torch.randint(-2, 2, (rows,), generator=g).float())
+    if zeros and rows > 1:
+        s[torch.rand(rows, generator=g) < 0.2] = 0.0
+    return s.cuda()
+
+
+def grad(kfac, g, q, s, biased, matrix, accumulate=False, start=0.0):
+    c_out, c_in = g.shape[1], q.shape[1]
+    out = torch.full((c_out, c_in + (1 if biased else 0)), start, device="cuda")
+    if matrix or not biased:
+        dw, db = out[:, :c_in], out[:, c_in] if biased else None
+    else:
+        dw, db = out[:, :c_in].contiguous(), out[:, c_in].contiguous()
+    kfac.kfac_weight_grad_q8(g, q, s, dw, dbias=db, accumulate=accumulate)
+    torch.cuda.synchronize()
+    return host64(dw), None if db is None else host64(db)
+
+
+GRAD = [(1, 1, 1), (1, 200, 3), (2, 8, 8), (7, 33, 65), (31, 130, 127), (32, 128, 128), (33, 129, 257), (64, 256, 256),
+        (65, 300, 40), (300, 1001, 77), (513, 64, 1000), (2048, 100, 60), (2049, 260, 250), (5000, 31, 17), (4100, 513, 300)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,c_in,c_out", GRAD)
+def test_weight_grad_of_whole_numbers(kfac_gpu, dtype, rows, c_in, c_out):
+    for pad, biased, matrix in ((0, True, True), (3, True, False), (1, False, False)):
+        q, s = codes(rows + pad, rows, c_in, pad, most=20), scales_of(rows, rows)
+        g = grads_of(c_in, rows, c_out, dtype, pad, whole=True)
+        dw, db, size, _ = qo.weight_grad(host64(g), host(q), host(s))
+        assert size.max() * 4 < 2 ** 24
+        got, gb = grad(kfac_gpu, g, q, s, biased, matrix)
+        assert same(got, dw) and (not biased or same(gb, db))
+        got, gb = grad(kfac_gpu, g, q, s, biased, matrix, accumulate=True, start=5.0)
+        assert same(got, dw + 5) and (not biased or same(gb, db + 5))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,c_in,c_out", [(33, 129, 57), (300, 256, 260), (1500, 70, 300)])
+def test_weight_grad(kfac_gpu, dtype, rows, c_in, c_out):
+    x = rows_of(1, rows, c_in, dtype, spread=0.5)
+    q, s = quantize(kfac_gpu, x)
+    g = grads_of(2, rows, c_out, dtype)
+    dw, db, size, bsize = qo.weight_grad(host64(g), host(q), host(s))
+    got, gb = grad(kfac_gpu, g, q, s, True, True)
+    n = rows * (3 if dtype == F32 else 1) + 8
+    assert (np.abs(got - dw) <= n * 2 * U * size).all()
+    assert (np.abs(gb - db) <= n * 2 * U * bsize).all()
+    say(dtype, rows, "relF", np.linalg.norm(got - dw) / np.linalg.norm(dw))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weight_grad_rows_that_take_no_part(kfac_gpu, dtype):
+    """Gradients of rows with scale 0 may hold anything; a row with scale NaN shows everywhere."""
+    rows, c_in, c_out = 150, 40, 30
+    q, s = codes(1, rows, c_in, most=20), scales_of(2, rows)
+    g = grads_of(3, rows, c_out, dtype, whole=True)
+    dw, db, _, _ = qo.weight_grad(host64(g), host(q), host(s))
+    g[s == 0] = float("nan")
+    q[s == 0] = 111
+    got, gb = grad(kfac_gpu, g, q, s, True, True)
+    assert same(got, dw) and same(gb, db)
+    s[:] = 0
+    got, gb = grad(kfac_gpu, g, q, s, True, True)
+    assert not got.any() and not gb.any()
+    s[77] = float("nan")
+    g[77] = 1.0
+    q[77] = 0
+    got, gb = grad(kfac_gpu, g, q, s, True, True)
+    assert np.isnan(got).all() and (gb == 1).all()
+    # an infinite gradient reaches its own outputs alone
+    s[:] = 1
+    g[:] = 1
+    g[3, 4] = float("inf")
+    q[:] = 1
+    got, gb = grad(kfac_gpu, g, q, s, True, True)
+    assert (got[4] == np.inf).all() and gb[4] == np.inf and np.isfinite(np.delete(got, 4, 0)).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weight_grad_of_far_scales(kfac_gpu, dtype):
+    """Rows of very different size: exact where the documentation says so."""
+    rows = 24
+    e = torch.arange(rows) - 20.0
+    s = torch.exp2(e).cuda()
+    q = codes(5, rows, 50)
+    g = torch.zeros(rows, rows, dtype=dtype, device="cuda")
+    g.fill_diagonal_(1.0)  # output o is row o alone
+    got, _ = grad(kfac_gpu, g, q, s, False, False)
+    assert same(got, qo.row_values(host(q), host64(s)))
+    for far in (2.0 ** 100, 2.0 ** -100):
+        got, _ = grad(kfac_gpu, g, q, s * far, False, False)
+        assert same(got, qo.row_values(host(q), host64(s) * far))
+
+
+def factors(kfac, layers, bias, full=False, decay=0.0, start=None, **kw):
+    """Packed factors (and the full ones) of [(q, s)]."""
+    orders = [q.shape[1] + (1 if bias else 0) for q, _ in layers]
+    packed = [torch.full((d * (d + 1) // 2,), 3.0, device="cuda") if start is None else start[i].clone()
+              for i, d in enumerate(orders)]
+    fulls = [torch.full((d, d), 9.0, device="cuda") for d in orders] if full else None
+    kfac.kfac_factors_q8([q for q, _ in layers], [s for _, s in layers], packed, A_full=fulls, bias=bias, ema_decay=decay,
+                         **kw)
+    torch.cuda.synchronize()
+    if full:
+        for f, p, d in zip(fulls, packed, orders):
+            i, j = np.triu_indices(d)
+            assert same(host(f)[i, j], host(p))
+            assert (host(f)[np.tril_indices(d, -1)] == 9).all()
+    return packed
+
+
+FACTOR = [(1, 1), (1, 5), (2, 64), (31, 128), (33, 129), (64, 255), (65, 257), (300, 100), (513, 384), (2048, 60),
+          (2049, 130), (5000, 33), (4100, 300)]
+
+
+@pytest.mark.parametrize("rows,cols", FACTOR)
+def test_factor_of_whole_numbers(kfac_gpu, rows, cols):
+    for pad, bias in ((0, True), (3, False)):
+        q, s = codes(rows + pad, rows, cols, pad, most=9), scales_of(cols, rows)
+        raw, size = qo.factor_packed(host(q), host(s), bias)
+        live = int((host(s) != 0).sum())
+        assert size.max() * live * 16 < 2 ** 24
+        got = host(factors(kfac_gpu, [(q, s)], bias, full=True)[0])
+        inv = np.float32(1) / np.float32(live) if live else np.float32(0)
+        want = (raw * live).astype(np.float32) * inv
+        # the corner is 1; others one product with the rounded 1 / C, in either order of a power of two
+        if bias and live:
+            want[-1] = 1
+        assert same(got, want), (rows, cols, np.abs(got - want).max())
+
+
+def test_factors_of_several_layers(kfac_gpu):
+    layers, xs = [], []
+    for i, (rows, cols) in enumerate([(700, 130), (33, 260), (1, 7), (2500, 64), (90, 40)]):
+        x = rows_of(i, rows, cols, F16, pad=i, spread=0.5)
+        xs.append(x)
+        layers.append(quantize(kfac_gpu, x, pad=i))
+    alone = [factors(kfac_gpu, [l], True)[0] for l in layers]
+    together = factors(kfac_gpu, layers, True, full=True)
+    for (q, s), a, t in zip(layers, alone, together):
+        assert same(host(a), host(t))
+        want, size = qo.factor_packed(host(q), host(s), True)
+        assert (np.abs(host64(a) - want) <= (q.shape[0] + 8) * 2 * U * size).all()
+        say(q.shape, "relF", np.linalg.norm(host64(a) - want) / np.linalg.norm(want))
+    old = [torch.rand_like(p) for p in together]
+    blended = factors(kfac_gpu, layers, True, full=True, decay=0.75, start=old)
+    for (q, s), o, b in zip(layers, old, blended):
+        want, size = qo.factor_packed(host(q), host(s), True, host64(o), 0.75)
+        assert (np.abs(host64(b) - want) <= (q.shape[0] + 12) * 2 * U * size).all()
+
+
+@pytest.mark.parametrize("bias", [True, False])
+def test_factor_without_rows(kfac_gpu, bias):
+    q, s = codes(1, 70, 50), torch.zeros(70, device="cuda")
+    none = (torch.zeros(0, 50, dtype=torch.int8, device="cuda"), torch.zeros(0, device="cuda"))
+    for layer in ((q, s), none):
+        assert not host(factors(kfac_gpu, [layer], bias, full=True)[0]).any()
+        old = [torch.rand(51 * 52 // 2 if bias else 50 * 51 // 2, device="cuda")]
+        assert same(host(factors(kfac_gpu, [layer], bias, full=True, decay=0.9, start=old)[0]), host(old[0]))
+
+
+def test_nothing_to_do(kfac_gpu):
+    e8, e32 = torch.zeros(0, 5, dtype=torch.int8, device="cuda"), torch.zeros(0, device="cuda")
+    x = torch.zeros(0, 5, device="cuda")
+    kfac_gpu.kfac_quantize_rows(x, e8, e32)
+    kfac_gpu.kfac_dequantize_rows(e8, e32, x)
+    w, v = codes(1, 4, 5), torch.ones(4, device="cuda")
+    kfac_gpu.kfac_linear_q8(x, e8, e32, w, v, torch.zeros(0, 4, device="cuda"))
+    # no input channels: the bias alone, and the bias gradient alone
+    q, s = torch.zeros(3, 0, dtype=torch.int8, device="cuda"), torch.ones(3, device="cuda")
+    y = torch.full((3, 4), 9.0, device="cuda")
+    b = torch.arange(4.0, device="cuda")
+    kfac_gpu.kfac_linear_q8(None, q, s, torch.zeros(4, 0, dtype=torch.int8, device="cuda"), v, y, bias=b)
+    assert same(host(y), np.tile(np.arange(4.0), (3, 1)))
+    g, db = torch.ones(3, 4, device="cuda"), torch.full((4,), 9.0, device="cuda")
+    kfac_gpu.kfac_weight_grad_q8(g, q, s, torch.zeros(4, 0, device="cuda"), dbias=db)
+    assert same(host(db), [3] * 4)
+    # no rows: zeros, or what was there
+    dw = torch.full((4, 5), 9.0, device="cuda")
+    kfac_gpu.kfac_weight_grad_q8(torch.zeros(0, 4, device="cuda"), e8, e32, dw, accumulate=True)
+    assert (dw == 9).all()
+    kfac_gpu.kfac_weight_grad_q8(torch.zeros(0, 4, device="cuda"), e8, e32, dw)
+    assert (dw == 0).all()
