@@ -31,61 +31,151 @@ __device__ inline float row_scale(unsigned amax) {
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum with it holds the rounded whole number in its low bits
 
+// How a row of largest magnitude `amax` (its bits) is written: a scale, its reciprocal, and the largest code.
 struct RowCode {
   float s, inv;
-  int most;  // 127, or 63 where 64 s would be infinite
+  int most;  // 127; 63 where 64 s would be infinite; 0 in a row with an infinity or a NaN
 };
 
 template <bool POW2>
 __device__ inline RowCode row_code(unsigned amax) {
   RowCode c;
   c.s = row_scale<POW2>(amax);
-  const bool bad = amax >= 0x7f800000u;
-  c.inv = bad ? 0.f : 1.f / c.s;
-  c.most = POW2 && !bad && c.s >= 5.3169119831396635e36f ? 63 : 127;  // 2^122
+  c.inv = 1.f / c.s;
+  c.most = amax >= 0x7f800000u ? 0 : POW2 && c.s >= 5.316911983139664e36f ? 63 : 127;  // 2^122
   return c;
 }
 
-// q of one element, as an integer. A row with an infinity or a NaN has none: all zeros.
+// The code of one element in the low 8 bits.
 template <bool POW2>
-__device__ inline int code_of(float x, const RowCode& c) {
-  if (c.inv == 0.f) return 0;
-  float t = fmaf(x, c.inv, kMagic) - kMagic;
-  if (!POW2) {
+__device__ inline unsigned code_of(float x, const RowCode& c) {
+  const float m = fmaf(x, c.inv, kMagic);  // by a power of two exact but for this one rounding
+  if constexpr (POW2) {
+    return __float_as_uint(m);
+  } else {
     // x - t s is exact (below a step, and a multiple of the smaller of both last places): put
     // right what the rounded reciprocal decided next to a half, ties to the even side
+    float t = m - kMagic;
     const float d = fmaf(-t, c.s, x), h = 0.5f * c.s;
     const float a = fabsf(d);
     if (a > h || (a == h && (static_cast<int>(t) & 1))) t += copysignf(1.f, d);
+    return static_cast<unsigned>(static_cast<int>(__builtin_amdgcn_fmed3f(t, -127.f, 127.f)));
   }
-  const int q = static_cast<int>(t);
-  return max(-c.most, min(c.most, q));
 }
 
-// A block per row: the largest magnitude, then the codes, the row's second reading from the caches.
-template <class T, bool POW2>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(int cols, const T* __restrict__ x, int64_t ld,
+// 8 elements of a row in registers as they came, and as floats.
+template <class T>
+struct Eight {
+  static constexpr int W = sizeof(T) * 2;  // words
+  unsigned w[W];
+  __device__ inline float get(int k) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
+    else if constexpr (std::is_same_v<T, __bf16>) return __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+    else return static_cast<float>(__builtin_bit_cast(v2h, w[k / 2])[k & 1]);
+  }
+  __device__ inline void load(const KG T* p, int left) {  // `left` elements are the row's
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
+    if (left >= 8) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const v4u v = __builtin_bit_cast(v4u, load_pack<false, T>(p + i * 4 / sizeof(T)));
+        w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < left) {
+          if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(p[k]);
+          else w[k / 2] |= unsigned(__builtin_bit_cast(unsigned short, T(p[k]))) << (16 * (k & 1));
+        }
+    }
+  }
+  // bits of the largest magnitude (infinities and NaN are larger than every number)
+  __device__ inline unsigned top(unsigned m) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(get(k)) & 0x7fffffffu);
+    return m;
+  }
+  template <bool POW2>
+  __device__ inline void store(KG int8_t* p, int left, const RowCode& c) const {
+    v2u out = {0, 0};
+    if (c.most == 127) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        unsigned b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k] = code_of<POW2>(get(4 * h + k), c);
+        out[h] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u), __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
+      }
+    } else if (c.most) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int q = static_cast<int8_t>(code_of<POW2>(get(k), c));
+        out[k / 4] |= unsigned(uint8_t(max(-c.most, min(c.most, q)))) << (8 * (k & 3));
+      }
+    }
+    put(p, left, out);
+  }
+  static __device__ inline void put(KG int8_t* p, int left, v2u out) {
+    if (left >= 8) {
+      *reinterpret_cast<KG typename Pack<int8_t, 8>::vec*>(p) = __builtin_bit_cast(typename Pack<int8_t, 8>::vec, out);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < left) p[k] = static_cast<int8_t>(out[k / 4] >> (8 * (k & 3)));
+    }
+  }
+};
+
+// TPR threads a row (a wave, or the block), each with U groups of 8 elements kept in registers between the
+// largest magnitude and the codes; U = 0: rows of any length, read twice.
+template <class T, bool POW2, int TPR, int U>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(int rows, int cols, const T* __restrict__ x, int64_t ld,
                                                             const uint8_t* __restrict__ mask, int8_t* __restrict__ q,
                                                             int64_t ldq, float* __restrict__ scale) {
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
+  const int t = threadIdx.x % TPR;
+  const int64_t row = int64_t(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR;
+  if (row >= rows) return;
   const KG T* xr = gp(x) + row * ld;
   KG int8_t* qr = gp(q) + row * ldq;
   if (mask && !gp(mask)[row]) {
-    for (int c = tid; c < cols; c += 256) qr[c] = 0;
-    if (tid == 0) gp(scale)[row] = 0.f;
+    for (int c = 8 * t; c < cols; c += 8 * TPR) Eight<T>::put(qr + c, cols - c, v2u{0, 0});
+    if (t == 0) gp(scale)[row] = 0.f;
     return;
   }
+  Eight<T> v[U ? U : 1];
   unsigned top = 0;
-  for (int c = tid; c < cols; c += 256) top = max(top, __float_as_uint(static_cast<float>(xr[c])) & 0x7fffffffu);
+  if constexpr (U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u].load(xr + 8 * (t + u * TPR), cols - 8 * (t + u * TPR));
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = v[u].top(top);
+  } else {
+    for (int c = 8 * t; c < cols; c += 8 * TPR) {
+      v[0].load(xr + c, cols - c);
+      top = v[0].top(top);
+    }
+  }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
-  __shared__ unsigned part[4];
-  if ((tid & 63) == 0) part[tid >> 6] = top;
-  __syncthreads();
-  const RowCode code = row_code<POW2>(max(max(part[0], part[1]), max(part[2], part[3])));
-  for (int c = tid; c < cols; c += 256) qr[c] = static_cast<int8_t>(code_of<POW2>(static_cast<float>(xr[c]), code));
-  if (tid == 0) gp(scale)[row] = code.s;
+  if constexpr (TPR > 64) {
+    __shared__ unsigned part[4];
+    if ((t & 63) == 0) part[t >> 6] = top;
+    __syncthreads();
+    top = max(max(part[0], part[1]), max(part[2], part[3]));
+  }
+  const RowCode code = row_code<POW2>(top);
+  if constexpr (U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u].template store<POW2>(qr + 8 * (t + u * TPR), cols - 8 * (t + u * TPR), code);
+  } else {
+    for (int c = 8 * t; c < cols; c += 8 * TPR) {
+      v[0].load(xr + c, cols - c);
+      v[0].template store<POW2>(qr + c, cols - c, code);
+    }
+  }
+  if (t == 0) gp(scale)[row] = code.s;
 }
 
 template <class T>
@@ -97,53 +187,290 @@ __device__ inline T held(float v) {
   return static_cast<T>(v);
 }
 
+// Groups of 8 elements, numbered through the rows, one a thread.
 template <class T>
-__global__ void __launch_bounds__(256) dequantize_rows_kernel(int cols, const int8_t* __restrict__ q, int64_t ldq,
+__global__ void __launch_bounds__(256) dequantize_rows_kernel(int cols, unsigned per_row, int64_t groups,
+                                                              const int8_t* __restrict__ q, int64_t ldq,
                                                               const float* __restrict__ scale, T* __restrict__ x,
                                                               int64_t ld) {
-  const int64_t row = blockIdx.x;
+  const int64_t g = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (g >= groups) return;
+  const int64_t row = groups >> 32 ? g / per_row : int64_t(unsigned(g) / per_row);
+  const int c = static_cast<int>(g - row * per_row) * 8, left = cols - c;
   const float s = gp(scale)[row];
-  for (int c = threadIdx.x; c < cols; c += 256)
-    gp(x)[row * ld + c] = held<T>(static_cast<float>(gp(q)[row * ldq + c]) * s);
+  const KG int8_t* from = gp(q) + row * ldq + c;
+  KG T* to = gp(x) + row * ld + c;
+  if (left >= 8) {
+    const auto v = *reinterpret_cast<const KG typename Pack<int8_t, 8>::vec*>(from);
+    constexpr int EV = 16 / sizeof(T);
+#pragma unroll
+    for (int k = 0; k < 8; k += EV) {
+      typename Pack<T>::vec out;
+#pragma unroll
+      for (int e = 0; e < EV; ++e) out[e] = held<T>(static_cast<float>(v[k + e]) * s);
+      store_pack<false, T>(to + k, out);
+    }
+  } else {
+    for (int k = 0; k < left; ++k) to[k] = held<T>(static_cast<float>(from[k]) * s);
+  }
 }
 
-// y = fp32(sum of q w) s v + b, a tile of 64 x 64 a block: 4 waves of 32 x 32, 64 elements of the sum a step.
-template <class T>
-__global__ void __launch_bounds__(256) linear_q8_kernel(int rows, int c_in, int c_out, const int8_t* __restrict__ q,
-                                                        int64_t ldq, const float* __restrict__ scale,
-                                                        const int8_t* __restrict__ w, int64_t ldw,
-                                                        const float* __restrict__ wscale, const T* __restrict__ bias,
-                                                        T* __restrict__ y, int64_t ldy) {
-  __shared__ __attribute__((aligned(16))) int8_t lds[2][64][80];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const unsigned across = (c_out + 63) / 64;
-  const int64_t r0 = int64_t(blockIdx.x / across) * 64, o0 = int64_t(blockIdx.x % across) * 64;
-  v16i acc;
+// ---- y = fp32(sum of q w) s v + b ------------------------------------------------
+
+struct LinearArgs {
+  int rows, c_in, c_out;
+  const int8_t* q;
+  const int8_t* w;
+  const float* scale;
+  const float* w_scale;
+  const void* bias;
+  void* y;
+  int64_t ldq, ldw, ldy;
+};
+
+// 16 codes of a row at k0, zeros past its end; nothing behind the row is read.
+__device__ inline v4i load_codes(const KG int8_t* row, int k0, int c_in) {
+  if (k0 + 16 <= c_in) return __builtin_bit_cast(v4i, load_pack<false, int8_t>(row + k0));
+  v4i v = {0, 0, 0, 0};
+  for (int k = 0; k < 16 && k0 + k < c_in; ++k) {
+    const int byte = int(uint8_t(row[k0 + k])) << (8 * (k & 3));
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0;
-  for (int k0 = 0; k0 < c_in; k0 += 64) {
-    for (int i = tid; i < 64 * 64; i += 256) {
-      const int r = i >> 6, k = i & 63;
-      lds[0][r][k] = r0 + r < rows && k0 + k < c_in ? gp(q)[(r0 + r) * ldq + k0 + k] : 0;
-      lds[1][r][k] = o0 + r < c_out && k0 + k < c_in ? gp(w)[(o0 + r) * ldw + k0 + k] : 0;
-    }
-    __syncthreads();
+    for (int i = 0; i < 4; ++i) v[i] |= (k >> 2) == i ? byte : 0;
+  }
+  return v;
+}
+
+// Tiles of 2 WT channels x 2 WT rows, four waves of WT x WT. The weights are the matrix instruction's
+// first operand, so that a lane holds 4 neighbouring channels of one row. Both operands lie along
+// the sum: 16 codes are 16 bytes of an LDS line, which holds the tile's rows of BK codes with their
+// groups of 16 bytes swizzled, so that 16 lanes that read one group of 16 rows meet every bank once.
+template <int WT>
+struct LinearTile {
+  static constexpr int T = 2 * WT, BK = WT == 32 ? 128 : 64, CPR = BK / 16, LOADS = 2 * T * CPR / 256, KS = BK / 32, F = WT / 32;
+  static constexpr int STAGE = 2 * T * BK;  // bytes of both operands
+  static constexpr int STAGES = 4;
+  static __device__ inline int swizzle(int row) { return (row / (256 / BK)) & (CPR - 1); }
+  static __device__ inline int at(int row, int chunk) { return row * BK + 16 * (chunk ^ swizzle(row)); }
+};
+
+// Waits until at most N of this wave's loads are on their way and its LDS operations are done, then for the
+// other waves.
+template <int N>
+__device__ inline void arrive() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// DIRECT: rows at multiples of 16 bytes go from memory into LDS without registers, up to three steps
+// ahead; others by registers, two ahead.
+template <class T, int WT, bool DIRECT>
+__global__ void __launch_bounds__(256) linear_q8_kernel(LinearArgs a, int across, int tiles) {
+  using L = LinearTile<WT>;
+  constexpr int kOut = 4 * 32 * (WT * sizeof(T) + 16) + 2 * L::T * sizeof(float), kIn = L::STAGE * (DIRECT ? L::STAGES : 2);
+  __shared__ __attribute__((aligned(16))) char lds[kOut > kIn ? kOut : kIn];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int v = xcd_virtual(blockIdx.x, gridDim.x, tiles);
+  if (v < 0) return;
+  // bands of 8 tiles of rows, walked channel tile by channel tile: the tiles that run at a time on an XCD
+  // share rows and weights in its L2
+  const int down = tiles / across, band = v / (8 * across), in = v - band * 8 * across, high = min(8, down - 8 * band);
+  const int o0 = in / high * L::T, r0 = (band * 8 + in % high) * L::T;
+
+  // rows past the last are that one again: what they give is not stored
+  const KG int8_t* const wb = gp(a.w) + o0 * a.ldw;
+  const KG int8_t* const qb = gp(a.q) + r0 * a.ldq;
+  const int slot = tid % L::CPR, chunk = slot ^ L::swizzle(tid / L::CPR);  // the same for all loads of a thread
+  unsigned off[L::LOADS];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = h * 32 + (lane >> 5) * 16;
-      const v4i a = *reinterpret_cast<const v4i*>(&lds[0][(wave >> 1) * 32 + (lane & 31)][k]);
-      const v4i b = *reinterpret_cast<const v4i*>(&lds[1][(wave & 1) * 32 + (lane & 31)][k]);
-      acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc, 0, 0, 0);
+  for (int i = 0; i < L::LOADS; ++i) {
+    const int row = (tid + 256 * i) / L::CPR;
+    const bool is_w = 2 * i < L::LOADS;
+    const int r = is_w ? min(row, a.c_out - 1 - o0) : min(row - L::T, a.rows - 1 - r0);
+    off[i] = static_cast<unsigned>(r) * static_cast<unsigned>(is_w ? a.ldw : a.ldq) + 16 * chunk;
+  }
+  v4i st[L::LOADS];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < L::LOADS; ++i)
+      st[i] = __builtin_bit_cast(v4i, load_pack<false, int8_t>((2 * i < L::LOADS ? wb : qb) + k0 + off[i]));
+  };
+  auto load_end = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < L::LOADS; ++i)
+      st[i] = load_codes((2 * i < L::LOADS ? wb : qb) + (off[i] - 16 * chunk), k0 + 16 * chunk, a.c_in);
+  };
+  auto load_any = [&](int k0) {
+    if (k0 + L::BK <= a.c_in) load(k0);
+    else load_end(k0);
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < L::LOADS; ++i) *reinterpret_cast<v4i*>(lds + buf * L::STAGE + 16 * (tid + 256 * i)) = st[i];
+  };
+  auto send = [&](int k0, int buf, int i) {  // memory to LDS: a wave's 64 groups of 16 bytes side by side
+    __builtin_amdgcn_global_load_lds((const KG void*)((2 * i < L::LOADS ? wb : qb) + k0 + off[i]),
+                                     (__attribute__((address_space(3))) void*)(lds + buf * L::STAGE + 16 * (64 * wave + 256 * i)),
+                                     16, 0, 0);
+  };
+  const int wo = (wave >> 1) * WT, wr = L::T + (wave & 1) * WT;
+  auto frag = [&](int buf, int row, int ks) {
+    return *reinterpret_cast<const v4i*>(lds + buf * L::STAGE + L::at(row + (lane & 31), 2 * ks + (lane >> 5)));
+  };
+  v16i acc[L::F][L::F];
+#pragma unroll
+  for (int i = 0; i < L::F; ++i)
+#pragma unroll
+    for (int j = 0; j < L::F; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+  const int steps = (a.c_in + L::BK - 1) / L::BK;
+  if (steps) {
+    v4i fa[2][L::F], fb[2][L::F];
+    auto read1 = [&](int buf, int ks, int set, int n) {  // operand n of 2 F
+      if (n & 1) fb[set][n / 2] = frag(buf, wr + 32 * (n / 2), ks);
+      else fa[set][n / 2] = frag(buf, wo + 32 * (n / 2), ks);
+    };
+    auto read = [&](int buf, int ks, int set) {
+#pragma unroll
+      for (int n = 0; n < 2 * L::F; ++n) read1(buf, ks, set, n);
+    };
+    // behind(n) is issued behind product n, while the matrix unit works on that
+    auto mma = [&](int set, auto&& behind) {
+#pragma unroll
+      for (int n = 0; n < L::F * L::F; ++n) {
+        const int i = n / L::F, j = n % L::F;
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+        behind(n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // The operands of the next 32 codes are read while the matrix unit works on these. The barrier stands
+    // before a step's last products, when its operands have all been read and the next step's have
+    // arrived: those are read behind them, and the step's buffer is filled again.
+    if constexpr (DIRECT) {
+      auto send_any = [&](int c) {
+        if ((c + 1) * L::BK <= a.c_in) {
+#pragma unroll
+          for (int i = 0; i < L::LOADS; ++i) send(c * L::BK, c % L::STAGES, i);
+        } else if (c < steps) {
+          load_end(c * L::BK);
+          store(c % L::STAGES);
+        }
+      };
+      for (int c = 0; c < L::STAGES - 1; ++c) send_any(c);
+      if (steps < L::STAGES) arrive<0>();
+      else arrive<(L::STAGES - 2) * L::LOADS>();
+      send_any(L::STAGES - 1);
+      read(0, 0, 0);
+      constexpr int N = L::F * L::F, R = 2 * L::F, per = (R + N - 1) / N;  // products and operands of 32 codes
+      constexpr int each = (L::LOADS + N - 1) / N, from = N - (L::LOADS + each - 1) / each;
+      // the operands behind the first products, what fetch sends behind the last
+      auto step = [&](int c, auto ahead, auto&& fetch) {
+#pragma unroll
+        for (int ks = 0; ks < L::KS; ++ks) {
+          const bool last = ks + 1 == L::KS;
+          // loads that may still be on their way when step c + 1's have arrived
+          if (last) arrive<decltype(ahead)::value>();
+          mma(ks & 1, [&](int n) {
+#pragma unroll
+            for (int k = n * per; k < n * per + per && k < R; ++k)
+              last ? read1((c + 1) % L::STAGES, 0, 0, k) : read1(c % L::STAGES, ks + 1, (ks + 1) & 1, k);
+#pragma unroll
+            for (int i = (n - from) * each; i < (n - from + 1) * each && i < L::LOADS; ++i)
+              if (last && i >= 0) fetch(i);
+          });
+        }
+      };
+      int c = 0;
+      for (; (c + L::STAGES + 1) * L::BK <= a.c_in; ++c)
+        step(c, std::integral_constant<int, (L::STAGES - 2) * L::LOADS>{},
+             [&](int i) { send((c + L::STAGES) * L::BK, c % L::STAGES, i); });
+      // the last steps: all that was sent is waited for
+      for (; c < steps; ++c)
+        step(c, std::integral_constant<int, 0>{}, [&](int i) {
+          if (i == 0) send_any(c + L::STAGES);
+        });
+    } else {
+      load_any(0);
+      store(0);
+      if (steps > 1) load_any(L::BK);
+      __syncthreads();
+      read(0, 0, 0);
+      auto step = [&](int cur, bool next, auto&& fetch) {
+        if (next) store(cur ^ 1);
+        fetch();
+#pragma unroll
+        for (int ks = 0; ks < L::KS; ++ks) {
+          if (ks + 1 < L::KS) {
+            read(cur, ks + 1, (ks + 1) & 1);
+          } else {
+            __syncthreads();
+            if (next) read(cur ^ 1, 0, 0);
+          }
+          mma(ks & 1, [](int) {});
+        }
+      };
+      int c = 0;
+      for (; (c + 3) * L::BK <= a.c_in; ++c) step(c & 1, true, [&] { load((c + 2) * L::BK); });
+      for (; c < steps; ++c)
+        step(c & 1, c + 1 < steps, [&] {
+          if (c + 2 < steps) load_any((c + 2) * L::BK);
+        });
     }
     __syncthreads();
   }
-  const int64_t o = o0 + (wave & 1) * 32 + (lane & 31);
-  if (o >= c_out) return;
-  const float v = gp(wscale)[o], add = bias ? static_cast<float>(gp(bias)[o]) : 0.f;
+
+  // The channels' scales and biases go through LDS. Then each wave brings 32 rows at a time into LDS
+  // lines of their channels and stores them 16 bytes a lane.
+  constexpr int PITCH = WT * sizeof(T) + 16, EV = 16 / sizeof(T), LANES = WT / EV;
+  float* const sv = reinterpret_cast<float*>(lds);
+  float* const sb = sv + L::T;
+  char* const mine = lds + 2 * L::T * sizeof(float) + wave * 32 * PITCH;
+  for (int c = tid; c < L::T; c += 256) {
+    const int o = min(o0 + c, a.c_out - 1);
+    sv[c] = gp(a.w_scale)[o];
+    sb[c] = a.bias ? static_cast<float>(gp(static_cast<const T*>(a.bias))[o]) : 0.f;
+  }
+  __syncthreads();
+  const int wo0 = o0 + wo, wr0 = r0 + wr - L::T;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int64_t r = r0 + (wave >> 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-    if (r < rows) gp(y)[r * ldy + o] = static_cast<T>(static_cast<float>(acc[e]) * gp(scale)[r] * v + add);
+  for (int j = 0; j < L::F; ++j) {
+    const int r = wr0 + 32 * j + (lane & 31);
+    const float s = gp(a.scale)[min(r, a.rows - 1)];
+#pragma unroll
+    for (int i = 0; i < L::F; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = 32 * i + 8 * g + 4 * (lane >> 5);
+        const v4f v = *reinterpret_cast<const v4f*>(sv + wo + c), b = *reinterpret_cast<const v4f*>(sb + wo + c);
+        typename Pack<T, 4>::vec out;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = static_cast<T>(static_cast<float>(acc[i][j][4 * g + e]) * s * v[e] + b[e]);
+        typedef T vec4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<vec4*>(mine + (lane & 31) * PITCH + c * sizeof(T)) = out;
+      }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int n = 0; n < 32 * LANES / 64; ++n) {
+      const int u = n * 64 + lane, row = u / LANES, c = u % LANES * EV;
+      const v4i raw = *reinterpret_cast<const v4i*>(mine + row * PITCH + c * sizeof(T));
+      const auto out = __builtin_bit_cast(typename Pack<T>::vec, raw);
+      const int64_t rr = wr0 + 32 * j + row;
+      const int o = wo0 + c;
+      if (rr < a.rows) {
+        KG T* p = gp(static_cast<T*>(a.y)) + rr * a.ldy + o;
+        if (o + EV <= a.c_out) {
+          store_pack<false, T>(p, out);
+        } else {
+#pragma unroll
+          for (int k = 0; k < EV; ++k)
+            if (o + k < a.c_out) p[k] = out[k];
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -154,18 +481,27 @@ static kfac_status sizes_ok(int32_t rows, int32_t cols, const char* what) {
   return KFAC_OK;
 }
 
-template <class T>
-static kfac_status launch_quantize(int32_t rows, int32_t cols, const void* x, int64_t ld, const uint8_t* mask, bool pow2,
+template <class T, bool POW2>
+static kfac_status launch_quantize(int32_t rows, int32_t cols, const void* x, int64_t ld, const uint8_t* mask,
                                    int8_t* q, int64_t ldq, float* scale, hipStream_t s) {
-  if (pow2) {
-    KFAC_LAUNCH(K_QUANTIZE, (quantize_rows_kernel<T, true>), dim3(rows), dim3(256), 0, s, cols,
-                static_cast<const T*>(x), ld, mask, q, ldq, scale);
-  } else {
-    KFAC_LAUNCH(K_QUANTIZE, (quantize_rows_kernel<T, false>), dim3(rows), dim3(256), 0, s, cols,
-                static_cast<const T*>(x), ld, mask, q, ldq, scale);
-  }
-  KFAC_CHECK_LAUNCH("quantize_rows_kernel");
-  return KFAC_OK;
+  auto go = [&](auto tpr, auto u) {
+    constexpr int TPR = decltype(tpr)::value;
+    const unsigned blocks = static_cast<unsigned>((int64_t(rows) + 256 / TPR - 1) / (256 / TPR));
+    KFAC_LAUNCH(K_QUANTIZE, (quantize_rows_kernel<T, POW2, TPR, decltype(u)::value>), dim3(blocks), dim3(256), 0, s, rows,
+                cols, static_cast<const T*>(x), ld, mask, q, ldq, scale);
+    KFAC_CHECK_LAUNCH("quantize_rows_kernel");
+    return KFAC_OK;
+  };
+  constexpr std::integral_constant<int, 64> wave;
+  constexpr std::integral_constant<int, 256> block;
+  if (cols <= 512) return go(wave, std::integral_constant<int, 1>{});
+  if (rows > 1024 && cols <= 2048) return go(wave, std::integral_constant<int, 4>{});
+  if (rows > 1024 && cols <= 4096) return go(wave, std::integral_constant<int, 8>{});
+  if (cols <= 2048) return go(block, std::integral_constant<int, 1>{});
+  if (cols <= 4096) return go(block, std::integral_constant<int, 2>{});
+  if (cols <= 8192) return go(block, std::integral_constant<int, 4>{});
+  if (cols <= 16384) return go(block, std::integral_constant<int, 8>{});
+  return go(block, std::integral_constant<int, 0>{});
 }
 
 static kfac_status quantize_checks(int32_t rows, int32_t cols, kfac_dtype dtype, const RowsOf& x, const uint8_t* mask,
@@ -189,8 +525,10 @@ extern "C" kfac_status kfac_quantize_rows(int32_t rows, int32_t cols, kfac_dtype
   if ((st = check_device())) return st;
   if (rows == 0) return KFAC_OK;
   return with_row_type(dtype, [&](auto tag) {
-    return launch_quantize<decltype(tag)>(rows, cols, x, ld_x, mask, pow2 == 1, q, ld_q, scale,
-                                          static_cast<hipStream_t>(stream));
+    using T = decltype(tag);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return pow2 ? launch_quantize<T, true>(rows, cols, x, ld_x, mask, q, ld_q, scale, s)
+                : launch_quantize<T, false>(rows, cols, x, ld_x, mask, q, ld_q, scale, s);
   });
 }
 
@@ -208,8 +546,11 @@ extern "C" kfac_status kfac_dequantize_rows(int32_t rows, int32_t cols, const in
   if (xs.empty()) return KFAC_OK;
   return with_row_type(dtype, [&](auto tag) {
     using T = decltype(tag);
-    KFAC_LAUNCH(K_DEQUANTIZE, dequantize_rows_kernel<T>, dim3(rows), dim3(256), 0, static_cast<hipStream_t>(stream), cols,
-                q, ld_q, scale, static_cast<T*>(x), ld_x);
+    const unsigned per_row = static_cast<unsigned>((int64_t(cols) + 7) / 8);
+    const int64_t groups = int64_t(rows) * per_row, blocks = (groups + 255) / 256;
+    if (blocks > INT32_MAX) return fail(KFAC_ERR_UNSUPPORTED, "more than 2^42 elements");
+    KFAC_LAUNCH(K_DEQUANTIZE, dequantize_rows_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                static_cast<hipStream_t>(stream), cols, per_row, groups, q, ld_q, scale, static_cast<T*>(x), ld_x);
     KFAC_CHECK_LAUNCH("dequantize_rows_kernel");
     return KFAC_OK;
   });
@@ -217,10 +558,22 @@ extern "C" kfac_status kfac_dequantize_rows(int32_t rows, int32_t cols, const in
 
 // 128^2 * (2^17 - 1) < 2^31: no sum leaves an int32, whatever the codes.
 constexpr int32_t kMaxTerms = (1 << 17) - 1;
+constexpr int64_t kMaxPitch = 1 << 23;  // 256 rows of a tile within 32-bit offsets
 
 static kfac_status linear_sizes(int32_t rows, int32_t c_in, int32_t c_out) {
   if (rows < 0 || c_in < 0 || c_out < 0) return fail(KFAC_ERR_INVALID, "negative rows, c_in or c_out");
   if (c_in > kMaxTerms) return fail(KFAC_ERR_UNSUPPORTED, "c_in %d: a sum of more than %d products", c_in, kMaxTerms);
+  return KFAC_OK;
+}
+
+template <class T, int WT, bool DIRECT>
+static kfac_status launch_linear(const LinearArgs& a, hipStream_t s) {
+  using L = LinearTile<WT>;
+  const int64_t across = (int64_t(a.c_out) + L::T - 1) / L::T, tiles = across * ((int64_t(a.rows) + L::T - 1) / L::T);
+  if (tiles > (1 << 30)) return fail(KFAC_ERR_UNSUPPORTED, "more than 2^30 tiles");
+  KFAC_LAUNCH(K_LINEAR_Q8, (linear_q8_kernel<T, WT, DIRECT>), dim3(xcd_grid(tiles)), dim3(256), 0, s, a,
+              static_cast<int>(across), static_cast<int>(tiles));
+  KFAC_CHECK_LAUNCH("linear_q8_kernel");
   return KFAC_OK;
 }
 
@@ -249,6 +602,8 @@ extern "C" kfac_status kfac_linear_q8(int32_t rows, int32_t c_in, int32_t c_out,
   for (const RowsOf* r : {&xs, &qs, &ss, &ws, &vs, &bs, &ys})
     if ((st = check_rows(*r))) return st;
   if (mask && !x) return fail(KFAC_ERR_INVALID, "mask without x");
+  for (const RowsOf* r : {&qs, &ws})
+    if (r->rows > 1 && r->ld >= kMaxPitch) return fail(KFAC_ERR_UNSUPPORTED, "%s: rows of 2^23 bytes and more", r->name);
   const RowsOf scr = scratch(workspace, linear_need(rows, c_in, c_out));
   if (x) st = check_apart({&ys, &scr, &qs, &ss, &xs, &ws, &vs, &bs, &ms}, 4);
   else st = check_apart({&ys, &scr, &qs, &ss, &ws, &vs, &bs}, 2);
@@ -260,16 +615,20 @@ extern "C" kfac_status kfac_linear_q8(int32_t rows, int32_t c_in, int32_t c_out,
   return with_row_type(dtype, [&](auto tag) {
     using T = decltype(tag);
     if (x) {
-      kfac_status e = launch_quantize<T>(rows, c_in, x, ld_x, mask, true, q, ld_q, scale, s);
+      kfac_status e = launch_quantize<T, true>(rows, c_in, x, ld_x, mask, q, ld_q, scale, s);
       if (e) return e;
     }
     if (c_out == 0) return KFAC_OK;
-    const int64_t tiles = (int64_t(c_out) + 63) / 64 * ((int64_t(rows) + 63) / 64);
-    if (tiles > INT32_MAX) return fail(KFAC_ERR_UNSUPPORTED, "too many tiles");
-    KFAC_LAUNCH(K_LINEAR_Q8, linear_q8_kernel<T>, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, rows, c_in,
-                c_out, q, ld_q, scale, w, ld_w, w_scale, static_cast<const T*>(bias), static_cast<T*>(y), ld_y);
-    KFAC_CHECK_LAUNCH("linear_q8_kernel");
-    return KFAC_OK;
+    const LinearArgs args = {rows, c_in, c_out, q, w, scale, w_scale, bias, y, ld_q, ld_w, ld_y};
+    const int64_t big = (int64_t(c_out) + 255) / 256 * ((int64_t(rows) + 255) / 256);
+    const int64_t mid = (int64_t(c_out) + 127) / 128 * ((int64_t(rows) + 127) / 128);
+    const bool direct = !((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(w) | uintptr_t(ld_q) | uintptr_t(ld_w)) & 15);
+    auto go = [&](auto wt) {
+      return direct ? launch_linear<T, decltype(wt)::value, true>(args, s) : launch_linear<T, decltype(wt)::value, false>(args, s);
+    };
+    if (big >= 192) return go(std::integral_constant<int, 128>{});
+    if (mid >= 128) return go(std::integral_constant<int, 64>{});
+    return go(std::integral_constant<int, 32>{});
   });
 }
 
