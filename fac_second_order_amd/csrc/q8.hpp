@@ -9,6 +9,7 @@
 
 namespace kfac {
 
+typedef unsigned short v4us __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
@@ -51,6 +52,15 @@ inline bool rows_share(const RowsOf& a, const RowsOf& b) {
   int64_t off = static_cast<int64_t>(b.begin() - a.begin()) % pitch;
   if (off < 0) off += pitch;
   return off < wa || off + wb > pitch;
+}
+
+// Waits until at most N of this wave's loads are on their way and its LDS operations are done, then for the
+// other waves.
+template <int N>
+__device__ inline void arrive() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // The part of a workspace that a call uses, as one row.

@@ -253,15 +253,6 @@ struct LinearTile {
   static __device__ inline int at(int row, int chunk) { return row * BK + 16 * (chunk ^ swizzle(row)); }
 };
 
-// Waits until at most N of this wave's loads are on their way and its LDS operations are done, then for the
-// other waves.
-template <int N>
-__device__ inline void arrive() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // DIRECT: rows at multiples of 16 bytes go from memory into LDS without registers, up to three steps
 // ahead; others by registers, two ahead.
 template <class T, int WT, bool DIRECT>

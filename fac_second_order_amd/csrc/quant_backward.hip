@@ -16,8 +16,7 @@
 
 namespace kfac {
 
-constexpr int LIST = 2048;  // rows that a list covers
-constexpr uint16_t kNoRow = 0xffff;
+constexpr int kSmallList = 2048, kBigList = 8192;  // rows that a list covers
 
 struct TnJob {
   const void* g;  // gradients; the factor has none
@@ -36,37 +35,35 @@ struct TnJob {
   int32_t bias, accumulate;
   float decay;
   int32_t begin;  // first work item
+  int32_t big;    // 256 x 256 tiles
 };
 
 // fp16 gradients and the factor are formed in fp16, others in bf16; fp32 ones in three parts.
 template <class T>
 constexpr int kParts = std::is_same_v<T, float> ? 3 : 1;
 
+// Codes 2 h and 2 h + 1 of four, times s, as two 16-bit numbers.
 template <bool HALF>
-__device__ inline v8s codes16(v2u u, float s) {
-  v8s out;
+__device__ inline unsigned two_codes(unsigned four, int h, float s) {
+  const unsigned w = four ^ 0x80808080u;  // code + 128
   if constexpr (HALF) {
     // 0x64 in front of a byte b is the fp16 number 1024 + b
     const v2h mid = {static_cast<_Float16>(1152.f), static_cast<_Float16>(1152.f)};
     const _Float16 sh = static_cast<_Float16>(s);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned w = u[i >> 1] ^ 0x80808080u;
-      const unsigned b = __builtin_amdgcn_perm(0x64646464u, w, (i & 1) ? 0x04030402u : 0x04010400u);
-      const v2h h = (__builtin_bit_cast(v2h, b) - mid) * v2h{sh, sh};
-      const unsigned bits = __builtin_bit_cast(unsigned, h);
-      out[2 * i] = static_cast<short>(bits);
-      out[2 * i + 1] = static_cast<short>(bits >> 16);
-    }
+    const unsigned b = __builtin_amdgcn_perm(0x64646464u, w, h ? 0x04030402u : 0x04010400u);
+    return __builtin_bit_cast(unsigned, (__builtin_bit_cast(v2h, b) - mid) * v2h{sh, sh});
   } else {
     const float mid = -128.f * s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const unsigned w = u[i >> 2] ^ 0x80808080u;
-      out[i] = __builtin_bit_cast(short, static_cast<__bf16>(fmaf(static_cast<float>((w >> (8 * (i & 3))) & 255u), s, mid)));
-    }
+    const v2bf out = {static_cast<__bf16>(fmaf(static_cast<float>((w >> (16 * h)) & 255u), s, mid)),
+                      static_cast<__bf16>(fmaf(static_cast<float>((w >> (16 * h + 8)) & 255u), s, mid))};
+    return __builtin_bit_cast(unsigned, out);
   }
-  return out;
+}
+
+template <bool HALF>
+__device__ inline v8s codes16(v2u u, float s) {
+  return __builtin_bit_cast(v8s, v4u{two_codes<HALF>(u[0], 0, s), two_codes<HALF>(u[0], 1, s),
+                                     two_codes<HALF>(u[1], 0, s), two_codes<HALF>(u[1], 1, s)});
 }
 
 // x = h[0] + h[1] + h[2], 8 bits of the significand each, cut and not rounded. An infinity stays one.
@@ -81,17 +78,20 @@ __device__ inline void cut3(float x, short (&h)[3]) {
   }
 }
 
+// The rows of a stretch that take part, with their scales times a unit; behind them rows that are none.
+template <int LIST>
 struct RowList {
-  uint16_t idx[LIST];
-  float s[LIST];
+  __attribute__((aligned(16))) uint16_t idx[LIST + 64];  // or kNone: none (and row 0)
+  __attribute__((aligned(16))) float s[LIST + 64];
   int32_t group[LIST / 64];
   float top[8];
 };
+constexpr uint16_t kNone = 0x8000;
 
-// The rows of [r0, r0 + n) with a scale, in order, with their scales times `unit`; filled up to a
-// multiple of 64 with none. Returns how many there are.
-template <int NT>
-__device__ inline int list_rows(const float* scale, int64_t r0, int n, float unit, RowList& l) {
+// The rows of [r0, r0 + n) with a scale, in order; filled up to a multiple of 64. Returns how many there are.
+// SHUFFLED: within 32 rows, row 8 i + j lies at 4 j + i.
+template <int NT, bool SHUFFLED, int LIST>
+__device__ inline int list_rows(const float* scale, int64_t r0, int n, float unit, RowList<LIST>& l) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int PER = LIST / NT;
   float s[PER];
@@ -101,26 +101,46 @@ __device__ inline int list_rows(const float* scale, int64_t r0, int n, float uni
   for (int i = 0; i < PER; ++i) {
     const int r = (wave + i * (NT / 64)) * 64 + lane;
     s[i] = r < n ? gp(scale)[r0 + r] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
     b[i] = __ballot(s[i] != 0.f);
     if (lane == 0) l.group[wave + i * (NT / 64)] = __popcll(b[i]);
   }
   __syncthreads();
-  int total = 0;
-  for (int g = 0; g < LIST / 64; ++g) total += l.group[g];
+  // rows before each group of 64: lane g adds up the groups below g, 64 groups at a time
+  int total = 0, before[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) before[i] = 0;
+#pragma unroll
+  for (int g0 = 0; g0 < LIST / 64; g0 += 64) {
+    int own = g0 + lane < LIST / 64 ? l.group[g0 + lane] : 0, sum = own;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const int up = __shfl_up(sum, o);
+      if (lane >= o) sum += up;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int g = wave + i * (NT / 64);
+      if (g >= g0 && g < g0 + 64) before[i] = total + __shfl(sum - own, g - g0);
+    }
+    total += __shfl(sum, 63);
+  }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int own = wave + i * (NT / 64);
-    int at = __popcll(b[i] & ((1ull << lane) - 1));
-    for (int g = 0; g < own; ++g) at += l.group[g];
+    const int at = before[i] + __popcll(b[i] & ((1ull << lane) - 1));
     if (s[i] != 0.f) {
-      l.idx[at] = static_cast<uint16_t>(own * 64 + lane);
-      l.s[at] = s[i] * unit;
+      const int to = SHUFFLED ? (at & ~31) | ((at & 7) << 2) | ((at >> 3) & 3) : at;
+      l.idx[to] = static_cast<uint16_t>((wave + i * (NT / 64)) * 64 + lane);
+      l.s[to] = s[i] * unit;
     }
   }
   const int whole = (total + 63) / 64 * 64;
   if (total + tid < whole) {
-    l.idx[total + tid] = kNoRow;
-    l.s[total + tid] = 0.f;
+    const int at = total + tid, to = SHUFFLED ? (at & ~31) | ((at & 7) << 2) | ((at >> 3) & 3) : at;
+    l.idx[to] = kNone;
+    l.s[to] = 0.f;
   }
   __syncthreads();
   return total;
@@ -128,8 +148,8 @@ __device__ inline int list_rows(const float* scale, int64_t r0, int n, float uni
 
 // 2^k such that the largest finite scale of the rows times it is 2^5: relative to that, fp16 holds
 // s q down to 2^-29 of the largest scale exactly (the sum with 1152 that makes a code stays finite).
-template <int NT>
-__device__ inline float scale_unit(const float* scale, int64_t r0, int n, RowList& l) {
+template <int NT, int LIST>
+__device__ inline float scale_unit(const float* scale, int64_t r0, int n, RowList<LIST>& l) {
   unsigned top = 0;
   for (int r = threadIdx.x; r < n; r += NT) {
     const unsigned b = __float_as_uint(gp(scale)[r0 + r]) & 0x7fffffffu;
@@ -158,13 +178,14 @@ struct Stage {
   static __device__ inline int col(int i) { return (threadIdx.x + i * NT) % perRow * 8; }
 
   // rows l.idx[k0 ..] + r0 of src, columns c0 .. of cols
-  __device__ inline void load(const E* src, int64_t ld, int64_t r0, const RowList& l, int k0, int c0, int cols) {
+  template <int LIST>
+  __device__ inline void load(const E* src, int64_t ld, int64_t r0, const RowList<LIST>& l, int k0, int c0, int cols) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint16_t r = l.idx[k0 + row(i)];
       const int c = c0 + col(i);
-      const KG E* p = gp(src) + (r0 + r) * ld + c;
-      if (r != kNoRow && c + 8 <= cols) {
+      const KG E* p = gp(src) + (r0 + (r & (kNone - 1))) * ld + c;
+      if (r != kNone && c + 8 <= cols) {
         if constexpr (std::is_same_v<E, int8_t>) {
           v[i] = __builtin_bit_cast(Raw, *reinterpret_cast<const KG typename Pack<int8_t, 8>::vec*>(p));
         } else if constexpr (std::is_same_v<E, float>) {
@@ -175,7 +196,7 @@ struct Stage {
         }
       } else {
         v[i] = Raw{};
-        if (r != kNoRow)
+        if (r != kNone)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (c + k < cols) {
@@ -195,7 +216,7 @@ __global__ void __launch_bounds__(256) q8_tn_kernel(TnJob d) {
   constexpr bool HALF = std::is_same_v<T, _Float16>;
   using G = std::conditional_t<FACTOR, int8_t, T>;
   __shared__ __attribute__((aligned(16))) short lds[P + 1][BK][PITCH];
-  __shared__ RowList list;
+  __shared__ RowList<kSmallList> list;
   __shared__ float colsum[TM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int tile = blockIdx.x % d.tiles, split = blockIdx.x / d.tiles;
@@ -216,9 +237,9 @@ __global__ void __launch_bounds__(256) q8_tn_kernel(TnJob d) {
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   const float unit = HALF ? scale_unit<NT>(d.scale, r_begin, r_count, list) : 1.f;
   int counted = 0;
-  for (int base = 0; base < r_count; base += LIST) {
+  for (int base = 0; base < r_count; base += kSmallList) {
     const int64_t r0 = r_begin + base;
-    const int n = list_rows<NT>(d.scale, r0, min(LIST, r_count - base), unit, list);
+    const int n = list_rows<NT, false>(d.scale, r0, min(kSmallList, r_count - base), unit, list);
     counted += n;
     for (int k0 = 0; k0 < n; k0 += BK) {
       Stage<G, TM, NT, BK> a;
@@ -345,6 +366,269 @@ __global__ void __launch_bounds__(256) q8_tn_kernel(TnJob d) {
   }
 }
 
+// ---- 256 x 256 tiles of the weight gradient ------------------------------------------
+
+// Four waves of 128 x 128, steps of 32 rows, which go from memory into registers four steps ahead and
+// from there into LDS one step ahead, the codes with their scales. Both operands lie in LDS a row a line of 512
+// bytes, its groups of 16 bytes moved by 64 bytes a row, so that the 4 rows that 16 lanes of a
+// transposing load meet lie in different banks. (Gradients sent from memory into LDS directly were
+// slower: the compiler has every transposing load wait for all that is on its way there.)
+//
+// For outputs and inputs in whole groups of 8. Groups past the last column are the first one again:
+// what they give is not stored.
+constexpr int BT = 256, BROWS = 32, BSTAGE = BROWS * BT * 2, BAHEAD = 4;
+
+template <class T>
+__global__ void __launch_bounds__(256) grad_big_kernel(TnJob d) {
+  constexpr bool HALF = std::is_same_v<T, _Float16>;
+  __shared__ __attribute__((aligned(16))) char lds[4 * BSTAGE];
+  __shared__ RowList<kBigList> list;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int v = xcd_virtual(blockIdx.x, gridDim.x, d.tiles * d.splits);
+  if (v < 0) return;
+  const int split = v / d.tiles, tile = v - split * d.tiles;
+  // bands of 4 tiles of outputs, so that the tiles that run at a time on an XCD share both operands
+  const int band = tile / (4 * d.nt), in = tile - band * 4 * d.nt, high = min(4, d.mt - 4 * band);
+  const int ti = band * 4 + in % high, tj = in / high;
+  const int o0 = ti * BT, k0 = tj * BT;
+  const int64_t r_begin = int64_t(split) * d.per_split;
+  const int r_count = static_cast<int>(min(int64_t(d.per_split), d.rows - r_begin));
+
+  // this thread's group of 8 columns, and its rows 8 i + row of a step
+  const int col = tid % 32, row = tid / 32, slot = col ^ (4 * (row & 3));
+  const int g_col = o0 + 8 * col < d.m ? 8 * col : 0, q_col = k0 + 8 * col < d.n ? 8 * col : 0;
+  const unsigned q_pitch = static_cast<unsigned>(d.ldq), g_pitch = static_cast<unsigned>(d.ldg) * 2;
+  char* const gbuf = lds;
+  char* const qbuf = lds + 2 * BSTAGE;
+  v2u qraw[BAHEAD][4];
+  v4u graw[BAHEAD][4];
+
+  const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
+  v16f acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  // Column sums of the gradients: the tiles along the inputs, and a tile's two waves that hold the same
+  // outputs, take turns, a step each. A lane adds up its column of the operands.
+  float sums[4] = {0.f, 0.f, 0.f, 0.f};
+  const int turn = d.bias ? 2 * tj + (wave & 1) : INT32_MAX, turns = 2 * d.nt;
+  auto add_up = [&](const v8s (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (HALF) sums[i] += static_cast<float>(__builtin_bit_cast(v8h, f[i])[k]);
+        else sums[i] += __uint_as_float(unsigned(static_cast<unsigned short>(f[i][k])) << 16);
+      }
+  };
+  const int s16 = lane & 15, kk = 8 * (lane >> 5) + (s16 >> 2), cc = 16 * ((lane >> 4) & 1) + 4 * (s16 & 3);
+  // where this lane's loads of the wave's four groups of 32 columns begin in a buffer
+  const char* ga[4];
+  const char* qa[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = kk * 512 + ((cc >> 3) | ((i ^ (kk & 3)) << 2)) * 16 + (cc & 7) * 2;
+    ga[i] = gbuf + 2 * wm + at;
+    qa[i] = qbuf + 2 * wn + at;
+  }
+  auto operand = [&](const char* from) {  // 8 rows of a column each lane
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)from);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(from + 4 * 512));
+    return v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  auto mma1 = [&](v8s a, v8s b, v16f c) {
+    if constexpr (HALF) return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+  };
+  const float unit = HALF ? scale_unit<256>(d.scale, r_begin, r_count, list) : 1.f;
+  for (int base = 0; base < r_count; base += kBigList) {
+    const int64_t r0 = r_begin + base;
+    const int n = list_rows<256, true>(d.scale, r0, min(kBigList, r_count - base), unit, list);
+    const int steps = (n + BROWS - 1) / BROWS;
+    if (!steps) continue;
+    const KG char* const g0 = reinterpret_cast<const KG char*>(gp(static_cast<const T*>(d.g)) + r0 * d.ldg + o0 + g_col);
+    const KG int8_t* const q0 = gp(d.q) + r0 * d.ldq + k0 + q_col;
+    // this thread's four rows of step c, and their scales
+    auto rows_of = [&](int c) { return *reinterpret_cast<const v4us*>(&list.idx[c * BROWS + 4 * row]); };
+    auto scales_of = [&](int c) { return *reinterpret_cast<const v4f*>(&list.s[c * BROWS + 4 * row]); };
+    // row i into registers
+    auto fetch_q = [&](unsigned short r, auto set, int i) {
+      qraw[set][i] = __builtin_bit_cast(v2u, *reinterpret_cast<const KG typename Pack<int8_t, 8>::vec*>(q0 + uint64_t(r & (kNone - 1)) * q_pitch));
+    };
+    auto fetch_g = [&](unsigned short r, auto set, int i) {
+      graw[set][i] = __builtin_bit_cast(v4u, load_pack<false, T>(reinterpret_cast<const KG T*>(g0 + uint64_t(r & (kNone - 1)) * g_pitch)));
+    };
+    // row i from registers into LDS: the gradients, and the codes, two at a time; whole: it is no row that is none
+    auto place_g = [&](auto set, auto buf, int i, bool whole, float s) {
+      v4u x = graw[set][i];
+      if (!whole && s == 0.f) x = v4u{0, 0, 0, 0};
+      *reinterpret_cast<v4u*>(gbuf + buf * BSTAGE + (8 * i + row) * 512 + 16 * slot) = x;
+    };
+    v4u placed;
+    auto place2 = [&](auto set, auto buf, int i, int h, float s) {
+      placed[h] = two_codes<HALF>(qraw[set][i][h >> 1], h & 1, s);
+      if (h == 3) *reinterpret_cast<v4u*>(qbuf + buf * BSTAGE + (8 * i + row) * 512 + 16 * slot) = placed;
+    };
+    v8s fa[2][4], fb[2][4];
+    auto read1 = [&](auto buf, int ks, int set, int n) {
+      if (n & 1) fb[set][n / 2] = operand(qa[n / 2] + buf * BSTAGE + 16 * ks * 512);
+      else fa[set][n / 2] = operand(ga[n / 2] + buf * BSTAGE + 16 * ks * 512);
+    };
+#define KFAC_AT(x) std::integral_constant<int, (x)>{}
+    auto first = [&](auto s) {
+      if (s < steps) {
+        const v4us r = rows_of(s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          fetch_q(r[i], s, i);
+          fetch_g(r[i], s, i);
+        }
+      }
+    };
+    first(KFAC_AT(0));
+    first(KFAC_AT(1));
+    first(KFAC_AT(2));
+    first(KFAC_AT(3));
+    v4f sc = scales_of(0);
+    auto place = [&](auto set, int i) {
+      place_g(set, set, i, false, sc[i]);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) place2(set, set, i, h, sc[i]);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) place(KFAC_AT(0), i);
+    if (1 < steps) {
+      sc = scales_of(1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) place(KFAC_AT(1), i);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 8; ++n) read1(KFAC_AT(0), 0, 0, n);
+
+    // One step: 16 products of its rows' first half, in whose shade the second half's operands are read and
+    // the next step's last two rows of codes placed; then, when everyone has read this step's
+    // operands and the next step's are there, 16 products of the second half, with the next step's
+    // first operands read, the first two rows of the step after that placed, and step c + 4 fetched.
+    int next = turn;
+    auto step = [&](int c, auto S, auto ALL) {
+      constexpr int s = decltype(S)::value;
+      constexpr bool all = decltype(ALL)::value;
+      v4us r = {0, 0, 0, 0};
+      v4f sn = {0, 0, 0, 0};
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        acc[n / 4][n % 4] = mma1(fa[0][n / 4], fb[0][n % 4], acc[n / 4][n % 4]);
+        if (n < 8) read1(KFAC_AT(s & 1), 1, 1, n);
+        if (n == 8 && (all || c + BAHEAD < steps)) r = rows_of(c + BAHEAD);
+        if (n == 8 && (all || c + 2 < steps)) sn = scales_of(c + 2);
+        if (all || c + 1 < steps) {
+          if (n >= 8) place2(KFAC_AT((s + 1) & 3), KFAC_AT((s + 1) & 1), n / 4, n % 4, sc[n / 4]);
+          if (n == 5 || n == 7) place_g(KFAC_AT((s + 1) & 3), KFAC_AT((s + 1) & 1), n / 2, all, sc[n / 2]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (c == next) {
+        add_up(fa[0]);
+        add_up(fa[1]);
+        next += turns;
+      }
+      __syncthreads();
+      sc = sn;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        acc[n / 4][n % 4] = mma1(fa[1][n / 4], fb[1][n % 4], acc[n / 4][n % 4]);
+        if (n < 8) read1(KFAC_AT((s + 1) & 1), 0, 0, n);
+        if (n % 2 && (all || c + 2 < steps)) {
+          place2(KFAC_AT((s + 2) & 3), KFAC_AT(s & 1), n / 8, n / 2 % 4, sc[n / 8]);
+          if (n == 9 || n == 11) place_g(KFAC_AT((s + 2) & 3), KFAC_AT(s & 1), n / 2 - 4, all, sc[n / 2 - 4]);
+        }
+        if (n >= 8 && n < 12 && (all || c + BAHEAD < steps)) fetch_q(r[n - 8], KFAC_AT(s), n - 8);
+        if (n >= 12 && (all || c + BAHEAD < steps)) fetch_g(r[n - 12], KFAC_AT(s), n - 12);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int c = 0;
+    for (; (c + 4 + BAHEAD) * BROWS <= n; c += 4) {
+      step(c, KFAC_AT(0), std::true_type{});
+      step(c + 1, KFAC_AT(1), std::true_type{});
+      step(c + 2, KFAC_AT(2), std::true_type{});
+      step(c + 3, KFAC_AT(3), std::true_type{});
+    }
+    for (; c < steps; c += 4) {
+      step(c, KFAC_AT(0), std::false_type{});
+      if (c + 1 < steps) step(c + 1, KFAC_AT(1), std::false_type{});
+      if (c + 2 < steps) step(c + 2, KFAC_AT(2), std::false_type{});
+      if (c + 3 < steps) step(c + 3, KFAC_AT(3), std::false_type{});
+    }
+#undef KFAC_AT
+  }
+  const float back = 1.f / unit;  // exact: a power of two
+  if (d.splits > 1) {
+    KG float* part = gp(d.part) + (int64_t(split) * d.tiles + ti * d.nt + tj) * (BT * BT);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        KG float* o = part + (wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * BT + wn + (lane & 31);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[32 * j] = acc[i][j][e] * back;
+      }
+  } else {
+    const int c = k0 + wn + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int r = o0 + wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+        KG float* o = gp(d.out) + int64_t(r) * d.ldo + c;
+        if (r < d.m) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c + 32 * j < d.n) {
+              const float x = acc[i][j][e] * back;
+              o[32 * j] = d.accumulate ? o[32 * j] + x : x;
+            }
+        }
+      }
+  }
+  if (d.bias) {
+    KG float* part = gp(d.part_col) + ((int64_t(split) * d.nt + tj) * 2 + (wave & 1)) * (int64_t(d.mt) * BT) + o0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = sums[i] + __shfl_xor(sums[i], 32);
+      if (lane < 32) part[wm + 32 * i + lane] = x;
+    }
+  }
+}
+
+// What the splits and the shares of the column sums left, added up in their order. Blocks of 256 outputs; the
+// last ones do the bias.
+__global__ void __launch_bounds__(256) grad_join_kernel(TnJob d, int64_t groups) {
+  const int64_t b = blockIdx.x;
+  if (b < groups) {
+    const int per_row = (d.n + 255) / 256;
+    const int64_t r = b / per_row;
+    const int c = static_cast<int>(b - r * per_row) * 256 + threadIdx.x;
+    if (c >= d.n) return;
+    const int64_t at = (r / BT * d.nt + c / BT) * (BT * BT) + (r % BT) * BT + c % BT;
+    float sum = 0.f;
+    for (int s = 0; s < d.splits; ++s) sum += gp(d.part)[int64_t(s) * d.tiles * (BT * BT) + at];
+    KG float* o = gp(d.out) + r * d.ldo + c;
+    *o = d.accumulate ? *o + sum : sum;
+    return;
+  }
+  const int64_t r = (b - groups) * 256 + threadIdx.x;
+  if (r >= d.m) return;
+  float sum = 0.f;
+  for (int s = 0; s < d.splits * d.nt * 2; ++s) sum += gp(d.part_col)[int64_t(s) * d.mt * BT + r];
+  KG float* o = gp(d.bias_out) + r * d.inc_b;
+  *o = d.accumulate ? *o + sum : sum;
+}
+
 // The splits' parts added up, a tile a block.
 template <bool FACTOR>
 __global__ void __launch_bounds__(256) q8_join_kernel(TnJob d) {
@@ -433,11 +717,41 @@ static kfac_status launch_tn(const TnJob& j, hipStream_t s) {
   return KFAC_OK;
 }
 
-static TnJob grad_job(int32_t rows, int32_t c_in, int32_t c_out) {
+// near: rows lie less than 2^32 bytes apart.
+static TnJob grad_job(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype, bool near) {
   TnJob j = {};
   j.rows = rows, j.m = c_out, j.n = c_in;
   plan(j, false);
+  const int64_t mt = (int64_t(c_out) + BT - 1) / BT, nt = (int64_t(c_in) + BT - 1) / BT;
+  if (dtype == KFAC_F32 || !near || c_in % 8 || c_out % 8 || mt * nt < 64 || rows < 256) return j;
+  j.big = true;
+  j.mt = static_cast<int32_t>(mt), j.nt = static_cast<int32_t>(nt), j.tiles = static_cast<int32_t>(mt * nt);
+  j.per_split = rows, j.splits = 1;
   return j;
+}
+
+static void carve_grad(TnJob& j, Carver& cv) {
+  if (!j.big) return carve(j, cv);
+  if (j.splits > 1) j.part = cv.take<float>(size_t(j.splits) * j.tiles * BT * BT);
+  j.part_col = cv.take<float>(size_t(j.splits) * j.nt * 2 * j.mt * BT);
+}
+
+template <class T>
+static kfac_status launch_grad(const TnJob& j, hipStream_t s) {
+  if constexpr (!std::is_same_v<T, float>) {
+    if (j.big) {
+      KFAC_LAUNCH(K_GRAD_Q8, grad_big_kernel<T>, dim3(xcd_grid(int64_t(j.tiles) * j.splits)), dim3(256), 0, s, j);
+      KFAC_CHECK_LAUNCH("grad_big_kernel");
+      const int64_t groups = j.splits > 1 ? int64_t(j.m) * ((j.n + 255) / 256) : 0;
+      const int64_t all = groups + (j.bias ? (j.m + 255) / 256 : 0);
+      if (all) {
+        KFAC_LAUNCH(K_GRAD_Q8_JOIN, grad_join_kernel, dim3(static_cast<unsigned>(all)), dim3(256), 0, s, j, groups);
+        KFAC_CHECK_LAUNCH("grad_join_kernel");
+      }
+      return KFAC_OK;
+    }
+  }
+  return launch_tn<T, false>(j, s);
 }
 
 extern "C" kfac_status kfac_weight_grad_q8_workspace(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype,
@@ -446,10 +760,13 @@ extern "C" kfac_status kfac_weight_grad_q8_workspace(int32_t rows, int32_t c_in,
   if (!row_dtype(dtype)) return fail(KFAC_ERR_UNSUPPORTED, "dtype %d", dtype);
   kfac_status st = sizes_fit(rows, c_out, c_in);
   if (st) return st;
-  TnJob j = grad_job(rows, c_in, c_out);
-  Carver cv;
-  carve(j, cv);
-  *bytes = cv.used;
+  *bytes = 0;
+  for (bool near : {false, true}) {
+    TnJob j = grad_job(rows, c_in, c_out, dtype, near);
+    Carver cv;
+    carve_grad(j, cv);
+    *bytes = std::max(*bytes, cv.used);
+  }
   return KFAC_OK;
 }
 
@@ -466,17 +783,18 @@ extern "C" kfac_status kfac_weight_grad_q8(int32_t rows, int32_t c_in, int32_t c
                bs = {dbias, dbias ? c_out : 0, 1, inc_db, 4, "dbias"};
   for (const RowsOf* r : {&gs, &qs, &ss, &ws, &bs})
     if ((st = check_rows(*r))) return st;
-  TnJob j = grad_job(rows, c_in, c_out);
+  const bool near = rows <= 1 || (ld_g < (int64_t(1) << 31) && ld_q < (int64_t(1) << 32));
+  TnJob j = grad_job(rows, c_in, c_out, dtype, near);
   Carver sizing, cv(workspace);
-  carve(j, sizing);
+  carve_grad(j, sizing);
   const RowsOf scr = scratch(workspace, sizing.used);
   if ((st = check_apart({&ws, &bs, &scr, &gs, &qs, &ss}, 3))) return st;
   if ((st = check_device())) return st;
   if ((st = check_workspace(workspace, ws_bytes, sizing.used))) return st;
-  carve(j, cv);
+  carve_grad(j, cv);
   j.g = gout, j.q = q, j.scale = scale, j.out = dweight, j.bias_out = dbias;
   j.ldg = ld_g, j.ldq = ld_q, j.ldo = ld_dw, j.inc_b = inc_db, j.bias = dbias != nullptr, j.accumulate = accumulate;
-  return with_row_type(dtype, [&](auto tag) { return launch_tn<decltype(tag), false>(j, static_cast<hipStream_t>(stream)); });
+  return with_row_type(dtype, [&](auto tag) { return launch_grad<decltype(tag)>(j, static_cast<hipStream_t>(stream)); });
 }
 
 static kfac_status factor_jobs(int32_t count, const int32_t* rows, const int32_t* cols, const int32_t* bias,

@@ -222,6 +222,30 @@ def test_weight_grad_of_whole_numbers(kfac_gpu, dtype, rows, c_in, c_out):
         assert same(got, dw + 5) and (not biased or same(gb, db + 5))
 
 
+# sizes that fill the card with large tiles: the last ones ragged, one list of rows and several, few and many steps
+LARGE = [(300, 2048, 2048), (1111, 1032, 4104), (256, 2056, 2000), (8300, 1024, 4096), (700, 4104, 1040), (333, 8192, 520)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("rows,c_in,c_out", LARGE)
+def test_large_weight_grad_of_whole_numbers(kfac_gpu, dtype, rows, c_in, c_out):
+    q, s = codes(rows, rows, c_in, 8 if rows % 2 else 0, most=20), scales_of(rows, rows, zeros=rows != 300)
+    g = grads_of(c_in, rows, c_out, dtype, 8 if rows % 2 else 0, whole=True)
+    g[s == 0] = float("nan")
+    live = s != 0
+    # sums of whole numbers below 2^53: exact in any order, also on the GPU
+    a = (q.double() * s.double()[:, None])[live].cuda()
+    want = host64(g[live].double().T.contiguous() @ a)
+    bias = host64(g[live].double().sum(0))
+    got, gb = grad(kfac_gpu, g, q, s, True, rows % 2 == 0)
+    assert same(got, want) and same(gb, bias)
+    got, gb = grad(kfac_gpu, g, q, s, True, rows % 2 == 1, accumulate=True, start=5.0)
+    assert same(got, want + 5) and same(gb, bias + 5)
+    s[:] = 0
+    got, gb = grad(kfac_gpu, g, q, s, True, True)
+    assert not got.any() and not gb.any()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,c_in,c_out", [(33, 129, 57), (300, 256, 260), (1500, 70, 300)])
 def test_weight_grad(kfac_gpu, dtype, rows, c_in, c_out):
