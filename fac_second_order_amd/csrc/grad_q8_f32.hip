@@ -1,0 +1,9 @@
+// Weight gradients from fp32 gradients and rows in 8 bits.
+#include "q8_tn_kernel.hpp"
+
+namespace kfac {
+
+template kfac_status launch_tiles<float, false, 2, false>(const TnArgs<false>&, hipStream_t);
+template kfac_status launch_tiles<float, false, 2, true>(const TnArgs<false>&, hipStream_t);
+
+}  // namespace kfac

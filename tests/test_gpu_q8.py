@@ -223,10 +223,11 @@ def test_weight_grad_of_whole_numbers(kfac_gpu, dtype, rows, c_in, c_out):
 
 
 # sizes that fill the card with large tiles: the last ones ragged, one list of rows and several, few and many steps
-LARGE = [(300, 2048, 2048), (1111, 1032, 4104), (256, 2056, 2000), (8300, 1024, 4096), (700, 4104, 1040), (333, 8192, 520)]
+LARGE = [(300, 2048, 2048), (1111, 1032, 4104), (256, 2056, 2000), (8300, 1024, 4096), (700, 4104, 1040), (333, 8192, 520),
+         (1001, 2051, 2049), (640, 777, 1001), (33000, 40, 24), (9001, 130, 9)]
 
 
-@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,c_in,c_out", LARGE)
 def test_large_weight_grad_of_whole_numbers(kfac_gpu, dtype, rows, c_in, c_out):
     q, s = codes(rows, rows, c_in, 8 if rows % 2 else 0, most=20), scales_of(rows, rows, zeros=rows != 300)
@@ -339,6 +340,35 @@ def test_factor_of_whole_numbers(kfac_gpu, rows, cols):
         if bias and live:
             want[-1] = 1
         assert same(got, want), (rows, cols, np.abs(got - want).max())
+
+
+@pytest.mark.parametrize("rows,cols", [(700, 2051), (300, 1500), (6200, 1032), (13000, 520), (128, 4096), (20000, 64)])
+def test_large_factor_of_whole_numbers(kfac_gpu, rows, cols):
+    for bias in (True, False):
+        q, s = codes(rows, rows, cols, 3, most=4), scales_of(cols, rows, zeros=rows != 300)
+        live = s != 0
+        n = int(live.sum())
+        a = (q.double() * s.double()[:, None])[live]
+        if bias:
+            a = torch.cat([a, torch.ones_like(a[:, :1])], 1)
+        sums = a.T.contiguous() @ a  # whole numbers of sixteenths: exact in any order
+        i, j = torch.triu_indices(a.shape[1], a.shape[1], device="cuda")
+        want = host(sums[i, j]).astype(np.float32) * (np.float32(1) / np.float32(n))
+        if bias:
+            want[-1] = 1
+        assert float((a.abs().T @ a.abs()).max()) * 16 < 2 ** 24
+        assert same(host(factors(kfac_gpu, [(q, s)], bias, full=cols < 2000)[0]), want)
+        both = factors(kfac_gpu, [(q, s)] * 2 + [(q[:50], s[:50])], bias)
+        assert same(host(both[0]), want) and same(host(both[1]), want)
+
+
+def test_factors_of_many_layers(kfac_gpu):
+    """More layers than one launch takes, of every kind of tile."""
+    layers = [(codes(i, 40 + 211 * i, w, most=9), scales_of(i, 40 + 211 * i))
+              for i, w in enumerate([3, 8, 17, 64, 120, 129, 200, 256, 300, 31, 5, 40, 72, 88, 96, 104, 112, 136, 144, 152])]
+    for (q, s), p in zip(layers, factors(kfac_gpu, layers, True, full=True)):
+        want, size = qo.factor_packed(host(q), host(s), True)
+        assert (np.abs(host64(p) - want) <= 3 * U * size).all()  # exact sums, 1 / C and one product
 
 
 def test_factors_of_several_layers(kfac_gpu):
