@@ -18,4 +18,5 @@ from ._lib import (  # noqa: F401
     kfac_timing_kernels, kfac_kernel_name, kfac_timing_enable, kfac_timing_only, kfac_timing_reset,
     kfac_timing_read,
 )
+from .checkpoint import Checkpoint  # noqa: F401
 from .step import KfacStep  # noqa: F401

@@ -31,6 +31,7 @@ import torch
 import torch.nn as nn
 
 from . import _lib as K
+from . import checkpoint as ck
 from .step import KfacStep
 
 
@@ -155,10 +156,22 @@ class KfacCapture:
     whose factors are the model's Fisher, trust_radius bounds its predicted KL divergence
     (the mean over the rows that count, to second order and as far as the Kronecker factors
     hold); after another loss's backward pass it bounds the quadratic form of that loss's
-    second moment."""
+    second moment.
+
+    checkpoint="int8": the fully connected layers keep their input rows in 8 bits (Checkpoint),
+    for autograd and the step together, instead of in 16 bits or more once for each; their weight
+    gradients and factors are those of the values that are kept (a row's error is at most
+    1/127 of its largest entry), their outputs and the gradients at their inputs are what they were.
+    matmul="int8", with it: their products are formed in 8-bit integers too (kfac_linear_q8), with
+    a scale for each row and each output, also in passes without gradients; the gradients at their inputs
+    take the weights as they are."""
 
     def __init__(self, model, damping=1e-3, ema_decay=0.95, refresh_every=1, precond_accum="f32",
-                 refine_inverse=False, max_grad_norm=None, trust_radius=None):
+                 refine_inverse=False, max_grad_norm=None, trust_radius=None, checkpoint=None, matmul=None):
+        if checkpoint not in (None, "int8") or matmul not in (None, "int8"):
+            raise ValueError("checkpoint and matmul must be None or 'int8'")
+        if matmul and not checkpoint:
+            raise ValueError("matmul='int8' needs checkpoint='int8': the quantised input is the checkpoint")
         self.model = model
         self.precond_accum = precond_accum
         self.refine_inverse = bool(refine_inverse)
@@ -183,7 +196,13 @@ class KfacCapture:
         self.kstep = None
         self.calls = 0
         self.hooks = []
+        # checkpoints that a layer's running forward pass has made, until its hook takes them
+        self.made, self.int8 = {}, matmul == "int8"
+        self.wrapped = []
         for i, (m, _) in enumerate(self.pairs):
+            if checkpoint and isinstance(m, nn.Linear):
+                self.wrapped.append((m, m.__dict__.get("forward")))
+                m.forward = self._checkpointed(i, m)
             self.hooks.append(m.register_forward_hook(self._fwd(i)))
             self.hooks.append(m.register_full_backward_hook(self._bwd(i)))
         for i, bn in enumerate(self.bns):
@@ -194,13 +213,29 @@ class KfacCapture:
         for h in self.hooks:
             h.remove()
         self.hooks = []
+        for m, before in self.wrapped:
+            if before is None:
+                del m.forward
+            else:
+                m.forward = before
+        self.wrapped = []
+
+    # layers that keep their input in 8 bits ------------------------------------
+    def _checkpointed(self, i, m):
+        def forward(x):
+            if torch.is_grad_enabled():
+                y, self.made[i] = ck.linear(x, m.weight, m.bias, self.int8)
+                return y
+            return ck.linear(x, m.weight, m.bias, True)[0] if self.int8 else nn.functional.linear(x, m.weight, m.bias)
+        return forward
 
     # hooks ------------------------------------------------------------------
     def _fwd(self, i):
         def hook(mod, inp, out):
             if torch.is_grad_enabled():
                 self.n = inp[0].shape[0]
-                self.act[i] = _nhwc_half(inp[0])
+                made = self.made.pop(i, None)
+                self.act[i] = _nhwc_half(inp[0]) if made is None else made
         return hook
 
     def _bwd(self, i):

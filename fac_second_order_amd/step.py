@@ -13,6 +13,7 @@ import math
 import torch
 
 from . import _lib as K
+from .checkpoint import Checkpoint
 
 
 def side_split(n_all, min_order=1024):
@@ -71,7 +72,10 @@ class KfacStep:
     divergence of the model's distribution where that is its Fisher: gout (and bn_fisher)
     the gradients of log-probabilities of outcomes drawn from the model, one sample each, as
     KfacCapture.policy_backward takes them. Of a loss's own gradients it predicts none: F
-    then scales with the loss."""
+    then scales with the loss.
+
+    act: tensors as kfac_factors takes them, or for fully connected layers a Checkpoint of
+    their rows, whose factor kfac_factors_q8 forms."""
 
     def __init__(self, layers, bn_layers=(), device="cuda", damping=1e-3, bn_shift=None,
                  in_dtype=torch.float16, precond_accum="f32", refine_inverse=False, side_stream=True,
@@ -161,14 +165,38 @@ class KfacStep:
         return self.full[len(self.layers):]
 
     def factors(self, act, gout, ema_decay=0.0, stream=None):
-        K.kfac_factors(self.layers, act, gout, self.A_packed, self.G_packed, ema_decay,
-                       self.workspace, stream)
+        act = self._factors_of_checkpoints(self.layers, act, None, ema_decay, stream)
+        if any(t is not None for t in (*act, *gout)):
+            K.kfac_factors(self.layers, act, gout, self.A_packed, self.G_packed, ema_decay,
+                           self.workspace, stream)
+
+    def _factors_of_checkpoints(self, layers, act, full, ema_decay, stream):
+        """Forms the factors of the layers whose act is a Checkpoint; act without those."""
+        at = [l for l, a in enumerate(act) if isinstance(a, Checkpoint)]
+        if not at:
+            return act
+        held = [act[l] for l in at]
+        rows, cols, bias = [len(a) for a in held], [a.shape[1] for a in held], [layers[l].bias for l in at]
+        self._room(K.kfac_factors_q8_workspace(rows, cols, bias), stream)
+        K.kfac_factors_q8([a.q for a in held], [a.scale for a in held], [self.A_packed[l] for l in at],
+                          None if full is None else [full[l] for l in at], bias, ema_decay, self.workspace, stream)
+        return [None if isinstance(a, Checkpoint) else a for a in act]
+
+    @staticmethod
+    def _check_checkpoints(layers, act):
+        for l, a in zip(layers, act):
+            if isinstance(a, Checkpoint):
+                if (l.h, l.w, l.kh, l.kw, l.h_out, l.w_out) != (1,) * 6 or tuple(a.shape) != (l.n, l.c_in):
+                    raise ValueError("a Checkpoint is of a fully connected layer's [n, c_in] rows")
 
     def _make_room(self, layers, bn_layers, stream):
         """A workspace that also serves these layers, where they are not those of the step."""
         need = 0 if layers is self.layers else K.kfac_factors_workspace(layers, self.in_code)
         if bn_layers is not self.bn_layers and bn_layers:
             need = max(need, K.kfac_bn_diag_workspace(bn_layers))
+        self._room(need, stream)
+
+    def _room(self, need, stream):
         if self.workspace.numel() < need + 256:
             on = torch.cuda.current_stream(self.device) if stream is None else stream
             self.workspace.record_stream(on)  # calls in flight there use the old one
@@ -179,6 +207,9 @@ class KfacStep:
         # the packed factors (the stored state) and the upper triangles that kfac_invert
         # reads, from the same kernels: no separate unpack pass
         L = len(self.layers)
+        act = self._factors_of_checkpoints(layers, act, self.full[:L], ema_decay, stream)
+        if all(t is None for t in (*act, *gout)):
+            return
         K.kfac_factors_full(layers, act, gout, self.A_packed, self.G_packed, self.full[:L], self.full[L:],
                             ema_decay, self.workspace, stream)
 
@@ -320,6 +351,8 @@ class KfacStep:
             raise ValueError("lr must be finite and >= 0")
         layers = _same_but_samples(layers, self.layers, K.kfac_layer._fields_, "layers")
         bn_layers = _same_but_samples(bn_layers, self.bn_layers, K.kfac_bn._fields_, "bn_layers")
+        if refresh:
+            self._check_checkpoints(layers, act)
         self._make_room(layers, bn_layers, stream)
         if bn_fisher is not None:
             fisher_layers = _same_but_samples(bn_fisher[0], self.bn_layers, K.kfac_bn._fields_, "bn_layers")
