@@ -246,9 +246,9 @@ __device__ inline v4i load_codes(const KG int8_t* row, int k0, int c_in) {
 // groups of 16 bytes swizzled, so that 16 lanes that read one group of 16 rows meet every bank once.
 template <int WT>
 struct LinearTile {
-  static constexpr int T = 2 * WT, BK = WT == 32 ? 128 : 64, CPR = BK / 16, LOADS = 2 * T * CPR / 256, KS = BK / 32, F = WT / 32;
+  static constexpr int T = 2 * WT, BK = 128, CPR = BK / 16, LOADS = 2 * T * CPR / 256, KS = BK / 32, F = WT / 32;
   static constexpr int STAGE = 2 * T * BK;  // bytes of both operands
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = WT == 32 ? 4 : 2;
   static __device__ inline int swizzle(int row) { return (row / (256 / BK)) & (CPR - 1); }
   static __device__ inline int at(int row, int chunk) { return row * BK + 16 * (chunk ^ swizzle(row)); }
 };
@@ -258,7 +258,8 @@ struct LinearTile {
 template <class T, int WT, bool DIRECT>
 __global__ void __launch_bounds__(256) linear_q8_kernel(LinearArgs a, int across, int tiles) {
   using L = LinearTile<WT>;
-  constexpr int kOut = 4 * 32 * (WT * sizeof(T) + 16) + 2 * L::T * sizeof(float), kIn = L::STAGE * (DIRECT ? L::STAGES : 2);
+  constexpr int kPitch = WT * sizeof(T) + 16, kRowsAt = sizeof(T) == 4 && L::F > 1 ? L::F / 2 : L::F;
+  constexpr int kOut = 4 * 32 * kRowsAt * kPitch + 2 * L::T * sizeof(float), kIn = L::STAGE * (DIRECT ? L::STAGES : 2);
   __shared__ __attribute__((aligned(16))) char lds[kOut > kIn ? kOut : kIn];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int v = xcd_virtual(blockIdx.x, gridDim.x, tiles);
@@ -315,6 +316,14 @@ __global__ void __launch_bounds__(256) linear_q8_kernel(LinearArgs a, int across
     for (int j = 0; j < L::F; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+  // what the end needs, on its way while the products are formed
+  const int channel = min(o0 + tid % L::T, a.c_out - 1);
+  const float channel_scale = gp(a.w_scale)[channel];
+  const float channel_bias = a.bias ? static_cast<float>(gp(static_cast<const T*>(a.bias))[channel]) : 0.f;
+  float row_scale[L::F];
+#pragma unroll
+  for (int j = 0; j < L::F; ++j) row_scale[j] = gp(a.scale)[min(r0 + wr - L::T + 32 * j + (lane & 31), a.rows - 1)];
 
   const int steps = (a.c_in + L::BK - 1) / L::BK;
   if (steps) {
@@ -413,42 +422,39 @@ __global__ void __launch_bounds__(256) linear_q8_kernel(LinearArgs a, int across
     __syncthreads();
   }
 
-  // The channels' scales and biases go through LDS. Then each wave brings 32 rows at a time into LDS
-  // lines of their channels and stores them 16 bytes a lane.
-  constexpr int PITCH = WT * sizeof(T) + 16, EV = 16 / sizeof(T), LANES = WT / EV;
+  // The channels' scales and biases go through LDS; then each wave brings its rows into LDS lines of their
+  // channels (fp32: half of them at a time) and stores them 16 bytes a lane.
   float* const sv = reinterpret_cast<float*>(lds);
   float* const sb = sv + L::T;
-  char* const mine = lds + 2 * L::T * sizeof(float) + wave * 32 * PITCH;
-  for (int c = tid; c < L::T; c += 256) {
-    const int o = min(o0 + c, a.c_out - 1);
-    sv[c] = gp(a.w_scale)[o];
-    sb[c] = a.bias ? static_cast<float>(gp(static_cast<const T*>(a.bias))[o]) : 0.f;
-  }
+  char* const mine = lds + 2 * L::T * sizeof(float) + wave * 32 * kRowsAt * kPitch;
+  if (tid < L::T) sv[tid] = channel_scale, sb[tid] = channel_bias;
   __syncthreads();
+  constexpr int EV = 16 / sizeof(T), LANES = WT / EV;
   const int wo0 = o0 + wo, wr0 = r0 + wr - L::T;
 #pragma unroll
-  for (int j = 0; j < L::F; ++j) {
-    const int r = wr0 + 32 * j + (lane & 31);
-    const float s = gp(a.scale)[min(r, a.rows - 1)];
+  for (int j0 = 0; j0 < L::F; j0 += kRowsAt) {
 #pragma unroll
     for (int i = 0; i < L::F; ++i)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int c = 32 * i + 8 * g + 4 * (lane >> 5);
         const v4f v = *reinterpret_cast<const v4f*>(sv + wo + c), b = *reinterpret_cast<const v4f*>(sb + wo + c);
-        typename Pack<T, 4>::vec out;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = static_cast<T>(static_cast<float>(acc[i][j][4 * g + e]) * s * v[e] + b[e]);
-        typedef T vec4 __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<vec4*>(mine + (lane & 31) * PITCH + c * sizeof(T)) = out;
+        for (int j = j0; j < j0 + kRowsAt; ++j) {
+          typedef T vec4 __attribute__((ext_vector_type(4)));
+          vec4 out;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = static_cast<T>(static_cast<float>(acc[i][j][4 * g + e]) * row_scale[j] * v[e] + b[e]);
+          *reinterpret_cast<vec4*>(mine + (32 * (j - j0) + (lane & 31)) * kPitch + c * sizeof(T)) = out;
+        }
       }
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int n = 0; n < 32 * LANES / 64; ++n) {
+    for (int n = 0; n < kRowsAt * 32 * LANES / 64; ++n) {
       const int u = n * 64 + lane, row = u / LANES, c = u % LANES * EV;
-      const v4i raw = *reinterpret_cast<const v4i*>(mine + row * PITCH + c * sizeof(T));
+      const v4i raw = *reinterpret_cast<const v4i*>(mine + row * kPitch + c * sizeof(T));
       const auto out = __builtin_bit_cast(typename Pack<T>::vec, raw);
-      const int64_t rr = wr0 + 32 * j + row;
+      const int64_t rr = wr0 + 32 * j0 + row;
       const int o = wo0 + c;
       if (rr < a.rows) {
         KG T* p = gp(static_cast<T*>(a.y)) + rr * a.ldy + o;
