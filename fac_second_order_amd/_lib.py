@@ -601,12 +601,19 @@ def kfac_preference_loss(logits, token, seq_begin, seq_logp, margin, loss, dlogi
 
 # rows in 8 bits ------------------------------------------------------------------
 
+# Small calls wait for the host: each tensor is asked once for what is needed of it, and the call's tensors
+# together for where they are.
+
 def _rows(t, what, dtype=None):
     """(rows, cols, dtype code or None, address, pitch) of a tensor of rows."""
-    if t.dim() != 2 or (t.dtype != dtype if dtype is not None else t.dtype not in _ANY_CODE):
+    shape, kind = t.shape, t.dtype
+    if len(shape) != 2 or (kind != dtype if dtype is not None else kind not in _ANY_CODE):
         raise TypeError(f"{what} must be [rows, cols] in {'float16, bfloat16 or float32' if dtype is None else dtype}")
-    rows, cols = t.shape
-    return rows, cols, _ANY_CODE.get(t.dtype), t.data_ptr(), _pitch(t, rows, cols, what)
+    rows, cols = shape
+    apart, within = t.stride()
+    if (cols > 1 and within != 1) or (rows > 1 and apart < cols):
+        raise TypeError(f"the rows of {what} must be contiguous and apart")
+    return rows, cols, _ANY_CODE.get(kind), t.data_ptr(), apart if rows > 1 else cols
 
 
 def _mask_at(mask, rows):
@@ -625,12 +632,29 @@ def _checkpoint(q, scale, rows=None, cols=None):
     return r, c, at, ld, _vector(scale, torch.float32, r, "scale")
 
 
-def _here(stream, *tensors):
-    """Refuses tensors, or a stream, of another device than the current one."""
-    tensors = [t for t in tensors if t is not None]
-    _on_device(tensors, "every tensor of the call")
-    if stream is not None and stream.device != tensors[0].device:
+def _stream_of(stream, tensors):
+    """The raw stream of a call whose tensors (None: not given) and stream are on the current device, refused if
+    they are not: the library launches there."""
+    at = {t.get_device() for t in tensors if t is not None}
+    here = at.pop()
+    if at or here < 0 or here != torch.cuda.current_device():
+        raise ValueError("every tensor of the call must be on the current HIP device")
+    if stream is None:
+        return _raw_stream(here) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    if stream.device.index != here:
         raise ValueError("stream must be of the current HIP device")
+    return stream.cuda_stream
+
+
+def _scratch(workspace, query, sizes, like, stream):
+    """_call_ws for a workspace that has been asked where it is."""
+    if workspace is None:
+        return _call_ws(None, query, sizes, like.device, stream)
+    if not workspace.is_contiguous():
+        raise TypeError("workspace must be contiguous")
+    at = workspace.data_ptr()
+    pad = -at % 256
+    return at + pad, max(0, workspace.nbytes - pad), workspace
 
 
 def kfac_quantize_rows(x, q, scale, mask=None, pow2=True, stream=None):
@@ -639,18 +663,17 @@ def kfac_quantize_rows(x, q, scale, mask=None, pow2=True, stream=None):
     rows, cols, code, at, ld = _rows(x, "x")
     _, _, q_at, q_ld, s_at = _checkpoint(q, scale, rows, cols)
     m_at = _mask_at(mask, rows)
-    _here(stream, x, q, scale, mask)
-    _check(_lib.kfac_quantize_rows(rows, cols, code, at, ld, m_at, 1 if pow2 else 0, q_at, q_ld, s_at,
-                                   _stream(stream)), "kfac_quantize_rows")
+    raw = _stream_of(stream, (x, q, scale, mask))
+    _check(_lib.kfac_quantize_rows(rows, cols, code, at, ld, m_at, 1 if pow2 else 0, q_at, q_ld, s_at, raw),
+           "kfac_quantize_rows")
 
 
 def kfac_dequantize_rows(q, scale, x, stream=None):
     """x <- scale * q (float16, bfloat16 or float32; see kfac.h)."""
     rows, cols, code, at, ld = _rows(x, "x")
     _, _, q_at, q_ld, s_at = _checkpoint(q, scale, rows, cols)
-    _here(stream, x, q, scale)
-    _check(_lib.kfac_dequantize_rows(rows, cols, q_at, q_ld, s_at, code, at, ld, _stream(stream)),
-           "kfac_dequantize_rows")
+    raw = _stream_of(stream, (x, q, scale))
+    _check(_lib.kfac_dequantize_rows(rows, cols, q_at, q_ld, s_at, code, at, ld, raw), "kfac_dequantize_rows")
 
 
 def kfac_linear_q8_workspace(rows, c_in, c_out):
@@ -673,10 +696,10 @@ def kfac_linear_q8(x, q, scale, w, w_scale, y, bias=None, mask=None, workspace=N
         _, _, _, x_at, x_ld = _rows(x, "x")
     b_at = None if bias is None else _vector(bias, y.dtype, c_out, "bias")
     m_at = _mask_at(mask, rows)
-    _here(stream, x, q, scale, w, w_scale, y, bias, mask)
-    ws, wsb, held = _call_ws(workspace, kfac_linear_q8_workspace, (rows, c_in, c_out), y.device, stream)
+    raw = _stream_of(stream, (x, q, scale, w, w_scale, y, bias, mask, workspace))
+    ws, wsb, held = _scratch(workspace, kfac_linear_q8_workspace, (rows, c_in, c_out), y, stream)
     _check(_lib.kfac_linear_q8(rows, c_in, c_out, code, x_at or None, x_ld, m_at, q_at, q_ld, s_at, w_at,
-                               w_ld, ws_at, b_at, y_at, y_ld, ws, wsb, _stream(stream)), "kfac_linear_q8")
+                               w_ld, ws_at, b_at, y_at, y_ld, ws, wsb, raw), "kfac_linear_q8")
 
 
 def kfac_weight_grad_q8_workspace(rows, c_in, c_out, dtype=torch.float32):
@@ -699,11 +722,10 @@ def kfac_weight_grad_q8(gout, q, scale, dweight, dbias=None, accumulate=False, w
         if dbias.dtype != torch.float32 or dbias.shape != (c_out,) or (c_out > 1 and dbias.stride(0) < 1):
             raise TypeError(f"dbias must be a float32 tensor of {c_out}")
         b_at, b_inc = dbias.data_ptr(), max(1, dbias.stride(0))
-    _here(stream, gout, q, scale, dweight, dbias)
-    ws, wsb, held = _call_ws(workspace, kfac_weight_grad_q8_workspace, (rows, c_in, c_out, gout.dtype), gout.device,
-                             stream)
+    raw = _stream_of(stream, (gout, q, scale, dweight, dbias, workspace))
+    ws, wsb, held = _scratch(workspace, kfac_weight_grad_q8_workspace, (rows, c_in, c_out, gout.dtype), gout, stream)
     _check(_lib.kfac_weight_grad_q8(rows, c_in, c_out, code, g_at, g_ld, q_at, q_ld, s_at, w_at, w_ld, b_at, b_inc,
-                                    1 if accumulate else 0, ws, wsb, _stream(stream)), "kfac_weight_grad_q8")
+                                    1 if accumulate else 0, ws, wsb, raw), "kfac_weight_grad_q8")
 
 
 def _per_layer(bias, n):
@@ -738,12 +760,12 @@ def kfac_factors_q8(q, scale, A_packed, A_full=None, bias=False, ema_decay=0.0, 
     orders = [c + b for c, b in zip(cols, bias)]
     p_at = [_vector(p, torch.float32, d * (d + 1) // 2, "A_packed") for p, d in zip(A_packed, orders)]
     f_at = [0 if f is None else _vector(f, torch.float32, d * d, "A_full") for f, d in zip(full, orders)]
-    _here(stream, *q, *scale, *A_packed, *full)
-    ws, wsb, held = _call_ws(workspace, kfac_factors_q8_workspace, (rows, cols, bias), q[0].device, stream)
+    raw = _stream_of(stream, (*q, *scale, *A_packed, *full, workspace))
+    ws, wsb, held = _scratch(workspace, kfac_factors_q8_workspace, (rows, cols, bias), q[0], stream)
     r, c, b, qa, ql, sa, pa, fa = (_halfwords(rows), _halfwords(cols), _halfwords(bias), _words(q_at), _words(q_ld),
                                    _words(s_at), _words(p_at), _words(f_at))
     _check(_lib.kfac_factors_q8(n, _at(r), _at(c), _at(b), _at(qa), _at(ql), _at(sa), _at(pa), _at(fa), float(ema_decay),
-                                ws, wsb, _stream(stream)), "kfac_factors_q8")
+                                ws, wsb, raw), "kfac_factors_q8")
 
 
 # timing -------------------------------------------------------------------

@@ -98,7 +98,7 @@ struct Eight {
     return m;
   }
   template <bool POW2>
-  __device__ inline void store(KG int8_t* p, int left, const RowCode& c) const {
+  __device__ inline v2u coded(const RowCode& c) const {
     v2u out = {0, 0};
     if (c.most == 127) {
 #pragma unroll
@@ -115,7 +115,7 @@ struct Eight {
         out[k / 4] |= unsigned(uint8_t(max(-c.most, min(c.most, q)))) << (8 * (k & 3));
       }
     }
-    put(p, left, out);
+    return out;
   }
   static __device__ inline void put(KG int8_t* p, int left, v2u out) {
     if (left >= 8) {
@@ -168,11 +168,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int rows, int cols, 
   const RowCode code = row_code<POW2>(top);
   if constexpr (U) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u].template store<POW2>(qr + 8 * (t + u * TPR), cols - 8 * (t + u * TPR), code);
+    for (int u = 0; u < U; ++u) Eight<T>::put(qr + 8 * (t + u * TPR), cols - 8 * (t + u * TPR), v[u].template coded<POW2>(code));
   } else {
     for (int c = 8 * t; c < cols; c += 8 * TPR) {
       v[0].load(xr + c, cols - c);
-      v[0].template store<POW2>(qr + c, cols - c, code);
+      Eight<T>::put(qr + c, cols - c, v[0].template coded<POW2>(code));
     }
   }
   if (t == 0) gp(scale)[row] = code.s;
@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(int cols, unsigned
 
 struct LinearArgs {
   int rows, c_in, c_out;
-  const int8_t* q;
+  int8_t* q;
   const int8_t* w;
-  const float* scale;
+  float* scale;
   const float* w_scale;
   const void* bias;
   void* y;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(256) linear_q8_kernel(LinearArgs a, int across
 
   // rows past the last are that one again: what they give is not stored
   const KG int8_t* const wb = gp(a.w) + o0 * a.ldw;
-  const KG int8_t* const qb = gp(a.q) + r0 * a.ldq;
+  const KG int8_t* const qb = gp(static_cast<const int8_t*>(a.q)) + r0 * a.ldq;
   const int slot = tid % L::CPR, chunk = slot ^ L::swizzle(tid / L::CPR);  // the same for all loads of a thread
   unsigned off[L::LOADS];
 #pragma unroll
@@ -471,6 +471,113 @@ __global__ void __launch_bounds__(256) linear_q8_kernel(LinearArgs a, int across
   }
 }
 
+// Few rows: the weights' way from memory is what it takes. A block has 16 channels and all rows, 16 NB of them
+// or fewer; its WAVES waves share the codes, 64 at a time, operands straight from memory into the
+// matrix unit's layout (16 bytes a lane), DEPTH of them on their way; the waves' sums meet in LDS.
+//
+// FUSED: the block first quantises the rows itself, its first weights on their way meanwhile, which saves a
+// launch; block 0 writes the checkpoint. For up to kFusedCodes codes, which each block has to form.
+constexpr int kFewRows = 32, kFusedCodes = 16384;
+
+template <class T, int NB, int WAVES, bool FUSED>
+__global__ void __launch_bounds__(64 * WAVES) linear_few_kernel(LinearArgs a, const T* __restrict__ x, int64_t ldx,
+                                                                const uint8_t* __restrict__ mask) {
+  constexpr int NT = 64 * WAVES, DEPTH = 4, U = FUSED ? kFusedCodes / 8 / NT + 1 : 1;
+  __shared__ __attribute__((aligned(16))) int sums[WAVES][NB][16][17];
+  __shared__ __attribute__((aligned(16))) int8_t codes[FUSED ? kFusedCodes + 64 * 16 : 16];
+  __shared__ float scales[16 * NB];
+  __shared__ unsigned tops[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int o0 = blockIdx.x * 16, chunks = (a.c_in + 63) / 64;
+  const KG int8_t* const w = gp(a.w) + int64_t(min(o0 + (lane & 15), a.c_out - 1)) * a.ldw;
+  const int k_lane = 16 * (lane >> 4), pitch = (a.c_in + 15) / 16 * 16 + 16;  // of the codes in LDS
+  auto load = [&](const KG int8_t* row, int c) {  // past the end: zeros
+    if (64 * c + 64 <= a.c_in) return __builtin_bit_cast(v4i, load_pack<false, int8_t>(row + 64 * c + k_lane));
+    return load_codes(row, 64 * c + k_lane, a.c_in);
+  };
+  const KG int8_t* q[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) q[b] = gp(static_cast<const int8_t*>(a.q)) + int64_t(min(16 * b + (lane & 15), a.rows - 1)) * a.ldq;
+  v4i wv[DEPTH], qv[DEPTH][NB];
+  auto load_all = [&](int d, int c) {
+    wv[d] = load(w, c);
+    if constexpr (!FUSED)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) qv[d][b] = load(q[b], c);
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) load_all(d, wave + d * WAVES);
+  if constexpr (FUSED) {
+    const int groups = pitch / 8, all = a.rows * groups;  // of 8 codes, with what is behind a row's end
+    Eight<T> v[U];
+    if (tid < 16) tops[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int g = tid + u * NT, r = g / groups, c = 8 * (g - r * groups);
+      const bool take = g < all && c < a.c_in && (!mask || gp(mask)[r]);
+      v[u].load(gp(x) + (take ? r * ldx + c : 0), take ? a.c_in - c : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int g = tid + u * NT;
+      if (g < all) atomicMax(&tops[g / groups], v[u].top(0));  // of whole numbers: any order
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int g = tid + u * NT, r = g / groups, c = 8 * (g - r * groups);
+      if (g >= all) continue;
+      RowCode code = row_code<true>(tops[r]);
+      if (mask && !gp(mask)[r]) code.s = 0.f;
+      const v2u out = v[u].template coded<true>(code);
+      *reinterpret_cast<v2u*>(codes + r * pitch + c) = out;
+      if (c == 0) scales[r] = code.s;
+      if (blockIdx.x == 0) {
+        if (c < a.c_in) Eight<T>::put(gp(a.q) + r * a.ldq + c, a.c_in - c, out);
+        if (c == 0) gp(a.scale)[r] = code.s;
+      }
+    }
+    __syncthreads();
+  } else {
+    if (tid < 16 * NB) scales[tid] = gp(a.scale)[min(tid, a.rows - 1)];
+  }
+  const int8_t* const mine = codes + min(lane & 15, a.rows - 1) * pitch;
+  v4i acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = v4i{0, 0, 0, 0};
+  for (int c = wave; c < chunks; c += WAVES * DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int at = c + d * WAVES;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        v4i v;
+        // past the end the weights are 0
+        if constexpr (FUSED) v = *reinterpret_cast<const v4i*>(mine + min(64 * at + k_lane, pitch - 16));
+        else v = qv[d][b];
+        acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[d], v, acc[b], 0, 0, 0);
+      }
+      load_all(d, at + DEPTH * WAVES);
+    }
+  }
+  // a lane has row lane % 16 and channels 4 (lane / 16) ..
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums[wave][b][lane & 15][4 * (lane >> 4) + e] = acc[b][e];
+  __syncthreads();
+  for (int u = tid; u < 256 * NB; u += NT) {
+    const int r = u >> 4, o = o0 + (u & 15);
+    if (r >= a.rows || o >= a.c_out) continue;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) sum += sums[i][r >> 4][r & 15][u & 15];
+    const float b = a.bias ? static_cast<float>(gp(static_cast<const T*>(a.bias))[o]) : 0.f;
+    gp(static_cast<T*>(a.y))[r * a.ldy + o] = static_cast<T>(static_cast<float>(sum) * scales[r] * gp(a.w_scale)[o] + b);
+  }
+}
+
 // ---- host -------------------------------------------------------------------
 
 static kfac_status sizes_ok(int32_t rows, int32_t cols, const char* what) {
@@ -574,6 +681,21 @@ static kfac_status launch_linear(const LinearArgs& a, hipStream_t s) {
   return KFAC_OK;
 }
 
+template <class T>
+static kfac_status launch_few(const LinearArgs& a, const T* x, int64_t ldx, const uint8_t* mask, hipStream_t s) {
+  const unsigned blocks = static_cast<unsigned>((int64_t(a.c_out) + 15) / 16);
+  auto go = [&](auto nb, auto fused) {
+    constexpr int W = 16;  // 4 or 8 waves: 10.7 us for one row of 4096 x 4096 instead of 10.2, 17.0 and 18.1 for 8192 x 8192 instead of 14.9
+    KFAC_LAUNCH(K_LINEAR_Q8, (linear_few_kernel<T, decltype(nb)::value, W, decltype(fused)::value>), dim3(blocks),
+                dim3(64 * W), 0, s, a, x, ldx, mask);
+    KFAC_CHECK_LAUNCH("linear_few_kernel");
+    return KFAC_OK;
+  };
+  if (x) return go(std::integral_constant<int, 1>{}, std::true_type{});
+  if (a.rows <= 16) return go(std::integral_constant<int, 1>{}, std::false_type{});
+  return go(std::integral_constant<int, 2>{}, std::false_type{});
+}
+
 static size_t linear_need(int32_t, int32_t, int32_t) { return 0; }
 
 extern "C" kfac_status kfac_linear_q8_workspace(int32_t rows, int32_t c_in, int32_t c_out, size_t* bytes) {
@@ -611,12 +733,15 @@ extern "C" kfac_status kfac_linear_q8(int32_t rows, int32_t c_in, int32_t c_out,
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return with_row_type(dtype, [&](auto tag) {
     using T = decltype(tag);
-    if (x) {
+    const LinearArgs args = {rows, c_in, c_out, q, w, scale, w_scale, bias, y, ld_q, ld_w, ld_y};
+    const bool few = rows <= kFewRows && c_out > 0;
+    const bool fused = few && x && rows <= 16 && int64_t(rows) * c_in <= kFusedCodes;
+    if (x && !fused) {
       kfac_status e = launch_quantize<T, true>(rows, c_in, x, ld_x, mask, q, ld_q, scale, s);
       if (e) return e;
     }
     if (c_out == 0) return KFAC_OK;
-    const LinearArgs args = {rows, c_in, c_out, q, w, scale, w_scale, bias, y, ld_q, ld_w, ld_y};
+    if (few) return launch_few<T>(args, fused ? static_cast<const T*>(x) : nullptr, ld_x, mask, s);
     const int64_t big = (int64_t(c_out) + 255) / 256 * ((int64_t(rows) + 255) / 256);
     const int64_t mid = (int64_t(c_out) + 127) / 128 * ((int64_t(rows) + 127) / 128);
     const bool direct = !((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(w) | uintptr_t(ld_q) | uintptr_t(ld_w)) & 15);
