@@ -3,9 +3,9 @@
 
 namespace kfac {
 
-template kfac_status launch_tiles<_Float16, false, 2, false>(const TnArgs<false>&, hipStream_t);
-template kfac_status launch_tiles<_Float16, false, 2, true>(const TnArgs<false>&, hipStream_t);
-template kfac_status launch_tiles<_Float16, false, 4, false>(const TnArgs<false>&, hipStream_t);
-template kfac_status launch_tiles<_Float16, false, 4, true>(const TnArgs<false>&, hipStream_t);
+template kfac_status launch_grad_tiles<_Float16, 2, false>(const TnArgs<false>&, hipStream_t);
+template kfac_status launch_grad_tiles<_Float16, 2, true>(const TnArgs<false>&, hipStream_t);
+template kfac_status launch_grad_tiles<_Float16, 4, false>(const TnArgs<false>&, hipStream_t);
+template kfac_status launch_grad_tiles<_Float16, 4, true>(const TnArgs<false>&, hipStream_t);
 
 }  // namespace kfac

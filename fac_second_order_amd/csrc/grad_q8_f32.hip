@@ -3,7 +3,7 @@
 
 namespace kfac {
 
-template kfac_status launch_tiles<float, false, 2, false>(const TnArgs<false>&, hipStream_t);
-template kfac_status launch_tiles<float, false, 2, true>(const TnArgs<false>&, hipStream_t);
+template kfac_status launch_grad_tiles<float, 2, false>(const TnArgs<false>&, hipStream_t);
+template kfac_status launch_grad_tiles<float, 2, true>(const TnArgs<false>&, hipStream_t);
 
 }  // namespace kfac

@@ -8,7 +8,7 @@
 // by the matrix unit. bf16 gradients meet a_t in bf16. fp16 gradients meet it in fp16, relative
 // to the largest scale of the block's rows (exact down to 2^-29 of that). fp32 gradients are cut
 // into three bf16 parts of 8 bits each, which is exact, and take three products. The factor is
-// formed in fp16.
+// formed in integers, rows of one scale after the other.
 //
 // Rows with s_t = 0 are taken out of a list of the block's rows, before anything of them is
 // read: their gradients may hold anything, and cost nothing.
@@ -53,11 +53,34 @@ struct TnJobs {
 };
 // A factor call's layers go in the kernels' arguments, this many a launch (under 4 KB).
 constexpr int kTnMany = 16;
+// Most rows of a block of the factor's tiles of 64 f (of tiles of 128, two blocks share a compute unit's LDS).
+constexpr int factor_rows(int f) { return f == 2 ? 4096 : 8192; }
 template <bool FACTOR>
 using TnArgs = TnJobs<FACTOR ? kTnMany : 1>;
 
-// Launches of the tile kernels, for T's type; ragged: columns that are no whole groups of 8.
-template <class T, bool FACTOR, int F, bool RAGGED>
-kfac_status launch_tiles(const TnArgs<FACTOR>& a, hipStream_t s);
+// Tile t of the factor's upper triangle of nb x nb tiles: bands of 4 rows of tiles, each column by column, so that the
+// tiles that run at a time on an XCD share the rows of both operands.
+__device__ inline void factor_tile(int t, int nb, int& ti, int& tj) {
+  int first = 0;
+  for (;;) {
+    const int left = nb - first, high = min(4, left), corner = high * (high + 1) / 2, all = corner + (left - high) * high;
+    if (t < all) {
+      int x = 0;
+      if (t >= corner) {
+        x = high + (t - corner) / high, t = (t - corner) % high;
+      } else {
+        while (t > x) t -= ++x;
+      }
+      ti = first + t, tj = first + x;
+      return;
+    }
+    t -= all, first += 4;
+  }
+}
+
+// Launches of the tile kernels. ragged: columns that are no whole groups of 8 (weight gradients) or 16.
+template <class T, int F, bool RAGGED>
+kfac_status launch_grad_tiles(const TnArgs<false>& a, hipStream_t s);
+kfac_status launch_factor_tiles(const TnArgs<true>& a, int f, bool ragged, hipStream_t s);
 
 }  // namespace kfac

@@ -111,8 +111,9 @@ __device__ inline int list_rows(const float* scale, int64_t r0, int n, float uni
 
 // 2^k such that the largest finite scale of the rows times it is 2^5: relative to that, fp16 holds
 // s q down to 2^-29 of the largest scale exactly (the sum with 1152 that makes a code stays finite).
-template <int NT, int LIST>
-__device__ inline float scale_unit(const float* scale, int64_t r0, int n, RowList<LIST>& l) {
+// scratch: NT / 64 floats.
+template <int NT>
+__device__ inline float scale_unit(const float* scale, int64_t r0, int n, float* scratch) {
   unsigned top = 0;
   for (int r = threadIdx.x; r < n; r += NT) {
     const unsigned b = __float_as_uint(gp(scale)[r0 + r]) & 0x7fffffffu;
@@ -120,10 +121,10 @@ __device__ inline float scale_unit(const float* scale, int64_t r0, int n, RowLis
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
-  if ((threadIdx.x & 63) == 0) l.top[threadIdx.x >> 6] = __uint_as_float(top);
+  if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = __uint_as_float(top);
   __syncthreads();
   float t = 0.f;
-  for (int i = 0; i < NT / 64; ++i) t = fmaxf(t, l.top[i]);
+  for (int i = 0; i < NT / 64; ++i) t = fmaxf(t, scratch[i]);
   __syncthreads();
   int e = static_cast<int>(__float_as_uint(t) >> 23);  // 2^(e - 127) <= t
   e = 127 + 5 - (e - 127);                              // of 2^5 / 2^(e - 127)
@@ -147,7 +148,7 @@ template <int F>
 struct Tile {
   static constexpr int T = 64 * F, LINE = 2 * T, OPERAND = kStep * LINE, GROUPS = T / 8, LIST = F == 2 ? 2048 : 8192;
   // by how many groups a row's line is moved
-  static __device__ inline int moved(int row) { return F == 3 ? (row << 1) & 4 : (row & 3) << 2; }
+  static __device__ inline int moved(int row) { return (row & 3) << 2; }
 };
 
 // What a thread reads of a group of 8, as it comes from memory.
@@ -203,32 +204,48 @@ struct PutFactor {
     out[o] = v;
     if (full) full[r * order + c] = v;
   }
+  // N entries (r[k], c[k]) at a time, of which `live` are written: the stored ones are on their way together
+  template <int N>
+  __device__ inline void all(const int (&r)[N], const int (&c)[N], const bool (&live)[N], float (&v)[N]) const {
+    int64_t o[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] = live[k] ? packed_off(r[k], c[k], order) : 0;
+    if (decay != 0.f) {
+      float old[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) old[k] = out[o[k]];
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = any ? decay * old[k] + (1.f - decay) * v[k] : old[k];
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (live[k]) out[o[k]] = v[k];
+    if (!full) return;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (live[k]) full[r[k] * order + c[k]] = v[k];
+  }
 };
 __device__ inline PutFactor put_factor(const TnJob& d, int counted) {
   return {gp(d.out), gp(d.full), d.decay, counted > 0, int64_t(d.m) + d.bias};
 }
 __device__ inline void put_grad(KG float* o, float v, int accumulate) { *o = accumulate ? *o + v : v; }
 
-template <class T_, bool FACTOR, int F, bool RAGGED>
-__global__ void __launch_bounds__(256, F == 2 ? 2 : 1) q8_tile_kernel(TnArgs<FACTOR> args) {
+template <class E, int F, bool RAGGED>
+__global__ void __launch_bounds__(256, F == 2 ? 2 : 1) grad_tile_kernel(TnArgs<false> args) {
   using L = Tile<F>;
-  using E = std::conditional_t<FACTOR, int8_t, T_>;  // elements of the first operand
-  constexpr int T = L::T, P = kParts<T_>, W = 32 * F;
-  constexpr bool HALF = std::is_same_v<T_, _Float16>;
+  constexpr int T = L::T, P = kParts<E>, W = 32 * F;
+  constexpr bool HALF = std::is_same_v<E, _Float16>;
   __shared__ __attribute__((aligned(16))) char lds[2 * (P + 1) * L::OPERAND];
   __shared__ RowList<L::LIST> list;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int v = xcd_virtual(blockIdx.x, gridDim.x, args.items);
   if (v < 0) return;
-  const TnJob& d = args.j[FACTOR ? args.owner(v, &TnJob::begin) : 0];
+  const TnJob& d = args.j[0];
   const int item = v - d.begin, split = item / d.tiles, tile = item - split * d.tiles;
-  int ti, tj;
-  if (FACTOR) {
-    upper_tile(tile, d.mt, ti, tj);
-  } else {  // bands of 4 tiles of outputs, so that the tiles that run at a time on an XCD share both operands
-    const int band = tile / (4 * d.nt), in = tile - band * 4 * d.nt, high = min(4, d.mt - 4 * band);
-    ti = band * 4 + in % high, tj = in / high;
-  }
+  // bands of 4 tiles of outputs, so that the tiles that run at a time on an XCD share both operands
+  const int band = tile / (4 * d.nt), in = tile - band * 4 * d.nt, high = min(4, d.mt - 4 * band);
+  const int ti = band * 4 + in % high, tj = in / high;
   const int o0 = ti * T, k0 = tj * T;
   const int64_t r_begin = int64_t(split) * d.per_split;
   const int r_count = static_cast<int>(min(int64_t(d.per_split), d.rows - r_begin));
@@ -263,12 +280,11 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) q8_tile_kernel(TnArgs<FAC
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   // Column sums of the first operand: the tiles of a row of tiles, and a tile's two waves that hold the same
   // columns, take turns, a step each; or the row's first tile does all. A lane adds up its column.
-  const int first_tj = FACTOR ? ti : 0;
-  const bool sums_here = d.bias && (!d.solo || tj == first_tj);
+  const bool sums_here = d.bias && (!d.solo || tj == 0);
   float sums[F];
 #pragma unroll
   for (int i = 0; i < F; ++i) sums[i] = 0.f;
-  const int turns = d.solo ? 2 : 2 * (d.nt - first_tj), turn = (d.solo ? 0 : 2 * (tj - first_tj)) + (wave & 1);
+  const int turns = d.solo ? 2 : 2 * d.nt, turn = (d.solo ? 0 : 2 * tj) + (wave & 1);
   const int s16 = lane & 15, kk = 8 * (lane >> 5) + (s16 >> 2), cc = 16 * ((lane >> 4) & 1) + 4 * (s16 & 3);
   // where this lane's loads of the wave's groups of 32 columns begin in a buffer
   const char* fa_at[F];
@@ -284,17 +300,15 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) q8_tile_kernel(TnArgs<FAC
     const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(from + 4 * L::LINE));
     return v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
-  const float unit = HALF ? scale_unit<256>(d.scale, r_begin, r_count, list) : 1.f;
-  const unsigned a_pitch = static_cast<unsigned>(FACTOR ? d.ldq : d.ldg * int64_t(sizeof(E))), b_pitch = static_cast<unsigned>(d.ldq);
-  int counted = 0;
+  const float unit = HALF ? scale_unit<256>(d.scale, r_begin, r_count, list.top) : 1.f;
+  const unsigned a_pitch = static_cast<unsigned>(d.ldg * int64_t(sizeof(E))), b_pitch = static_cast<unsigned>(d.ldq);
   for (int base = 0; base < r_count; base += L::LIST) {
     const int64_t r0 = r_begin + base;
     const int n = list_rows<256>(d.scale, r0, min(L::LIST, r_count - base), unit, list);
-    counted += n;
     const int steps = (n + kStep - 1) / kStep;
     if (!steps) continue;
     const KG char* const b0 = reinterpret_cast<const KG char*>(gp(d.q)) + r0 * d.ldq;
-    const KG char* const a0 = FACTOR ? b0 : static_cast<const KG char*>((const KG void*)gp(static_cast<const char*>(d.g))) + r0 * d.ldg * int64_t(sizeof(E));
+    const KG char* const a0 = gp(static_cast<const char*>(d.g)) + r0 * d.ldg * int64_t(sizeof(E));
     // rows of a step from the list, and their scales
     auto rows_of = [&](int c, int (&r)[F]) {
 #pragma unroll
@@ -324,10 +338,7 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) q8_tile_kernel(TnArgs<FAC
       if constexpr (RAGGED)
         if (h == 0) araw[set][i].shift(a_cut[i]);
       char* const to = abuf + buf * P * L::OPERAND + at[i];
-      if constexpr (FACTOR) {
-        parts[0][h] = two_codes<HALF>(araw[set][i].w[h >> 1], h & 1, s[i]);
-        if (h == 3) *reinterpret_cast<v4u*>(to) = parts[0];
-      } else if constexpr (P == 1) {
+      if constexpr (P == 1) {
         if (h == 0) {
           v4u x = araw[set][i].w;
           if (!whole && s[i] == 0.f) x = v4u{0, 0, 0, 0};
@@ -456,19 +467,16 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) q8_tile_kernel(TnArgs<FAC
   }
 
   // a lane's accumulators: column lane % 32, rows 8 (e / 4) + 4 (lane / 32) + e % 4
-  const float back = 1.f / unit, colback = FACTOR ? back : 1.f;  // exact: powers of two
-  const float inv_r = FACTOR && counted ? 1.f / static_cast<float>(counted) : 0.f;
-  const PutFactor put = put_factor(d, counted);
-  if (FACTOR && d.part_rows && tile == 0 && tid == 0) gp(d.part_rows)[split] = counted;  // somebody joins
+  const float back = 1.f / unit;  // exact: a power of two
   if (d.splits > 1) {
-    KG float* part = gp(d.part) + (int64_t(split) * d.tiles + (FACTOR ? tile : ti * d.nt + tj)) * (T * T);
+    KG float* part = gp(d.part) + (int64_t(split) * d.tiles + ti * d.nt + tj) * (T * T);
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         KG float* o = part + (wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * T + wn + (lane & 31);
 #pragma unroll
-        for (int j = 0; j < F; ++j) o[32 * j] = FACTOR ? acc[i][j][e] * back * back : acc[i][j][e] * back;
+        for (int j = 0; j < F; ++j) o[32 * j] = acc[i][j][e] * back;
         __builtin_amdgcn_sched_barrier(0);
       }
   } else {
@@ -478,11 +486,7 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) q8_tile_kernel(TnArgs<FAC
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int rr = o0 + wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        if constexpr (FACTOR) {
-#pragma unroll
-          for (int j = 0; j < F; ++j)
-            if (rr <= c + 32 * j && c + 32 * j < d.n) put(rr, c + 32 * j, acc[i][j][e] * back * back * inv_r);
-        } else if (rr < d.m) {
+        if (rr < d.m) {
           KG float* o = gp(d.out) + int64_t(rr) * d.ldo + c;
 #pragma unroll
           for (int j = 0; j < F; ++j)
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) q8_tile_kernel(TnArgs<FAC
   }
   if (!sums_here) return;
 #pragma unroll
-  for (int i = 0; i < F; ++i) sums[i] = (sums[i] + __shfl_xor(sums[i], 32)) * colback;
+  for (int i = 0; i < F; ++i) sums[i] += __shfl_xor(sums[i], 32);
   if (!d.solo) {
     KG float* part = gp(d.part_col) + (int64_t(split) * d.shares + turn) * (int64_t(d.mt) * T) + o0;
 #pragma unroll
@@ -511,21 +515,14 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) q8_tile_kernel(TnArgs<FAC
   for (int i = 0; i < F; ++i) {
     const int c = o0 + wm + 32 * i + lane;
     if ((wave & 1) || lane >= 32 || c >= d.m) continue;
-    const float x = sums[i] + other[wm + 32 * i + lane];
-    if (FACTOR) {
-      put(c, d.m, x * inv_r);
-      if (c == 0) put(d.m, d.m, counted ? 1.f : 0.f);
-    } else {
-      put_grad(gp(d.bias_out) + c * d.inc_b, x, d.accumulate);
-    }
+    put_grad(gp(d.bias_out) + c * d.inc_b, sums[i] + other[wm + 32 * i + lane], d.accumulate);
   }
 }
 
-template <class T, bool FACTOR, int F, bool RAGGED>
-kfac_status launch_tiles(const TnArgs<FACTOR>& a, hipStream_t s) {
-  KFAC_LAUNCH(FACTOR ? K_FACTOR_Q8 : K_GRAD_Q8, (q8_tile_kernel<T, FACTOR, F, RAGGED>), dim3(xcd_grid(a.items)), dim3(256),
-              0, s, a);
-  KFAC_CHECK_LAUNCH("q8_tile_kernel");
+template <class T, int F, bool RAGGED>
+kfac_status launch_grad_tiles(const TnArgs<false>& a, hipStream_t s) {
+  KFAC_LAUNCH(K_GRAD_Q8, (grad_tile_kernel<T, F, RAGGED>), dim3(xcd_grid(a.items)), dim3(256), 0, s, a);
+  KFAC_CHECK_LAUNCH("grad_tile_kernel");
   return KFAC_OK;
 }
 

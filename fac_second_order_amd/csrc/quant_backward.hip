@@ -48,6 +48,11 @@ struct Stage {
   }
 };
 
+// A factor's scale: NaN, if it is neither 0 nor a power of two.
+__device__ inline float power_of_two(float s) {
+  return __float_as_uint(s) & 0x807fffffu ? __uint_as_float(0x7fc00000u) : s;
+}
+
 // The plain kernel: any sizes and pitches, tiles of 128 x 128, a step's rows staged and then multiplied. For
 // operands of fewer than 8 columns, and rows 2^32 bytes and more apart.
 template <class T, bool FACTOR>
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int tile = blockIdx.x % d.tiles, split = blockIdx.x / d.tiles;
   int ti, tj;
-  if (FACTOR) upper_tile(tile, d.mt, ti, tj);
+  if (FACTOR) factor_tile(tile, d.mt, ti, tj);
   else ti = tile / d.nt, tj = tile % d.nt;
   const int64_t r_begin = int64_t(split) * d.per_split;
   const int r_count = static_cast<int>(min(int64_t(d.per_split), d.rows - r_begin));
@@ -75,7 +80,7 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-  const float unit = HALF ? scale_unit<NT>(d.scale, r_begin, r_count, list) : 1.f;
+  const float unit = HALF ? scale_unit<NT>(d.scale, r_begin, r_count, list.top) : 1.f;
   int counted = 0;
   for (int base = 0; base < r_count; base += kSmallList) {
     const int64_t r0 = r_begin + base;
@@ -92,7 +97,7 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
       for (int i = 0; i < a.N; ++i) {
         const int r = a.row(i), c = a.col(i);
         if constexpr (FACTOR) {
-          *reinterpret_cast<v8s*>(&lds[0][r][c]) = codes16<HALF>(a.v[i], list.s[k0 + r]);
+          *reinterpret_cast<v8s*>(&lds[0][r][c]) = codes16<HALF>(a.v[i], power_of_two(list.s[k0 + r]));
         } else if constexpr (P == 3) {
           v8s h[3];
 #pragma unroll
@@ -110,7 +115,7 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
 #pragma unroll
       for (int i = 0; i < b.N; ++i) {
         const int r = b.row(i), c = b.col(i);
-        *reinterpret_cast<v8s*>(&lds[P][r][c]) = codes16<HALF>(b.v[i], list.s[k0 + r]);
+        *reinterpret_cast<v8s*>(&lds[P][r][c]) = codes16<HALF>(b.v[i], FACTOR ? power_of_two(list.s[k0 + r]) : list.s[k0 + r]);
       }
       __syncthreads();
       if (sums && tid < TM) {
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(256) q8_join_kernel(TnArgs<FACTOR> args) {
   if (item < here) {
     const int per = T * T / kJoin, tile = item / per, x = item % per * kJoin + 4 * tid;
     int ti, tj;
-    if (FACTOR) upper_tile(tile, d.mt, ti, tj);
+    if (FACTOR) factor_tile(tile, d.mt, ti, tj);
     else ti = tile / d.nt, tj = tile % d.nt;
     const int r = ti * T + x / T, c = tj * T + x % T;
     if (r >= d.m || c >= d.n || (FACTOR && r > c + 3)) return;
@@ -238,21 +243,27 @@ __global__ void __launch_bounds__(256) q8_join_kernel(TnArgs<FACTOR> args) {
       for (int k = 0; k < 4; ++k) sum += v[k];
     }
     for (; s < d.splits; ++s) sum += *reinterpret_cast<const KG v4f*>(from + s * apart);
+    if constexpr (FACTOR) {
+      const int rs[4] = {r, r, r, r}, cs[4] = {c, c + 1, c + 2, c + 3};
+      bool live[4];
+      float x[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (c + k >= d.n) continue;
-      if (!FACTOR) put_grad(gp(d.out) + int64_t(r) * d.ldo + c + k, sum[k], d.accumulate);
-      else if (r <= c + k) put(r, c + k, sum[k] * inv_r);
+      for (int k = 0; k < 4; ++k) live[k] = cs[k] < d.n && r <= cs[k], x[k] = sum[k] * inv_r;
+      put.all(rs, cs, live, x);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + k < d.n) put_grad(gp(d.out) + int64_t(r) * d.ldo + c + k, sum[k], d.accumulate);
     }
     return;
   }
   __shared__ float part[4][64];
-  const int c = (item - here) * 64 + (tid & 63), ti = min(c, d.m - 1) / T;
-  const int shares = !d.f ? 1 : FACTOR ? 2 * (d.nt - ti) : 2 * d.nt, all = d.splits * shares;
+  const int c = (item - here) * 64 + (tid & 63);
+  const int all = d.splits * d.shares;
   float sum = 0.f;
   if (c < d.m)
     for (int k = tid >> 6; k < all; k += 4)
-      sum += gp(d.part_col)[(int64_t(k / shares) * d.shares + k % shares) * (int64_t(d.mt) * T) + c];
+      sum += gp(d.part_col)[int64_t(k) * (int64_t(d.mt) * T) + c];
   part[tid >> 6][tid & 63] = sum;
   __syncthreads();
   if (tid >= 64 || c >= d.m) return;
@@ -275,47 +286,57 @@ static void set_tiles(TnJob& j, int f, bool factor) {
   j.mt = static_cast<int32_t>((int64_t(j.m) + T - 1) / T);
   j.nt = std::max(1, static_cast<int32_t>((int64_t(j.n) + T - 1) / T));  // a bias alone has its tiles too
   j.tiles = factor ? j.mt * (j.mt + 1) / 2 : j.mt * j.nt;
-  j.shares = f ? 2 * j.nt : 1;
+  j.shares = !f ? 1 : factor ? 2 : 2 * j.nt;
 }
 
-// Tile edge and splits of the rows by what they are expected to take, in us: rounds over the compute units of the
-// steps of one tile (measured on full cards), what a block spends before and after, and the parts' way
-// through memory. `share`: the part of the card that the job has. most: rows that one sum may run over.
-static void plan(TnJob& j, bool factor, kfac_dtype dtype, bool near, double share, int64_t most) {
+// Tile edge and splits of the rows by what they are expected to take, in us, which is returned: rounds over the
+// compute units of the steps of one tile (measured on full cards; a factor's scales add some), what a block
+// spends before and after, and the parts' way through memory. `share`: the part of the card that the job has;
+// `only`: this tile edge, unless 0.
+static double plan(TnJob& j, bool factor, kfac_dtype dtype, bool near, double share, int only) {
   const int64_t rows = std::max(j.rows, 1);
-  if (!near || j.m < 8 || j.n < 8) {
+  const int least = factor ? 16 : 8, rows_a_step = factor ? 64 : kStep;
+  double best = 0;
+  if (!near || j.m < least || j.n < least) {
     set_tiles(j, 0, factor);
-    int64_t splits = std::min<int64_t>((rows + 511) / 512, 512 / std::max(1, j.tiles));
-    splits = std::max<int64_t>({1, splits, (rows + most - 1) / most});
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>((rows + 511) / 512, 512 / std::max(1, j.tiles)));
     j.per_split = static_cast<int32_t>((rows + splits - 1) / splits);
   } else {
-    double best = 0;
-    int best_f = 2;
+    int best_f = 0;
     int64_t best_splits = 1;
-    const int64_t steps = (rows + kStep - 1) / kStep;
-    for (int f : {2, 3, 4}) {
-      if ((dtype == KFAC_F32 && f > 2) || (!factor && f == 3)) continue;
+    const int64_t steps = (rows + rows_a_step - 1) / rows_a_step;
+    for (int f : {1, 2, 3, 4}) {
+      if (factor ? f == 4 : f == 1 || f == 3 || (f == 4 && dtype == KFAC_F32)) continue;
+      if (only && f != only) continue;
       set_tiles(j, f, factor);
-      const double slots = std::max(1.0, kCus * share * (f == 2 ? 2 : 1));
-      const double step = f == 4 ? 0.95 : f == 3 ? 0.62 : dtype == KFAC_F32 ? 1.2 : 0.55;
-      const double part_us = double(j.tiles) * tile_edge(j) * tile_edge(j) * 8 / 4.5e6;
-      for (int64_t s = std::max<int64_t>(1, (rows + most - 1) / most); s <= 128 && (s == 1 || steps / s >= 4); ++s) {
-        const double us = std::ceil(double(j.tiles) * s / slots) * (5 + std::ceil(double(steps) / s) * step) +
-                          (s > 1 ? 5 + s * part_us / share : 0);
+      const double entries = double(j.tiles) * tile_edge(j) * tile_edge(j);
+      const double slots = std::max(1.0, kCus * share * (f == 1 ? 3 : f == 2 ? 2 : 1));
+      const double step = factor ? (f == 1 ? 0.6 : 0.55) : f == 4 ? 0.95 : dtype == KFAC_F32 ? 1.2 : 0.55;
+      const int64_t fewest = factor ? (rows + factor_rows(f) - 1) / factor_rows(f) : 1;
+      for (int64_t s = fewest; s <= std::max<int64_t>(fewest, 128) && (s == fewest || steps / s >= 4); s += 1 + s / 8) {
+        const double rounds = std::ceil(double(j.tiles) * s / slots), each = std::ceil(double(steps) / s);
+        double us;
+        if (factor) {
+          us = rounds * (6 + 4 * f + (each + 4) * step);
+          us += s > 1 ? 6 + 0.15 * s + entries * (10 + 2 * s) / (6e6 * share) : 2 * f * f;
+        } else {
+          us = rounds * (8 + each * step) + (s > 1 ? 5 + s * entries * 8 / (4.5e6 * share) : 0);
+        }
         if (best == 0 || us < best) best = us, best_f = f, best_splits = s;
       }
     }
     set_tiles(j, best_f, factor);
-    j.per_split = static_cast<int32_t>((steps + best_splits - 1) / best_splits * kStep);
+    j.per_split = static_cast<int32_t>((steps + best_splits - 1) / best_splits * rows_a_step);
   }
   j.splits = static_cast<int32_t>((rows + j.per_split - 1) / j.per_split);
   // one tile's waves add up the columns alone where that saves a launch and takes little
-  j.solo = j.f && j.splits == 1 && (j.nt == 1 || rows <= 1024);
+  j.solo = j.f && j.splits == 1 && (factor || j.nt == 1 || rows <= 1024);
+  return best;
 }
 
-static void carve(TnJob& j, Carver& cv) {
+static void carve(TnJob& j, bool factor, Carver& cv) {
   const int T = tile_edge(j);
-  if (j.splits > 1) j.part = cv.take<float>(size_t(j.splits) * j.tiles * T * T);
+  if (j.splits > 1 || (factor && j.f)) j.part = cv.take<float>(size_t(j.splits) * j.tiles * T * T);
   if (j.splits == 1 && (!j.f || j.solo)) return;
   j.part_col = cv.take<float>(size_t(j.splits) * j.shares * j.mt * T);
   j.part_rows = cv.take<int32_t>(j.splits);
@@ -350,12 +371,15 @@ static kfac_status launch_jobs(TnJob* j, int n, bool ragged, hipStream_t s) {
   a.n = n, a.items = static_cast<int32_t>(items), a.joins = static_cast<int32_t>(joins);
   const int f = j[0].f;
   kfac_status st = KFAC_OK;
-  if (f == 0) st = launch_plain<T, FACTOR>(j[0], s);
-  else if (f == 2) st = ragged ? launch_tiles<T, FACTOR, 2, true>(a, s) : launch_tiles<T, FACTOR, 2, false>(a, s);
-  if constexpr (FACTOR)
-    if (f == 3) st = ragged ? launch_tiles<T, FACTOR, 3, true>(a, s) : launch_tiles<T, FACTOR, 3, false>(a, s);
-  if constexpr (!std::is_same_v<T, float>)
-    if (f == 4) st = ragged ? launch_tiles<T, FACTOR, 4, true>(a, s) : launch_tiles<T, FACTOR, 4, false>(a, s);
+  if (f == 0) {
+    st = launch_plain<T, FACTOR>(j[0], s);
+  } else if constexpr (FACTOR) {
+    st = launch_factor_tiles(a, f, ragged, s);
+  } else {
+    if (f == 2) st = ragged ? launch_grad_tiles<T, 2, true>(a, s) : launch_grad_tiles<T, 2, false>(a, s);
+    if constexpr (!std::is_same_v<T, float>)
+      if (f == 4) st = ragged ? launch_grad_tiles<T, 4, true>(a, s) : launch_grad_tiles<T, 4, false>(a, s);
+  }
   if (st || !joins) return st;
   KFAC_LAUNCH(FACTOR ? K_FACTOR_Q8_JOIN : K_GRAD_Q8_JOIN, q8_join_kernel<FACTOR>, dim3(static_cast<unsigned>(joins)),
               dim3(256), 0, s, a);
@@ -367,7 +391,7 @@ static kfac_status launch_jobs(TnJob* j, int n, bool ragged, hipStream_t s) {
 static TnJob grad_job(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype, bool bias, bool near) {
   TnJob j = {};
   j.rows = rows, j.m = c_out, j.n = c_in, j.bias = bias;
-  plan(j, false, dtype, near, 1.0, INT32_MAX);
+  plan(j, false, dtype, near, 1.0, 0);
   return j;
 }
 
@@ -381,7 +405,7 @@ extern "C" kfac_status kfac_weight_grad_q8_workspace(int32_t rows, int32_t c_in,
   for (bool near : {false, true}) {
     TnJob j = grad_job(rows, c_in, c_out, dtype, true, near);
     Carver cv;
-    carve(j, cv);
+    carve(j, false, cv);
     *bytes = std::max(*bytes, cv.used);
   }
   return KFAC_OK;
@@ -403,12 +427,12 @@ extern "C" kfac_status kfac_weight_grad_q8(int32_t rows, int32_t c_in, int32_t c
   const bool near = rows <= 1 || (ld_g < (int64_t(1) << 31) && ld_q < (int64_t(1) << 32));
   TnJob j = grad_job(rows, c_in, c_out, dtype, dbias != nullptr, near);
   Carver sizing, cv(workspace);
-  carve(j, sizing);
+  carve(j, false, sizing);
   const RowsOf scr = scratch(workspace, sizing.used);
   if ((st = check_apart({&ws, &bs, &scr, &gs, &qs, &ss}, 3))) return st;
   if ((st = check_device())) return st;
   if ((st = check_workspace(workspace, ws_bytes, sizing.used))) return st;
-  carve(j, cv);
+  carve(j, false, cv);
   j.g = gout, j.q = q, j.scale = scale, j.out = dweight, j.bias_out = dbias;
   j.ldg = ld_g, j.ldq = ld_q, j.ldo = ld_dw, j.inc_b = inc_db, j.accumulate = accumulate;
   if (c_out == 0 || (c_in == 0 && !dbias)) return KFAC_OK;
@@ -417,13 +441,18 @@ extern "C" kfac_status kfac_weight_grad_q8(int32_t rows, int32_t c_in, int32_t c
   });
 }
 
-// Rows that a factor's fp32 sum runs over: behind rectifiers it grows all the way, and the matrix unit's
-// cuts lose up to 1.2e-10 of it a row (6.6e-7 over 5570 rows).
-constexpr int64_t kFactorRows = 6144;
+// A layer whose rows lie far apart is the plain kernel's.
+static TnJob factor_job(int32_t rows, int32_t cols, int32_t bias, double share, int f, bool near, double* us) {
+  TnJob j = {};
+  j.rows = rows, j.m = j.n = cols, j.bias = bias;
+  const double t = plan(j, true, KFAC_F16, near, share, f);
+  if (us) *us = t;
+  return j;
+}
 
-// ld: the layers' pitches, which the workspace query does not know (NULL: none is far).
+// The layers' jobs: near, if their rows lie less than 2^32 bytes apart, and far, if not.
 static kfac_status factor_jobs(int32_t count, const int32_t* rows, const int32_t* cols, const int32_t* bias,
-                               const int64_t* ld, std::vector<TnJob>& jobs) {
+                               std::vector<TnJob>& near, std::vector<TnJob>& far) {
   if (count < 0) return fail(KFAC_ERR_INVALID, "negative count");
   if (count > 0 && (!rows || !cols || !bias)) return fail(KFAC_ERR_INVALID, "NULL array");
   double work = 0;
@@ -435,30 +464,39 @@ static kfac_status factor_jobs(int32_t count, const int32_t* rows, const int32_t
     if (bias[i] != 0 && bias[i] != 1) return fail(KFAC_ERR_INVALID, "layer %d: bias must be 0 or 1", i);
     work += work_of(i);
   }
-  for (int i = 0; i < count; ++i) {
-    TnJob j = {};
-    j.rows = rows[i], j.m = j.n = cols[i], j.bias = bias[i];
-    const bool near = !ld || rows[i] <= 1 || ld[i] < (int64_t(1) << 32);
-    plan(j, true, KFAC_F16, near, work_of(i) / work, kFactorRows);
-    jobs.push_back(j);
+  // one tile edge for all layers, so that they run side by side: the one whose slowest layer is soonest done
+  double best = 0;
+  for (int f : {1, 2, 3}) {
+    std::vector<TnJob> jobs;
+    double slowest = 0;
+    for (int i = 0; i < count; ++i) {
+      double us = 0;
+      jobs.push_back(factor_job(rows[i], cols[i], bias[i], work_of(i) / work, f, true, &us));
+      slowest = std::max(slowest, us);
+    }
+    if (f == 1 || slowest < best) best = slowest, near = std::move(jobs);
   }
+  for (int i = 0; i < count; ++i) far.push_back(factor_job(rows[i], cols[i], bias[i], 1.0, 0, false, nullptr));
   return KFAC_OK;
+}
+
+// A layer's workspace, whichever of its jobs it turns out to have.
+static size_t factor_bytes(TnJob near, TnJob far) {
+  Carver one, other;
+  carve(near, true, one);
+  carve(far, true, other);
+  return std::max(one.used, other.used);
 }
 
 extern "C" kfac_status kfac_factors_q8_workspace(int32_t count, const int32_t* rows, const int32_t* cols,
                                                  const int32_t* bias, size_t* bytes) {
   if (!bytes) return fail(KFAC_ERR_INVALID, "bytes is NULL");
   return guarded([&] {
+    std::vector<TnJob> near, far;
+    kfac_status st = factor_jobs(count, rows, cols, bias, near, far);
+    if (st) return st;
     size_t need = 0;
-    const std::vector<int64_t> far(std::max(count, 0), int64_t(1) << 32);
-    for (const int64_t* ld : {static_cast<const int64_t*>(nullptr), far.data()}) {
-      std::vector<TnJob> jobs;
-      kfac_status st = factor_jobs(count, rows, cols, bias, ld, jobs);
-      if (st) return st;
-      Carver cv;
-      for (TnJob& j : jobs) carve(j, cv);
-      need = std::max(need, cv.used);
-    }
+    for (int i = 0; i < count; ++i) need += factor_bytes(near[i], far[i]);
     *bytes = need;
     return KFAC_OK;
   });
@@ -470,12 +508,17 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
                                 size_t ws_bytes, hipStream_t s) {
   if (!(ema_decay >= 0.f && ema_decay <= 1.f)) return fail(KFAC_ERR_INVALID, "ema_decay must be in [0, 1]");
   if (count > 0 && (!q || !ld_q || !scale || !A_packed)) return fail(KFAC_ERR_INVALID, "NULL array");
-  std::vector<TnJob> jobs;
-  kfac_status st = factor_jobs(count, rows, cols, bias, ld_q, jobs);
+  std::vector<TnJob> jobs, far;
+  kfac_status st = factor_jobs(count, rows, cols, bias, jobs, far);
   if (st) return st;
-  Carver sizing;
-  for (TnJob& j : jobs) carve(j, sizing);
-  std::vector<RowsOf> all = {scratch(workspace, sizing.used)};
+  std::vector<size_t> bytes;
+  size_t need = 0;
+  for (int i = 0; i < count; ++i) {
+    bytes.push_back(factor_bytes(jobs[i], far[i]));
+    need += bytes[i];
+    if (rows[i] > 1 && ld_q[i] >= (int64_t(1) << 32)) jobs[i] = far[i];
+  }
+  std::vector<RowsOf> all = {scratch(workspace, need)};
   for (int i = 0; i < count; ++i) {
     const int64_t d = cols[i] + bias[i];
     all.push_back({A_packed[i], 1, d * (d + 1) / 2, 0, 4, "A_packed"});
@@ -493,21 +536,23 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
   }
   if ((st = check_apart(each.data(), static_cast<int>(each.size()), written))) return st;
   if ((st = check_device())) return st;
-  if ((st = check_workspace(workspace, ws_bytes, sizing.used))) return st;
-  Carver cv(workspace);
+  if ((st = check_workspace(workspace, ws_bytes, need))) return st;
+  char* here = static_cast<char*>(workspace);
   for (int i = 0; i < count; ++i) {
     TnJob& j = jobs[i];
-    carve(j, cv);
+    Carver cv(here);
+    carve(j, true, cv);
+    here += bytes[i];
     j.q = q[i], j.scale = scale[i], j.ldq = ld_q[i], j.out = A_packed[i], j.full = A_full ? A_full[i] : nullptr;
     j.decay = ema_decay;
   }
   // a launch for the layers of one kind
   std::vector<TnJob> some;
-  for (int f : {4, 3, 2, 0})
+  for (int f : {3, 2, 1, 0})
     for (bool ragged : {false, true}) {
       some.clear();
       for (const TnJob& j : jobs)
-        if (j.f == f && (f == 0 ? !ragged : bool(j.m & 7) == ragged)) some.push_back(j);
+        if (j.f == f && (f == 0 ? !ragged : bool(j.m & 15) == ragged)) some.push_back(j);
       const size_t most = f ? kTnMany : 1;
       for (size_t i = 0; i < some.size(); i += most)
         if ((st = launch_jobs<_Float16, true>(&some[i], static_cast<int>(std::min(most, some.size() - i)), ragged, s))) return st;

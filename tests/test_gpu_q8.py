@@ -391,6 +391,38 @@ def test_factors_of_several_layers(kfac_gpu):
         assert (np.abs(host64(b) - want) <= (q.shape[0] + 12) * 2 * U * size).all()
 
 
+def test_factor_of_scales(kfac_gpu):
+    """Rows of every scale there is: each adds up by itself; a scale that is none makes the factor NaN."""
+    rows, cols = 700, 40
+    q = codes(9, rows, cols, most=9)
+    s = torch.exp2((torch.arange(rows) % 200 - 100).float() / 2).floor().clamp(min=2.0 ** -50).cuda()
+    s = torch.exp2(torch.log2(s).floor())
+    want, size = qo.factor_packed(host(q), host(s), True)
+    got = host64(factors(kfac_gpu, [(q, s)], True)[0])
+    assert (np.abs(got - want) <= (150 + 8) * 2 * U * size).all()       # a sum of 2^12 at most 150 scales' sums
+    # the same rows, all far away: powers of two throughout, infinite where a float is
+    for far in (2.0 ** 30, 2.0 ** -30):
+        again = host(factors(kfac_gpu, [(q, s * far)], False)[0])
+        with np.errstate(over="ignore"):
+            assert same(again, (host64(factors(kfac_gpu, [(q, s)], False)[0]) * far * far).astype(np.float32))
+    for bad in (1.5, float("nan"), float("inf"), -1.0, 2.0 ** -130):
+        t = s.clone()
+        t[5] = bad
+        assert np.isnan(host(factors(kfac_gpu, [(q, t)], False)[0])).all()
+
+
+@pytest.mark.parametrize("rows, cols", [(6000, 200), (20000, 70), (900, 1040), (8192, 17)])
+def test_factor_of_full_sums(kfac_gpu, rows, cols):
+    """Codes of one size and columns of one sign: sums as large as they get, of scales that do not fit into 32 bits."""
+    sign = torch.where(torch.arange(cols) % 3 == 0, -127, 127).to(torch.int8).cuda()
+    q = sign.expand(rows, cols).contiguous()
+    s = torch.exp2(-(torch.arange(rows) % 9).float()).cuda()
+    want, size = qo.factor_packed(host(q), host(s), True)
+    got = host64(factors(kfac_gpu, [(q, s)], True)[0])
+    # at most 9 scales' exact sums a block, 5 blocks, the mean and the blending: each rounds once or twice
+    assert (np.abs(got - want) <= (9 + 5 + 8) * 2 * U * size).all()
+
+
 @pytest.mark.parametrize("bias", [True, False])
 def test_factor_without_rows(kfac_gpu, bias):
     q, s = codes(1, 70, 50), torch.zeros(70, device="cuda")
