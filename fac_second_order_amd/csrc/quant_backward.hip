@@ -220,8 +220,11 @@ __global__ void __launch_bounds__(256) q8_join_kernel(TnArgs<FACTOR> args) {
   const TnJob& d = args.j[FACTOR ? args.owner(blockIdx.x, &TnJob::join_begin) : 0];
   const int T = tile_edge(d), item = blockIdx.x - d.join_begin, here = static_cast<int>(join_tiles(d));
   int counted = 0;
-  if (FACTOR)
-    for (int s = 0; s < d.splits; ++s) counted += gp(d.part_rows)[s];
+  if (FACTOR) {
+    for (int s = tid & 63; s < d.splits; s += 64) counted += gp(d.part_rows)[s];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) counted += __shfl_xor(counted, o);
+  }
   const float inv_r = counted ? 1.f / static_cast<float>(counted) : 0.f;
   const PutFactor put = put_factor(d, counted);
   if (item < here) {
@@ -235,12 +238,12 @@ __global__ void __launch_bounds__(256) q8_join_kernel(TnArgs<FACTOR> args) {
     const int64_t apart = int64_t(d.tiles) * (T * T);
     v4f sum = {0.f, 0.f, 0.f, 0.f};
     int s = 0;
-    for (; s + 4 <= d.splits; s += 4) {
-      v4f v[4];
+    for (; s + 8 <= d.splits; s += 8) {
+      v4f v[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const KG v4f*>(from + (s + k) * apart);
+      for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const KG v4f*>(from + (s + k) * apart);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum += v[k];
+      for (int k = 0; k < 8; ++k) sum += v[k];
     }
     for (; s < d.splits; ++s) sum += *reinterpret_cast<const KG v4f*>(from + s * apart);
     if constexpr (FACTOR) {
@@ -262,8 +265,8 @@ __global__ void __launch_bounds__(256) q8_join_kernel(TnArgs<FACTOR> args) {
   const int all = d.splits * d.shares;
   float sum = 0.f;
   if (c < d.m)
-    for (int k = tid >> 6; k < all; k += 4)
-      sum += gp(d.part_col)[int64_t(k) * (int64_t(d.mt) * T) + c];
+#pragma unroll 8
+    for (int k = tid >> 6; k < all; k += 4) sum += gp(d.part_col)[int64_t(k) * (int64_t(d.mt) * T) + c];
   part[tid >> 6][tid & 63] = sum;
   __syncthreads();
   if (tid >= 64 || c >= d.m) return;
