@@ -314,16 +314,16 @@ static double plan(TnJob& j, bool factor, kfac_dtype dtype, bool near, double sh
       set_tiles(j, f, factor);
       const double entries = double(j.tiles) * tile_edge(j) * tile_edge(j);
       const double slots = std::max(1.0, kCus * share * (f == 1 ? 3 : f == 2 ? 2 : 1));
-      const double step = factor ? (f == 1 ? 0.6 : 0.55) : f == 4 ? 0.95 : dtype == KFAC_F32 ? 1.2 : 0.55;
+      const double step = factor ? (f == 1 ? 0.6 : 0.55) : f == 4 ? 0.95 : dtype == KFAC_F32 ? 2.0 : 0.6;
       const int64_t fewest = factor ? (rows + factor_rows(f) - 1) / factor_rows(f) : 1;
-      for (int64_t s = fewest; s <= std::max<int64_t>(fewest, 128) && (s == fewest || steps / s >= 4); s += 1 + s / 8) {
+      for (int64_t s = fewest; s <= std::max<int64_t>(fewest, 128) && (s == fewest || steps / s >= 4); s += factor ? 1 + s / 8 : 1) {
         const double rounds = std::ceil(double(j.tiles) * s / slots), each = std::ceil(double(steps) / s);
         double us;
         if (factor) {
           us = rounds * (6 + 4 * f + (each + 4) * step);
           us += s > 1 ? 6 + 0.15 * s + entries * (10 + 2 * s) / (6e6 * share) : 2 * f * f;
         } else {
-          us = rounds * (8 + each * step) + (s > 1 ? 5 + s * entries * 8 / (4.5e6 * share) : 0);
+          us = rounds * (8 + each * step) + (s > 1 ? 4 + entries * (1 + s) / 1e6 : 0);
         }
         if (best == 0 || us < best) best = us, best_f = f, best_splits = s;
       }
