@@ -171,6 +171,12 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     column(ti * T + c, a_col[i], a_cut[i]);
     column(tj * T + c, b_col[i], b_cut[i]);
   }
+  bool cuts = false;  // of the wave: only the last tiles of ragged operands have any
+  if constexpr (RAGGED) {
+#pragma unroll
+    for (int i = 0; i < G; ++i) cuts |= (a_cut[i] | b_cut[i]) != 0;
+    cuts = __any(cuts);
+  }
   Raw16 araw[kFactorAhead][G], braw[kFactorAhead][G];
 
   const int wm = (wave >> 1) * 32 * F, wn = (wave & 1) * 32 * F;
@@ -279,7 +285,7 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     auto place = [&](auto set, auto buf, int k) {
       const int i = k / 2;
       Raw16& x = k & 1 ? araw[set][i] : braw[set][i];
-      if constexpr (RAGGED) x.shift(k & 1 ? a_cut[i] : b_cut[i]);
+      if (RAGGED && cuts) x.shift(k & 1 ? a_cut[i] : b_cut[i]);
       *reinterpret_cast<v4u*>((k & 1 ? abuf : bbuf) + buf * L::OPERAND + at[i]) = x.w & some[set][i];
     };
     v4i fa[2][F], fb[2][F];

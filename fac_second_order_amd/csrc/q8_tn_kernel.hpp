@@ -40,7 +40,21 @@ __device__ inline void cut3(float x, short (&h)[3]) {
     const unsigned b = __float_as_uint(r) & 0xffff0000u;
     h[p] = static_cast<short>(b >> 16);
     const float top = __uint_as_float(b);
-    r = r == top ? 0.f : r - top;
+    r = p == 0 && r == top ? 0.f : r - top;  // what is left of the first cut is finite, or NaN
+  }
+}
+// The same of two numbers, each part's two 16 bits in one register.
+__device__ inline void cut3(float x, float y, unsigned (&h)[3]) {
+  float r[2] = {x, y};
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const unsigned b[2] = {__float_as_uint(r[0]), __float_as_uint(r[1])};
+    h[p] = __builtin_amdgcn_perm(b[1], b[0], 0x07060302u);  // the upper halves
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float top = __uint_as_float(b[k] & 0xffff0000u);
+      r[k] = p == 0 && r[k] == top ? 0.f : r[k] - top;
+    }
   }
 }
 
@@ -267,6 +281,12 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) grad_tile_kernel(TnArgs<f
     column(k0 + c, d.n, b_col[i], b_cut[i]);
     a_col[i] *= sizeof(E);
   }
+  bool cuts = false;  // of the wave: only the last tiles of ragged operands have any
+  if constexpr (RAGGED) {
+#pragma unroll
+    for (int i = 0; i < F; ++i) cuts |= (a_cut[i] | b_cut[i]) != 0;
+    cuts = __any(cuts);
+  }
   Raw8<E> araw[kAhead][F];
   Raw8<int8_t> braw[kAhead][F];
 
@@ -330,13 +350,13 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) grad_tile_kernel(TnArgs<f
       const int i = k / 8, h = k % 4;
       if (k % 8 < 4) {
         if constexpr (RAGGED)
-          if (h == 0) braw[set][i].shift(b_cut[i]);
+          if (h == 0 && cuts) braw[set][i].shift(b_cut[i]);
         made[h] = two_codes<HALF>(braw[set][i].w[h >> 1], h & 1, s[i]);
         if (h == 3) *reinterpret_cast<v4u*>(bbuf + buf * L::OPERAND + at[i]) = made;
         return;
       }
       if constexpr (RAGGED)
-        if (h == 0) araw[set][i].shift(a_cut[i]);
+        if (h == 0 && cuts) araw[set][i].shift(a_cut[i]);
       char* const to = abuf + buf * P * L::OPERAND + at[i];
       if constexpr (P == 1) {
         if (h == 0) {
@@ -345,14 +365,13 @@ __global__ void __launch_bounds__(256, F == 2 ? 2 : 1) grad_tile_kernel(TnArgs<f
           *reinterpret_cast<v4u*>(to) = x;
         }
       } else {
-        short lo[3], hi[3];
+        unsigned two[3];
         float x0 = araw[set][i].x[2 * h], x1 = araw[set][i].x[2 * h + 1];
         if (!whole && s[i] == 0.f) x0 = x1 = 0.f;
-        cut3(x0, lo);
-        cut3(x1, hi);
+        cut3(x0, x1, two);
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-          parts[p][h] = unsigned(static_cast<unsigned short>(lo[p])) | unsigned(static_cast<unsigned short>(hi[p])) << 16;
+          parts[p][h] = two[p];
           if (h == 3) *reinterpret_cast<v4u*>(to + p * L::OPERAND) = parts[p];
         }
       }
