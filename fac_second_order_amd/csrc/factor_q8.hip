@@ -128,17 +128,6 @@ struct Raw16 {
   }
 };
 
-// What all lanes share, in scalar registers.
-__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ inline float uniform(float x) { return __uint_as_float(uniform(static_cast<int>(__float_as_uint(x)))); }
-template <typename P>
-__device__ inline KG P* uniform(KG P* p) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  const uint64_t lo = static_cast<unsigned>(uniform(static_cast<int>(a)));
-  const uint64_t hi = static_cast<unsigned>(uniform(static_cast<int>(a >> 32)));
-  return reinterpret_cast<KG P*>(hi << 32 | lo);
-}
-
 template <int F, bool RAGGED>
 __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<true> args) {
   using L = FactorTile<F>;
