@@ -15,10 +15,10 @@
 // of T bytes. The transposing loads give a lane 8 rows of a column; the groups of 16 bytes of a
 // line are moved so that the 8 rows that 32 lanes meet lie in different banks.
 //
-// 8192 x 4096: 97 us with tiles of 192 (253 tiles, a block each; 1.4e15 operations a second), 113 + 23 with 128,
-// 170 with 64; in 16 bits with the scales multiplied in it took 155 + 22. What bounds it are the waits of the
-// one wave a SIMD at a step's barrier: the matrix unit is busy for half of the time, LDS for a
-// quarter, and fetching four steps ahead (119) brings nothing. Tiles of 256 spill when the sums change their
+// 8192 x 4096, 5564 rows of which count: 97 us with tiles of 192 (253 tiles, a block each; 0.96e15 operations a second),
+// 113 + 23 with 128, 170 with 64; in 16 bits with the scales multiplied in it took 155 + 22. What bounds it are the
+// waits of the one wave a SIMD: the matrix unit is busy for a quarter of the time, LDS for
+// another, and fetching four steps ahead (119) brings nothing. Tiles of 256 spill when the sums change their
 // scale. Small factors take tiles of 64 (32 x 2048: 14 us, 19 and 30 with larger ones), sets of layers
 // one edge for all.
 #include "q8_tn_kernel.hpp"

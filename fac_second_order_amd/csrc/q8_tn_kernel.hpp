@@ -157,12 +157,17 @@ __device__ inline float scale_unit(const float* scale, int64_t r0, int n, float*
 }
 
 
-// Tiles of T x T, T = 64 F, four waves of 32 F x 32 F, steps of 32 rows, which go from memory into registers four
+// Tiles of T x T, T = 64 F, four waves of 32 F x 32 F, steps of 32 rows, which go from memory into registers AHEAD
 // steps ahead and from there into LDS one step ahead, the codes with their scales and fp32 gradients cut
 // into their parts. An operand lies in LDS a row a line of T 16-bit numbers, its groups of 8 moved by 4 in
 // turn, so that the 4 rows that 16 lanes of a transposing load meet lie in different banks. (Gradients
 // sent from memory into LDS directly were slower: the compiler has every transposing load wait for
 // all that is on its way there.)
+//
+// 8192 x 4096 x 4096 bf16, 5570 rows of which count: 179 us, 1.04e15 operations a second, with tiles of 256 (128: 282); the
+// library's product of 16-bit operands that lie so runs at 1.16e15. What is left is a block's start and end, 25 us,
+// and the steps' one barrier. 4099 x 1001 x 777 fp32, three products: 39 us, bound by the cutting (250 vector
+// instructions a thread and step).
 //
 // A thread holds F groups of 8 columns of each operand a step. RAGGED: the last group of a row that has
 // no 8 columns left is read from 8 columns before the row's end, and shifted. Groups past the end are the
