@@ -423,6 +423,24 @@ def test_factor_of_full_sums(kfac_gpu, rows, cols):
     assert (np.abs(got - want) <= (9 + 5 + 8) * 2 * U * size).all()
 
 
+def test_rows_far_apart(kfac_gpu):
+    """Rows 2^32 bytes apart, beside a layer of ordinary ones in one call: whole numbers, so that nothing is rounded."""
+    close = codes(3, 3, 40, most=9)
+    wide = torch.empty(2 ** 33 + 64, dtype=torch.int8, device="cuda")
+    far = wide.as_strided((3, 40), (2 ** 32, 1))
+    far.copy_(close)
+    s = torch.tensor([1.0, 0.0, 2.0], device="cuda")
+    q, t = codes(4, 5000, 64, most=9), torch.ones(5000, device="cuda")
+    alone = [host(factors(kfac_gpu, [layer], True)[0]) for layer in ((close, s), (q, t), (close, s))]
+    together = factors(kfac_gpu, [(far, s), (q, t), (close, s)], True)
+    for a, b in zip(alone, together):
+        assert same(a, host(b))
+    assert same(alone[0], qo.factor_packed(host(close), host(s), True)[0])
+    g = codes(5, 3, 30, most=9).half()
+    for a, b in zip(grad(kfac_gpu, g, close, s, True, False), grad(kfac_gpu, g, far, s, True, False)):
+        assert same(a, b)
+
+
 @pytest.mark.parametrize("bias", [True, False])
 def test_factor_without_rows(kfac_gpu, bias):
     q, s = codes(1, 70, 50), torch.zeros(70, device="cuda")
