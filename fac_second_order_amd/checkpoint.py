@@ -15,8 +15,8 @@ from . import _lib as K
 
 
 class Checkpoint:
-    """Rows q [rows, cols] (int8) with a scale [rows] (float32) each; a scale of 0 marks a row
-    that takes no part (kfac.h)."""
+    """Rows q [rows, cols] (int8) with a scale [rows] (float32) each, a power of two (with others a
+    factor formed from it is NaN); a scale of 0 marks a row that takes no part (kfac.h)."""
 
     def __init__(self, q, scale):
         if q.dim() != 2 or q.dtype != torch.int8 or scale.dtype != torch.float32 or scale.shape != q.shape[:1]:
