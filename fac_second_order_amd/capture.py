@@ -139,6 +139,17 @@ def _nhwc_half(x):
     return x.detach().permute(0, 2, 3, 1).to(torch.float16).contiguous()
 
 
+class _Taken:
+    """The forward of a fully connected layer while a capture has it: `run`, which keeps the layer's
+    input, or is what the layer itself was given for a forward."""
+
+    def __init__(self, run):
+        self.run = run
+
+    def __call__(self, *args, **kwargs):
+        return self.run(*args, **kwargs)
+
+
 class KfacCapture:
     """K-FAC for a model whose `kfac_modules()` lists (Conv2d or Linear, BatchNorm2d
     or None) pairs. Call `step(lr)` after `loss.backward()`: it forms the factors
@@ -164,7 +175,8 @@ class KfacCapture:
     1/127 of its largest entry), their outputs and the gradients at their inputs are what they were.
     matmul="int8", with it: their products are formed in 8-bit integers too (kfac_linear_q8), with
     a scale for each row and each output, also in passes without gradients; the gradients at their inputs
-    take the weights as they are."""
+    take the weights as they are. Both are of layers whose product is nn.Linear's: one with a forward of its
+    own, its class's or set on it, runs that, and its input is kept as without them."""
 
     def __init__(self, model, damping=1e-3, ema_decay=0.95, refresh_every=1, precond_accum="f32",
                  refine_inverse=False, max_grad_norm=None, trust_radius=None, checkpoint=None, matmul=None):
@@ -200,9 +212,10 @@ class KfacCapture:
         self.made, self.int8 = {}, matmul == "int8"
         self.wrapped = []
         for i, (m, _) in enumerate(self.pairs):
-            if checkpoint and isinstance(m, nn.Linear):
-                self.wrapped.append((m, m.__dict__.get("forward")))
-                m.forward = self._checkpointed(i, m)
+            if checkpoint and isinstance(m, nn.Linear) and type(m).forward is nn.Linear.forward:
+                before = m.__dict__.get("forward")
+                self.wrapped.append((m, before))
+                m.forward = _Taken(self._checkpointed(i, m) if before is None else before)
             self.hooks.append(m.register_forward_hook(self._fwd(i)))
             self.hooks.append(m.register_full_backward_hook(self._bwd(i)))
         for i, bn in enumerate(self.bns):

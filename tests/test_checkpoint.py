@@ -118,3 +118,31 @@ def test_step_refuses_other_checkpoints(monkeypatch, act, lay):
     with pytest.raises(ValueError):
         st.step([act], [torch.zeros(5, 4)], [torch.zeros(4, 4)])
     assert not calls.q8 and not calls.plain
+
+
+class Tenfold(torch.nn.Linear):
+    def forward(self, input):
+        return 10 * super().forward(input)
+
+
+def test_layers_with_a_forward_of_their_own():
+    """A class's forward, and one set on a layer, are what runs; their inputs are kept as without the option."""
+    net = Net()
+    net.a = Tenfold(5, 6)
+    plain = net.b.forward
+    net.b.forward = lambda x: plain(x) - 3
+    x = torch.randn(2, 5)
+    want = net(x).detach()
+    cap = cap_mod.KfacCapture(net, checkpoint="int8", matmul="int8")
+    with torch.no_grad():
+        assert torch.equal(net(x), want)
+    seen = []
+    handle = net.b.register_forward_pre_hook(lambda m, inp: seen.append(inp[0].detach()))
+    out = net(x)
+    assert torch.equal(out, want) and not cap.made
+    assert torch.equal(cap.act[0], x.half()) and torch.equal(cap.act[1], seen[0].half())
+    out.sum().backward()
+    assert torch.equal(net.a.weight.grad, torch.autograd.grad(net(x).sum(), net.a.weight)[0])
+    handle.remove()
+    cap.remove()
+    assert "forward" not in net.a.__dict__ and torch.equal(net(x), want)
