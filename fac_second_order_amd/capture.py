@@ -24,7 +24,9 @@ Layout conventions (the library's):
     log p(y), y drawn from the model at every row that counts (eq. 3, the Fisher), with
     coefficient 1; rows that do not count are in neither factor.
 """
+import copy
 import math
+import types
 from dataclasses import dataclass
 
 import torch
@@ -141,13 +143,20 @@ def _nhwc_half(x):
 
 class _Taken:
     """The forward of a fully connected layer while a capture has it: `run`, which keeps the layer's
-    input, or is what the layer itself was given for a forward."""
+    input, or is `before`, what the layer itself was given for a forward (None: nothing). A copy of the layer has what
+    the layer had before: the capture is not the copy's."""
 
-    def __init__(self, run):
-        self.run = run
+    def __init__(self, layer, before, run):
+        self.layer, self.before, self.run = layer, before, run
 
     def __call__(self, *args, **kwargs):
         return self.run(*args, **kwargs)
+
+    def __deepcopy__(self, memo):
+        if self.before is not None:
+            return copy.deepcopy(self.before, memo)
+        layer = copy.deepcopy(self.layer, memo)  # that of the copy, where it is the layer that is being copied
+        return types.MethodType(type(layer).forward, layer)
 
 
 class KfacCapture:
@@ -215,7 +224,7 @@ class KfacCapture:
             if checkpoint and isinstance(m, nn.Linear) and type(m).forward is nn.Linear.forward:
                 before = m.__dict__.get("forward")
                 self.wrapped.append((m, before))
-                m.forward = _Taken(self._checkpointed(i, m) if before is None else before)
+                m.forward = _Taken(m, before, self._checkpointed(i, m) if before is None else before)
             self.hooks.append(m.register_forward_hook(self._fwd(i)))
             self.hooks.append(m.register_full_backward_hook(self._bwd(i)))
         for i, bn in enumerate(self.bns):
@@ -242,10 +251,10 @@ class KfacCapture:
             return ck.linear(x, m.weight, m.bias, True)[0] if self.int8 else nn.functional.linear(x, m.weight, m.bias)
         return forward
 
-    # hooks ------------------------------------------------------------------
+    # hooks: a copy of the model has them too, and its passes are not the capture's -------
     def _fwd(self, i):
         def hook(mod, inp, out):
-            if torch.is_grad_enabled():
+            if mod is self.pairs[i][0] and torch.is_grad_enabled():
                 self.n = inp[0].shape[0]
                 made = self.made.pop(i, None)
                 self.act[i] = _nhwc_half(inp[0]) if made is None else made
@@ -253,6 +262,8 @@ class KfacCapture:
 
     def _bwd(self, i):
         def hook(mod, grad_in, grad_out):
+            if mod is not self.pairs[i][0]:
+                return
             g = grad_out[0]
             if self.score_scale is None:
                 self.gout[i] = _nhwc_half(g * (self.n / self.loss_scale))
@@ -266,7 +277,7 @@ class KfacCapture:
 
     def _bn_fwd(self, i):
         def hook(mod, inp, out):
-            if torch.is_grad_enabled():
+            if mod is self.bns[i] and torch.is_grad_enabled():
                 x = inp[0].detach().float()
                 var, mean = torch.var_mean(x, dim=(0, 2, 3), unbiased=False, keepdim=True)
                 xh = (x - mean) * torch.rsqrt(var + mod.eps)
@@ -276,6 +287,8 @@ class KfacCapture:
 
     def _bn_bwd(self, i):
         def hook(mod, grad_in, grad_out):
+            if mod is not self.bns[i]:
+                return
             if self.score_scale is None:
                 to, g = self.bgout, grad_out[0] * (self.n / self.loss_scale)
                 if not self.own_loss:

@@ -146,3 +146,39 @@ def test_layers_with_a_forward_of_their_own():
     handle.remove()
     cap.remove()
     assert "forward" not in net.a.__dict__ and torch.equal(net(x), want)
+
+
+@pytest.mark.parametrize("kw", [{}, {"checkpoint": "int8"}, {"checkpoint": "int8", "matmul": "int8"}])
+def test_copies_of_a_model(kw):
+    """A copy computes with its own weights, in 16 bits or more, and nothing of its passes is captured."""
+    import copy
+    net = Net()
+    fourfold = lambda x: torch.nn.functional.linear(x, net.b.weight) * 4  # noqa: E731
+    net.b.forward = fourfold
+    cap = cap_mod.KfacCapture(net, **kw)
+    for twin in (copy.deepcopy(net), copy.deepcopy(copy.deepcopy(net))):
+        assert twin.b.forward is fourfold
+        with torch.no_grad():
+            for p in twin.a.parameters():
+                p.zero_()
+            assert not twin.a(torch.ones(2, 5)).any()
+        x = torch.ones(3, 5)
+        twin.a(x).sum().backward()
+        assert torch.equal(twin.a.weight.grad, torch.full((6, 5), 3.0)) and net.a.weight.grad is None
+        assert cap.n == 0 and not cap.made and cap.act == cap.gout == [None, None]
+    alone = copy.deepcopy(net.a)
+    with torch.no_grad():
+        alone.bias.fill_(2)
+        alone.weight.zero_()
+        assert (alone(torch.ones(1, 5)) == 2).all()
+    cap.remove()
+    assert "forward" not in net.a.__dict__ and net.b.forward is fourfold
+
+
+def test_copies_of_normalised_models(monkeypatch):
+    import copy
+    from test_capture import ConvNet
+    net = ConvNet()
+    cap = cap_mod.KfacCapture(net)
+    copy.deepcopy(net)(torch.randn(2, 3, 4, 4)).sum().backward()
+    assert cap.xhat == cap.bgout == [None] and cap.act == cap.gout == [None, None]
