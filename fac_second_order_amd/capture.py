@@ -244,11 +244,11 @@ class KfacCapture:
 
     # layers that keep their input in 8 bits ------------------------------------
     def _checkpointed(self, i, m):
-        def forward(x):
+        def forward(input):
             if torch.is_grad_enabled():
-                y, self.made[i] = ck.linear(x, m.weight, m.bias, self.int8)
+                y, self.made[i] = ck.linear(input, m.weight, m.bias, self.int8)
                 return y
-            return ck.linear(x, m.weight, m.bias, True)[0] if self.int8 else nn.functional.linear(x, m.weight, m.bias)
+            return ck.linear(input, m.weight, m.bias, True)[0] if self.int8 else nn.functional.linear(input, m.weight, m.bias)
         return forward
 
     # hooks: a copy of the model has them too, and its passes are not the capture's -------

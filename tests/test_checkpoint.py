@@ -182,3 +182,12 @@ def test_copies_of_normalised_models(monkeypatch):
     cap = cap_mod.KfacCapture(net)
     copy.deepcopy(net)(torch.randn(2, 3, 4, 4)).sum().backward()
     assert cap.xhat == cap.bgout == [None] and cap.act == cap.gout == [None, None]
+
+
+def test_input_by_name():
+    net = Net()
+    cap = cap_mod.KfacCapture(net, checkpoint="int8")
+    x = torch.randn(2, 5)
+    with torch.no_grad():
+        assert torch.equal(net.a(input=x), torch.nn.functional.linear(x, net.a.weight, net.a.bias))
+    cap.remove()
