@@ -427,7 +427,8 @@ extern "C" kfac_status kfac_weight_grad_q8(int32_t rows, int32_t c_in, int32_t c
                bs = {dbias, dbias ? c_out : 0, 1, inc_db, 4, "dbias"};
   for (const RowsOf* r : {&gs, &qs, &ss, &ws, &bs})
     if ((st = check_rows(*r))) return st;
-  const bool near = rows <= 1 || (ld_g < (int64_t(1) << 31) && ld_q < (int64_t(1) << 32));
+  constexpr int64_t kFar = int64_t(1) << 32;  // bytes between rows, which the tile kernel holds in 32 bits
+  const bool near = rows <= 1 || (ld_g < kFar / gs.size && ld_q < kFar);
   TnJob j = grad_job(rows, c_in, c_out, dtype, dbias != nullptr, near);
   Carver sizing, cv(workspace);
   carve(j, false, sizing);

@@ -473,3 +473,18 @@ def test_nothing_to_do(kfac_gpu):
     assert (dw == 9).all()
     kfac_gpu.kfac_weight_grad_q8(torch.zeros(0, 4, device="cuda"), e8, e32, dw)
     assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("dtype, apart", [(F32, 2 ** 30), (F32, 2 ** 30 + 8), (F16, 2 ** 31), (BF16, 2 ** 31 - 8)])
+def test_gradient_rows_far_apart(kfac_gpu, dtype, apart):
+    """Rows of gradients up to 2^32 bytes and more apart, beside the same rows close to each other: whole numbers."""
+    close = codes(6, 3, 30, most=9).to(dtype)
+    wide = torch.empty(2 * apart + 64, dtype=dtype, device="cuda")
+    far = wide.as_strided((3, 30), (apart, 1))
+    far.copy_(close)
+    q, s = codes(7, 3, 40, most=9), torch.tensor([1.0, 0.0, 2.0], device="cuda")
+    want = grad(kfac_gpu, close, q, s, True, False)
+    dw, db, _, _ = qo.weight_grad(host64(close), host(q), host(s))
+    assert same(want[0], dw) and same(want[1], db)
+    for a, b in zip(want, grad(kfac_gpu, far, q, s, True, False)):
+        assert same(a, b)
