@@ -11,17 +11,15 @@ constexpr int kParts = std::is_same_v<T, float> ? 3 : 1;
 // Codes 2 h and 2 h + 1 of four, times s, as two 16-bit numbers.
 template <bool HALF>
 __device__ inline unsigned two_codes(unsigned four, int h, float s) {
-  const unsigned w = four ^ 0x80808080u;  // code + 128
   if constexpr (HALF) {
-    // 0x64 in front of a byte b is the fp16 number 1024 + b
+    // code + 128 = b, and 0x64 in front of b is the fp16 number 1024 + b
     const v2h mid = {static_cast<_Float16>(1152.f), static_cast<_Float16>(1152.f)};
     const _Float16 sh = static_cast<_Float16>(s);
-    const unsigned b = __builtin_amdgcn_perm(0x64646464u, w, h ? 0x04030402u : 0x04010400u);
+    const unsigned b = __builtin_amdgcn_perm(0x64646464u, four ^ 0x80808080u, h ? 0x04030402u : 0x04010400u);
     return __builtin_bit_cast(unsigned, (__builtin_bit_cast(v2h, b) - mid) * v2h{sh, sh});
-  } else {
-    const float mid = -128.f * s;
-    const v2bf out = {static_cast<__bf16>(fmaf(static_cast<float>((w >> (16 * h)) & 255u), s, mid)),
-                      static_cast<__bf16>(fmaf(static_cast<float>((w >> (16 * h + 8)) & 255u), s, mid))};
+  } else {  // the code itself times s: its own byte's conversion and a product, finite wherever s q is
+    auto code = [&](int k) { return static_cast<float>(static_cast<int8_t>(four >> (8 * k))); };
+    const v2bf out = {static_cast<__bf16>(code(2 * h) * s), static_cast<__bf16>(code(2 * h + 1) * s)};
     return __builtin_bit_cast(unsigned, out);
   }
 }

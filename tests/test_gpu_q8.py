@@ -488,3 +488,21 @@ def test_gradient_rows_far_apart(kfac_gpu, dtype, apart):
     assert same(want[0], dw) and same(want[1], db)
     for a, b in zip(want, grad(kfac_gpu, far, q, s, True, False)):
         assert same(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("cols", [40, 5])     # in tiles, and too few columns for one
+def test_weight_grad_of_the_largest_rows(kfac_gpu, dtype, cols):
+    """Rows up to the largest finite number: s q is finite, and so is what a small gradient makes of it."""
+    top = float(torch.finfo(F32).max)
+    x = torch.zeros(40, cols, device="cuda")
+    x[:] = torch.linspace(-1, 1, cols, device="cuda") * top
+    x[1::2] *= 0.6
+    x[5], x[6, 0] = 0.0, top
+    q, s = quantize(kfac_gpu, x)
+    assert {2.0 ** 121, 2.0 ** 122} < set(s.tolist())
+    g = torch.zeros(40, 40, dtype=dtype, device="cuda")
+    g.fill_diagonal_(2.0 ** -9)
+    s[5] = 2.0 ** 118       # its codes are 0
+    got, gb = grad(kfac_gpu, g, q, s, True, False)
+    assert same(got, qo.row_values(host(q), host64(s)) * 2.0 ** -9) and (gb == 2.0 ** -9).all()
