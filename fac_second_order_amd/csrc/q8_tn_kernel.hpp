@@ -120,7 +120,8 @@ __device__ inline int list_rows(const float* scale, int64_t r0, int n, float uni
     const int at = before[i] + __popcll(b[i] & ((1ull << lane) - 1));
     if (s[i] != 0.f) {
       l.idx[at] = static_cast<uint16_t>((wave + i * (NT / 64)) * 64 + lane);
-      l.s[at] = s[i] * unit;
+      const float scaled = s[i] * unit;
+      l.s[at] = scaled == 0.f ? 1.17549435e-38f : scaled;  // 0 stands for no row: one far below the unit is none of those
     }
   }
   const int whole = (total + 63) / 64 * 64;

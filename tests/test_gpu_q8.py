@@ -506,3 +506,16 @@ def test_weight_grad_of_the_largest_rows(kfac_gpu, dtype, cols):
     s[5] = 2.0 ** 118       # its codes are 0
     got, gb = grad(kfac_gpu, g, q, s, True, False)
     assert same(got, qo.row_values(host(q), host64(s)) * 2.0 ** -9) and (gb == 2.0 ** -9).all()
+
+
+@pytest.mark.parametrize("rows", [2, 40, 1500])
+@pytest.mark.parametrize("cols", [40, 5])
+def test_bias_gradient_of_far_scales(kfac_gpu, rows, cols):
+    """A row that fp16 cannot hold beside the largest scale has its share of the bias gradient all the same."""
+    q = codes(8, rows, cols, most=9)
+    s = torch.full((rows,), 2.0 ** -100, device="cuda")
+    s[0] = 2.0 ** 100
+    for dtype in TYPES:
+        g = grads_of(9, rows, 40, dtype, whole=True)
+        _, gb = grad(kfac_gpu, g, q, s, True, False)
+        assert same(gb, host64(g).sum(0))
