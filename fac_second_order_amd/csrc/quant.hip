@@ -56,9 +56,10 @@ __device__ inline unsigned code_of(float x, const RowCode& c) {
     // x - t s is exact (below a step, and a multiple of the smaller of both last places): put
     // right what the rounded reciprocal decided next to a half, ties to the even side
     float t = m - kMagic;
-    const float d = fmaf(-t, c.s, x), h = 0.5f * c.s;
-    const float a = fabsf(d);
-    if (a > h || (a == h && (static_cast<int>(t) & 1))) t += copysignf(1.f, d);
+    // (against twice it: half the smallest scales is no float)
+    const float d = fmaf(-t, c.s, x);
+    const float twice = 2.f * fabsf(d);
+    if (twice > c.s || (twice == c.s && (static_cast<int>(t) & 1))) t += copysignf(1.f, d);
     return static_cast<unsigned>(static_cast<int>(__builtin_amdgcn_fmed3f(t, -127.f, 127.f)));
   }
 }

@@ -519,3 +519,18 @@ def test_bias_gradient_of_far_scales(kfac_gpu, rows, cols):
         g = grads_of(9, rows, 40, dtype, whole=True)
         _, gb = grad(kfac_gpu, g, q, s, True, False)
         assert same(gb, host64(g).sum(0))
+
+
+def test_quantize_halves_of_the_smallest_scales(kfac_gpu):
+    """Scales next to 2^-126, whose halves are no floats: quotients half a last place beside every half step."""
+    S = 2 ** 23 + 1 + 2 * np.arange(400, dtype=np.int64)           # scales in units of 2^-149
+    x = np.zeros((len(S), 1 + 2 * 127), dtype=np.float64)
+    x[:, 0] = 127 * S
+    for k in range(127):
+        x[:, 1 + 2 * k] = ((2 * k + 1) * S) // 2                   # (k + 1/2) S is half a whole number
+        x[:, 2 + 2 * k] = -((2 * k + 1) * S + 1) // 2
+    x = (x * 2.0 ** -149).astype(np.float32)
+    q, s = quantize(kfac_gpu, torch.from_numpy(x).cuda(), None, False)
+    want, scale = qo.quantize_rows(x, None, False)
+    assert same(host(s), scale) and len(set(scale)) > 200
+    assert same(host(q), want)
