@@ -140,8 +140,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int rows, int cols, 
   if (row >= rows) return;
   const KG T* xr = gp(x) + row * ld;
   KG int8_t* qr = gp(q) + row * ldq;
+  const unsigned end = cols;  // unsigned: a column past the last may lie past the largest int
   if (mask && !gp(mask)[row]) {
-    for (int c = 8 * t; c < cols; c += 8 * TPR) Eight<T>::put(qr + c, cols - c, v2u{0, 0});
+    for (unsigned c = 8 * t; c < end; c += 8 * TPR) Eight<T>::put(qr + c, end - c, v2u{0, 0});
     if (t == 0) gp(scale)[row] = 0.f;
     return;
   }
@@ -153,8 +154,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int rows, int cols, 
 #pragma unroll
     for (int u = 0; u < U; ++u) top = v[u].top(top);
   } else {
-    for (int c = 8 * t; c < cols; c += 8 * TPR) {
-      v[0].load(xr + c, cols - c);
+    for (unsigned c = 8 * t; c < end; c += 8 * TPR) {
+      v[0].load(xr + c, end - c);
       top = v[0].top(top);
     }
   }
@@ -171,9 +172,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int rows, int cols, 
 #pragma unroll
     for (int u = 0; u < U; ++u) Eight<T>::put(qr + 8 * (t + u * TPR), cols - 8 * (t + u * TPR), v[u].template coded<POW2>(code));
   } else {
-    for (int c = 8 * t; c < cols; c += 8 * TPR) {
-      v[0].load(xr + c, cols - c);
-      Eight<T>::put(qr + c, cols - c, v[0].template coded<POW2>(code));
+    for (unsigned c = 8 * t; c < end; c += 8 * TPR) {
+      v[0].load(xr + c, end - c);
+      Eight<T>::put(qr + c, end - c, v[0].template coded<POW2>(code));
     }
   }
   if (t == 0) gp(scale)[row] = code.s;

@@ -534,3 +534,19 @@ def test_quantize_halves_of_the_smallest_scales(kfac_gpu):
     want, scale = qo.quantize_rows(x, None, False)
     assert same(host(s), scale) and len(set(scale)) > 200
     assert same(host(q), want)
+
+
+@pytest.mark.parametrize("cols", [2 ** 31 - 1, 2 ** 31 - 2044])
+def test_the_longest_rows(kfac_gpu, cols):
+    at = torch.tensor([0, 5, 2 ** 30 + 1, cols - 2050, cols - 9, cols - 1], device="cuda")
+    x = torch.zeros(1, cols, dtype=F16, device="cuda")
+    x[0, at] = torch.tensor([1.0, -2.0, 3.0, 127.0, -5.0, 6.0], dtype=F16, device="cuda")
+    q, s = quantize(kfac_gpu, x)
+    assert float(s) == 1.0 and q[0, at].tolist() == [1, -2, 3, 127, -5, 6]
+    assert int(torch.count_nonzero(q)) == 6
+    x.fill_(9.0)
+    kfac_gpu.kfac_dequantize_rows(q, s, x)
+    assert x[0, at].tolist() == [1, -2, 3, 127, -5, 6] and int(torch.count_nonzero(x)) == 6
+    q.fill_(9)
+    kfac_gpu.kfac_quantize_rows(x, q, s, mask=torch.zeros(1, dtype=torch.bool, device="cuda"))
+    assert float(s) == 0.0 and not q.any()
