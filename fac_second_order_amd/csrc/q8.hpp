@@ -78,6 +78,9 @@ kfac_status check_apart(const RowsOf* const (&buf)[N], int written) {
   return check_apart(buf, static_cast<int>(N), written);
 }
 
+// A launch has fewer than 2^32 threads: most blocks of 256, in whole eights.
+constexpr int64_t kMostBlocks = (int64_t(1) << 24) - 8;
+
 // The element types as the kernels take them.
 template <class F>
 kfac_status with_row_type(kfac_dtype d, F f) {

@@ -191,14 +191,14 @@ __device__ inline T held(float v) {
 
 // 8192 x 4096 bf16: 16.5 us, 6.1 TB/s. Groups of 8 elements, numbered through the rows, one a thread.
 template <class T>
-__global__ void __launch_bounds__(256) dequantize_rows_kernel(int cols, unsigned per_row, int64_t groups,
+__global__ void __launch_bounds__(256) dequantize_rows_kernel(int cols, unsigned per_row, unsigned groups,
                                                               const int8_t* __restrict__ q, int64_t ldq,
                                                               const float* __restrict__ scale, T* __restrict__ x,
                                                               int64_t ld) {
-  const int64_t g = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const unsigned g = blockIdx.x * 256 + threadIdx.x;
   if (g >= groups) return;
-  const int64_t row = groups >> 32 ? g / per_row : int64_t(unsigned(g) / per_row);
-  const int c = static_cast<int>(g - row * per_row) * 8, left = cols - c;
+  const int64_t row = g / per_row;
+  const int c = static_cast<int>(g % per_row) * 8, left = cols - c;
   const float s = gp(scale)[row];
   const KG int8_t* from = gp(q) + row * ldq + c;
   KG T* to = gp(x) + row * ld + c;
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(256) linear_q8_kernel(LinearArgs a, int across
 //
 // FUSED: the block first quantises the rows itself, its first weights on their way meanwhile, which saves a
 // launch; block 0 writes the checkpoint. For up to kFusedCodes codes, which each block has to form.
-constexpr int kFewRows = 32, kFusedCodes = 16384;
+constexpr int kFewRows = 32, kFusedCodes = 16384, kFewChannels = 1 << 25;  // 1024 threads for 16 of them
 
 template <class T, int NB, int WAVES, bool FUSED>
 __global__ void __launch_bounds__(64 * WAVES) linear_few_kernel(LinearArgs a, const T* __restrict__ x, int64_t ldx,
@@ -595,11 +595,13 @@ template <class T, bool POW2>
 static kfac_status launch_quantize(int32_t rows, int32_t cols, const void* x, int64_t ld, const uint8_t* mask,
                                    int8_t* q, int64_t ldq, float* scale, hipStream_t s) {
   auto go = [&](auto tpr, auto u) {
-    constexpr int TPR = decltype(tpr)::value;
-    const unsigned blocks = static_cast<unsigned>((int64_t(rows) + 256 / TPR - 1) / (256 / TPR));
-    KFAC_LAUNCH(K_QUANTIZE, (quantize_rows_kernel<T, POW2, TPR, decltype(u)::value>), dim3(blocks), dim3(256), 0, s, rows,
-                cols, static_cast<const T*>(x), ld, mask, q, ldq, scale);
-    KFAC_CHECK_LAUNCH("quantize_rows_kernel");
+    constexpr int TPR = decltype(tpr)::value, PER = 256 / TPR;
+    for (int64_t r = 0; r < rows; r += kMostBlocks * PER) {
+      const int n = static_cast<int>(std::min<int64_t>(rows - r, kMostBlocks * PER));
+      KFAC_LAUNCH(K_QUANTIZE, (quantize_rows_kernel<T, POW2, TPR, decltype(u)::value>), dim3((n + PER - 1) / PER), dim3(256),
+                  0, s, n, cols, static_cast<const T*>(x) + r * ld, ld, mask ? mask + r : nullptr, q + r * ldq, ldq, scale + r);
+      KFAC_CHECK_LAUNCH("quantize_rows_kernel");
+    }
     return KFAC_OK;
   };
   constexpr std::integral_constant<int, 64> wave;
@@ -658,11 +660,15 @@ extern "C" kfac_status kfac_dequantize_rows(int32_t rows, int32_t cols, const in
   return with_row_type(dtype, [&](auto tag) {
     using T = decltype(tag);
     const unsigned per_row = static_cast<unsigned>((int64_t(cols) + 7) / 8);
-    const int64_t groups = int64_t(rows) * per_row, blocks = (groups + 255) / 256;
-    if (blocks > INT32_MAX) return fail(KFAC_ERR_UNSUPPORTED, "more than 2^42 elements");
-    KFAC_LAUNCH(K_DEQUANTIZE, dequantize_rows_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                static_cast<hipStream_t>(stream), cols, per_row, groups, q, ld_q, scale, static_cast<T*>(x), ld_x);
-    KFAC_CHECK_LAUNCH("dequantize_rows_kernel");
+    const int64_t most = kMostBlocks * 256 / per_row;  // rows a launch
+    for (int64_t r = 0; r < rows; r += most) {
+      const int64_t n = std::min(rows - r, most);
+      const unsigned groups = static_cast<unsigned>(n * per_row);
+      KFAC_LAUNCH(K_DEQUANTIZE, dequantize_rows_kernel<T>, dim3((groups + 255) / 256), dim3(256), 0,
+                  static_cast<hipStream_t>(stream), cols, per_row, groups, q + r * ld_q, ld_q, scale + r,
+                  static_cast<T*>(x) + r * ld_x, ld_x);
+      KFAC_CHECK_LAUNCH("dequantize_rows_kernel");
+    }
     return KFAC_OK;
   });
 }
@@ -674,6 +680,9 @@ constexpr int64_t kMaxPitch = 1 << 23;  // 256 rows of a tile within 32-bit offs
 static kfac_status linear_sizes(int32_t rows, int32_t c_in, int32_t c_out) {
   if (rows < 0 || c_in < 0 || c_out < 0) return fail(KFAC_ERR_INVALID, "negative rows, c_in or c_out");
   if (c_in > kMaxTerms) return fail(KFAC_ERR_UNSUPPORTED, "c_in %d: a sum of more than %d products", c_in, kMaxTerms);
+  // as many take tiles of 256
+  if ((int64_t(rows) + 255) / 256 * ((int64_t(c_out) + 255) / 256) > kMostBlocks)
+    return fail(KFAC_ERR_UNSUPPORTED, "%d x %d: more than 2^24 - 8 tiles of 256 x 256", rows, c_out);
   return KFAC_OK;
 }
 
@@ -681,7 +690,6 @@ template <class T, int WT, bool DIRECT>
 static kfac_status launch_linear(const LinearArgs& a, hipStream_t s) {
   using L = LinearTile<WT>;
   const int64_t across = (int64_t(a.c_out) + L::T - 1) / L::T, tiles = across * ((int64_t(a.rows) + L::T - 1) / L::T);
-  if (tiles > (1 << 30)) return fail(KFAC_ERR_UNSUPPORTED, "more than 2^30 tiles");
   KFAC_LAUNCH(K_LINEAR_Q8, (linear_q8_kernel<T, WT, DIRECT>), dim3(xcd_grid(tiles)), dim3(256), 0, s, a,
               static_cast<int>(across), static_cast<int>(tiles));
   KFAC_CHECK_LAUNCH("linear_q8_kernel");
@@ -744,7 +752,7 @@ extern "C" kfac_status kfac_linear_q8(int32_t rows, int32_t c_in, int32_t c_out,
     // few rows: 32 x 4096 x 4096 bf16 11.0 us (in tiles 13.4), 32 x 8192 x 1024 16.0 (21.7); short sums gain
     // nothing (17 x 1024 x 8192 11.2, in tiles 7.4, the call's 13.2 and 13.5 being the host's). Fused with the quantising:
     // 1 x 4096 x 4096 8.5, else 6.4 + 7.5, 16 x 1024 x 4096 9.8, else 7.0 + 6.5: a launch less, 3 us a call
-    const bool few = rows <= kFewRows && c_out > 0;
+    const bool few = rows <= kFewRows && c_out > 0 && c_out <= kFewChannels;
     const bool fused = few && x && rows <= 16 && int64_t(rows) * c_in <= kFusedCodes;
     if (x && !fused) {
       kfac_status e = launch_quantize<T, true>(rows, c_in, x, ld_x, mask, q, ld_q, scale, s);

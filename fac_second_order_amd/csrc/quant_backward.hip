@@ -370,7 +370,7 @@ static kfac_status launch_jobs(TnJob* j, int n, bool ragged, hipStream_t s) {
     joins += join_items(j[i]);
     a.j[i] = j[i];
   }
-  if (items > (1 << 30) || joins > (1 << 30)) return fail(KFAC_ERR_UNSUPPORTED, "too many tiles");
+  if (items > kMostBlocks || joins > kMostBlocks) return fail(KFAC_ERR_UNSUPPORTED, "too many tiles: more than a launch takes");
   a.n = n, a.items = static_cast<int32_t>(items), a.joins = static_cast<int32_t>(joins);
   const int f = j[0].f;
   kfac_status st = KFAC_OK;

@@ -446,8 +446,8 @@ kfac_status kfac_dequantize_rows(int32_t rows, int32_t cols, const int8_t* q, in
  * exact in 32 bits, the rest is formed in fp32 and rounded once. With x, q and scale are
  * outputs: the call first quantises x (pow2 1; mask as there), and they are the checkpoint for
  * the backward pass. x NULL: q and scale are given (mask NULL). A scale of 0 gives y = bias.
- * c_in of 2^17 or more, rows of q or w 2^23 bytes apart or more, and more than 2^30 tiles give
- * KFAC_ERR_UNSUPPORTED.
+ * c_in of 2^17 or more, rows of q or w 2^23 bytes apart or more, and more than 2^24 - 8 tiles of
+ * 256 x 256 give KFAC_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 kfac_status kfac_linear_q8_workspace(int32_t rows, int32_t c_in, int32_t c_out, size_t* bytes);
 kfac_status kfac_linear_q8(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype, const void* x, int64_t ld_x,

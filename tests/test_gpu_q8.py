@@ -550,3 +550,39 @@ def test_the_longest_rows(kfac_gpu, cols):
     q.fill_(9)
     kfac_gpu.kfac_quantize_rows(x, q, s, mask=torch.zeros(1, dtype=torch.bool, device="cuda"))
     assert float(s) == 0.0 and not q.any()
+
+
+def test_more_rows_than_a_launch_takes(kfac_gpu):
+    """2^26 rows are a launch's at four a block, 2^32 groups of 8 elements one's that are read back."""
+    rows = 2 ** 26 + 3
+    x = torch.ones(rows, 2, dtype=F16, device="cuda")
+    x[-4:] = 3.0
+    mask = torch.ones(rows, dtype=torch.bool, device="cuda")
+    mask[-2] = mask[-40] = False
+    q, s = quantize(kfac_gpu, x, mask)
+    assert bool((q[:-4] == 64).sum() == 2 * (rows - 5)) and not q[-40].any()
+    assert q[-4:].tolist() == [[96, 96], [96, 96], [0, 0], [96, 96]]
+    assert s[-4:].tolist() == [2.0 ** -5, 2.0 ** -5, 0.0, 2.0 ** -5] and float(s[-40]) == 0.0 and float(s[0]) == 2.0 ** -6
+    del x, q, s, mask
+    rows = 2 ** 31 - 1
+    q = torch.ones(rows, 9, dtype=torch.int8, device="cuda")
+    s = torch.ones(rows, device="cuda")
+    q[-1], s[-2] = 5, 0.5
+    out = torch.zeros(rows, 9, dtype=F16, device="cuda")
+    kfac_gpu.kfac_dequantize_rows(q, s, out)
+    for part in out[:-2].split(2 ** 28):
+        assert bool((part == 1).all())
+    assert (out[-2] == 0.5).all() and (out[-1] == 5).all()
+
+
+def test_more_channels_than_a_launch_of_few_rows_takes(kfac_gpu):
+    for c_out in (2 ** 25, 2 ** 26 + 40):
+        w = torch.ones(c_out, 16, dtype=torch.int8, device="cuda")
+        w[-1] = 3
+        v = torch.ones(c_out, device="cuda")
+        v[-2] = 0.5
+        q, s = torch.ones(2, 16, dtype=torch.int8, device="cuda"), torch.tensor([1.0, 2.0], device="cuda")
+        y = torch.zeros(2, c_out, device="cuda")
+        kfac_gpu.kfac_linear_q8(None, q, s, w, v, y)
+        assert bool((y[:, :-2] == torch.tensor([[16.0], [32.0]], device="cuda")).all())
+        assert y[:, -2:].tolist() == [[8.0, 48.0], [16.0, 96.0]]

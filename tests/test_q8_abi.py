@@ -221,3 +221,11 @@ def test_binding_refuses_types(lib, call):
 def test_binding_refuses_sizes_and_devices(lib, call):
     with pytest.raises(ValueError):
         call(lib)
+
+
+def test_products_of_more_tiles_than_a_launch_takes(lib):
+    so, sz = lib._lib, c.c_size_t()
+    assert so.kfac_linear_q8_workspace(1 << 20, 8, 1 << 20, c.byref(sz)) == -2 and b"tiles" in so.kfac_last_error()
+    assert so.kfac_linear_q8_workspace((1 << 20) - 256, 8, 1 << 20, c.byref(sz)) == 0
+    assert so.kfac_linear_q8_workspace((1 << 31) - 1, 8, (1 << 31) - 1, c.byref(sz)) == -2
+    assert so.kfac_linear_q8_workspace((1 << 31) - 1, 8, 1, c.byref(sz)) == 0
