@@ -689,16 +689,17 @@ def kfac_linear_q8(x, q, scale, w, w_scale, y, bias=None, mask=None, workspace=N
     rows, c_out, code, y_at, y_ld = _rows(y, "y")
     _, c_in, q_at, q_ld, s_at = _checkpoint(q, scale, rows)
     _, _, w_at, w_ld, ws_at = _checkpoint(w, w_scale, c_out, c_in)
-    x_at = x_ld = 0
+    x_at, x_ld = None, 0
     if x is not None:
         if x.shape != q.shape or x.dtype != y.dtype:
             raise TypeError("x must have the shape of q and the type of y")
         _, _, _, x_at, x_ld = _rows(x, "x")
+        x_at = x_at or 256  # an empty tensor has no address, and none is not rows that are given as codes
     b_at = None if bias is None else _vector(bias, y.dtype, c_out, "bias")
     m_at = _mask_at(mask, rows)
     raw = _stream_of(stream, (x, q, scale, w, w_scale, y, bias, mask, workspace))
     ws, wsb, held = _scratch(workspace, kfac_linear_q8_workspace, (rows, c_in, c_out), y, stream)
-    _check(_lib.kfac_linear_q8(rows, c_in, c_out, code, x_at or None, x_ld, m_at, q_at, q_ld, s_at, w_at,
+    _check(_lib.kfac_linear_q8(rows, c_in, c_out, code, x_at, x_ld, m_at, q_at, q_ld, s_at, w_at,
                                w_ld, ws_at, b_at, y_at, y_ld, ws, wsb, raw), "kfac_linear_q8")
 
 

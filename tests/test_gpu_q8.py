@@ -586,3 +586,15 @@ def test_more_channels_than_a_launch_of_few_rows_takes(kfac_gpu):
         kfac_gpu.kfac_linear_q8(None, q, s, w, v, y)
         assert bool((y[:, :-2] == torch.tensor([[16.0], [32.0]], device="cuda")).all())
         assert y[:, -2:].tolist() == [[8.0, 48.0], [16.0, 96.0]]
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_linear_of_rows_without_columns(kfac_gpu, rows):
+    """Their checkpoint is written: a scale of 1, or 0 where the mask says so."""
+    x, q = torch.zeros(rows, 0, device="cuda"), torch.zeros(rows, 0, dtype=torch.int8, device="cuda")
+    w, v, b = torch.zeros(4, 0, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda"), torch.arange(4.0, device="cuda")
+    mask = torch.arange(rows, device="cuda") != 1
+    for m, want in ((None, [1.0] * rows), (mask, mask.float().tolist())):
+        s, y = torch.full((rows,), float("nan"), device="cuda"), torch.full((rows, 4), 9.0, device="cuda")
+        kfac_gpu.kfac_linear_q8(x, q, s, w, v, y, bias=b, mask=m)
+        assert s.tolist() == want and same(host(y), np.tile(np.arange(4.0), (rows, 1)))
