@@ -230,6 +230,11 @@ struct LinearArgs {
   int64_t ldq, ldw, ldy;
 };
 
+// A row with scale 0 takes no part, whatever the channel's scale holds.
+__device__ inline float entry(int sum, float s, float v, float b) {
+  return s == 0.f ? b : static_cast<float>(sum) * s * v + b;
+}
+
 // 16 codes of a row at k0, zeros past its end; nothing behind the row is read.
 __device__ inline v4i load_codes(const KG int8_t* row, int k0, int c_in) {
   if (k0 + 16 <= c_in) return __builtin_bit_cast(v4i, load_pack<false, int8_t>(row + k0));
@@ -450,7 +455,8 @@ __global__ void __launch_bounds__(256) linear_q8_kernel(LinearArgs a, int across
           typedef T vec4 __attribute__((ext_vector_type(4)));
           vec4 out;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) out[e] = static_cast<T>(static_cast<float>(acc[i][j][4 * g + e]) * row_scale[j] * v[e] + b[e]);
+          for (int e = 0; e < 4; ++e)
+            out[e] = static_cast<T>(entry(acc[i][j][4 * g + e], row_scale[j], v[e], b[e]));
           *reinterpret_cast<vec4*>(mine + (32 * (j - j0) + (lane & 31)) * kPitch + c * sizeof(T)) = out;
         }
       }
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(64 * WAVES) linear_few_kernel(LinearArgs a, co
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) sum += sums[i][r >> 4][r & 15][u & 15];
     const float b = a.bias ? static_cast<float>(gp(static_cast<const T*>(a.bias))[o]) : 0.f;
-    gp(static_cast<T*>(a.y))[r * a.ldy + o] = static_cast<T>(static_cast<float>(sum) * scales[r] * gp(a.w_scale)[o] + b);
+    gp(static_cast<T*>(a.y))[r * a.ldy + o] = static_cast<T>(entry(sum, scales[r], gp(a.w_scale)[o], b));
   }
 }
 

@@ -598,3 +598,22 @@ def test_linear_of_rows_without_columns(kfac_gpu, rows):
         s, y = torch.full((rows,), float("nan"), device="cuda"), torch.full((rows, 4), 9.0, device="cuda")
         kfac_gpu.kfac_linear_q8(x, q, s, w, v, y, bias=b, mask=m)
         assert s.tolist() == want and same(host(y), np.tile(np.arange(4.0), (rows, 1)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [5, 20, 300])
+def test_linear_of_weights_that_are_no_numbers(kfac_gpu, dtype, rows):
+    """A channel whose weights held a NaN is NaN in every row but those that take no part: their y is the bias."""
+    c_out = 130
+    x = rows_of(3, rows, 64, dtype)
+    mask = torch.arange(rows, device="cuda") % 3 != 1
+    w, v = codes(4, c_out, 64), torch.ones(c_out, device="cuda")
+    w[7], v[7], v[9] = 0, float("nan"), float("inf")
+    b = torch.randn(c_out, device="cuda").to(dtype)
+    q, s = torch.zeros(rows, 64, dtype=torch.int8, device="cuda"), torch.zeros(rows, device="cuda")
+    for bias in (b, None):
+        y = torch.full((rows, c_out), 9.0, dtype=dtype, device="cuda")
+        kfac_gpu.kfac_linear_q8(x, q, s, w, v, y, bias=bias, mask=mask)
+        alone = torch.zeros_like(b) if bias is None else b
+        assert torch.equal(y[~mask], alone.expand(rows, c_out)[~mask])
+        assert torch.isnan(y[mask][:, 7]).all() and torch.isfinite(y[:, :7]).all()
