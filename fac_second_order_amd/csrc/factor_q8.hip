@@ -178,9 +178,11 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
 #pragma unroll
     for (int j = 0; j < F; ++j) acc[i][j] = v16i{};
   }
-  // column sums, by the diagonal tiles: a block's two waves that hold the same columns take turns, a step each. (Not
-  // tiles in turns: each block has its own order of rows.)
+  // Column sums, by the diagonal tiles: of a block's two waves that hold the same columns one has the even groups of 32
+  // and the other the odd ones. A wave has all rows of its columns, so that what is rounded is a whole scale's sum,
+  // which does not know the rows' order. (Not tiles in turns: each block has its own order of rows.)
   const bool sums_here = d.bias && tj == ti;
+  const int sums_at = sums_here ? wave & 1 : -1;  // its first group
   const int s16 = lane & 15, kk = 16 * (lane >> 5) + (s16 >> 1), cc = 16 * ((lane >> 4) & 1) + 8 * (s16 & 1);
   const char* fa_at[F];
   const char* fb_at[F];
@@ -208,6 +210,10 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
   // a lane's accumulators of (i, j): column 32 j + lane % 32 of the wave, rows 32 i + 8 (e / 4) + 4 (lane / 32) + e % 4
   const int lane_at = (wm + 4 * (lane >> 5)) * T + wn + (lane & 31);
   auto entry = [](int i, int j, int e) { return (32 * i + 8 * (e >> 2) + (e & 3)) * T + 32 * j; };
+  // the sum of columns i, of rows of scale rel, to fp32: the lanes' halves, which have 16 rows each in turn, first
+  auto add_columns = [&](int i, float rel) __attribute__((always_inline)) {
+    sums[i] = fmaf(static_cast<float>(isum[i] + __shfl_xor(isum[i], 32)), rel, sums[i]);
+  };
   // the sums, of rows of scale s, to fp32
   auto flush = [&](float s) __attribute__((always_inline)) {
     const float rel = s * unit, rel2 = rel * rel;
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     asm volatile("" : "+v"(here));  // addresses are formed here, not kept over the loop
 #pragma unroll
     for (int i = 0; i < F; ++i) {
-      sums[i] = fmaf(static_cast<float>(isum[i]), rel, sums[i]);
+      add_columns(i, rel);
 #pragma unroll
       for (int j = 0; j < F; ++j) {
         const v16f all = __builtin_convertvector(acc[i][j], v16f) * rel2;
@@ -286,11 +292,14 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     auto mma = [&](int set, int n) {
       acc[n / F][n % F] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[set][n / F], fb[set][n % F], acc[n / F][n % F], 0, 0, 0);
     };
-    auto add_up = [&](int set) {
+    auto add_up = [&](auto FIRST) {  // its groups of columns, FIRST, FIRST + 2, ..
 #pragma unroll
-      for (int i = 0; i < F; ++i)
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) isum[i] = __builtin_amdgcn_sdot4(fa[set][i][k], 0x01010101, isum[i], false);
+        for (int set = 0; set < 2; ++set)
+#pragma unroll
+          for (int i = decltype(FIRST)::value; i < F; i += 2)
+            isum[i] = __builtin_amdgcn_sdot4(fa[set][i][k], 0x01010101, isum[i], false);
     };
 #define KFAC_AT(x) std::integral_constant<int, (x)>{}
     int r[G];
@@ -308,7 +317,6 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < R; ++k) read(KFAC_AT(0), 0, 0, k);
-    int next = sums_here ? wave & 1 : INT32_MAX;
     bound = uint64_t(uniform(list.n[0])) << 14, bound_col = bound >> 7;
     int c = 0;
     bool edge = false;  // the next step's rows have another scale
@@ -334,11 +342,8 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (c == next) {
-        add_up(0);
-        add_up(1);
-        next += 2;
-      }
+      if (sums_at == 0) add_up(KFAC_AT(0));
+      else if (sums_at == 1) add_up(KFAC_AT(1));
       __syncthreads();
 #pragma unroll
       for (int n = 0; n < MN; ++n) {
@@ -430,30 +435,19 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
       __builtin_amdgcn_sched_barrier(0);
     }
   if (!sums_here) return;
+  KG float* const col = d.solo ? nullptr : gp(d.part_col) + int64_t(split) * (int64_t(d.mt) * T);
 #pragma unroll
   for (int i = 0; i < F; ++i) {
-    sums[i] = fmaf(static_cast<float>(isum[i]), rel, sums[i]);
-    sums[i] = (sums[i] + __shfl_xor(sums[i], 32)) * back;
-  }
-  if (!d.solo) {
-    KG float* col = gp(d.part_col) + (int64_t(split) * d.shares + (wave & 1)) * (int64_t(d.mt) * T) + ti * T;
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-      if (lane < 32) col[wm + 32 * i + lane] = sums[i];
-    return;
-  }
-  float* const other = reinterpret_cast<float*>(lds);
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < F; ++i)
-    if ((wave & 1) && lane < 32) other[wm + 32 * i + lane] = sums[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < F; ++i) {
+    add_columns(i, rel);
+    const float sum = sums[i] * back;
     const int c = ti * T + wm + 32 * i + lane;
-    if ((wave & 1) || lane >= 32 || c >= d.m) continue;
-    put(c, d.m, (sums[i] + other[wm + 32 * i + lane]) * inv_r);
-    if (c == 0) put(d.m, d.m, counted ? 1.f : 0.f);
+    if ((i & 1) != sums_at || lane >= 32) continue;
+    if (!d.solo) {
+      col[c] = sum;
+    } else if (c < d.m) {
+      put(c, d.m, sum * inv_r);
+      if (c == 0) put(d.m, d.m, counted ? 1.f : 0.f);
+    }
   }
 }
 

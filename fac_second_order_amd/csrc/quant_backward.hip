@@ -289,7 +289,7 @@ static void set_tiles(TnJob& j, int f, bool factor) {
   j.mt = static_cast<int32_t>((int64_t(j.m) + T - 1) / T);
   j.nt = std::max(1, static_cast<int32_t>((int64_t(j.n) + T - 1) / T));  // a bias alone has its tiles too
   j.tiles = factor ? j.mt * (j.mt + 1) / 2 : j.mt * j.nt;
-  j.shares = !f ? 1 : factor ? 2 : 2 * j.nt;
+  j.shares = !f || factor ? 1 : 2 * j.nt;
 }
 
 // Tile edge and splits of the rows by what they are expected to take, in us, which is returned: rounds over the

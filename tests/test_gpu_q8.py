@@ -617,3 +617,30 @@ def test_linear_of_weights_that_are_no_numbers(kfac_gpu, dtype, rows):
         alone = torch.zeros_like(b) if bias is None else b
         assert torch.equal(y[~mask], alone.expand(rows, c_out)[~mask])
         assert torch.isnan(y[mask][:, 7]).all() and torch.isfinite(y[:, :7]).all()
+
+
+@pytest.mark.parametrize("rows, cols, octaves", [(8192, 300, 22), (8192, 70, 22), (8192, 1500, 20), (100352, 200, 15),
+                                                 (100352, 64, 20)])
+def test_factor_is_deterministic(kfac_gpu, rows, cols, octaves):
+    """The same bits from run to run, over scales that do not fit into 32 bits together."""
+    q = codes(rows, rows, cols) | 64                            # sums far from 0
+    g = torch.Generator().manual_seed(cols)
+    s = torch.exp2(-torch.randint(0, octaves, (rows,), generator=g).float()).cuda()
+    first = factors(kfac_gpu, [(q, s)], True)[0]
+    want, size = qo.factor_packed(host(q[:, :64]), host(s), True) if cols == 64 else (None, None)
+    for _ in range(6):
+        assert torch.equal(factors(kfac_gpu, [(q, s)], True)[0], first)
+    if want is not None:
+        assert (np.abs(host64(first) - want) <= (octaves + 60) * 2 * U * size).all()
+
+
+@pytest.mark.parametrize("rows", [63, 200, 440])
+@pytest.mark.parametrize("cols", [33, 130, 900, 2600])
+def test_factor_does_not_know_the_rows_order(kfac_gpu, rows, cols):
+    """Rows of one scale add up exactly: in any order of the rows of a block the same bits."""
+    q = codes(rows, rows, cols) | 64
+    s = torch.exp2(-(torch.arange(rows) % 23).float()).cuda()
+    first = factors(kfac_gpu, [(q, s)], True)[0]
+    for seed in range(4):
+        p = torch.randperm(rows, generator=torch.Generator().manual_seed(seed)).cuda()
+        assert torch.equal(factors(kfac_gpu, [(q[p].contiguous(), s[p].contiguous())], True)[0], first)
