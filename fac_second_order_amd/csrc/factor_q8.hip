@@ -100,7 +100,7 @@ __device__ inline int sort_rows(const float* scale, int64_t r0, int n, SortedRow
   if (steps && first + steps == all)  // the last scale's
     for (int k = 0; k < kFactorAhead + 3; ++k) l.step[all + k] = 0, l.s[all + k] = l.s[all - 1], l.n[all + k] = 0;
   __syncthreads();
-  // the order within a class is that of the atomics: its sum is exact
+  // the order within a class is that of the atomics: its whole sum is exact, and no part of it is rounded
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (256 * i >= n) break;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
   const float inv_r = counted ? 1.f / static_cast<float>(counted) : 0.f;
   const float rel = bad ? __uint_as_float(0x7fc00000u) : s_here * unit, rel2 = rel * rel;
   const PutFactor put = put_factor(d, counted);
-  if (d.part_rows && tile == 0 && tid == 0) gp(d.part_rows)[split] = counted;  // somebody joins
+  if (d.part_rows && tile == 0 && tid == 0) gp(d.part_rows)[split] = bad ? -counted : counted;  // somebody joins
   unsigned here = lane_at;
   asm volatile("" : "+v"(here));
 #pragma unroll
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
       col[c] = sum;
     } else if (c < d.m) {
       put(c, d.m, sum * inv_r);
-      if (c == 0) put(d.m, d.m, counted ? 1.f : 0.f);
+      if (c == 0) put(d.m, d.m, corner(counted, bad));
     }
   }
 }

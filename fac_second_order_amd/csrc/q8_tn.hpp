@@ -27,7 +27,7 @@ struct TnJob {
   float* bias_out;     // db, or NULL
   float* part;         // [splits][tiles][T * T], with splits > 1
   float* part_col;     // [splits][shares][tile rows][T]: column sums, unless one tile has them (solo)
-  int32_t* part_rows;  // [splits]: rows that count
+  int32_t* part_rows;  // [splits]: rows that count, negative if one has a scale that is none
   int64_t ldg, ldq, ldo, inc_b;
   int32_t m, n, rows;  // columns of both operands
   int32_t mt, nt;      // tiles along them

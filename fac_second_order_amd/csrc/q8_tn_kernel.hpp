@@ -258,6 +258,10 @@ struct PutFactor {
 __device__ inline PutFactor put_factor(const TnJob& d, int counted) {
   return {gp(d.out), gp(d.full), d.decay, counted > 0, int64_t(d.m) + d.bias};
 }
+// The bias column's own entry: the rows' ones, NaN as all of the factor if one of them has a scale that is none.
+__device__ inline float corner(int counted, bool bad) {
+  return bad ? __uint_as_float(0x7fc00000u) : counted ? 1.f : 0.f;
+}
 __device__ inline void put_grad(KG float* o, float v, int accumulate) { *o = accumulate ? *o + v : v; }
 
 template <class E, int F, bool RAGGED>

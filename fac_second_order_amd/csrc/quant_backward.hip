@@ -219,11 +219,14 @@ __global__ void __launch_bounds__(256) q8_join_kernel(TnArgs<FACTOR> args) {
   const int tid = threadIdx.x;
   const TnJob& d = args.j[FACTOR ? args.owner(blockIdx.x, &TnJob::join_begin) : 0];
   const int T = tile_edge(d), item = blockIdx.x - d.join_begin, here = static_cast<int>(join_tiles(d));
-  int counted = 0;
+  int counted = 0, bad = 0;
   if (FACTOR) {
-    for (int s = tid & 63; s < d.splits; s += 64) counted += gp(d.part_rows)[s];
+    for (int s = tid & 63; s < d.splits; s += 64) {
+      const int n = gp(d.part_rows)[s];
+      counted += abs(n), bad |= n < 0;
+    }
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) counted += __shfl_xor(counted, o);
+    for (int o = 32; o > 0; o >>= 1) counted += __shfl_xor(counted, o), bad |= __shfl_xor(bad, o);
   }
   const float inv_r = counted ? 1.f / static_cast<float>(counted) : 0.f;
   const PutFactor put = put_factor(d, counted);
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(256) q8_join_kernel(TnArgs<FACTOR> args) {
   sum = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
   if (FACTOR) {
     put(c, d.m, sum * inv_r);
-    if (c == 0) put(d.m, d.m, counted ? 1.f : 0.f);
+    if (c == 0) put(d.m, d.m, corner(counted, bad));
   } else {
     put_grad(gp(d.bias_out) + c * d.inc_b, sum, d.accumulate);
   }

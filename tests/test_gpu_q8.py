@@ -644,3 +644,18 @@ def test_factor_does_not_know_the_rows_order(kfac_gpu, rows, cols):
     for seed in range(4):
         p = torch.randperm(rows, generator=torch.Generator().manual_seed(seed)).cuda()
         assert torch.equal(factors(kfac_gpu, [(q[p].contiguous(), s[p].contiguous())], True)[0], first)
+
+
+@pytest.mark.parametrize("rows, cols", [(70, 40), (9000, 40), (300, 900)])
+def test_factor_of_a_scale_that_is_none(kfac_gpu, rows, cols):
+    """All of it is NaN, the bias column's own entry too, whatever the other rows are."""
+    q = codes(1, rows, cols, most=9)
+    for bad in (1.5, float("nan"), float("inf"), -1.0, 2.0 ** -130):
+        s = torch.ones(rows, device="cuda")
+        s[rows - 3] = bad
+        old = [torch.rand((cols + 1) * (cols + 2) // 2, device="cuda")]
+        for decay in (0.0, 0.5):
+            assert np.isnan(host(factors(kfac_gpu, [(q, s)], True, full=False, decay=decay, start=old)[0])).all()
+        s[:] = 0
+        s[rows - 3] = bad
+        assert np.isnan(host(factors(kfac_gpu, [(q, s)], True)[0])).all()
