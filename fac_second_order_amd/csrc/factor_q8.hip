@@ -118,6 +118,7 @@ struct Raw16 {
   __device__ inline void load(const KG char* p) {
     w = __builtin_bit_cast(v4u, load_pack<false, int8_t>(reinterpret_cast<const KG int8_t*>(p)));
   }
+  __device__ inline v4u codes(int) const { return w; }
   __device__ inline void shift(int k) {  // drops the first k
     uint64_t lo = uint64_t(w[1]) << 32 | w[0], hi = uint64_t(w[3]) << 32 | w[2];
     const int b = 8 * (k & 7);
@@ -128,8 +129,40 @@ struct Raw16 {
   }
 };
 
-template <int F, bool RAGGED>
+// The first n of 16 codes, 0 <= n <= 16, and zeros, by loads from both ends that may overlap: nothing behind them is read.
+struct Raw16Some {
+  uint64_t a, b;
+  unsigned c;
+  template <int N>
+  static __device__ inline uint64_t bytes(const KG char* p) {
+    uint64_t w = 0;
+    const auto v = load_pack<false, int8_t, N>(reinterpret_cast<const KG int8_t*>(p));
+    __builtin_memcpy(&w, &v, N);
+    return w;
+  }
+  __device__ inline void load(const KG char* p, int n) {
+    a = 0, b = 0, c = 0;
+    if (n >= 8) a = bytes<8>(p), b = bytes<8>(p + n - 8);
+    else if (n >= 4) a = bytes<4>(p), b = bytes<4>(p + n - 4);
+    else if (n > 0) a = uint8_t(p[0]), b = uint8_t(p[n / 2]), c = uint8_t(p[n - 1]);
+  }
+  __device__ inline v4u codes(int n) const {
+    uint64_t lo = a, hi = 0;
+    if (n > 8) hi = b >> (8 * (16 - n));
+    else if (n >= 4) lo |= n < 8 ? b << (8 * (n - 4)) : 0;
+    else if (n > 0) lo |= b << (8 * (n / 2)) | uint64_t(c) << (8 * (n - 1));
+    return v4u{unsigned(lo), unsigned(lo >> 32), unsigned(hi), unsigned(hi >> 32)};
+  }
+};
+
+// COLS: how the columns are read. kWhole: in groups of 16; kRagged: the last group of a row shifted; kAny, in tiles
+// of 64: as many of a group as there are, for rows of fewer than 16 columns or 2^32 bytes and more apart (100352 x 8:
+// 31 us, 1000 x 12: 17, a row of one 10.4).
+enum { kWhole, kRagged, kAny };
+
+template <int F, int COLS>
 __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<true> args) {
+  constexpr bool RAGGED = COLS == kRagged;
   using L = FactorTile<F>;
   constexpr int T = L::T, G = L::FETCH, BUFS = kFactorAhead;
   __shared__ __attribute__((aligned(16))) char lds[2 * BUFS * L::OPERAND];
@@ -146,7 +179,8 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
   char* const abuf = lds;
   char* const bbuf = lds + BUFS * L::OPERAND;
 
-  // this thread's groups of 16 columns: row of a step, place in its line, offset in its rows, codes to shift out
+  // this thread's groups of 16 columns: row of a step, place in its line, offset in its rows, codes to shift out (kAny:
+  // columns that there are)
   int row[G], at[G], a_col[G], b_col[G], a_cut[G], b_cut[G];
 #pragma unroll
   for (int i = 0; i < G; ++i) {
@@ -154,19 +188,24 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     row[i] = u / L::GROUPS;
     at[i] = row[i] * T + 16 * ((u % L::GROUPS) ^ L::moved(row[i]));
     auto column = [&](int c, int& off, int& cut) {
+      if constexpr (COLS == kAny) {
+        cut = max(0, min(16, d.m - c)), off = cut ? c : 0;
+        return;
+      }
       off = c + 16 <= d.m ? c : RAGGED && c < d.m ? d.m - 16 : 0;
       cut = RAGGED && c < d.m && c + 16 > d.m ? c + 16 - d.m : 0;
     };
     column(ti * T + c, a_col[i], a_cut[i]);
     column(tj * T + c, b_col[i], b_cut[i]);
   }
-  bool cuts = false;  // of the wave: only the last tiles of ragged operands have any
+  [[maybe_unused]] bool cuts = false;  // of the wave: only the last tiles of ragged operands have any
   if constexpr (RAGGED) {
 #pragma unroll
     for (int i = 0; i < G; ++i) cuts |= (a_cut[i] | b_cut[i]) != 0;
     cuts = __any(cuts);
   }
-  Raw16 araw[kFactorAhead][G], braw[kFactorAhead][G];
+  using Raw = std::conditional_t<COLS == kAny, Raw16Some, Raw16>;
+  Raw araw[kFactorAhead][G], braw[kFactorAhead][G];
 
   const int wm = (wave >> 1) * 32 * F, wn = (wave & 1) * 32 * F;
   v16i acc[F][F];
@@ -259,7 +298,8 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     for (int o = 32; o > 0; o >>= 1) high = max(high, __shfl_xor(high, o));
     return static_cast<uint64_t>(uniform(high));
   };
-  const unsigned pitch = static_cast<unsigned>(d.ldq);
+  using Pitch = std::conditional_t<COLS == kAny, uint64_t, unsigned>;
+  const Pitch pitch = static_cast<Pitch>(d.ldq);
   if (steps) {
     const KG char* const q0 = uniform(reinterpret_cast<const KG char*>(gp(d.q)) + r_begin * d.ldq);
     unsigned some[kFactorAhead][G];  // of what the registers hold: ~0, or 0 for no row
@@ -274,14 +314,20 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     auto fetch = [&](auto set, int k, const int (&r)[G]) {  // 2 G loads
       const int i = k / 2;
       const KG char* from = q0 + uint64_t(unsigned(r[i])) * pitch;
-      if (k & 1) araw[set][i].load(from + a_col[i]);
-      else braw[set][i].load(from + b_col[i]);
+      if constexpr (COLS == kAny) {
+        if (k & 1) araw[set][i].load(from + a_col[i], a_cut[i]);
+        else braw[set][i].load(from + b_col[i], b_cut[i]);
+      } else {
+        if (k & 1) araw[set][i].load(from + a_col[i]);
+        else braw[set][i].load(from + b_col[i]);
+      }
     };
     auto place = [&](auto set, auto buf, int k) {
       const int i = k / 2;
-      Raw16& x = k & 1 ? araw[set][i] : braw[set][i];
-      if (RAGGED && cuts) x.shift(k & 1 ? a_cut[i] : b_cut[i]);
-      *reinterpret_cast<v4u*>((k & 1 ? abuf : bbuf) + buf * L::OPERAND + at[i]) = x.w & some[set][i];
+      Raw& x = k & 1 ? araw[set][i] : braw[set][i];
+      if constexpr (RAGGED)
+        if (cuts) x.shift(k & 1 ? a_cut[i] : b_cut[i]);
+      *reinterpret_cast<v4u*>((k & 1 ? abuf : bbuf) + buf * L::OPERAND + at[i]) = x.codes(k & 1 ? a_cut[i] : b_cut[i]) & some[set][i];
     };
     v4i fa[2][F], fb[2][F];
     constexpr int R = 2 * F, MN = F * F;
@@ -451,17 +497,18 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
   }
 }
 
-template <int F, bool RAGGED>
+template <int F, int COLS>
 static kfac_status launch(const TnArgs<true>& a, hipStream_t s) {
-  KFAC_LAUNCH(K_FACTOR_Q8, (factor_q8_kernel<F, RAGGED>), dim3(xcd_grid(a.items)), dim3(256), 0, s, a);
+  KFAC_LAUNCH(K_FACTOR_Q8, (factor_q8_kernel<F, COLS>), dim3(xcd_grid(a.items)), dim3(256), 0, s, a);
   KFAC_CHECK_LAUNCH("factor_q8_kernel");
   return KFAC_OK;
 }
 
 kfac_status launch_factor_tiles(const TnArgs<true>& a, int f, bool ragged, hipStream_t s) {
-  if (f == 1) return ragged ? launch<1, true>(a, s) : launch<1, false>(a, s);
-  if (f == 2) return ragged ? launch<2, true>(a, s) : launch<2, false>(a, s);
-  return ragged ? launch<3, true>(a, s) : launch<3, false>(a, s);
+  if (a.j[0].any) return launch<1, kAny>(a, s);
+  if (f == 1) return ragged ? launch<1, kRagged>(a, s) : launch<1, kWhole>(a, s);
+  if (f == 2) return ragged ? launch<2, kRagged>(a, s) : launch<2, kWhole>(a, s);
+  return ragged ? launch<3, kRagged>(a, s) : launch<3, kWhole>(a, s);
 }
 
 }  // namespace kfac

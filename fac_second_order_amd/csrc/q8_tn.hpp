@@ -34,7 +34,8 @@ struct TnJob {
   int32_t tiles, splits, per_split;
   int32_t bias, accumulate;
   float decay;
-  int32_t f;       // tiles of 64 f x 64 f; 0: the plain kernel
+  int32_t f;       // tiles of 64 f x 64 f; 0: the plain kernel, of gradients
+  int32_t any;     // a factor of any columns and pitch (kAny)
   int32_t solo;    // with splits = 1: a row of tiles' first one adds up the columns alone
   int32_t shares;  // who adds up the columns of a row of tiles
   int32_t begin, join_begin;  // first work items

@@ -1,5 +1,5 @@
-// Weight gradients and Kronecker factors from rows in 8 bits: the plain kernel, what joins the parts of the
-// tiles, and the entry points.
+// Weight gradients and Kronecker factors from rows in 8 bits: the plain kernel of gradients, what joins the parts of
+// the tiles, and the entry points.
 #include "q8_tn_kernel.hpp"
 
 namespace kfac {
@@ -48,29 +48,21 @@ struct Stage {
   }
 };
 
-// A factor's scale: NaN, if it is neither 0 nor a power of two.
-__device__ inline float power_of_two(float s) {
-  return __float_as_uint(s) & 0x807fffffu ? __uint_as_float(0x7fc00000u) : s;
-}
-
 // The plain kernel: any sizes and pitches, tiles of 128 x 128, a step's rows staged and then multiplied. For
 // operands of fewer than 8 columns, and rows 2^32 bytes and more apart.
-template <class T, bool FACTOR>
+template <class T>
 __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
   constexpr int TM = 128, TN = 128, NT = 256, BK = 32, PITCH = 128 + 32, P = kParts<T>;
   constexpr bool HALF = std::is_same_v<T, _Float16>;
-  using G = std::conditional_t<FACTOR, int8_t, T>;
   __shared__ __attribute__((aligned(16))) short lds[P + 1][BK][PITCH];
   __shared__ RowList<kSmallList> list;
   __shared__ float colsum[TM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int tile = blockIdx.x % d.tiles, split = blockIdx.x / d.tiles;
-  int ti, tj;
-  if (FACTOR) factor_tile(tile, d.mt, ti, tj);
-  else ti = tile / d.nt, tj = tile % d.nt;
+  const int ti = tile / d.nt, tj = tile % d.nt;
   const int64_t r_begin = int64_t(split) * d.per_split;
   const int r_count = static_cast<int>(min(int64_t(d.per_split), d.rows - r_begin));
-  const bool sums = FACTOR ? ti == tj : d.bias && tj == 0;  // this block adds up the columns of its first operand
+  const bool sums = d.bias && tj == 0;  // this block adds up the columns of its first operand
   if (tid < TM) colsum[tid] = 0.f;
 
   v16f acc[2][2];
@@ -81,24 +73,19 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   const float unit = HALF ? scale_unit<NT>(d.scale, r_begin, r_count, list.top) : 1.f;
-  int counted = 0;
   for (int base = 0; base < r_count; base += kSmallList) {
     const int64_t r0 = r_begin + base;
     const int n = list_rows<NT>(d.scale, r0, min(kSmallList, r_count - base), unit, list);
-    counted += n;
     for (int k0 = 0; k0 < n; k0 += BK) {
-      Stage<G, TM, NT, BK> a;
+      Stage<T, TM, NT, BK> a;
       Stage<int8_t, TN, NT, BK> b;
-      const G* src = FACTOR ? reinterpret_cast<const G*>(d.q) : static_cast<const G*>(d.g);
-      a.load(src, FACTOR ? d.ldq : d.ldg, r0, list, k0, ti * TM, d.m);
+      a.load(static_cast<const T*>(d.g), d.ldg, r0, list, k0, ti * TM, d.m);
       b.load(d.q, d.ldq, r0, list, k0, tj * TN, d.n);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < a.N; ++i) {
         const int r = a.row(i), c = a.col(i);
-        if constexpr (FACTOR) {
-          *reinterpret_cast<v8s*>(&lds[0][r][c]) = codes16<HALF>(a.v[i], power_of_two(list.s[k0 + r]));
-        } else if constexpr (P == 3) {
+        if constexpr (P == 3) {
           v8s h[3];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -115,7 +102,7 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
 #pragma unroll
       for (int i = 0; i < b.N; ++i) {
         const int r = b.row(i), c = b.col(i);
-        *reinterpret_cast<v8s*>(&lds[P][r][c]) = codes16<HALF>(b.v[i], FACTOR ? power_of_two(list.s[k0 + r]) : list.s[k0 + r]);
+        *reinterpret_cast<v8s*>(&lds[P][r][c]) = codes16<HALF>(b.v[i], list.s[k0 + r]);
       }
       __syncthreads();
       if (sums && tid < TM) {
@@ -157,7 +144,6 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
   }
   __syncthreads();
   const float back = 1.f / unit;  // exact: a power of two
-  const float colback = FACTOR ? back : 1.f;
   if (d.splits > 1) {
     KG float* part = gp(d.part) + (int64_t(split) * d.tiles + tile) * (TM * TN);
 #pragma unroll
@@ -168,14 +154,11 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
         for (int e = 0; e < 16; ++e) {
           const int r = (wave >> 1) * 64 + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
           const int c = (wave & 1) * 64 + 32 * j + (lane & 31);
-          part[r * TN + c] = FACTOR ? acc[i][j][e] * back * back : acc[i][j][e] * back;
+          part[r * TN + c] = acc[i][j][e] * back;
         }
-    if (sums && tid < TM) gp(d.part_col)[(int64_t(split) * d.mt + ti) * TM + tid] = colsum[tid] * colback;
-    if (tile == 0 && tid == 0) gp(d.part_rows)[split] = counted;
+    if (sums && tid < TM) gp(d.part_col)[(int64_t(split) * d.mt + ti) * TM + tid] = colsum[tid];
     return;
   }
-  const float inv_r = counted ? 1.f / static_cast<float>(counted) : 0.f;
-  const PutFactor put = put_factor(d, counted);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -184,20 +167,11 @@ __global__ void __launch_bounds__(256) q8_plain_kernel(TnJob d) {
       for (int e = 0; e < 16; ++e) {
         const int64_t r = int64_t(ti) * TM + (wave >> 1) * 64 + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
         const int64_t c = int64_t(tj) * TN + (wave & 1) * 64 + 32 * j + (lane & 31);
-        if (FACTOR) {
-          if (r <= c && c < d.n) put(r, c, acc[i][j][e] * back * back * inv_r);
-        } else if (r < d.m && c < d.n) {
-          put_grad(gp(d.out) + r * d.ldo + c, acc[i][j][e] * back, d.accumulate);
-        }
+        if (r < d.m && c < d.n) put_grad(gp(d.out) + r * d.ldo + c, acc[i][j][e] * back, d.accumulate);
       }
-  if (!d.bias || !sums || tid >= TM) return;
+  if (!sums || tid >= TM) return;
   const int64_t r = int64_t(ti) * TM + tid;
-  if (FACTOR) {
-    if (r < d.m) put(r, d.m, colsum[tid] * colback * inv_r);
-    if (tile == 0 && tid == 0) put(d.m, d.m, counted ? 1.f : 0.f);
-  } else if (r < d.m) {
-    put_grad(gp(d.bias_out) + r * d.inc_b, colsum[tid], d.accumulate);
-  }
+  if (r < d.m) put_grad(gp(d.bias_out) + r * d.inc_b, colsum[tid], d.accumulate);
 }
 
 // ---- joining ------------------------------------------------------------------------
@@ -298,12 +272,14 @@ static void set_tiles(TnJob& j, int f, bool factor) {
 // Tile edge and splits of the rows by what they are expected to take, in us, which is returned: rounds over the
 // compute units of the steps of one tile (measured on full cards; a factor's scales add some), what a block
 // spends before and after, and the parts' way through memory. `share`: the part of the card that the job has;
-// `only`: this tile edge, unless 0.
+// `only`: this tile edge, unless 0. A factor of few columns or far rows has tiles of 64.
 static double plan(TnJob& j, bool factor, kfac_dtype dtype, bool near, double share, int only) {
   const int64_t rows = std::max(j.rows, 1);
   const int least = factor ? 16 : 8, rows_a_step = factor ? 64 : kStep;
   double best = 0;
-  if (!near || j.m < least || j.n < least) {
+  const bool plain = !near || j.m < least || j.n < least;
+  j.any = factor && plain;
+  if (plain && !factor) {
     set_tiles(j, 0, factor);
     const int64_t splits = std::max<int64_t>(1, std::min<int64_t>((rows + 511) / 512, 512 / std::max(1, j.tiles)));
     j.per_split = static_cast<int32_t>((rows + splits - 1) / splits);
@@ -313,7 +289,7 @@ static double plan(TnJob& j, bool factor, kfac_dtype dtype, bool near, double sh
     const int64_t steps = (rows + rows_a_step - 1) / rows_a_step;
     for (int f : {1, 2, 3, 4}) {
       if (factor ? f == 4 : f == 1 || f == 3 || (f == 4 && dtype == KFAC_F32)) continue;
-      if (only && f != only) continue;
+      if (j.any ? f != 1 : only && f != only) continue;
       set_tiles(j, f, factor);
       const double entries = double(j.tiles) * tile_edge(j) * tile_edge(j);
       const double slots = std::max(1.0, kCus * share * (f == 1 ? 3 : f == 2 ? 2 : 1));
@@ -354,15 +330,15 @@ static kfac_status sizes_fit(int64_t rows, int64_t m, int64_t n) {
   return KFAC_OK;
 }
 
-template <class T, bool FACTOR>
+template <class T>
 static kfac_status launch_plain(const TnJob& j, hipStream_t s) {
   if (j.m == 0 || (j.n == 0 && !j.bias)) return KFAC_OK;
-  KFAC_LAUNCH(FACTOR ? K_FACTOR_Q8 : K_GRAD_Q8, (q8_plain_kernel<T, FACTOR>), dim3(j.tiles * j.splits), dim3(256), 0, s, j);
+  KFAC_LAUNCH(K_GRAD_Q8, q8_plain_kernel<T>, dim3(j.tiles * j.splits), dim3(256), 0, s, j);
   KFAC_CHECK_LAUNCH("q8_plain_kernel");
   return KFAC_OK;
 }
 
-// Jobs of one tile edge (0: one job for the plain kernel), and what joins their parts.
+// Jobs of one kind (a gradient, or factors of one tile edge), and what joins their parts.
 template <class T, bool FACTOR>
 static kfac_status launch_jobs(TnJob* j, int n, bool ragged, hipStream_t s) {
   TnArgs<FACTOR> a = {};
@@ -377,11 +353,10 @@ static kfac_status launch_jobs(TnJob* j, int n, bool ragged, hipStream_t s) {
   a.n = n, a.items = static_cast<int32_t>(items), a.joins = static_cast<int32_t>(joins);
   const int f = j[0].f;
   kfac_status st = KFAC_OK;
-  if (f == 0) {
-    st = launch_plain<T, FACTOR>(j[0], s);
-  } else if constexpr (FACTOR) {
+  if constexpr (FACTOR) {
     st = launch_factor_tiles(a, f, ragged, s);
   } else {
+    if (f == 0) st = launch_plain<T>(j[0], s);
     if (f == 2) st = ragged ? launch_grad_tiles<T, 2, true>(a, s) : launch_grad_tiles<T, 2, false>(a, s);
     if constexpr (!std::is_same_v<T, float>)
       if (f == 4) st = ragged ? launch_grad_tiles<T, 4, true>(a, s) : launch_grad_tiles<T, 4, false>(a, s);
@@ -448,7 +423,6 @@ extern "C" kfac_status kfac_weight_grad_q8(int32_t rows, int32_t c_in, int32_t c
   });
 }
 
-// A layer whose rows lie far apart is the plain kernel's.
 static TnJob factor_job(int32_t rows, int32_t cols, int32_t bias, double share, int f, bool near, double* us) {
   TnJob j = {};
   j.rows = rows, j.m = j.n = cols, j.bias = bias;
@@ -479,7 +453,7 @@ static kfac_status factor_jobs(int32_t count, const int32_t* rows, const int32_t
     for (int i = 0; i < count; ++i) {
       double us = 0;
       jobs.push_back(factor_job(rows[i], cols[i], bias[i], work_of(i) / work, f, true, &us));
-      slowest = std::max(slowest, us);
+      if (!jobs[i].any) slowest = std::max(slowest, us);
     }
     if (f == 1 || slowest < best) best = slowest, near = std::move(jobs);
   }
@@ -555,15 +529,16 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
   }
   // a launch for the layers of one kind
   std::vector<TnJob> some;
-  for (int f : {3, 2, 1, 0})
-    for (bool ragged : {false, true}) {
-      some.clear();
-      for (const TnJob& j : jobs)
-        if (j.f == f && (f == 0 ? !ragged : bool(j.m & 15) == ragged)) some.push_back(j);
-      const size_t most = f ? kTnMany : 1;
-      for (size_t i = 0; i < some.size(); i += most)
-        if ((st = launch_jobs<_Float16, true>(&some[i], static_cast<int>(std::min(most, some.size() - i)), ragged, s))) return st;
-    }
+  for (int kind = 0; kind < 7; ++kind) {
+    const int f = 3 - kind / 2, any = kind == 6;
+    const bool ragged = kind & 1;
+    some.clear();
+    for (const TnJob& j : jobs)
+      if (any ? j.any : !j.any && j.f == f && bool(j.m & 15) == ragged) some.push_back(j);
+    for (size_t i = 0; i < some.size(); i += kTnMany)
+      if ((st = launch_jobs<_Float16, true>(&some[i], static_cast<int>(std::min<size_t>(kTnMany, some.size() - i)), ragged, s)))
+        return st;
+  }
   return KFAC_OK;
 }
 

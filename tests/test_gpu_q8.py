@@ -659,3 +659,57 @@ def test_factor_of_a_scale_that_is_none(kfac_gpu, rows, cols):
         s[:] = 0
         s[rows - 3] = bad
         assert np.isnan(host(factors(kfac_gpu, [(q, s)], True)[0])).all()
+
+
+def far_copy(q, apart):
+    """The same rows, `apart` bytes from each other."""
+    wide = torch.empty((len(q) - 1) * apart + 4096, dtype=torch.int8, device="cuda")
+    far = wide.as_strided(q.shape, (apart, 1))
+    far.copy_(q)
+    return far
+
+
+@pytest.mark.parametrize("rows, cols", [(1, 1), (5, 7), (64, 15), (700, 3), (3000, 8), (9000, 15), (100352, 2), (40000, 12)])
+@pytest.mark.parametrize("bias", [True, False])
+def test_factor_of_few_columns(kfac_gpu, rows, cols, bias):
+    """No row is lost for its size: the last column has entries in rows alone that are 2^-40 of the others."""
+    q = codes(rows, rows, cols, pad=1)
+    s = torch.exp2(-(torch.arange(rows) % 5).float()).cuda()
+    if rows > 2:
+        small = torch.arange(rows, device="cuda") % 3 == 1
+        s[small] *= 2.0 ** -40
+        q[~small, -1] = 0
+        s[2] = 0.0
+    want, size = qo.factor_packed(host(q), host(s), bias)
+    first = factors(kfac_gpu, [(q, s)], bias, full=True)[0]
+    # 10 scales' exact sums a block, 128 blocks at most, the mean: each rounds once or twice
+    assert (np.abs(host64(first) - want) <= (10 + 128 + 8) * 2 * U * size).all()
+    assert torch.equal(factors(kfac_gpu, [(q, s)], bias)[0], first)
+    several = factors(kfac_gpu, [(q, s)] * 3 + [(codes(1, 30, 40), torch.ones(30, device="cuda"))], bias)
+    assert all(torch.equal(several[k], first) for k in range(3))
+    old = [torch.rand_like(first)]
+    got = factors(kfac_gpu, [(q, s)], bias, full=True, decay=0.75, start=old)[0]
+    want, size = qo.factor_packed(host(q), host(s), bias, host64(old[0]), 0.75)
+    assert (np.abs(host64(got) - want) <= (10 + 128 + 12) * 2 * U * size).all()
+    for bad in (1.5, float("nan"), float("inf"), -1.0, 2.0 ** -130):
+        t = s.clone()
+        t[rows // 2] = bad
+        assert np.isnan(host(factors(kfac_gpu, [(q, t)], bias)[0])).all()
+
+
+@pytest.mark.parametrize("cols", [5, 40, 203])
+def test_factor_of_rows_far_apart(kfac_gpu, cols):
+    """The same bits as those of the rows close to each other, also over scales that are far from each other."""
+    close = codes(2, 5, cols)
+    far = far_copy(close, 2 ** 32 + 1)
+    for s in ([1.0, 2.0, 4.0, 0.0, 1.0], [1.0, 2.0 ** -60, 2.0 ** 30, 2.0 ** -60, 0.5], [1.0, 2.0 ** -130, 1.0, 1.0, 1.0],
+              [float("inf")] + [1.0] * 4):
+        s = torch.tensor(s, device="cuda")
+        for bias in (True, False):
+            a, b = (host(factors(kfac_gpu, [(q, s)], bias, full=True)[0]) for q in (close, far))
+            assert same(a, b)
+            if (s == 2.0 ** -60).any():
+                want, size = qo.factor_packed(host(close), host(s), bias)
+                assert (np.abs(a - want) <= 12 * 2 * U * size).all()
+            else:
+                assert np.isnan(a).all() == (not torch.isfinite(s).all() or bool((s == 2.0 ** -130).any()))
