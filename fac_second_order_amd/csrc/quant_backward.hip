@@ -316,9 +316,10 @@ static double plan(TnJob& j, bool factor, kfac_dtype dtype, bool near, double sh
   return best;
 }
 
+// A factor's sums need room beside the splits' parts: where they leave 32 bits, which one row's cannot.
 static void carve(TnJob& j, bool factor, Carver& cv) {
   const int T = tile_edge(j);
-  if (j.splits > 1 || (factor && j.f)) j.part = cv.take<float>(size_t(j.splits) * j.tiles * T * T);
+  if (j.splits > 1 || (factor && j.rows > 1)) j.part = cv.take<float>(size_t(j.splits) * j.tiles * T * T);
   if (j.splits == 1 && (!j.f || j.solo)) return;
   j.part_col = cv.take<float>(size_t(j.splits) * j.shares * j.mt * T);
   j.part_rows = cv.take<int32_t>(j.splits);
@@ -461,12 +462,24 @@ static kfac_status factor_jobs(int32_t count, const int32_t* rows, const int32_t
   return KFAC_OK;
 }
 
-// A layer's workspace, whichever of its jobs it turns out to have.
-static size_t factor_bytes(TnJob near, TnJob far) {
-  Carver one, other;
-  carve(near, true, one);
-  carve(far, true, other);
-  return std::max(one.used, other.used);
+static size_t bytes_of(TnJob j) {
+  Carver cv;
+  carve(j, true, cv);
+  return cv.used;
+}
+
+// Layers run side by side as long as their parts and sums fit here, and in launches one after another, which use the
+// same room, where they do not: such layers fill the card each.
+constexpr size_t kRoom = size_t(128) << 20;
+
+// The workspace of a call, whichever of its jobs each layer turns out to have.
+static size_t factors_room(const std::vector<TnJob>& near, const std::vector<TnJob>& far) {
+  size_t all = 0, largest = 0;
+  for (size_t i = 0; i < near.size(); ++i) {
+    const size_t one = std::max(bytes_of(near[i]), bytes_of(far[i]));
+    all += one, largest = std::max(largest, one);
+  }
+  return std::max(largest, std::min(all, kRoom));
 }
 
 extern "C" kfac_status kfac_factors_q8_workspace(int32_t count, const int32_t* rows, const int32_t* cols,
@@ -476,9 +489,7 @@ extern "C" kfac_status kfac_factors_q8_workspace(int32_t count, const int32_t* r
     std::vector<TnJob> near, far;
     kfac_status st = factor_jobs(count, rows, cols, bias, near, far);
     if (st) return st;
-    size_t need = 0;
-    for (int i = 0; i < count; ++i) need += factor_bytes(near[i], far[i]);
-    *bytes = need;
+    *bytes = factors_room(near, far);
     return KFAC_OK;
   });
 }
@@ -492,13 +503,9 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
   std::vector<TnJob> jobs, far;
   kfac_status st = factor_jobs(count, rows, cols, bias, jobs, far);
   if (st) return st;
-  std::vector<size_t> bytes;
-  size_t need = 0;
-  for (int i = 0; i < count; ++i) {
-    bytes.push_back(factor_bytes(jobs[i], far[i]));
-    need += bytes[i];
+  const size_t need = factors_room(jobs, far);
+  for (int i = 0; i < count; ++i)
     if (rows[i] > 1 && ld_q[i] >= (int64_t(1) << 32)) jobs[i] = far[i];
-  }
   std::vector<RowsOf> all = {scratch(workspace, need)};
   for (int i = 0; i < count; ++i) {
     const int64_t d = cols[i] + bias[i];
@@ -518,16 +525,12 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
   if ((st = check_apart(each.data(), static_cast<int>(each.size()), written))) return st;
   if ((st = check_device())) return st;
   if ((st = check_workspace(workspace, ws_bytes, need))) return st;
-  char* here = static_cast<char*>(workspace);
   for (int i = 0; i < count; ++i) {
     TnJob& j = jobs[i];
-    Carver cv(here);
-    carve(j, true, cv);
-    here += bytes[i];
     j.q = q[i], j.scale = scale[i], j.ldq = ld_q[i], j.out = A_packed[i], j.full = A_full ? A_full[i] : nullptr;
     j.decay = ema_decay;
   }
-  // a launch for the layers of one kind
+  // a launch for the layers of one kind, or several
   std::vector<TnJob> some;
   for (int kind = 0; kind < 7; ++kind) {
     const int f = 3 - kind / 2, any = kind == 6;
@@ -535,9 +538,12 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
     some.clear();
     for (const TnJob& j : jobs)
       if (any ? j.any : !j.any && j.f == f && bool(j.m & 15) == ragged) some.push_back(j);
-    for (size_t i = 0; i < some.size(); i += kTnMany)
-      if ((st = launch_jobs<_Float16, true>(&some[i], static_cast<int>(std::min<size_t>(kTnMany, some.size() - i)), ragged, s)))
-        return st;
+    for (size_t i = 0, n; i < some.size(); i += n) {
+      Carver cv(workspace);
+      for (n = 0; n < kTnMany && i + n < some.size() && (n == 0 || cv.used + bytes_of(some[i + n]) <= kRoom); ++n)
+        carve(some[i + n], true, cv);
+      if ((st = launch_jobs<_Float16, true>(&some[i], static_cast<int>(n), ragged, s))) return st;
+    }
   }
   return KFAC_OK;
 }

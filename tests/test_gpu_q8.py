@@ -713,3 +713,23 @@ def test_factor_of_rows_far_apart(kfac_gpu, cols):
                 assert (np.abs(a - want) <= 12 * 2 * U * size).all()
             else:
                 assert np.isnan(a).all() == (not torch.isfinite(s).all() or bool((s == 2.0 ** -130).any()))
+
+
+def test_factors_of_wide_layers(kfac_gpu):
+    """Layers whose sums take more room than a call has run one after another; scales that do not fit together."""
+    rows, cols = 9, 7920
+    q = codes(rows, rows, cols)
+    s = torch.exp2(torch.tensor([0.0, -30, -60, -1, 0, -2, -90, -30, 5])).cuda()
+    narrow = (codes(2, 300, 70, most=9), scales_of(3, 300))
+    need = kfac_gpu.kfac_factors_q8_workspace([rows] * 4 + [300], [cols] * 4 + [70], True)
+    ws = torch.full((need + 256 + 4096,), 9, dtype=torch.uint8, device="cuda")
+    at = -ws.data_ptr() % 256
+    got = factors(kfac_gpu, [(q, s)] * 4 + [narrow], True, workspace=ws[at:at + need])
+    assert (ws[at + need:] == 9).all()
+    assert all(torch.equal(got[0], p) for p in got[1:4])
+    a = torch.cat([q.double() * s.double()[:, None], torch.ones(rows, 1, device="cuda", dtype=torch.float64)], 1)
+    i, j = torch.triu_indices(cols + 1, cols + 1, device="cuda")
+    want, size = (t.T.contiguous() @ t / rows for t in (a, a.abs()))
+    assert bool(((got[0].double() - want[i, j]).abs() <= (rows + 8) * 2 * U * size[i, j]).all())
+    want, size = qo.factor_packed(host(narrow[0]), host(narrow[1]), True)
+    assert (np.abs(host64(got[4]) - want) <= 3 * U * size).all()

@@ -229,3 +229,17 @@ def test_products_of_more_tiles_than_a_launch_takes(lib):
     assert so.kfac_linear_q8_workspace((1 << 20) - 256, 8, 1 << 20, c.byref(sz)) == 0
     assert so.kfac_linear_q8_workspace((1 << 31) - 1, 8, (1 << 31) - 1, c.byref(sz)) == -2
     assert so.kfac_linear_q8_workspace((1 << 31) - 1, 8, 1, c.byref(sz)) == 0
+
+
+def test_workspace_of_factors(lib):
+    """It does not grow with the layers, and one row needs none."""
+    L = lib
+    assert L.kfac_factors_q8_workspace([1], [8192], True) == 0
+    one = L.kfac_factors_q8_workspace([7], [7920], True)
+    assert 0 < one < 160 << 20
+    assert one <= L.kfac_factors_q8_workspace([7] * 5, [7920, 7904, 7888, 7872, 7856], True) < 160 << 20
+    small = L.kfac_factors_q8_workspace([300], [64], True)
+    assert 0 < small < 1 << 20
+    assert L.kfac_factors_q8_workspace([300] * 7, [64] * 7, True) <= 7 * (1 << 20)
+    for rows, cols, n in [(100, 8192, 3), (2048, 8192, 5), (32768, 64, 100), (8192, 4096, 40), (32768, 1000, 9), (5, 12, 64)]:
+        assert L.kfac_factors_q8_workspace([rows] * n, [cols] * n, True) <= 256 << 20
