@@ -749,7 +749,8 @@ def kfac_factors_q8_workspace(rows, cols, bias):
 
 def kfac_factors_q8(q, scale, A_packed, A_full=None, bias=False, ema_decay=0.0, workspace=None, stream=None):
     """A_packed[l] <- packed factor of layer l from its checkpoint q[l], scale[l], with bias (one
-    for all layers, or a list) the column of ones; A_full[l] as in kfac_factors_full (see kfac.h)."""
+    for all layers, or a list) the column of ones; A_full[l] as in kfac_factors_full. A layer whose
+    A_packed[l] is None is left out, and has its share in the plan (see kfac.h)."""
     n = len(q)
     if len(scale) != n or len(A_packed) != n or (A_full is not None and len(A_full) != n):
         raise ValueError("q, scale, A_packed and A_full need one entry for each layer")
@@ -759,7 +760,8 @@ def kfac_factors_q8(q, scale, A_packed, A_full=None, bias=False, ema_decay=0.0, 
         return
     rows, cols, q_at, q_ld, s_at = map(list, zip(*map(_checkpoint, q, scale)))
     orders = [c + b for c, b in zip(cols, bias)]
-    p_at = [_vector(p, torch.float32, d * (d + 1) // 2, "A_packed") for p, d in zip(A_packed, orders)]
+    p_at = [0 if p is None else _vector(p, torch.float32, d * (d + 1) // 2, "A_packed") for p, d in zip(A_packed, orders)]
+    q_at, s_at = ([a if p else 0 for a, p in zip(at, p_at)] for at in (q_at, s_at))
     f_at = [0 if f is None else _vector(f, torch.float32, d * d, "A_full") for f, d in zip(full, orders)]
     raw = _stream_of(stream, (*q, *scale, *A_packed, *full, workspace))
     ws, wsb, held = _scratch(workspace, kfac_factors_q8_workspace, (rows, cols, bias), q[0], stream)

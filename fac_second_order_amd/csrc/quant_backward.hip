@@ -506,14 +506,17 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
   const size_t need = factors_room(jobs, far);
   for (int i = 0; i < count; ++i)
     if (rows[i] > 1 && ld_q[i] >= (int64_t(1) << 32)) jobs[i] = far[i];
+  auto left_out = [&](int i) { return !q[i] && !scale[i] && !A_packed[i]; };
   std::vector<RowsOf> all = {scratch(workspace, need)};
   for (int i = 0; i < count; ++i) {
+    if (left_out(i)) continue;
     const int64_t d = cols[i] + bias[i];
     all.push_back({A_packed[i], 1, d * (d + 1) / 2, 0, 4, "A_packed"});
     if (A_full && A_full[i]) all.push_back({A_full[i], 1, d * d, 0, 4, "A_full"});
   }
   const int written = static_cast<int>(all.size());
   for (int i = 0; i < count; ++i) {
+    if (left_out(i)) continue;
     all.push_back({q[i], rows[i], cols[i], ld_q[i], 1, "q"});
     all.push_back({scale[i], rows[i], 1, 1, 4, "scale"});
   }
@@ -534,6 +537,7 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
   // two launches 41
   if (std::any_of(jobs.begin(), jobs.end(), [](const TnJob& j) { return j.any; }))
     for (TnJob& j : jobs) j.any = j.f == 1;
+  jobs.erase(std::remove_if(jobs.begin(), jobs.end(), [](const TnJob& j) { return !j.out; }), jobs.end());
   // a launch for the layers of one kind, or several
   std::vector<TnJob> some;
   for (int kind = 0; kind < 7; ++kind) {

@@ -165,21 +165,24 @@ class KfacStep:
         return self.full[len(self.layers):]
 
     def factors(self, act, gout, ema_decay=0.0, stream=None):
-        act = self._factors_of_checkpoints(self.layers, act, None, ema_decay, stream)
+        act = self._factors_of_checkpoints(self.layers, act, act, None, ema_decay, stream)
         if any(t is not None for t in (*act, *gout)):
             K.kfac_factors(self.layers, act, gout, self.A_packed, self.G_packed, ema_decay,
                            self.workspace, stream)
 
-    def _factors_of_checkpoints(self, layers, act, full, ema_decay, stream):
-        """Forms the factors of the layers whose act is a Checkpoint; act without those."""
-        at = [l for l, a in enumerate(act) if isinstance(a, Checkpoint)]
-        if not at:
+    def _factors_of_checkpoints(self, layers, act, every, full, ema_decay, stream):
+        """Forms the factors of the layers whose act is a Checkpoint; act without those. `every`: the step's, of which
+        act may be a part."""
+        if not any(isinstance(a, Checkpoint) for a in act):
             return act
-        held = [act[l] for l in at]
+        at = [l for l, a in enumerate(every) if isinstance(a, Checkpoint)]
+        held = [every[l] for l in at]
         rows, cols, bias = [len(a) for a in held], [a.shape[1] for a in held], [layers[l].bias for l in at]
         self._room(K.kfac_factors_q8_workspace(rows, cols, bias), stream)
-        K.kfac_factors_q8([a.q for a in held], [a.scale for a in held], [self.A_packed[l] for l in at],
-                          None if full is None else [full[l] for l in at], bias, ema_decay, self.workspace, stream)
+        K.kfac_factors_q8([a.q for a in held], [a.scale for a in held],
+                          [self.A_packed[l] if act[l] is not None else None for l in at],
+                          None if full is None else [full[l] if act[l] is not None else None for l in at], bias, ema_decay,
+                          self.workspace, stream)
         return [None if isinstance(a, Checkpoint) else a for a in act]
 
     @staticmethod
@@ -203,11 +206,11 @@ class KfacStep:
             with torch.cuda.stream(on):
                 self.workspace = torch.empty(need + 256, dtype=torch.uint8, device=self.device)
 
-    def _factors_full(self, layers, act, gout, ema_decay, stream):
+    def _factors_full(self, layers, act, every, gout, ema_decay, stream):
         # the packed factors (the stored state) and the upper triangles that kfac_invert
         # reads, from the same kernels: no separate unpack pass
         L = len(self.layers)
-        act = self._factors_of_checkpoints(layers, act, self.full[:L], ema_decay, stream)
+        act = self._factors_of_checkpoints(layers, act, every, self.full[:L], ema_decay, stream)
         if all(t is None for t in (*act, *gout)):
             return
         K.kfac_factors_full(layers, act, gout, self.A_packed, self.G_packed, self.full[:L], self.full[L:],
@@ -382,7 +385,7 @@ class KfacStep:
             self._bn(all_bn, bn_layers, xhat, bn_gout, 1.0, bn_params, lr, stream)
             return
         if not self.side:
-            self._factors_full(layers, act, gout, ema_decay, stream)
+            self._factors_full(layers, act, act, gout, ema_decay, stream)
             self._invert(self.main, self._info_main, self.workspace, stream)
             self._refine(stream)
             self.precondition(grads, weights, lr, stream)
@@ -394,7 +397,7 @@ class KfacStep:
         # factors are formed (a factor call plans its row splits over every layer,
         # whichever inputs it is given: the same bits as one call)
         first, rest = self._factor_inputs(act, gout)
-        self._factors_full(layers, first[0], first[1], ema_decay, main)
+        self._factors_full(layers, first[0], act, first[1], ema_decay, main)
         formed = torch.cuda.Event()
         formed.record(main)
         side.wait_event(formed)
@@ -403,7 +406,7 @@ class KfacStep:
             lay = [l for l in range(len(self.layers)) if rest[0][l] is not None or rest[1][l] is not None]
             for part in self._groups(lay, self._factor_cost, self.MAIN_CALLS["factors"]):
                 ps = set(part)
-                self._factors_full(layers, [a if l in ps else None for l, a in enumerate(rest[0])],
+                self._factors_full(layers, [a if l in ps else None for l, a in enumerate(rest[0])], act,
                                    [g if l in ps else None for l, g in enumerate(rest[1])], ema_decay,
                                    main)
             self._invert(self.main, self._info_main, self.workspace, main)

@@ -479,7 +479,9 @@ kfac_status kfac_weight_grad_q8(int32_t rows, int32_t c_in, int32_t c_out, kfac_
  * written like kfac_factors_full's: packed, and where A_full (NULL, or an entry of it NULL) is
  * given into the upper triangle of a full matrix too; ema_decay as there. A layer without a row
  * that counts keeps its stored factor, or gets zeros with ema_decay = 0. Host arrays: rows,
- * cols, bias, q, ld_q, scale, A_packed, A_full. Scales are those of kfac_quantize_rows with
+ * cols, bias, q, ld_q, scale, A_packed, A_full. A layer whose q, scale and A_packed are NULL is left
+ * out: its sizes and pitch take part in the plan alone, so that several calls over the same layers
+ * give the bits of one. Scales are those of kfac_quantize_rows with
  * pow2 = 1; a layer with one that is neither 0 nor a power of two from 2^-126 on gets a factor
  * of NaN. Rows of one scale add up exactly, so that no row is lost for its size, and the
  * fp32 sums are those of a few additions however many rows there are. Deterministic.

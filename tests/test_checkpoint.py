@@ -191,3 +191,18 @@ def test_input_by_name():
     with torch.no_grad():
         assert torch.equal(net.a(input=x), torch.nn.functional.linear(x, net.a.weight, net.a.bias))
     cap.remove()
+
+
+def test_parts_of_a_step_plan_for_all_of_it(monkeypatch):
+    calls = Calls(monkeypatch)
+    st = step_mod.KfacStep([layer(5, 3, 4), layer(5, 4, 2, bias=0), layer(5, 2, 2)], device="cpu")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: None)
+    act, none = [held(5, 3), torch.zeros(5, 4), held(5, 2, 7)], [None] * 3
+    st._factors_full(st.layers, [act[0], None, None], act, none, 0.5, None)
+    (q, s, packed, full, *_), = calls.q8
+    assert [t.data_ptr() for t in q] == [act[0].q.data_ptr(), act[2].q.data_ptr()]
+    assert packed[0] is st.A_packed[0] and packed[1] is None and full[0] is st.full[0] and full[1] is None
+    calls.q8.clear()
+    st._factors_full(st.layers, [None, act[1], None], act, none, 0.5, None)
+    assert not calls.q8 and len(calls.plain) == 1

@@ -290,3 +290,26 @@ def test_workspace_guard(kfac_gpu):
     kfac_gpu.kfac_weight_grad_q8(c.gout, c.q, c.s, c.dw[:, :520], dbias=c.dw[:, 520], workspace=big[at:at + need])
     torch.cuda.synchronize()
     assert (big[at + need:] == 9).all() and (big[:at] == 9).all()
+
+
+@pytest.mark.parametrize("sizes, rows", [([600, 1100, 700, 40], 3000), ([40, 1500, 9, 520, 64], 700)])
+def test_two_streams_give_the_bits_of_one(kfac_gpu, sizes, rows):
+    """Factors of checkpoints that are formed in several calls, over scales that do not fit into 32 bits."""
+    from fac_second_order_amd.capture import KfacCapture
+    from fac_second_order_amd.step import KfacStep
+    torch.manual_seed(6)
+    net = Mlp(sizes).cuda()
+    cap = KfacCapture(net, damping=0.1, checkpoint="int8")
+    x = torch.randn(rows, sizes[0], device="cuda") * torch.exp2(-(torch.arange(rows, device="cuda") % 23).float())[:, None]
+    torch.nn.functional.cross_entropy(net(x), torch.randint(0, sizes[-1], (rows,), device="cuda")).backward()
+    layers, _ = cap._geometry()
+    grads = [cap._to_matrix(m, grad=True) for m in net.layers]
+    steps = [KfacStep(layers, (), "cuda", damping=0.1, side_stream=side) for side in (True, False)]
+    assert steps[0].side and not steps[1].side
+    for turn in range(2):
+        for st in steps:
+            st.step(cap.act, cap.gout, grads, ema_decay=0.5 * turn)
+        torch.cuda.synchronize()
+        for a, b in zip(*([*st.A_packed, *st.G_packed, *st.out] for st in steps)):
+            assert torch.equal(a, b)
+    cap.remove()

@@ -243,3 +243,16 @@ def test_workspace_of_factors(lib):
     assert L.kfac_factors_q8_workspace([300] * 7, [64] * 7, True) <= 7 * (1 << 20)
     for rows, cols, n in [(100, 8192, 3), (2048, 8192, 5), (32768, 64, 100), (8192, 4096, 40), (32768, 1000, 9), (5, 12, 64)]:
         assert L.kfac_factors_q8_workspace([rows] * n, [cols] * n, True) <= 256 << 20
+
+
+def test_factors_that_are_left_out(lib):
+    """All of a layer's arrays are NULL, or none; what is left out is not looked at."""
+    so = lib._lib
+    past = factors(so)
+    two = dict(rows=(4, 4), cols=(8, 8), bias=(0, 1), ld=(8, 0))
+    assert factors(so, q=(A, None), s=(B, None), A_packed=(C, None), **two) == past
+    assert factors(so, q=(None,), s=(None,), A_packed=(None,)) == past
+    for k, v in (("q", A), ("s", B), ("A_packed", C)):
+        assert factors(so, **{**dict(q=(None,), s=(None,), A_packed=(None,)), k: (v,)}) == -1
+    with pytest.raises(ValueError):    # in the binding too: then a device is asked for
+        lib.kfac_factors_q8([rows(4, 8, I8)], [torch.zeros(4)], [None])
