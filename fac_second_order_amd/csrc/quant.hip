@@ -755,10 +755,12 @@ extern "C" kfac_status kfac_linear_q8(int32_t rows, int32_t c_in, int32_t c_out,
   return with_row_type(dtype, [&](auto tag) {
     using T = decltype(tag);
     const LinearArgs args = {rows, c_in, c_out, q, w, scale, w_scale, bias, y, ld_q, ld_w, ld_y};
-    // few rows: 32 x 4096 x 4096 bf16 11.0 us (in tiles 13.4), 32 x 8192 x 1024 16.0 (21.7); short sums gain
-    // nothing (17 x 1024 x 8192 11.2, in tiles 7.4, the call's 13.2 and 13.5 being the host's). Fused with the quantising:
-    // 1 x 4096 x 4096 8.5, else 6.4 + 7.5, 16 x 1024 x 4096 9.8, else 7.0 + 6.5: a launch less, 3 us a call
-    const bool few = rows <= kFewRows && c_out > 0 && c_out <= kFewChannels;
+    // Few rows, kernels by themselves, codes given, in us, in tiles in brackets: 1 x 4096 x 4096 bf16 5.9 (11.4), 16 x 1024 x
+    // 4096 4.5 (5.0), 16 x 512 x 8192 4.5 (3.9). More than 16 rows: 32 x 4096 x 4096 9.1 (11.6), 17 x 2048 x 4096 6.3 (7.6), but
+    // 17 x 1024 x 4096 5.4 (5.0), and with more channels than the card takes blocks for at a time, 17 x 1024 x 8192 9.4 (5.6),
+    // 32 x 8192 x 8192 28.0 (21.0). Fused with the quantising, the whole call: 1 x 4096 x 4096 8.5, else 6.4 + 7.5, 16 x 1024 x
+    // 4096 9.8, else 7.0 + 6.5: a launch less, 3 us a call
+    const bool few = c_out > 0 && (rows <= 16 ? c_out <= kFewChannels : rows <= kFewRows && c_in > 1024 && c_out <= 4096);
     const bool fused = few && x && rows <= 16 && int64_t(rows) * c_in <= kFusedCodes;
     if (x && !fused) {
       kfac_status e = launch_quantize<T, true>(rows, c_in, x, ld_x, mask, q, ld_q, scale, s);

@@ -733,3 +733,10 @@ def test_factors_of_wide_layers(kfac_gpu):
     assert bool(((got[0].double() - want[i, j]).abs() <= (rows + 8) * 2 * U * size[i, j]).all())
     want, size = qo.factor_packed(host(narrow[0]), host(narrow[1]), True)
     assert (np.abs(host64(got[4]) - want) <= 3 * U * size).all()
+
+
+@pytest.mark.parametrize("rows,c_in,c_out", [(16, 600, 4097), (17, 1024, 4096), (17, 1025, 4096), (32, 1100, 4097), (33, 1025, 100),
+                                             (20, 2000, 64), (32, 1030, 4090), (18, 40, 8200)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_linear_next_to_few_rows(kfac_gpu, dtype, rows, c_in, c_out):
+    test_linear(kfac_gpu, dtype, rows, c_in, c_out)
