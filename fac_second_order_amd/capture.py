@@ -223,8 +223,9 @@ class KfacCapture:
         for i, (m, _) in enumerate(self.pairs):
             if checkpoint and isinstance(m, nn.Linear) and type(m).forward is nn.Linear.forward:
                 before = m.__dict__.get("forward")
+                plain = getattr(m.forward, "__func__", None) is nn.Linear.forward and m.forward.__self__ is m
                 self.wrapped.append((m, before))
-                m.forward = _Taken(m, before, self._checkpointed(i, m) if before is None else before)
+                m.forward = _Taken(m, before, self._checkpointed(i, m) if plain else before)
             self.hooks.append(m.register_forward_hook(self._fwd(i)))
             self.hooks.append(m.register_full_backward_hook(self._bwd(i)))
         for i, bn in enumerate(self.bns):

@@ -206,3 +206,16 @@ def test_parts_of_a_step_plan_for_all_of_it(monkeypatch):
     calls.q8.clear()
     st._factors_full(st.layers, [None, act[1], None], act, none, 0.5, None)
     assert not calls.q8 and len(calls.plain) == 1
+
+
+def test_a_copy_is_captured_like_its_original():
+    import copy
+    net = Net()
+    cap = cap_mod.KfacCapture(net, checkpoint="int8")
+    twin = copy.deepcopy(net)
+    cap.remove()
+    cap = cap_mod.KfacCapture(twin, checkpoint="int8")
+    with pytest.raises(ValueError):     # its layers keep their inputs in 8 bits: on a GPU
+        twin.a(torch.ones(2, 5))
+    cap.remove()
+    assert torch.equal(twin(torch.ones(2, 5)), net(torch.ones(2, 5)))
