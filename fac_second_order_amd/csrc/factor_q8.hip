@@ -118,7 +118,7 @@ struct Raw16 {
   __device__ inline void load(const KG char* p) {
     w = __builtin_bit_cast(v4u, load_pack<false, int8_t>(reinterpret_cast<const KG int8_t*>(p)));
   }
-  __device__ inline v4u codes(int) const { return w; }
+  __device__ inline v4u codes(int, int) const { return w; }
   __device__ inline void shift(int k) {  // drops the first k
     uint64_t lo = uint64_t(w[1]) << 32 | w[0], hi = uint64_t(w[3]) << 32 | w[2];
     const int b = 8 * (k & 7);
@@ -130,6 +130,7 @@ struct Raw16 {
 };
 
 // The first n of 16 codes, 0 <= n <= 16, and zeros, by loads from both ends that may overlap: nothing behind them is read.
+// In rows of fewer than 16 columns, `row` of them and not 0, n is that or 0, and what is to be done the same for all lanes.
 struct Raw16Some {
   uint64_t a, b;
   unsigned c;
@@ -140,24 +141,29 @@ struct Raw16Some {
     __builtin_memcpy(&w, &v, N);
     return w;
   }
-  __device__ inline void load(const KG char* p, int n) {
-    a = 0, b = 0, c = 0;
+  __device__ inline void load_n(const KG char* p, int n) {
     if (n >= 8) a = bytes<8>(p), b = bytes<8>(p + n - 8);
     else if (n >= 4) a = bytes<4>(p), b = bytes<4>(p + n - 4);
     else if (n > 0) a = uint8_t(p[0]), b = uint8_t(p[n / 2]), c = uint8_t(p[n - 1]);
   }
-  __device__ inline v4u codes(int n) const {
+  __device__ inline v4u codes_n(int n) const {
     uint64_t lo = a, hi = 0;
     if (n > 8) hi = b >> (8 * (16 - n));
     else if (n >= 4) lo |= n < 8 ? b << (8 * (n - 4)) : 0;
     else if (n > 0) lo |= b << (8 * (n / 2)) | uint64_t(c) << (8 * (n - 1));
     return v4u{unsigned(lo), unsigned(lo >> 32), unsigned(hi), unsigned(hi >> 32)};
   }
+  __device__ inline void load(const KG char* p, int n, int row) {
+    a = 0, b = 0, c = 0;
+    if (!row) load_n(p, n);
+    else if (n) load_n(p, row);
+  }
+  __device__ inline v4u codes(int n, int row) const { return row ? codes_n(row) : codes_n(n); }
 };
 
 // COLS: how the columns are read. kWhole: in groups of 16; kRagged: the last group of a row shifted; kAny, in tiles
 // of 64: as many of a group as there are, for rows of fewer than 16 columns or 2^32 bytes and more apart (100352 x 8:
-// 31 us, 1000 x 12: 17, a row of one 10.4).
+// 28 us, 1000 x 12: 16; a row of one 8.4 by itself, of 16 in one group 7.1: the loads' cases).
 enum { kWhole, kRagged, kAny };
 
 template <int F, int COLS>
@@ -178,6 +184,7 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
   const int r_count = static_cast<int>(min(int64_t(d.per_split), d.rows - r_begin));
   char* const abuf = lds;
   char* const bbuf = lds + BUFS * L::OPERAND;
+  const bool same = COLS == kAny && ti == tj;  // one operand is both
 
   // this thread's groups of 16 columns: row of a step, place in its line, offset in its rows, codes to shift out (kAny:
   // columns that there are)
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
   for (int i = 0; i < F; ++i) {
     auto place = [&](int c) { return kk * T + 16 * (((c + cc) >> 4) ^ L::moved(kk)) + (cc & 15); };
     fa_at[i] = abuf + place(wm + 32 * i);
-    fb_at[i] = bbuf + place(wn + 32 * i);
+    fb_at[i] = (same ? abuf : bbuf) + place(wn + 32 * i);
   }
   typedef int v2i __attribute__((ext_vector_type(2)));
   typedef v2i __attribute__((address_space(3))) lds_v2i;
@@ -239,6 +246,7 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     return v4i{lo[0], lo[1], hi[0], hi[1]};
   };
   KG float* const part = uniform(gp(d.part) + (int64_t(split) * d.tiles + tile) * (T * T));
+  const int narrow = COLS == kAny && d.m < 16 ? d.m : 0;
   bool flushed = false, bad = false;
   int counted = 0;
   const int steps = sort_rows<F>(d.scale, r_begin, r_count, list, counted, bad);
@@ -315,8 +323,8 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
       const int i = k / 2;
       const KG char* from = q0 + uint64_t(unsigned(r[i])) * pitch;
       if constexpr (COLS == kAny) {
-        if (k & 1) araw[set][i].load(from + a_col[i], a_cut[i]);
-        else braw[set][i].load(from + b_col[i], b_cut[i]);
+        if (k & 1) araw[set][i].load(from + a_col[i], a_cut[i], narrow);
+        else if (!same) braw[set][i].load(from + b_col[i], b_cut[i], narrow);
       } else {
         if (k & 1) araw[set][i].load(from + a_col[i]);
         else braw[set][i].load(from + b_col[i]);
@@ -324,10 +332,11 @@ __global__ void __launch_bounds__(256, F == 3 ? 1 : 2) factor_q8_kernel(TnArgs<t
     };
     auto place = [&](auto set, auto buf, int k) {
       const int i = k / 2;
+      if (same && !(k & 1)) return;
       Raw& x = k & 1 ? araw[set][i] : braw[set][i];
       if constexpr (RAGGED)
         if (cuts) x.shift(k & 1 ? a_cut[i] : b_cut[i]);
-      *reinterpret_cast<v4u*>((k & 1 ? abuf : bbuf) + buf * L::OPERAND + at[i]) = x.codes(k & 1 ? a_cut[i] : b_cut[i]) & some[set][i];
+      *reinterpret_cast<v4u*>((k & 1 ? abuf : bbuf) + buf * L::OPERAND + at[i]) = x.codes(k & 1 ? a_cut[i] : b_cut[i], narrow) & some[set][i];
     };
     v4i fa[2][F], fb[2][F];
     constexpr int R = 2 * F, MN = F * F;

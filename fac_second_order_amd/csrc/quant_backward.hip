@@ -533,8 +533,8 @@ static kfac_status factors_impl(int32_t count, const int32_t* rows, const int32_
     j.q = q[i], j.scale = scale[i], j.ldq = ld_q[i], j.out = A_packed[i], j.full = A_full ? A_full[i] : nullptr;
     j.decay = ema_decay;
   }
-  // layers in tiles of 64 go with those of few columns, if there are any: 4 of 20000 x 64 and one of 20000 x 8 25 us, in
-  // two launches 41
+  // layers in tiles of 64 go with those of few columns, if there are any: 4 of 20000 x 64 and one of 20000 x 8 24 us, in
+  // two launches 40
   if (std::any_of(jobs.begin(), jobs.end(), [](const TnJob& j) { return j.any; }))
     for (TnJob& j : jobs) j.any = j.f == 1;
   jobs.erase(std::remove_if(jobs.begin(), jobs.end(), [](const TnJob& j) { return !j.out; }), jobs.end());
