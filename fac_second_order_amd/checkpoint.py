@@ -3,7 +3,8 @@
 K-FAC needs a fully connected layer's input twice after the forward pass (Osawa et al., CVPR
 2019, eq. 5 and 7): for the weight gradient g^T a that is preconditioned, and for the factor
 A = E[a a^T]. A Checkpoint holds it as whole numbers of 8 bits with a power of two for each
-row, half the memory of fp16; autograd and the step share it. Its values are what both
+row, half the memory of fp16; autograd and the step share it (what made the input may keep it
+for a backward pass of its own, as a ReLU does). Its values are what both
 are formed from (kfac_weight_grad_q8, kfac_factors_q8): s q is exact in 16 bits, so neither
 rounds anything further. Every number is computed by libkfac; there is no CPU path.
 """

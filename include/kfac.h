@@ -463,7 +463,8 @@ kfac_status kfac_linear_q8(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype
  * ld_dw = inc_db = c_in + 1 and dbias = dweight + c_in the matrix that kfac_precondition reads.
  * accumulate = 1 adds to what they hold. With scales that are powers of two the products are
  * exact (fp16: those of rows whose scale is at least 2^-29 of the largest) and summed in fp32;
- * with others scale * q is rounded to 16 bits first. Deterministic.
+ * with others scale * q is rounded to 16 bits first (fp16: the scale, then the product). dbias takes
+ * nothing of a row but its gradient: a scale of NaN does not show there. Deterministic.
  * ------------------------------------------------------------------------- */
 kfac_status kfac_weight_grad_q8_workspace(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype, size_t* bytes);
 kfac_status kfac_weight_grad_q8(int32_t rows, int32_t c_in, int32_t c_out, kfac_dtype dtype, const void* gout,
