@@ -26,6 +26,7 @@ Layout conventions (the library's):
 """
 import copy
 import math
+import threading
 import types
 from dataclasses import dataclass
 
@@ -148,9 +149,20 @@ class _Taken:
 
     def __init__(self, layer, before, run):
         self.layer, self.before, self.run = layer, before, run
+        self.calling = threading.local()
+
+    def note(self):
+        """A pre-hook of the layer: whose forward is about to be called. A shallow copy (a replica) has this very one."""
+        def hook(mod, args):
+            if mod.__dict__.get("forward") is self:
+                self.calling.layer = mod
+        return hook
 
     def __call__(self, *args, **kwargs):
-        return self.run(*args, **kwargs)
+        layer, self.calling.layer = getattr(self.calling, "layer", None), None
+        if layer is None or layer is self.layer or self.before is not None:
+            return self.run(*args, **kwargs)
+        return type(layer).forward(layer, *args, **kwargs)
 
     def __deepcopy__(self, memo):
         if self.before is not None:
@@ -229,7 +241,8 @@ class KfacCapture:
                 before = m.__dict__.get("forward")
                 plain = getattr(m.forward, "__func__", None) is nn.Linear.forward and m.forward.__self__ is m
                 self.wrapped.append((m, before))
-                m.forward = _Taken(m, before, self._checkpointed(i, m) if plain else before)
+                m.forward = _Taken(m, None if plain else before, self._checkpointed(i, m) if plain else before)
+                self.hooks.append(m.register_forward_pre_hook(m.forward.note()))
             self.hooks.append(m.register_forward_hook(self._fwd(i)))
             self.hooks.append(m.register_full_backward_hook(self._bwd(i)))
         for i, bn in enumerate(self.bns):

@@ -219,3 +219,27 @@ def test_a_copy_is_captured_like_its_original():
         twin.a(torch.ones(2, 5))
     cap.remove()
     assert torch.equal(twin(torch.ones(2, 5)), net(torch.ones(2, 5)))
+
+
+def test_shallow_copies_of_layers():
+    """Replicas and other copies that share a layer's attributes compute with their own weights."""
+    import copy
+    net = Net()
+    cap = cap_mod.KfacCapture(net, checkpoint="int8")
+    x = torch.randn(2, 5)
+    for twin in (net.a._replicate_for_data_parallel(), copy.copy(net.a)):
+        twin.__dict__["_parameters"] = {}
+        twin.weight, twin.bias = torch.nn.Parameter(torch.zeros(6, 5)), torch.nn.Parameter(torch.full((6,), 2.0))
+        for _ in range(2):
+            out = twin(x)
+            assert torch.equal(out, torch.full((2, 6), 2.0))
+            out.sum().backward()
+            assert twin.bias.grad is not None and net.a.bias.grad is None
+            with torch.no_grad():
+                want = torch.nn.functional.linear(x, net.a.weight, net.a.bias)
+                assert torch.equal(net.a(x), want) and torch.equal(net.a.forward(x), want)
+        assert cap.act == [None, None] and cap.n == 0 and not cap.made
+    with pytest.raises(ValueError):     # the layer itself keeps its input: on a GPU
+        net.a(x)
+    cap.remove()
+    assert not net.a._forward_pre_hooks and "forward" not in net.a.__dict__
